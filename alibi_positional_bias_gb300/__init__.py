@@ -26,9 +26,11 @@ __all__ = [
     "alibi_selftest_fwd_timeout", "alibi_decode_underflow_bf16",
     "alibi_slopes_explicit", "alibi_attn_probs_f32_ex", "AlibiFwdOptions", "alibi_attn_bwd", "alibi_attn_bwd_f32",
     "alibi_kv_block_norms", "alibi_attn_decode_skip",
+    "alibi_kv4_block_bytes", "alibi_kv4_cache", "alibi_kv4_write", "alibi_kv4_read", "alibi_attn_decode_kv4",
 ]
 
 ALIBI_OK, ALIBI_ERR_INVALID, ALIBI_ERR_UNSUPPORTED, ALIBI_ERR_CUDA, ALIBI_ERR_TIMEOUT, ALIBI_ERR_CHECK = 0, -1, -2, -3, -4, -5
+ALIBI_ERR_RANGE = -6
 ALIBI_FWD_SKIP_UNDERFLOW, ALIBI_FWD_CLAMP, ALIBI_FWD_LOGDIST, ALIBI_FWD_SOFTCAP = 1, 2, 4, 8
 ALIBI_FWD_NOMINAL_ORDER = 16
 
@@ -102,6 +104,14 @@ def load(build_if_missing: bool = False):
         lib.alibi_selftest_fwd_timeout.restype = I
         lib.alibi_decode_underflow_bf16.argtypes = [vp, vp, I, I, I, I, F, vp, vp]
         lib.alibi_decode_underflow_bf16.restype = I
+        lib.alibi_kv4_block_bytes.argtypes = [I]
+        lib.alibi_kv4_block_bytes.restype = I
+        lib.alibi_kv4_write.argtypes = [vp, vp, vp, vp, vp, I, I, I, I, I, vp]
+        lib.alibi_kv4_write.restype = I
+        lib.alibi_kv4_read.argtypes = [vp, vp, vp, vp, vp, I, I, I, I, I, I, vp]
+        lib.alibi_kv4_read.restype = I
+        lib.alibi_attn_decode_kv4.argtypes = [vp, vp, vp, vp, vp, I, I, I, I, I, I, I, ctypes.POINTER(F), vp]
+        lib.alibi_attn_decode_kv4.restype = I
         for name in ("alibi_attn_fwd", "alibi_attn_fwd_f32", "alibi_attn_decode", "alibi_attn_decode_splits",
                      "alibi_attn_probs_f32",
                      "alibi_attn_underflow_bf16", "alibi_check_error", "alibi_slopes"):
@@ -386,6 +396,126 @@ def alibi_attn_decode_noalloc(q, kcache, vcache, out, stream=None):
     _check(load().alibi_attn_decode_noalloc(_ptr(q), _ptr(kcache), _ptr(vcache), _ptr(out), B, H, L, d,
                                             _stream(stream, q.device)), "alibi_attn_decode_noalloc")
     return out
+
+
+def alibi_kv4_block_bytes(d: int) -> int:
+    """Bytes of one 32-token block of the 4-bit KV cache for head size d."""
+    n = load().alibi_kv4_block_bytes(int(d))
+    if n < 0:
+        raise AlibiError(n, "alibi_kv4_block_bytes")
+    return n
+
+
+def alibi_kv4_cache(B: int, H: int, C: int, d: int, device=None):
+    """An empty 4-bit KV cache for B sequences of up to C tokens (a multiple of 32) and H KV heads of
+    size d: uint8 [B, H, C / 32, alibi_kv4_block_bytes(d)], uninitialised (rows are used once written)."""
+    import torch
+    if C < 1 or C % 32 != 0:
+        raise ValueError(f"C must be a positive multiple of 32, got {C}")
+    return torch.empty((B, H, C // 32, alibi_kv4_block_bytes(d)), dtype=torch.uint8,
+                       device="cuda" if device is None else device)
+
+
+def _need_kv4(cache, B, H, d):
+    """Check a 4-bit cache of B sequences and (if given) H heads of size d; returns its (heads, capacity)."""
+    import torch
+    _need(cache, torch.uint8, None, "cache")
+    if cache.dim() != 4 or cache.shape[0] != B or cache.shape[3] != 36 * max(d, 32) or H not in (None, cache.shape[1]):
+        raise ValueError(f"cache must have shape ({B}, {'heads' if H is None else H}, C / 32, {36 * max(d, 32)}), "
+                         f"got {tuple(cache.shape)}")
+    return cache.shape[1], cache.shape[2] * 32
+
+
+def _need_same_device(first, *rest):
+    for t in rest:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"all tensors must be on one device, got {first.device} and {t.device}")
+
+
+def _on(device):
+    """The library launches on the current device: make it the tensors' own."""
+    import torch
+    return torch.cuda.device(device)
+
+
+def _kv4_span(pos, count, B):
+    import torch
+    for t, name in ((pos, "pos"), (count, "count")):
+        if t is not None:
+            _need(t, torch.int32, (B,), name)
+
+
+def alibi_kv4_write(k, v, cache, pos=None, count=None, stream=None) -> None:
+    """Quantise new keys and values [B, H, T, d] (bf16) and write them into the 4-bit cache
+    (alibi_kv4_cache): token t < count[b] of sequence b to row pos[b] + t. pos and count are int32
+    CUDA tensors [B] (None: 0 and T). Sequences that do not fit are left out and reported by
+    alibi_check_error."""
+    import torch
+    _need(k, torch.bfloat16, None, "k")
+    if k.dim() != 4:
+        raise ValueError(f"k must have shape (B, H, T, d), got {tuple(k.shape)}")
+    B, H, T, d = k.shape
+    _need(v, torch.bfloat16, k.shape, "v")
+    _, C = _need_kv4(cache, B, H, d)
+    _kv4_span(pos, count, B)
+    _need_same_device(cache, k, v, pos, count)
+    with _on(cache.device):
+        _check(load().alibi_kv4_write(_ptr(k), _ptr(v), _ptr(cache), _ptr(pos), _ptr(count), B, H, T, C, d,
+                                      _stream(stream, cache.device)), "alibi_kv4_write")
+
+
+def alibi_kv4_read(cache, k, v, pos=None, count=None, stream=None):
+    """Read rows of the 4-bit cache back into k and v [B, H, T, d] (both bf16, or both fp32 for the
+    held values exactly): row pos[b] + t of sequence b to token t < count[b]; other tokens of k and v
+    are left as they were. pos and count as in alibi_kv4_write. Returns (k, v)."""
+    import torch
+    _need(k, torch.float32 if getattr(k, "dtype", None) == torch.float32 else torch.bfloat16, None, "k")
+    if k.dim() != 4:
+        raise ValueError(f"k must have shape (B, H, T, d), got {tuple(k.shape)}")
+    B, H, T, d = k.shape
+    _need(v, k.dtype, k.shape, "v")
+    _, C = _need_kv4(cache, B, H, d)
+    _kv4_span(pos, count, B)
+    _need_same_device(cache, k, v, pos, count)
+    with _on(cache.device):
+        _check(load().alibi_kv4_read(_ptr(cache), _ptr(k), _ptr(v), _ptr(pos), _ptr(count), B, H, T, C, d,
+                                     int(k.dtype == torch.float32), _stream(stream, cache.device)), "alibi_kv4_read")
+    return k, v
+
+
+def alibi_attn_decode_kv4(q, cache, lens=None, L=None, out=None, lse=None, slopes=None, stream=None):
+    """ALiBi attention of the newest T tokens of each sequence over the 4-bit cache that holds them.
+    q: bf16 [B, H, T, d], or [B, H, d] for one token; cache: uint8 [B, H_kv, C / 32, bytes], H a multiple
+    of H_kv; lens: int32 CUDA tensor [B] of lengths (None: all L); L: a bound on them (None: the
+    capacity C); slopes: H values (None: alibi_slopes(H)). Returns (out, lse): bf16 like q, fp32
+    without the last dimension."""
+    import torch
+    _need(q, torch.bfloat16, None, "q")
+    if q.dim() not in (3, 4):
+        raise ValueError(f"q must have shape (B, H, T, d) or (B, H, d), got {tuple(q.shape)}")
+    B, H, d = q.shape[0], q.shape[1], q.shape[-1]
+    T = q.shape[2] if q.dim() == 4 else 1
+    Hkv, C = _need_kv4(cache, B, None, d)
+    if lens is not None:
+        _need(lens, torch.int32, (B,), "lens")
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+    _need(out, torch.bfloat16, q.shape, "out")
+    _need(lse, torch.float32, q.shape[:-1], "lse")
+    _need_same_device(cache, q, lens, out, lse)
+    m = None
+    if slopes is not None:
+        m = np.ascontiguousarray(slopes, dtype=np.float32)
+        if m.shape != (H,):
+            raise ValueError(f"slopes: expected shape ({H},), got {m.shape}")
+    with _on(cache.device):
+        _check(load().alibi_attn_decode_kv4(_ptr(q), _ptr(cache), _ptr(lens), _ptr(out), _ptr(lse), B, H, Hkv, T,
+                                            C if L is None else int(L), C, d,
+                                            None if m is None else m.ctypes.data_as(ctypes.POINTER(ctypes.c_float)),
+                                            _stream(stream, cache.device)), "alibi_attn_decode_kv4")
+    return out, lse
 
 
 def alibi_attn_decode_splits(B: int, H: int, L: int, d: int) -> int:

@@ -332,6 +332,7 @@ const char *alibi_status_str(int status)
         case ALIBI_ERR_CUDA: return "ALIBI_ERR_CUDA: CUDA call or kernel launch failed";
         case ALIBI_ERR_TIMEOUT: return "ALIBI_ERR_TIMEOUT: a bounded device-side wait expired";
         case ALIBI_ERR_CHECK: return "ALIBI_ERR_CHECK: a debug-build address check failed";
+        case ALIBI_ERR_RANGE: return "ALIBI_ERR_RANGE: a position or length in device memory is outside the cache";
         default: return "unknown alibi status";
     }
 }
@@ -638,6 +639,7 @@ int alibi_check_error(void *stream)
     if (h[0] != 0u && cudaMemset(w, 0, sizeof(h)) != cudaSuccess) return ALIBI_ERR_CUDA;
     if (h[0] & ALIBI_DEV_CHECK) return ALIBI_ERR_CHECK;
     if (h[0] & ALIBI_DEV_TIMEOUT) return ALIBI_ERR_TIMEOUT;
+    if (h[0] == ALIBI_DEV_RANGE) return ALIBI_ERR_RANGE;
     if (h[0] != 0u) return ALIBI_ERR_CUDA;
     return ALIBI_OK;
 }

@@ -12,6 +12,7 @@ namespace alibi {
 constexpr uint32_t ALIBI_DEV_TIMEOUT = 1u;
 constexpr uint32_t ALIBI_DEV_BADSTATE = 2u;
 constexpr uint32_t ALIBI_DEV_CHECK = 4u;  // a debug-checks build found a bad address (checks.h)
+constexpr uint32_t ALIBI_DEV_RANGE = 8u;  // a position or length in device memory was outside the cache
 
 // Every device-side wait gives up after this long (ns).
 constexpr uint64_t kWaitLimitNs = 1000000000ull;

@@ -55,8 +55,10 @@ typedef enum {
     ALIBI_ERR_UNSUPPORTED = -2, /* valid request the library does not implement (e.g. d) */
     ALIBI_ERR_CUDA = -3,        /* a CUDA runtime/driver call or kernel launch failed    */
     ALIBI_ERR_TIMEOUT = -4,     /* a bounded device-side wait expired (see alibi_check_error) */
-    ALIBI_ERR_CHECK = -5        /* debug-checks build only: a kernel found a bad TMA / TMEM / shared
+    ALIBI_ERR_CHECK = -5,       /* debug-checks build only: a kernel found a bad TMA / TMEM / shared
                                    address, recorded it and skipped the access */
+    ALIBI_ERR_RANGE = -6        /* a kernel found a position or length in device memory outside the
+                                   cache and left that sequence out (see alibi_check_error) */
 } alibi_status;
 
 /* Library version as an integer (major * 10000 + minor * 100 + patch). */
@@ -292,6 +294,81 @@ ALIBI_API int alibi_attn_decode_noalloc(const void *q, const void *kcache, const
                       int B, int H, int L, int d, void *stream);
 
 /*
+ * 4-bit KV cache. The pages' KV-cache paragraph ("ALiBi: Attention with Linear
+ * Biases") keeps keys and values as they were computed; this cache holds them
+ * in 4.5 bits per element, grows in place and gives each sequence a length of
+ * its own, kept in device memory so that a captured graph follows it.
+ *
+ * cache: device uint8 [B, H_kv, C / 32, alibi_kv4_block_bytes(d)], 16-byte
+ * aligned, C a multiple of 32 (the capacity in tokens, at most 2^24). Rows that
+ * were never written hold whatever the buffer held; no call looks at them.
+ * d in {16, 32, 64, 128} (16 is stored as 32, with zeros).
+ *
+ * What it holds. A group is 32 consecutive elements of one token's key or value
+ * row (d = 16: all 16). x_m is its element of largest magnitude, the positive
+ * one if +x and -x tie. The group's scale is s = -x_m / 8, a bf16 number, and
+ * element x is held as the code u = min(15, floor(x / s + 8.5)) in 0..15, which
+ * stands for s (u - 8): x_m itself is exact, an element is off by at most |s| / 2,
+ * or by at most |s| within |s| / 2 of -x_m. The codes are those of exact
+ * arithmetic, the same on every device. A group whose largest magnitude is below
+ * 2^-100 is held as zeros; a group with an infinity or a NaN is all NaN.
+ *
+ * Layout of a block (32 tokens of one head; D = max(d, 32); byte of the pair of
+ * elements e, e + 1, the even one in the low four bits):
+ *   keys    row r, e = 32 n + 8 c + i:  r D/2 + c D/8 + 4 n + i/2
+ *   values  row r = 16 t + 8 p + 2 c + z, e = 32 n + 4 g + i:
+ *           16 D + 8 D t + 512 (n/2) + (4 g + c) min(D/4, 16) + 8 (n%2) + 4 p + 2 z + i/2
+ *   scales  row r, group n, keys (y = 0) or values (1), bf16:
+ *           32 D + r D/8 + 2 (y D/32 + n)
+ * It is the order in which the decode's tensor-core operands are unpacked. A byte
+ * never holds parts of two tokens, so writers of different rows do not race.
+ */
+
+/* Bytes of one block of the 4-bit cache (36 max(d, 32)), or a negative alibi_status. Host-only. */
+ALIBI_API int alibi_kv4_block_bytes(int d);
+
+/*
+ * Quantise new tokens and write them into the cache: token t < count[b] of
+ * sequence b goes to row pos[b] + t. k, v: device bf16 [B, H, T, d] (H the KV
+ * heads); pos, count: device int32 [B], or NULL for 0 and T. Other rows of the
+ * cache, and tokens from count[b] on, are left as they were. A sequence with
+ * pos[b] < 0, count[b] < 0, count[b] > T or pos[b] + count[b] > C is left out
+ * whole, and alibi_check_error returns ALIBI_ERR_RANGE. T in [1, C].
+ */
+ALIBI_API int alibi_kv4_write(const void *k, const void *v, void *cache, const int *pos, const int *count, int B,
+                              int H, int T, int C, int d, void *stream);
+
+/*
+ * Read rows back: row pos[b] + t of sequence b to token t < count[b] of k and v,
+ * device [B, H, T, d], fp32 = 0: bf16 (each value rounded once, to nearest even),
+ * fp32 = 1: fp32 (the held values exactly). Tokens from count[b] on are left as
+ * they were. pos, count and their errors as in alibi_kv4_write.
+ */
+ALIBI_API int alibi_kv4_read(const void *cache, void *k, void *v, const int *pos, const int *count, int B, int H,
+                             int T, int C, int d, int fp32, void *stream);
+
+/*
+ * Decode over the 4-bit cache: the attention of the newest T tokens of each
+ * sequence, whose keys and values are in the cache already. Query t of sequence
+ * b has position i = len[b] - T + t and sees rows j <= i:
+ *   x_j = q.k_j / sqrt(d) - m_h (i - j),  out = sum_j softmax_j(x) v_j,
+ * k and v the values the cache holds. q, out: device bf16 [B, H, T, d]; lse:
+ * device fp32 [B, H, T] = ln sum_j exp(x_j), or NULL. H query heads share
+ * Hkv KV heads, H / Hkv consecutive ones each (H a multiple of Hkv). T in [1, 16]:
+ * one token, or a few drafted ones checked at once. lens: device int32 [B], the
+ * lengths with the T tokens included, or NULL (every sequence has L); 0 <=
+ * lens[b] <= L <= C. L bounds the work that is planned: pass the largest length
+ * if it is known, or C in a graph that is replayed while the sequences grow. A
+ * query with i < 0 sees no row: its out is 0 and its lse -inf. A sequence
+ * with lens[b] outside [0, L] gets NaN in out and lse, and alibi_check_error returns
+ * ALIBI_ERR_RANGE. slopes: optional HOST array of H slopes as in
+ * alibi_fwd_options (NULL: alibi_slopes(H)).
+ * Rows past a sequence's length are not used, whatever they hold.
+ */
+ALIBI_API int alibi_attn_decode_kv4(const void *q, const void *cache, const int *lens, void *out, float *lse, int B,
+                                    int H, int Hkv, int T, int L, int C, int d, const float *slopes, void *stream);
+
+/*
  * Attention weights of the fp32 path (test and analysis export):
  * P[b,h,i,j] = exp(q_i.k_j/sqrt(d) - m_h (i - j) - lse[b,h,i]) for j <= i,
  * 0 for j > i. q, k: device fp32 [B, H, N, d]; lse: device fp32 [B, H, N]
@@ -364,7 +441,8 @@ ALIBI_API int alibi_selftest_fwd_timeout(const void *q, const void *k, const voi
  * ALIBI_ERR_CHECK if a kernel of the debug-checks build (the same library compiled
  * with -DALIBI_CHECKS: every TMA coordinate, TMEM address and shared-memory operand
  * tested before use) found a bad one (the second word of the status records the
- * check and the value), else ALIBI_OK. The word accumulates until it is collected here, but an
+ * check and the value), ALIBI_ERR_RANGE if a call on the 4-bit cache found a position or
+ * length outside it, else ALIBI_OK. The word accumulates until it is collected here, but an
  * uncollected error does not affect later calls: a kernel's waits give up early
  * only on a failure inside the same CTA, so calls made after a timeout compute
  * their results normally (the timeout is still reported by the next check).
