@@ -1,12 +1,40 @@
 // ALiBi attention of the newest tokens of each sequence over its 4-bit KV cache.
 //
 // Row (h, t) of sequence b is the query of head h at position i = len_b - T + t, with
-// len_b tokens in the cache (the new ones included), and h / (H / H_kv) its KV head:
+// len_b tokens in the cache (the new ones included), and h / G its KV head, G = H / H_kv:
 //   x_j = q.k_j / sqrt(d) - m_h (i - j),  j <= i,   out = sum_j softmax_j(x) v_j,
 // with k and v the values s (u - 8) that the cache's codes stand for (kv4.h).
+//
+// The G T rows of a KV head share its keys, so up to 8 rows form a chunk that one CTA
+// takes over one slice of the sequence. Each warp streams stages of 4608 bytes (128 / D
+// blocks) from HBM through a ring of its own in shared memory (cp.async.bulk, one
+// mbarrier per stage, no synchronisation between warps) and works on tiles of 16 tokens:
+//
+//   scores   acc_n = (U_n - 8) Q_n^T per group n of 32 elements, mma.m16n8k16 with u - 8 and
+//            q as fp16 operands, both exact: four bits under the exponent of 1024 are 1024 + u
+//            (or 1024 + 16 u), and one add or fma per pair leaves u - 8; q is scaled to
+//            [2^14, 2^15) per row, which holds elements down to 2^-32 of the row's largest.
+//            s_jn acc_n is the group's share of q.k_j: exact products summed in fp32. (Masked
+//            bits alone are operands too, the subnormals u 2^-24 and u 2^-20, without the add; but
+//            the tensor core aligns products by their nominal exponents, which cost 10 and 6
+//            bits of the sum, and the offset 8 then cancels against those: errors of
+//            2^-17 of 8 |s| were measured.)
+//   softmax  in base 2: p_j = 2^(x_j - R), summed in fp32, with a reference R of each row that is
+//            raised when some x_j exceeds it by 8.
+//   values   O^T += (U - 8)^T P^T per group, P_jn = p_j s_jn as fp16, taken as
+//            2^(x_j + e_j - M) (s_jn 2^-e_j), with
+//            2^(e_j - 1) <= max_n |s_jn| < 2^e_j and a second reference M for x_j + e_j, so
+//            it neither overflows nor vanishes whatever the magnitude of the values. Its
+//            rounding to 11 bits is the only one below fp32: off by at most 2^-11 of each
+//            product, a quarter of the bf16 output's own step.
+//
+// Warps, and then slices, are merged in fp32; the CTA that finishes a chunk last merges
+// its slices, so no CTA waits for another.
 
+#include <cfloat>
 #include <cmath>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "alibi.h"
 #include "kv4.h"
@@ -15,86 +43,513 @@
 namespace alibi {
 namespace {
 
+constexpr int kWarps = 8;
+constexpr int kStages = 3;          // ring depth of each warp
+constexpr int kStageBytes = 4608;   // 128 / D blocks of 36 D bytes
+constexpr int kRows = 8;            // query rows of a chunk (the columns of an mma)
+constexpr int kSmem = kWarps * kStages * kStageBytes;
+
 struct HeadSlopes {
     float log2e[kMaxHeads];
 };
 
 struct DecodeKv4Params {
-    const __nv_bfloat16 *q;  // [B, H, T, d]
+    const __nv_bfloat16 *q;  // [B, H, T, d]: the G T rows of a KV head are consecutive
     const uint8_t *cache;    // [B, H_kv, C / 32, block]
     const int *lens;         // [B] or null
     __nv_bfloat16 *out;      // [B, H, T, d]
     float *lse;              // [B, H, T] or null
+    float *part;             // [B H_kv chunks][splits][kRows][D + 2], used when splits > 1
+    unsigned *count;         // [B H_kv chunks] splits finished, zero at launch
     uint32_t *status;
-    int H, Hkv, T, L, C, d;
-    float c1;  // log2(e) / sqrt(d)
+    int Hkv, T, L, blocks, d;  // blocks: C / 32
+    int rows, chunks, splits;  // G T, ceil(G T / 8)
+    float c1;                  // 2^-14 log2(e) / sqrt(d)
     HeadSlopes slopes;
 };
 
-constexpr int kWarps = 4;
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Transpose of an 8 x 8 matrix of halves spread over the warp (lane 4 i + c: row i, columns 2c, 2c + 1).
+__device__ __forceinline__ uint32_t transpose8(uint32_t a)
+{
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
+{
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// N words (1, 2 or 4) of shared memory in one load
+template <int N>
+__device__ __forceinline__ void lds(uint32_t (&w)[N], const uint8_t *p)
+{
+    if constexpr (N == 4) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(p);
+        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+    } else if constexpr (N == 2) {
+        const uint2 x = *reinterpret_cast<const uint2 *>(p);
+        w[0] = x.x, w[1] = x.y;
+    } else {
+        w[0] = *reinterpret_cast<const uint32_t *>(p);
+    }
+}
+
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c)
+{
+    uint32_t d;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+
+// The codes of a word as four fp16 pairs: r[i] = (u_i - 8, u_{i+4} - 8).
+__device__ __forceinline__ void unpack(uint32_t w, uint32_t (&r)[4])
+{
+    constexpr uint32_t k1024 = 0x64006400u, k1032 = 0x64086408u, kSixteenth = 0x2c002c00u, kMinus72 = 0xd480d480u;
+    const uint32_t t = w >> 8;
+    r[0] = hsub2((w & 0x000f000fu) | k1024, k1032);
+    r[1] = hfma2((w & 0x00f000f0u) | k1024, kSixteenth, kMinus72);
+    r[2] = hsub2((t & 0x000f000fu) | k1024, k1032);
+    r[3] = hfma2((t & 0x00f000f0u) | k1024, kSixteenth, kMinus72);
+}
 
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32) decode_kv4_kernel(const __grid_constant__ DecodeKv4Params p)
+struct State {  // of one warp; column k of a lane is row 2c + k of the chunk
+    static constexpr int NG = D / 32;
+    uint32_t q[NG][4];      // B operands: row lane / 4, elements 32 n + 8 c + (i, i + 4)
+    float kappa[2];         // from s acc to base-2 logits
+    float slope[2];         // m log2(e)
+    int pos[2];
+    float R[2], M[2], l[2];
+    float acc[NG][2][4];    // elements 32 n + 4 g + (0, 2) in [0], + (1, 3) in [1]; columns (2c, 2c + 1)
+};
+
+// One tile of 16 tokens from j0 at `blk` (its half of a block: `half`). MASK: some query does not see all of them.
+template <int D, bool MASK>
+__device__ __forceinline__ void tile(State<D> &st, const uint8_t *blk, int half, int j0, int lane)
 {
-    constexpr int E = D / 32;  // elements per lane
-    __shared__ float sm_m[kWarps], sm_l[kWarps], sm_o[kWarps][D];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int row = blockIdx.x;  // (b, h, t)
-    const int t = row % p.T, bh = row / p.T, h = bh % p.H, b = bh / p.H;
-    const int len = p.lens ? p.lens[b] : p.L;
-    const bool bad = len < 0 || len > p.L;
-    if (bad && h == 0 && t == 0 && threadIdx.x == 0) atomicOr(p.status, ALIBI_DEV_RANGE);
-    const int at = bad ? -1 : len - p.T + t;
-    const uint8_t *cache = p.cache + static_cast<size_t>(b * p.Hkv + h / (p.H / p.Hkv)) * (p.C / kv4::kBlock) *
-                                         kv4::block_bytes(D);
-    float q[E], o[E], m = -INFINITY, l = 0.0f;
+    constexpr int NG = D / 32;
+    const int g = lane >> 2, c = lane & 3;
+    uint32_t kw[2][NG], sw[2][NG], vw[NG][2];
+    const uint8_t *kp = blk + half * 8 * D + g * (D / 2) + c * (D / 8);
+    const uint8_t *sp = blk + 32 * D + (half * 16 + g) * (D / 8);
+    lds<NG>(kw[0], kp);
+    lds<NG>(kw[1], kp + 4 * D);
+    lds<NG>(sw[0], sp);
+    lds<NG>(sw[1], sp + D);
+    const uint8_t *vp = blk + 16 * D + half * 8 * D;
+    if constexpr (NG == 1) {
+        lds<2>(vw[0], vp + lane * 8);
+    } else {
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-        const int e = E * lane + i;
-        q[i] = e < p.d ? __bfloat162float(p.q[static_cast<size_t>(row) * p.d + e]) * p.c1 : 0.0f;
-        o[i] = 0.0f;
+        for (int n = 0; n < NG; n += 2) {
+            uint32_t w[4];
+            lds<4>(w, vp + n * 256 + lane * 16);
+            vw[n][0] = w[0], vw[n][1] = w[1], vw[n + 1][0] = w[2], vw[n + 1][1] = w[3];
+        }
     }
-    for (int j = warp; j <= at; j += kWarps) {
-        const uint8_t *blk = cache + static_cast<size_t>(j / kv4::kBlock) * kv4::block_bytes(D);
-        const int r = j % kv4::kBlock;
-        float x = 0.0f, v[E];
+
+    // logits: x[2 h + k] of token g + 8 h and row 2c + k
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            const int e = E * lane + i, sh = 4 * (e & 1);
-            const float sk = __uint_as_float(
-                uint32_t(*reinterpret_cast<const uint16_t *>(blk + kv4::scale_byte(D, r, 0, e / 32))) << 16);
-            const float sv = __uint_as_float(
-                uint32_t(*reinterpret_cast<const uint16_t *>(blk + kv4::scale_byte(D, r, 1, e / 32))) << 16);
-            x = fmaf(q[i], sk * (float((blk[kv4::key_byte(D, r, e & ~1)] >> sh) & 15) - 8.0f), x);
-            v[i] = sv * (float((blk[kv4::value_byte(D, r, e & ~1)] >> sh) & 15) - 8.0f);
+    for (int n = 0; n < NG; ++n) {
+        uint32_t a[4], b[4];
+        unpack(kw[0][n], a);
+        unpack(kw[1][n], b);
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+        mma16816(s, a[0], b[0], a[1], b[1], st.q[n][0], st.q[n][1]);
+        mma16816(s, a[2], b[2], a[3], b[3], st.q[n][2], st.q[n][3]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float sk = (n & 1) ? bf16_hi(sw[h][n / 2]) : bf16_lo(sw[h][n / 2]);
+            x[2 * h] = fmaf(sk, s[2 * h], x[2 * h]);
+            x[2 * h + 1] = fmaf(sk, s[2 * h + 1], x[2 * h + 1]);
+        }
+    }
+    const int j = j0 + g;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const float bias = st.slope[k] * static_cast<float>(j - st.pos[k]);
+        x[k] = fmaf(st.kappa[k], x[k], bias);
+        x[2 + k] = fmaf(st.kappa[k], x[2 + k], fmaf(8.0f, st.slope[k], bias));
+        if (MASK) {
+            if (j > st.pos[k]) x[k] = -INFINITY;
+            if (j + 8 > st.pos[k]) x[2 + k] = -INFINITY;
+        }
+    }
+
+    // e_j from the largest exponent of the value scales (a NaN scale: +inf, which leads to the slow path)
+    float e[2], down[2];
+    uint32_t big[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t m;
+        if constexpr (NG == 1)
+            m = sw[h][0] >> 16 & 0x7fffu;
+        else if constexpr (NG == 2)
+            m = max(sw[h][1] & 0x7fffu, sw[h][1] >> 16 & 0x7fffu);
+        else {
+            m = __vmaxu2(sw[h][2] & 0x7fff7fffu, sw[h][3] & 0x7fff7fffu);
+            m = max(m & 0xffffu, m >> 16);
+        }
+        big[h] = m >> 7;
+        e[h] = big[h] == 255u ? INFINITY : static_cast<float>(static_cast<int>(big[h]) - 126);
+    }
+    float y[4], top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        y[i] = x[i] + e[i >> 1];
+        top = fmaxf(top, fmaxf(x[i] - st.R[i & 1] - 8.0f, y[i] - st.M[i & 1] - 15.0f));
+    }
+    if (__any_sync(0xffffffffu, top > 0.0f)) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (big[h] == 255u) {  // leave the NaN groups out
+                uint32_t m = 0;
+#pragma unroll
+                for (int n = 0; n < NG; ++n) {
+                    const uint32_t w = NG == 1 ? sw[h][0] >> 16 : sw[h][NG / 2 + n / 2] >> (16 * (n & 1));
+                    if ((w & 0x7f80u) != 0x7f80u) m = max(m, w >> 7 & 0xffu);
+                }
+                big[h] = m;
+                const float ee = static_cast<float>(static_cast<int>(m) - 126);
+                y[2 * h] = x[2 * h] + ee;
+                y[2 * h + 1] = x[2 * h + 1] + ee;
+            }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            float mx = fmaxf(x[k], x[2 + k]), my = fmaxf(y[k], y[2 + k]);
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) {
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, off));
+            }
+            const float r = fmaxf(st.R[k], mx), m = fmaxf(st.M[k], my - 7.0f);
+            st.l[k] *= ex2_approx(st.R[k] - r);
+            const float be = ex2_approx(st.M[k] - m);
+            st.R[k] = r;
+            st.M[k] = m;
+#pragma unroll
+            for (int n = 0; n < NG; ++n) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    st.acc[n][i][k] *= be;
+                    st.acc[n][i][2 + k] *= be;
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) down[h] = __uint_as_float((253u - big[h]) << 23);  // 2^-e
+    float w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        st.l[i & 1] += ex2_approx(x[i] - st.R[i & 1]);
+        w[i] = ex2_approx(y[i] - st.M[i & 1]);
+    }
+#pragma unroll
+    for (int n = 0; n < NG; ++n) {
+        uint32_t pb[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t word = sw[h][NG == 1 ? 0 : NG / 2 + n / 2];
+            const float sv = ((NG == 1 || (n & 1)) ? bf16_hi(word) : bf16_lo(word)) * down[h];
+            float p0 = w[2 * h] * sv, p1 = w[2 * h + 1] * sv;
+            if (MASK) {  // a NaN scale of a token that the query does not see stays out
+                if (j + 8 * h > st.pos[0]) p0 = 0.0f;
+                if (j + 8 * h > st.pos[1]) p1 = 0.0f;
+            }
+            pb[h] = transpose8(pack_f16x2(p0, p1));
+        }
+        uint32_t a[4], b[4];
+        unpack(vw[n][0], a);
+        unpack(vw[n][1], b);
+        mma16816(st.acc[n][0], a[0], a[2], b[0], b[2], pb[0], pb[1]);
+        mma16816(st.acc[n][1], a[1], a[3], b[1], b[3], pb[0], pb[1]);
+    }
+}
+
+// Merge of n partials of 4 elements of a row: `at(i)` gives partial i's R, l and mean. The weights l 2^(R - max R)
+// are normalised before they meet the means, so nothing overflows.
+struct Merged {
+    float R, l;
+    float4 o;
+};
+
+template <class RL, class Mean>
+__device__ __forceinline__ Merged merge(int n, RL rl, Mean mean)
+{
+    Merged m = {-FLT_MAX, 0.0f, make_float4(0.f, 0.f, 0.f, 0.f)};
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) m.R = fmaxf(m.R, rl(i).x);
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+        const float2 x = rl(i);
+        m.l = fmaf(x.y, ex2_approx(x.x - m.R), m.l);
+    }
+    const float inv = m.l == 0.0f ? 0.0f : 1.0f / m.l;
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+        const float2 x = rl(i);
+        const float a = x.y * ex2_approx(x.x - m.R) * inv;
+        const float4 v = mean(i);
+        m.o.x = fmaf(v.x, a, m.o.x), m.o.y = fmaf(v.y, a, m.o.y);
+        m.o.z = fmaf(v.z, a, m.o.z), m.o.w = fmaf(v.w, a, m.o.w);
+    }
+    return m;
+}
+
+// One row's result: 4 elements of out, and lse by the thread of element 0.
+__device__ __forceinline__ void finish(const DecodeKv4Params &p, size_t row, int e, const Merged &m, bool bad)
+{
+    const float nan = __uint_as_float(0x7fc00000u);
+    if (e < p.d) {
+        uint2 w;
+        w.x = bad ? 0x7fc07fc0u : pack_bf16x2(m.o.x, m.o.y);
+        w.y = bad ? 0x7fc07fc0u : pack_bf16x2(m.o.z, m.o.w);
+        *reinterpret_cast<uint2 *>(p.out + row * p.d + e) = w;
+    }
+    if (e == 0 && p.lse) p.lse[row] = bad ? nan : m.l == 0.0f ? -INFINITY : (m.R + log2f(m.l)) * 0.6931471805599453f;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid_constant__ DecodeKv4Params p)
+{
+    constexpr int NG = D / 32, SB = 128 / D, kBlk = 36 * D;
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ __align__(8) uint64_t full[kWarps][kStages];
+    __shared__ bool last;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const int split = static_cast<int>(blockIdx.x % p.splits), unit = static_cast<int>(blockIdx.x / p.splits);
+    const int chunk = unit % p.chunks, bk = unit / p.chunks, hk = bk % p.Hkv, b = bk / p.Hkv;
+    const int row0 = chunk * kRows, nrows = min(kRows, p.rows - row0);
+    const int len_in = p.lens ? __ldg(p.lens + b) : p.L;
+    const bool bad = len_in < 0 || len_in > p.L;
+    const int len = bad ? 0 : len_in;
+
+    if (threadIdx.x == 0) {
+        cta_err_init(kWaitLimitNs);
+        cta_check_init(p.status, ring, kSmem);
+        if (bad && split == 0) atomicOr(p.status, ALIBI_DEV_RANGE);
+    }
+    if (lane == 0) {
+        for (int i = 0; i < kStages; ++i) mbar_init(&full[warp][i], 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+
+    // this CTA's stages [s0, s1) of the sequence, dealt to its warps in turn
+    const int nblk = (len + kv4::kBlock - 1) / kv4::kBlock, nst = (nblk + SB - 1) / SB;
+    const int per = nst / p.splits, extra = nst % p.splits;
+    const int s0 = split * per + min(split, extra), s1 = s0 + per + (split < extra ? 1 : 0);
+    const uint8_t *src = p.cache + static_cast<size_t>(bk) * p.blocks * kBlk;
+    uint8_t *mine = ring + warp * (kStages * kStageBytes);
+    auto fetch = [&](int s, int slot) {
+        const uint32_t bytes = static_cast<uint32_t>(min(SB, nblk - s * SB)) * kBlk;
+        mbar_arrive_expect_tx(&full[warp][slot], bytes);
+        bulk_load(mine + slot * kStageBytes, src + static_cast<size_t>(s) * kStageBytes, bytes, &full[warp][slot]);
+    };
+    if (lane == 0)
+        for (int i = 0; i < kStages; ++i)
+            if (s0 + warp + i * kWarps < s1) fetch(s0 + warp + i * kWarps, i);
+
+    State<D> st;
+    {
+        // this lane's slice of row g: the 8 elements from 8 c of every group
+        uint32_t qw[NG][4], top = 0;
+        const bool in = g < nrows;
+        const __nv_bfloat16 *qp = p.q + (static_cast<size_t>(bk) * p.rows + row0 + (in ? g : 0)) * p.d;
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (in && 32 * n + 8 * c < p.d) w = *reinterpret_cast<const uint4 *>(qp + 32 * n + 8 * c);
+            qw[n][0] = w.x, qw[n][1] = w.y, qw[n][2] = w.z, qw[n][3] = w.w;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top = __vmaxu2(top, qw[n][i] & 0x7fff7fffu);
+        }
+        top = max(top & 0xffffu, top >> 16);
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const uint32_t ex = max(top >> 7, 14u);
+        const float up = __uint_as_float((268u - ex) << 23);  // 2^14 over the largest element's power of two
+        const float kappa = __uint_as_float(ex << 23) * p.c1;
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                st.q[n][i] = (i & 1) ? pack_f16x2(bf16_hi(qw[n][i / 2]) * up, bf16_hi(qw[n][2 + i / 2]) * up)
+                                     : pack_f16x2(bf16_lo(qw[n][i / 2]) * up, bf16_lo(qw[n][2 + i / 2]) * up);
+                st.acc[n][0][i] = st.acc[n][1][i] = 0.0f;
+            }
         }
 #pragma unroll
-        for (int off = 16; off; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-        x = fmaf(-p.slopes.log2e[h], static_cast<float>(at - j), x);
-        const float mn = fmaxf(m, x), a = ex2_approx(m - mn), w = ex2_approx(x - mn);
-        m = mn;
-        l = fmaf(l, a, w);
-#pragma unroll
-        for (int i = 0; i < E; ++i) o[i] = fmaf(o[i], a, w * v[i]);
+        for (int k = 0; k < 2; ++k) {
+            const int r = min(row0 + 2 * c + k, p.rows - 1);
+            const int G = p.rows / p.T;
+            st.kappa[k] = __shfl_sync(0xffffffffu, kappa, (2 * c + k) * 4);
+            st.slope[k] = p.slopes.log2e[hk * G + r / p.T];
+            st.pos[k] = len - p.T + r % p.T;
+            st.R[k] = st.M[k] = -FLT_MAX;
+            st.l[k] = 0.0f;
+        }
     }
-    if (lane == 0) sm_m[warp] = m, sm_l[warp] = l;
+
+    int slot = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    int s = s0 + warp;
+    for (; s < s1; s += kWarps) {
+        ok = mbar_wait(&full[warp][slot], phase, p.status, 0x60);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        const uint8_t *stage = mine + slot * kStageBytes;
+#pragma unroll 1
+        for (int t = 0; t < 2 * SB; ++t) {
+            const int j0 = s * (SB * kv4::kBlock) + t * kv4::kTile;
+            if (j0 >= len) break;
+            if (j0 + kv4::kTile > len - p.T + 1)
+                tile<D, true>(st, stage + (t >> 1) * kBlk, t & 1, j0, lane);
+            else
+                tile<D, false>(st, stage + (t >> 1) * kBlk, t & 1, j0, lane);
+        }
+        __syncwarp();
+        if (lane == 0 && s + kStages * kWarps < s1) fetch(s + kStages * kWarps, slot);
+        if (++slot == kStages) slot = 0, phase ^= 1u;
+    }
+    if (s < s1) {  // a wait ran out (recorded): let the copies in flight land before the ring is reused
+        for (int i = 0; i < kStages && s < s1; ++i, s += kWarps) {
+            mbar_wait(&full[warp][slot], phase, p.status, 0x61, true);
+            if (++slot == kStages) slot = 0, phase ^= 1u;
+        }
+    }
+
+    // the warp's partial: reference R, l = sum of p, and the mean of v (never beyond the largest |v|)
+    float *pw = reinterpret_cast<float *>(mine);  // [kRows][D + 4], then R and l of each row
+    constexpr int kRowStride = D + 4;
 #pragma unroll
-    for (int i = 0; i < E; ++i) sm_o[warp][E * lane + i] = o[i];
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) st.l[k] += __shfl_xor_sync(0xffffffffu, st.l[k], off);
+        const float f = ex2_approx(st.M[k] - st.R[k]) * (st.l[k] == 0.0f ? 0.0f : 1.0f / st.l[k]);
+        const int r = 2 * c + k;
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+            const float4 o = make_float4(st.acc[n][0][k] * f, st.acc[n][1][k] * f, st.acc[n][0][2 + k] * f,
+                                         st.acc[n][1][2 + k] * f);
+            *reinterpret_cast<float4 *>(pw + r * kRowStride + 32 * n + 4 * g) = o;
+        }
+        if (g == 0) {
+            *reinterpret_cast<float2 *>(pw + kRows * kRowStride + 2 * r) = make_float2(st.R[k], st.l[k]);
+        }
+    }
     __syncthreads();
-    float M = -INFINITY, Ls = 0.0f;
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w]);
-    for (int w = 0; w < kWarps; ++w) Ls += sm_m[w] == -INFINITY ? 0.0f : sm_l[w] * ex2_approx(sm_m[w] - M);
-    const float none = bad ? __uint_as_float(0x7fc00000u) : 0.0f;
-    for (int e = threadIdx.x; e < p.d; e += kWarps * 32) {
-        float O = 0.0f;
-        for (int w = 0; w < kWarps; ++w) O += sm_m[w] == -INFINITY ? 0.0f : sm_o[w][e] * ex2_approx(sm_m[w] - M);
-        p.out[static_cast<size_t>(row) * p.d + e] = __float2bfloat16_rn(at < 0 ? none : O / Ls);
+
+    const size_t out0 = static_cast<size_t>(bk) * p.rows + row0;
+    constexpr int kPart = kRows * (D + 2);  // floats of a split's partial: means, then (R, l) of each row
+    float *mypart = p.part + (static_cast<size_t>(unit) * p.splits + split) * kPart;
+    for (int i = threadIdx.x; i < nrows * (D / 4); i += kWarps * 32) {
+        const int r = i / (D / 4), e = i % (D / 4) * 4;
+        const float *base = reinterpret_cast<const float *>(ring);
+        constexpr int kStep = kStages * kStageBytes / 4;
+        const Merged m = merge(
+            kWarps, [&](int w) { return *reinterpret_cast<const float2 *>(base + w * kStep + kRows * kRowStride + 2 * r); },
+            [&](int w) { return *reinterpret_cast<const float4 *>(base + w * kStep + r * kRowStride + e); });
+        if (p.splits == 1) {
+            finish(p, out0 + r, e, m, bad);
+        } else {
+            *reinterpret_cast<float4 *>(mypart + r * D + e) = m.o;
+            if (e == 0) *reinterpret_cast<float2 *>(mypart + kRows * D + 2 * r) = make_float2(m.R, m.l);
+        }
     }
-    if (p.lse && threadIdx.x == 0)
-        p.lse[row] = bad ? none : at < 0 ? -INFINITY : (M + log2f(Ls)) * 0.6931471805599453f;
+    if (p.splits == 1) return;
+    // Count this split as done once its partial is visible device-wide; the CTA that counts a
+    // chunk last merges it.
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) last = atomicAdd(p.count + unit, 1u) == static_cast<unsigned>(p.splits - 1);
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    const float *parts = p.part + static_cast<size_t>(unit) * p.splits * kPart;
+    for (int i = threadIdx.x; i < nrows * (D / 4); i += kWarps * 32) {
+        const int r = i / (D / 4), e = i % (D / 4) * 4;
+        const Merged m = merge(
+            p.splits, [&](int k) { return __ldcg(reinterpret_cast<const float2 *>(parts + k * kPart + kRows * D + 2 * r)); },
+            [&](int k) { return __ldcg(reinterpret_cast<const float4 *>(parts + k * kPart + r * D + e)); });
+        finish(p, out0 + r, e, m, bad);
+    }
+}
+
+// Slices per chunk: the number that minimises (waves of CTAs) x (stages per CTA + a fixed cost
+// of a CTA's start and merge, in stages) plus the merge over slices.
+int splits_for(long long units, int nst)
+{
+    const long long slots = 2LL * num_sms();
+    int best = 1;
+    long long best_cost = -1;
+    const int most = (nst + kWarps - 1) / kWarps;  // a stage for every warp
+    for (int s = 1; s <= most && s <= 512; ++s) {
+        const long long waves = (units * s + slots - 1) / slots;
+        const long long cost = waves * ((nst + s - 1) / s + 12) * 8 + (s > 1 ? 64 + s : 0);
+        if (best_cost < 0 || cost < best_cost) {
+            best_cost = cost;
+            best = s;
+        }
+    }
+    return best;
 }
 
 bool aligned(const void *p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+template <int D>
+cudaError_t launch(DecodeKv4Params &p, long long units, cudaStream_t stream)
+{
+    const void *fn = reinterpret_cast<const void *>(&decode_kv4_kernel<D>);
+    cudaError_t e = prepare_kernel(fn, kSmem, 0);
+    if (e != cudaSuccess) return e;
+    const int nst = (p.L + 128 / D * kv4::kBlock - 1) / (128 / D * kv4::kBlock);
+    p.splits = splits_for(units, nst);
+    if (units * p.splits > 0x7fffffffLL) return cudaErrorInvalidValue;
+    char *ws = nullptr;
+    if (p.splits > 1) {
+        const size_t pb = (static_cast<size_t>(units) * p.splits * kRows * (D + 2) * sizeof(float) + 255) & ~size_t(255);
+        const size_t cb = static_cast<size_t>(units) * sizeof(unsigned);
+        e = cudaMallocFromPoolAsync(reinterpret_cast<void **>(&ws), pb + cb, decode_pool(), stream);
+        if (e != cudaSuccess) return e;
+        p.part = reinterpret_cast<float *>(ws);
+        p.count = reinterpret_cast<unsigned *>(ws + pb);
+        e = cudaMemsetAsync(p.count, 0, cb, stream);
+    }
+    if (e == cudaSuccess) {
+        decode_kv4_kernel<D><<<static_cast<unsigned>(units * p.splits), kWarps * 32, kSmem, stream>>>(p);
+        e = cudaGetLastError();
+    }
+    if (ws) {
+        const cudaError_t f = cudaFreeAsync(ws, stream);
+        if (e == cudaSuccess) e = f;
+    }
+    return e;
+}
 
 }  // namespace
 }  // namespace alibi
@@ -125,22 +580,26 @@ extern "C" int alibi_attn_decode_kv4(const void *q, const void *cache, const int
     p.lens = lens;
     p.out = static_cast<__nv_bfloat16 *>(out);
     p.lse = lse;
+    p.part = nullptr;
+    p.count = nullptr;
     p.status = device_status_word();
     if (!p.status) return ALIBI_ERR_CUDA;
-    p.H = H;
     p.Hkv = Hkv;
     p.T = T;
     p.L = L;
-    p.C = C;
+    p.blocks = C / kv4::kBlock;
     p.d = d;
-    p.c1 = 1.4426950408889634f / sqrtf(static_cast<float>(d));
+    p.rows = H / Hkv * T;
+    p.chunks = (p.rows + kRows - 1) / kRows;
+    p.c1 = 0x1p-14f * 1.4426950408889634f / sqrtf(static_cast<float>(d));
     for (int h = 0; h < H; ++h) p.slopes.log2e[h] = s.log2e[h];
-    const unsigned grid = static_cast<unsigned>(B * H * T);
+    const long long units = static_cast<long long>(B) * Hkv * p.chunks;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
     switch (kv4::padded(d)) {
-        case 128: decode_kv4_kernel<128><<<grid, kWarps * 32, 0, st>>>(p); break;
-        case 64: decode_kv4_kernel<64><<<grid, kWarps * 32, 0, st>>>(p); break;
-        default: decode_kv4_kernel<32><<<grid, kWarps * 32, 0, st>>>(p); break;
+        case 128: e = launch<128>(p, units, st); break;
+        case 64: e = launch<64>(p, units, st); break;
+        default: e = launch<32>(p, units, st); break;
     }
-    return cudaGetLastError() == cudaSuccess ? ALIBI_OK : ALIBI_ERR_CUDA;
+    return e == cudaSuccess ? ALIBI_OK : ALIBI_ERR_CUDA;
 }

@@ -26,6 +26,7 @@ enum : uint32_t {
     TMEM_COLS = 3,   // TMEM columns outside the CTA's allocation
     TMEM_LANES = 4,  // TMEM lanes outside the warp's quadrant
     SMEM_DESC = 5,   // MMA / copy operand outside the shared-memory window
+    BULK_LOAD = 6,   // untiled load: source, destination or size off the 16-byte grid, or destination outside the window
 };
 
 // 16-bit elements: a tiled copy starts on a 16-byte boundary when x is a multiple of 8.
@@ -39,6 +40,12 @@ ALIBI_HD inline bool tma_store_coords(int x, int y, int z) { return tma_x_aligne
 ALIBI_HD inline bool smem_range(uint32_t saddr, uint32_t bytes, uint32_t align, uint32_t lo, uint32_t hi)
 {
     return (saddr & (align - 1)) == 0 && saddr >= lo && saddr <= hi && bytes <= hi - saddr;
+}
+
+// An untiled bulk copy starts on 16-byte boundaries and copies whole 16-byte units.
+ALIBI_HD inline bool bulk_aligned(uint64_t gaddr, uint32_t saddr, uint32_t bytes)
+{
+    return ((gaddr | saddr | bytes) & 15u) == 0 && bytes != 0;
 }
 
 // TMEM address = (lane << 16) | column. `width` columns from the address's column lie

@@ -243,6 +243,19 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const void *tmap, int x, 
         : "memory");
 }
 
+// Untiled load of `bytes` contiguous bytes into shared memory, completing on `bar`.
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
+{
+#ifdef ALIBI_CHECKS
+    if (!check::bulk_aligned(reinterpret_cast<uint64_t>(src), smem_u32(dst), bytes) || !check_smem(smem_u32(dst), bytes, 16))
+        return check_fail(check::BULK_LOAD, smem_u32(dst));
+#endif
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar))
+        : "memory");
+}
+
 // 3-D tiled store of one box from shared memory (bulk-group completion). The
 // source must stay unchanged until bulk_wait_read() has returned; rows and columns
 // outside the tensor are not written.

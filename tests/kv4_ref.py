@@ -116,7 +116,7 @@ def decode(q, kh, vh, lens, m):
     of |q_e| 16 |s| are added and scaled with at most 40 roundings of 2^-24 (below 2^-18), the bias
     m (i - j) and its conversion to base 2 with 4: dx_j = 2^-18 sum_e |q_e| 16 |s_je| / sqrt(d) +
     2^-21 (m (i - j) + |x_j|) + 2^-34 max|q| sum_e 16 |s_je| / sqrt(d), the last term for elements of q
-    more than 2^28 times smaller than the row's largest, whose 16-bit form is inexact. A weight's
+    more than 2^32 times smaller than the row's largest, whose 16-bit form is inexact. A weight's
     relative error is then dx_j plus the same of the normaliser, plus 2^-11 for the rounding of weight
     times scale to 16 bits, plus 2^-20 for the exponentials and the sums of codes (up to 16 |s| each, fp32):
       |out - ref| <= sum_j W_j ((2^-11 + dx_j + D) |v_j| + 2^-19 16 |s_j|) + 2^-31 16 N max_j,n W_j |s_jn|,
