@@ -123,15 +123,23 @@ __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c)
     return d;
 }
 
+// (w & mask) | k1024 as the one operation it is
+__device__ __forceinline__ uint32_t under1024(uint32_t w, uint32_t mask)
+{
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(w), "r"(mask), "r"(0x64006400u));
+    return d;
+}
+
 // The codes of a word as four fp16 pairs: r[i] = (u_i - 8, u_{i+4} - 8).
 __device__ __forceinline__ void unpack(uint32_t w, uint32_t (&r)[4])
 {
-    constexpr uint32_t k1024 = 0x64006400u, k1032 = 0x64086408u, kSixteenth = 0x2c002c00u, kMinus72 = 0xd480d480u;
+    constexpr uint32_t k1032 = 0x64086408u, kSixteenth = 0x2c002c00u, kMinus72 = 0xd480d480u;
     const uint32_t t = w >> 8;
-    r[0] = hsub2((w & 0x000f000fu) | k1024, k1032);
-    r[1] = hfma2((w & 0x00f000f0u) | k1024, kSixteenth, kMinus72);
-    r[2] = hsub2((t & 0x000f000fu) | k1024, k1032);
-    r[3] = hfma2((t & 0x00f000f0u) | k1024, kSixteenth, kMinus72);
+    r[0] = hsub2(under1024(w, 0x000f000fu), k1032);
+    r[1] = hfma2(under1024(w, 0x00f000f0u), kSixteenth, kMinus72);
+    r[2] = hsub2(under1024(t, 0x000f000fu), k1032);
+    r[3] = hfma2(under1024(t, 0x00f000f0u), kSixteenth, kMinus72);
 }
 
 template <int D>
@@ -174,12 +182,12 @@ __device__ __forceinline__ void tile(State<D> &st, const uint8_t *blk, int half,
     float x[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int n = 0; n < NG; ++n) {
-        uint32_t a[4], b[4];
-        unpack(kw[0][n], a);
-        unpack(kw[1][n], b);
+        uint32_t k0[4], k1[4];
+        unpack(kw[0][n], k0);
+        unpack(kw[1][n], k1);
         float s[4] = {0.f, 0.f, 0.f, 0.f};
-        mma16816(s, a[0], b[0], a[1], b[1], st.q[n][0], st.q[n][1]);
-        mma16816(s, a[2], b[2], a[3], b[3], st.q[n][2], st.q[n][3]);
+        mma16816(s, k0[0], k1[0], k0[1], k1[1], st.q[n][0], st.q[n][1]);
+        mma16816(s, k0[2], k1[2], k0[3], k1[3], st.q[n][2], st.q[n][3]);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const float sk = (n & 1) ? bf16_hi(sw[h][n / 2]) : bf16_lo(sw[h][n / 2]);
@@ -199,8 +207,9 @@ __device__ __forceinline__ void tile(State<D> &st, const uint8_t *blk, int half,
         }
     }
 
-    // e_j from the largest exponent of the value scales (a NaN scale: +inf, which leads to the slow path)
-    float e[2], down[2];
+    // e_j from the largest exponent of the value scales. A NaN scale counts as 2^129 here, which either sends the
+    // warp to the slow path, where it is left out, or is below M anyway.
+    float e[2];
     uint32_t big[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -214,15 +223,16 @@ __device__ __forceinline__ void tile(State<D> &st, const uint8_t *blk, int half,
             m = max(m & 0xffffu, m >> 16);
         }
         big[h] = m >> 7;
-        e[h] = big[h] == 255u ? INFINITY : static_cast<float>(static_cast<int>(big[h]) - 126);
+        e[h] = __uint_as_float(0x4b000000u | big[h]) - (8388608.0f + 126.0f);
     }
-    float y[4], top = -INFINITY;
+    float a[4], b[4], top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        y[i] = x[i] + e[i >> 1];
-        top = fmaxf(top, fmaxf(x[i] - st.R[i & 1] - 8.0f, y[i] - st.M[i & 1] - 15.0f));
+        a[i] = x[i] - st.R[i & 1];
+        b[i] = x[i] + e[i >> 1] - st.M[i & 1];
+        top = fmaxf(top, fmaxf(a[i], b[i]));
     }
-    if (__any_sync(0xffffffffu, top > 0.0f)) {
+    if (__any_sync(0xffffffffu, top > 8.0f)) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
             if (big[h] == 255u) {  // leave the NaN groups out
@@ -233,19 +243,17 @@ __device__ __forceinline__ void tile(State<D> &st, const uint8_t *blk, int half,
                     if ((w & 0x7f80u) != 0x7f80u) m = max(m, w >> 7 & 0xffu);
                 }
                 big[h] = m;
-                const float ee = static_cast<float>(static_cast<int>(m) - 126);
-                y[2 * h] = x[2 * h] + ee;
-                y[2 * h + 1] = x[2 * h + 1] + ee;
+                e[h] = static_cast<float>(static_cast<int>(m) - 126);
             }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            float mx = fmaxf(x[k], x[2 + k]), my = fmaxf(y[k], y[2 + k]);
+            float mx = fmaxf(x[k], x[2 + k]), my = fmaxf(x[k] + e[0], x[2 + k] + e[1]);
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) {
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
                 my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, off));
             }
-            const float r = fmaxf(st.R[k], mx), m = fmaxf(st.M[k], my - 7.0f);
+            const float r = fmaxf(st.R[k], mx), m = fmaxf(st.M[k], my);
             st.l[k] *= ex2_approx(st.R[k] - r);
             const float be = ex2_approx(st.M[k] - m);
             st.R[k] = r;
@@ -258,15 +266,21 @@ __device__ __forceinline__ void tile(State<D> &st, const uint8_t *blk, int half,
                     st.acc[n][i][2 + k] *= be;
                 }
             }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                a[2 * h + k] = x[2 * h + k] - r;
+                b[2 * h + k] = x[2 * h + k] + e[h] - m;
+            }
         }
     }
+    // P <= 2^8 2^7: the 2^7 keeps small weights off fp16's subnormals. (No scale: the shift overflows, and meets zeros.)
+    float down[2], w[4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) down[h] = __uint_as_float((253u - big[h]) << 23);  // 2^-e
-    float w[4];
+    for (int h = 0; h < 2; ++h) down[h] = __uint_as_float((260u - big[h]) << 23);  // 2^(7 - e)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        st.l[i & 1] += ex2_approx(x[i] - st.R[i & 1]);
-        w[i] = ex2_approx(y[i] - st.M[i & 1]);
+        st.l[i & 1] += ex2_approx(a[i]);
+        w[i] = ex2_approx(b[i]);
     }
 #pragma unroll
     for (int n = 0; n < NG; ++n) {
@@ -282,11 +296,11 @@ __device__ __forceinline__ void tile(State<D> &st, const uint8_t *blk, int half,
             }
             pb[h] = transpose8(pack_f16x2(p0, p1));
         }
-        uint32_t a[4], b[4];
-        unpack(vw[n][0], a);
-        unpack(vw[n][1], b);
-        mma16816(st.acc[n][0], a[0], a[2], b[0], b[2], pb[0], pb[1]);
-        mma16816(st.acc[n][1], a[1], a[3], b[1], b[3], pb[0], pb[1]);
+        uint32_t v0[4], v1[4];
+        unpack(vw[n][0], v0);
+        unpack(vw[n][1], v1);
+        mma16816(st.acc[n][0], v0[0], v0[2], v1[0], v1[2], pb[0], pb[1]);
+        mma16816(st.acc[n][1], v0[1], v0[3], v1[1], v1[3], pb[0], pb[1]);
     }
 }
 
@@ -359,7 +373,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
     }
     __syncthreads();
 
-    // this CTA's stages [s0, s1) of the sequence, dealt to its warps in turn
+    // This CTA's stages [s0, s1) of the sequence, dealt to its warps in turn from the newest to the oldest: the
+    // bias falls on the way, so the references R and M settle in the first tiles. (Oldest first, a
+    // steep head raises them at every tile.)
     const int nblk = (len + kv4::kBlock - 1) / kv4::kBlock, nst = (nblk + SB - 1) / SB;
     const int per = nst / p.splits, extra = nst % p.splits;
     const int s0 = split * per + min(split, extra), s1 = s0 + per + (split < extra ? 1 : 0);
@@ -370,9 +386,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
         mbar_arrive_expect_tx(&full[warp][slot], bytes);
         bulk_load(mine + slot * kStageBytes, src + static_cast<size_t>(s) * kStageBytes, bytes, &full[warp][slot]);
     };
+    const int mine_end = s1 - 1 - warp;  // this warp's stages, newest first: mine_end, mine_end - kWarps, ...
     if (lane == 0)
         for (int i = 0; i < kStages; ++i)
-            if (s0 + warp + i * kWarps < s1) fetch(s0 + warp + i * kWarps, i);
+            if (mine_end - i * kWarps >= s0) fetch(mine_end - i * kWarps, i);
 
     State<D> st;
     {
@@ -418,26 +435,26 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
     int slot = 0;
     uint32_t phase = 0;
     bool ok = true;
-    int s = s0 + warp;
-    for (; s < s1; s += kWarps) {
+    int s = mine_end;
+    for (; s >= s0; s -= kWarps) {
         ok = mbar_wait(&full[warp][slot], phase, p.status, 0x60);
         if (!__all_sync(0xffffffffu, ok)) break;
         const uint8_t *stage = mine + slot * kStageBytes;
 #pragma unroll 1
-        for (int t = 0; t < 2 * SB; ++t) {
+        for (int t = 2 * SB - 1; t >= 0; --t) {
             const int j0 = s * (SB * kv4::kBlock) + t * kv4::kTile;
-            if (j0 >= len) break;
+            if (j0 >= len) continue;
             if (j0 + kv4::kTile > len - p.T + 1)
                 tile<D, true>(st, stage + (t >> 1) * kBlk, t & 1, j0, lane);
             else
                 tile<D, false>(st, stage + (t >> 1) * kBlk, t & 1, j0, lane);
         }
         __syncwarp();
-        if (lane == 0 && s + kStages * kWarps < s1) fetch(s + kStages * kWarps, slot);
+        if (lane == 0 && s - kStages * kWarps >= s0) fetch(s - kStages * kWarps, slot);
         if (++slot == kStages) slot = 0, phase ^= 1u;
     }
-    if (s < s1) {  // a wait ran out (recorded): let the copies in flight land before the ring is reused
-        for (int i = 0; i < kStages && s < s1; ++i, s += kWarps) {
+    if (s >= s0) {  // a wait ran out (recorded): let the copies in flight land before the ring is reused
+        for (int i = 0; i < kStages && s >= s0; ++i, s -= kWarps) {
             mbar_wait(&full[warp][slot], phase, p.status, 0x61, true);
             if (++slot == kStages) slot = 0, phase ^= 1u;
         }
@@ -450,7 +467,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
     for (int k = 0; k < 2; ++k) {
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) st.l[k] += __shfl_xor_sync(0xffffffffu, st.l[k], off);
-        const float f = ex2_approx(st.M[k] - st.R[k]) * (st.l[k] == 0.0f ? 0.0f : 1.0f / st.l[k]);
+        const float f = ex2_approx(st.M[k] - st.R[k] - 7.0f) * (st.l[k] == 0.0f ? 0.0f : 1.0f / st.l[k]);
         const int r = 2 * c + k;
 #pragma unroll
         for (int n = 0; n < NG; ++n) {
