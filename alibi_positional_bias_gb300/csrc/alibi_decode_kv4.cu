@@ -148,106 +148,107 @@ struct State {  // of one warp; column k of a lane is row 2c + k of the chunk
     uint32_t q[NG][4];      // B operands: row lane / 4, elements 32 n + 8 c + (i, i + 4)
     float kappa[2];         // from s acc to base-2 logits
     float slope[2];         // m log2(e)
-    int pos[2];
+    float pos[2];           // position less lane / 4
     float R[2], M[2], l[2];
     float acc[NG][2][4];    // elements 32 n + 4 g + (0, 2) in [0], + (1, 3) in [1]; columns (2c, 2c + 1)
 };
 
-// One tile of 16 tokens from j0 at `blk` (its half of a block: `half`). MASK: some query does not see all of them.
+// One block of 32 tokens from j0: two tiles whose chains of products, exponentials and products overlap. MASK: some
+// query does not see all of them.
 template <int D, bool MASK>
-__device__ __forceinline__ void tile(State<D> &st, const uint8_t *blk, int half, int j0, int lane)
+__device__ __forceinline__ void block32(State<D> &st, const uint8_t *blk, int j0, int lane)
 {
     constexpr int NG = D / 32;
     const int g = lane >> 2, c = lane & 3;
-    uint32_t kw[2][NG], sw[2][NG], vw[NG][2];
-    const uint8_t *kp = blk + half * 8 * D + g * (D / 2) + c * (D / 8);
-    const uint8_t *sp = blk + 32 * D + (half * 16 + g) * (D / 8);
-    lds<NG>(kw[0], kp);
-    lds<NG>(kw[1], kp + 4 * D);
-    lds<NG>(sw[0], sp);
-    lds<NG>(sw[1], sp + D);
-    const uint8_t *vp = blk + 16 * D + half * 8 * D;
-    if constexpr (NG == 1) {
-        lds<2>(vw[0], vp + lane * 8);
-    } else {
-#pragma unroll
-        for (int n = 0; n < NG; n += 2) {
-            uint32_t w[4];
-            lds<4>(w, vp + n * 256 + lane * 16);
-            vw[n][0] = w[0], vw[n][1] = w[1], vw[n + 1][0] = w[2], vw[n + 1][1] = w[3];
-        }
-    }
 
-    // logits: x[2 h + k] of token g + 8 h and row 2c + k
-    float x[4] = {0.f, 0.f, 0.f, 0.f};
+    // logits: x[i][k] of token g + 8 i and row 2c + k; sv: the words of the tokens' value scales
+    float x[4][2];
+    uint32_t sv[4][NG];
 #pragma unroll
-    for (int n = 0; n < NG; ++n) {
-        uint32_t k0[4], k1[4];
-        unpack(kw[0][n], k0);
-        unpack(kw[1][n], k1);
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
-        mma16816(s, k0[0], k1[0], k0[1], k1[1], st.q[n][0], st.q[n][1]);
-        mma16816(s, k0[2], k1[2], k0[3], k1[3], st.q[n][2], st.q[n][3]);
+    for (int t = 0; t < 2; ++t) {
+        uint32_t kw[2][NG];
+        const uint8_t *kp = blk + (t * 16 + g) * (D / 2) + c * (D / 8);
+        const uint8_t *sp = blk + 32 * D + (t * 16 + g) * (D / 8);
+        lds<NG>(kw[0], kp);
+        lds<NG>(kw[1], kp + 4 * D);
+        lds<NG>(sv[2 * t], sp);
+        lds<NG>(sv[2 * t + 1], sp + D);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const float sk = (n & 1) ? bf16_hi(sw[h][n / 2]) : bf16_lo(sw[h][n / 2]);
-            x[2 * h] = fmaf(sk, s[2 * h], x[2 * h]);
-            x[2 * h + 1] = fmaf(sk, s[2 * h + 1], x[2 * h + 1]);
+        for (int n = 0; n < NG; ++n) {
+            uint32_t k0[4], k1[4];
+            unpack(kw[0][n], k0);
+            unpack(kw[1][n], k1);
+            float s[4] = {0.f, 0.f, 0.f, 0.f};
+            mma16816(s, k0[0], k1[0], k0[1], k1[1], st.q[n][0], st.q[n][1]);
+            mma16816(s, k0[2], k1[2], k0[3], k1[3], st.q[n][2], st.q[n][3]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t w = sv[2 * t + h][n / 2];
+                const float sk = (n & 1) ? bf16_hi(w) : bf16_lo(w);
+                x[2 * t + h][0] = n == 0 ? sk * s[2 * h] : fmaf(sk, s[2 * h], x[2 * t + h][0]);
+                x[2 * t + h][1] = n == 0 ? sk * s[2 * h + 1] : fmaf(sk, s[2 * h + 1], x[2 * t + h][1]);
+            }
         }
     }
-    const int j = j0 + g;
+    const float jf = static_cast<float>(j0);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        const float bias = st.slope[k] * static_cast<float>(j - st.pos[k]);
-        x[k] = fmaf(st.kappa[k], x[k], bias);
-        x[2 + k] = fmaf(st.kappa[k], x[2 + k], fmaf(8.0f, st.slope[k], bias));
-        if (MASK) {
-            if (j > st.pos[k]) x[k] = -INFINITY;
-            if (j + 8 > st.pos[k]) x[2 + k] = -INFINITY;
+        const float bias = st.slope[k] * (jf - st.pos[k]);  // whole numbers below 2^24: exact; pos is less g
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[i][k] = fmaf(st.kappa[k], x[i][k], i == 0 ? bias : fmaf(8.0f * i, st.slope[k], bias));
+            if (MASK && jf + 8.0f * i > st.pos[k]) x[i][k] = -INFINITY;
         }
     }
 
     // e_j from the largest exponent of the value scales. A NaN scale counts as 2^129 here, which either sends the
     // warp to the slow path, where it is left out, or is below M anyway.
-    float e[2];
-    uint32_t big[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        uint32_t m;
-        if constexpr (NG == 1)
-            m = sw[h][0] >> 16 & 0x7fffu;
-        else if constexpr (NG == 2)
-            m = max(sw[h][1] & 0x7fffu, sw[h][1] >> 16 & 0x7fffu);
-        else {
-            m = __vmaxu2(sw[h][2] & 0x7fff7fffu, sw[h][3] & 0x7fff7fffu);
-            m = max(m & 0xffffu, m >> 16);
-        }
-        big[h] = m >> 7;
-        e[h] = __uint_as_float(0x4b000000u | big[h]) - (8388608.0f + 126.0f);
-    }
-    float a[4], b[4], top = -INFINITY;
+    float e[4];
+    uint32_t big[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        a[i] = x[i] - st.R[i & 1];
-        b[i] = x[i] + e[i >> 1] - st.M[i & 1];
-        top = fmaxf(top, fmaxf(a[i], b[i]));
+        uint32_t m;
+        if constexpr (NG == 1)
+            m = sv[i][0] >> 16 & 0x7fffu;
+        else if constexpr (NG == 2)
+            m = max(sv[i][1] & 0x7fffu, sv[i][1] >> 16 & 0x7fffu);
+        else {
+            m = __vmaxu2(sv[i][2] & 0x7fff7fffu, sv[i][3] & 0x7fff7fffu);
+            m = max(m & 0xffffu, m >> 16);
+        }
+        big[i] = m >> 7;
+        e[i] = __uint_as_float(0x4b000000u | big[i]) - (8388608.0f + 126.0f);
     }
+    float a[4][2], b[4][2], top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            a[i][k] = x[i][k] - st.R[k];
+            b[i][k] = x[i][k] + e[i] - st.M[k];
+            top = fmaxf(top, fmaxf(a[i][k], b[i][k]));
+        }
     if (__any_sync(0xffffffffu, top > 8.0f)) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-            if (big[h] == 255u) {  // leave the NaN groups out
+        for (int i = 0; i < 4; ++i)
+            if (big[i] == 255u) {  // leave the NaN groups out
                 uint32_t m = 0;
 #pragma unroll
                 for (int n = 0; n < NG; ++n) {
-                    const uint32_t w = NG == 1 ? sw[h][0] >> 16 : sw[h][NG / 2 + n / 2] >> (16 * (n & 1));
+                    const uint32_t w = NG == 1 ? sv[i][0] >> 16 : sv[i][NG / 2 + n / 2] >> (16 * (n & 1));
                     if ((w & 0x7f80u) != 0x7f80u) m = max(m, w >> 7 & 0xffu);
                 }
-                big[h] = m;
-                e[h] = static_cast<float>(static_cast<int>(m) - 126);
+                big[i] = m;
+                e[i] = static_cast<float>(static_cast<int>(m) - 126);
             }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            float mx = fmaxf(x[k], x[2 + k]), my = fmaxf(x[k] + e[0], x[2 + k] + e[1]);
+            float mx = -INFINITY, my = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                mx = fmaxf(mx, x[i][k]);
+                my = fmaxf(my, x[i][k] + e[i]);
+            }
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) {
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
@@ -267,40 +268,60 @@ __device__ __forceinline__ void tile(State<D> &st, const uint8_t *blk, int half,
                 }
             }
 #pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                a[i][k] = x[i][k] - r;
+                b[i][k] = x[i][k] + e[i] - m;
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            st.l[k] += ex2_approx(a[i][k]);
+            b[i][k] = ex2_approx(b[i][k]);
+        }
+
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        uint32_t vw[NG][2];
+        const uint8_t *vp = blk + 16 * D + t * 8 * D;
+        if constexpr (NG == 1) {
+            lds<2>(vw[0], vp + lane * 8);
+        } else {
+#pragma unroll
+            for (int n = 0; n < NG; n += 2) {
+                uint32_t w[4];
+                lds<4>(w, vp + n * 256 + lane * 16);
+                vw[n][0] = w[0], vw[n][1] = w[1], vw[n + 1][0] = w[2], vw[n + 1][1] = w[3];
+            }
+        }
+        // P <= 2^8 2^7: the 2^7 keeps small weights off fp16's subnormals. (No scale: the shift overflows, and meets
+        // zeros.)
+        float down[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) down[h] = __uint_as_float((260u - big[2 * t + h]) << 23);  // 2^(7 - e)
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+            uint32_t pb[2];
+#pragma unroll
             for (int h = 0; h < 2; ++h) {
-                a[2 * h + k] = x[2 * h + k] - r;
-                b[2 * h + k] = x[2 * h + k] + e[h] - m;
+                const int i = 2 * t + h;
+                const uint32_t word = sv[i][NG == 1 ? 0 : NG / 2 + n / 2];
+                const float s = ((NG == 1 || (n & 1)) ? bf16_hi(word) : bf16_lo(word)) * down[h];
+                float p0 = b[i][0] * s, p1 = b[i][1] * s;
+                if (MASK) {  // a NaN scale of a token that the query does not see stays out
+                    if (jf + 8.0f * i > st.pos[0]) p0 = 0.0f;
+                    if (jf + 8.0f * i > st.pos[1]) p1 = 0.0f;
+                }
+                pb[h] = transpose8(pack_f16x2(p0, p1));
             }
+            uint32_t v0[4], v1[4];
+            unpack(vw[n][0], v0);
+            unpack(vw[n][1], v1);
+            mma16816(st.acc[n][0], v0[0], v0[2], v1[0], v1[2], pb[0], pb[1]);
+            mma16816(st.acc[n][1], v0[1], v0[3], v1[1], v1[3], pb[0], pb[1]);
         }
-    }
-    // P <= 2^8 2^7: the 2^7 keeps small weights off fp16's subnormals. (No scale: the shift overflows, and meets zeros.)
-    float down[2], w[4];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) down[h] = __uint_as_float((260u - big[h]) << 23);  // 2^(7 - e)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        st.l[i & 1] += ex2_approx(a[i]);
-        w[i] = ex2_approx(b[i]);
-    }
-#pragma unroll
-    for (int n = 0; n < NG; ++n) {
-        uint32_t pb[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t word = sw[h][NG == 1 ? 0 : NG / 2 + n / 2];
-            const float sv = ((NG == 1 || (n & 1)) ? bf16_hi(word) : bf16_lo(word)) * down[h];
-            float p0 = w[2 * h] * sv, p1 = w[2 * h + 1] * sv;
-            if (MASK) {  // a NaN scale of a token that the query does not see stays out
-                if (j + 8 * h > st.pos[0]) p0 = 0.0f;
-                if (j + 8 * h > st.pos[1]) p1 = 0.0f;
-            }
-            pb[h] = transpose8(pack_f16x2(p0, p1));
-        }
-        uint32_t v0[4], v1[4];
-        unpack(vw[n][0], v0);
-        unpack(vw[n][1], v1);
-        mma16816(st.acc[n][0], v0[0], v0[2], v1[0], v1[2], pb[0], pb[1]);
-        mma16816(st.acc[n][1], v0[1], v0[3], v1[1], v1[3], pb[0], pb[1]);
     }
 }
 
@@ -426,7 +447,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
             const int G = p.rows / p.T;
             st.kappa[k] = __shfl_sync(0xffffffffu, kappa, (2 * c + k) * 4);
             st.slope[k] = p.slopes.log2e[hk * G + r / p.T];
-            st.pos[k] = len - p.T + r % p.T;
+            st.pos[k] = static_cast<float>(len - p.T + r % p.T - g);
             st.R[k] = st.M[k] = -FLT_MAX;
             st.l[k] = 0.0f;
         }
@@ -441,13 +462,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
         if (!__all_sync(0xffffffffu, ok)) break;
         const uint8_t *stage = mine + slot * kStageBytes;
 #pragma unroll 1
-        for (int t = 2 * SB - 1; t >= 0; --t) {
-            const int j0 = s * (SB * kv4::kBlock) + t * kv4::kTile;
+        for (int t = SB - 1; t >= 0; --t) {
+            const int j0 = (s * SB + t) * kv4::kBlock;
             if (j0 >= len) continue;
-            if (j0 + kv4::kTile > len - p.T + 1)
-                tile<D, true>(st, stage + (t >> 1) * kBlk, t & 1, j0, lane);
+            if (j0 + kv4::kBlock > len - p.T + 1)
+                block32<D, true>(st, stage + t * kBlk, j0, lane);
             else
-                tile<D, false>(st, stage + (t >> 1) * kBlk, t & 1, j0, lane);
+                block32<D, false>(st, stage + t * kBlk, j0, lane);
         }
         __syncwarp();
         if (lane == 0 && s - kStages * kWarps >= s0) fetch(s - kStages * kWarps, slot);
