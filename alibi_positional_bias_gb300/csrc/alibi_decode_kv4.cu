@@ -46,7 +46,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kStages = 3;          // ring depth of each warp
 constexpr int kStageBytes = 4608;   // 128 / D blocks of 36 D bytes
-constexpr int kRows = 8;            // query rows of a chunk (the columns of an mma)
+constexpr int kRows = 8;            // query rows of a chunk, at most (the columns of an mma)
 constexpr int kSmem = kWarps * kStages * kStageBytes;
 
 struct HeadSlopes {
@@ -142,27 +142,29 @@ __device__ __forceinline__ void unpack(uint32_t w, uint32_t (&r)[4])
     r[3] = hfma2(under1024(t, 0x00f000f0u), kSixteenth, kMinus72);
 }
 
-template <int D>
-struct State {  // of one warp; column k of a lane is row 2c + k of the chunk
+// State of one warp. KC = 2: the chunk's 8 rows are the mma's 8 columns, and a lane has rows 2c and 2c + 1. KC = 1: up to
+// 4 rows, each in an even column, so that a lane has row c alone and does half the work per score.
+template <int D, int KC>
+struct State {
     static constexpr int NG = D / 32;
-    uint32_t q[NG][4];      // B operands: row lane / 4, elements 32 n + 8 c + (i, i + 4)
-    float kappa[2];         // from s acc to base-2 logits
-    float slope[2];         // m log2(e)
-    float pos[2];           // position less lane / 4
-    float R[2], M[2], l[2];
-    float acc[NG][2][4];    // elements 32 n + 4 g + (0, 2) in [0], + (1, 3) in [1]; columns (2c, 2c + 1)
+    uint32_t q[NG][4];      // B operands: column lane / 4, elements 32 n + 8 c + (i, i + 4)
+    float kappa[KC];        // from s acc to base-2 logits
+    float slope[KC];        // m log2(e)
+    float pos[KC];          // position less lane / 4
+    float R[KC], M[KC], l[KC];
+    float acc[NG][2][4];    // elements 32 n + 4 g + (0, 2) in [0], + (1, 3) in [1]; columns 2c, 2c + 1
 };
 
 // One block of 32 tokens from j0: two tiles whose chains of products, exponentials and products overlap. MASK: some
 // query does not see all of them.
-template <int D, bool MASK>
-__device__ __forceinline__ void block32(State<D> &st, const uint8_t *blk, int j0, int lane)
+template <int D, int KC, bool MASK>
+__device__ __forceinline__ void block32(State<D, KC> &st, const uint8_t *blk, int j0, int lane)
 {
     constexpr int NG = D / 32;
     const int g = lane >> 2, c = lane & 3;
 
     // logits: x[i][k] of token g + 8 i and row 2c + k; sv: the words of the tokens' value scales
-    float x[4][2];
+    float x[4][KC];
     uint32_t sv[4][NG];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -185,14 +187,15 @@ __device__ __forceinline__ void block32(State<D> &st, const uint8_t *blk, int j0
             for (int h = 0; h < 2; ++h) {
                 const uint32_t w = sv[2 * t + h][n / 2];
                 const float sk = (n & 1) ? bf16_hi(w) : bf16_lo(w);
-                x[2 * t + h][0] = n == 0 ? sk * s[2 * h] : fmaf(sk, s[2 * h], x[2 * t + h][0]);
-                x[2 * t + h][1] = n == 0 ? sk * s[2 * h + 1] : fmaf(sk, s[2 * h + 1], x[2 * t + h][1]);
+#pragma unroll
+                for (int k = 0; k < KC; ++k)
+                    x[2 * t + h][k] = n == 0 ? sk * s[2 * h + k] : fmaf(sk, s[2 * h + k], x[2 * t + h][k]);
             }
         }
     }
     const float jf = static_cast<float>(j0);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
+    for (int k = 0; k < KC; ++k) {
         const float bias = st.slope[k] * (jf - st.pos[k]);  // whole numbers below 2^24: exact; pos is less g
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -219,16 +222,17 @@ __device__ __forceinline__ void block32(State<D> &st, const uint8_t *blk, int j0
         big[i] = m >> 7;
         e[i] = __uint_as_float(0x4b000000u | big[i]) - (8388608.0f + 126.0f);
     }
-    float a[4][2], b[4][2], top = -INFINITY;
+    float a[4][KC], b[4][KC], top = -INFINITY, topb = -INFINITY;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < KC; ++k) {
             a[i][k] = x[i][k] - st.R[k];
             b[i][k] = x[i][k] + e[i] - st.M[k];
-            top = fmaxf(top, fmaxf(a[i][k], b[i][k]));
+            top = fmaxf(top, a[i][k]);
+            topb = fmaxf(topb, b[i][k]);
         }
-    if (__any_sync(0xffffffffu, top > 8.0f)) {
+    if (__any_sync(0xffffffffu, fmaxf(top, topb) > 8.0f)) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (big[i] == 255u) {  // leave the NaN groups out
@@ -242,7 +246,7 @@ __device__ __forceinline__ void block32(State<D> &st, const uint8_t *blk, int j0
                 e[i] = static_cast<float>(static_cast<int>(m) - 126);
             }
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < KC; ++k) {
             float mx = -INFINITY, my = -INFINITY;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -273,14 +277,18 @@ __device__ __forceinline__ void block32(State<D> &st, const uint8_t *blk, int j0
                 b[i][k] = x[i][k] + e[i] - m;
             }
         }
+        topb = 0.0f;
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < KC; ++k) {
             st.l[k] += ex2_approx(a[i][k]);
             b[i][k] = ex2_approx(b[i][k]);
         }
+    // Every P_jn of the block rounds to zero (2^(b + 7) below 2^-25): nothing to add. With ALiBi most of a long
+    // sequence ends here.
+    if (!__any_sync(0xffffffffu, !(topb <= -33.0f))) return;
 
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -309,12 +317,14 @@ __device__ __forceinline__ void block32(State<D> &st, const uint8_t *blk, int j0
                 const int i = 2 * t + h;
                 const uint32_t word = sv[i][NG == 1 ? 0 : NG / 2 + n / 2];
                 const float s = ((NG == 1 || (n & 1)) ? bf16_hi(word) : bf16_lo(word)) * down[h];
-                float p0 = b[i][0] * s, p1 = b[i][1] * s;
-                if (MASK) {  // a NaN scale of a token that the query does not see stays out
-                    if (jf + 8.0f * i > st.pos[0]) p0 = 0.0f;
-                    if (jf + 8.0f * i > st.pos[1]) p1 = 0.0f;
+                float pr[2] = {0.0f, 0.0f};
+#pragma unroll
+                for (int k = 0; k < KC; ++k) {
+                    pr[k] = b[i][k] * s;
+                    // a NaN scale of a token that the query does not see stays out
+                    if (MASK && jf + 8.0f * i > st.pos[k]) pr[k] = 0.0f;
                 }
-                pb[h] = transpose8(pack_f16x2(p0, p1));
+                pb[h] = transpose8(pack_f16x2(pr[0], pr[1]));
             }
             uint32_t v0[4], v1[4];
             unpack(vw[n][0], v0);
@@ -368,7 +378,7 @@ __device__ __forceinline__ void finish(const DecodeKv4Params &p, size_t row, int
     if (e == 0 && p.lse) p.lse[row] = bad ? nan : m.l == 0.0f ? -INFINITY : (m.R + log2f(m.l)) * 0.6931471805599453f;
 }
 
-template <int D>
+template <int D, int KC>
 __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid_constant__ DecodeKv4Params p)
 {
     constexpr int NG = D / 32, SB = 128 / D, kBlk = 36 * D;
@@ -412,12 +422,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
         for (int i = 0; i < kStages; ++i)
             if (mine_end - i * kWarps >= s0) fetch(mine_end - i * kWarps, i);
 
-    State<D> st;
+    State<D, KC> st;
     {
-        // this lane's slice of row g: the 8 elements from 8 c of every group
+        // this lane's slice of the row in column g: the 8 elements from 8 c of every group
         uint32_t qw[NG][4], top = 0;
-        const bool in = g < nrows;
-        const __nv_bfloat16 *qp = p.q + (static_cast<size_t>(bk) * p.rows + row0 + (in ? g : 0)) * p.d;
+        const int qr = KC == 2 ? g : g >> 1;
+        const bool in = qr < nrows && (KC == 2 || (g & 1) == 0);
+        const __nv_bfloat16 *qp = p.q + (static_cast<size_t>(bk) * p.rows + row0 + (in ? qr : 0)) * p.d;
 #pragma unroll
         for (int n = 0; n < NG; ++n) {
             uint4 w = make_uint4(0, 0, 0, 0);
@@ -442,8 +453,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
             }
         }
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int r = min(row0 + 2 * c + k, p.rows - 1);
+        for (int k = 0; k < KC; ++k) {
+            const int r = min(row0 + KC * c + k, p.rows - 1);
             const int G = p.rows / p.T;
             st.kappa[k] = __shfl_sync(0xffffffffu, kappa, (2 * c + k) * 4);
             st.slope[k] = p.slopes.log2e[hk * G + r / p.T];
@@ -466,9 +477,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
             const int j0 = (s * SB + t) * kv4::kBlock;
             if (j0 >= len) continue;
             if (j0 + kv4::kBlock > len - p.T + 1)
-                block32<D, true>(st, stage + t * kBlk, j0, lane);
+                block32<D, KC, true>(st, stage + t * kBlk, j0, lane);
             else
-                block32<D, false>(st, stage + t * kBlk, j0, lane);
+                block32<D, KC, false>(st, stage + t * kBlk, j0, lane);
         }
         __syncwarp();
         if (lane == 0 && s - kStages * kWarps >= s0) fetch(s - kStages * kWarps, slot);
@@ -485,11 +496,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
     float *pw = reinterpret_cast<float *>(mine);  // [kRows][D + 4], then R and l of each row
     constexpr int kRowStride = D + 4;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
+    for (int k = 0; k < KC; ++k) {
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) st.l[k] += __shfl_xor_sync(0xffffffffu, st.l[k], off);
         const float f = ex2_approx(st.M[k] - st.R[k] - 7.0f) * (st.l[k] == 0.0f ? 0.0f : 1.0f / st.l[k]);
-        const int r = 2 * c + k;
+        const int r = KC * c + k;
 #pragma unroll
         for (int n = 0; n < NG; ++n) {
             const float4 o = make_float4(st.acc[n][0][k] * f, st.acc[n][1][k] * f, st.acc[n][0][2 + k] * f,
@@ -559,10 +570,10 @@ int splits_for(long long units, int nst)
 
 bool aligned(const void *p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-template <int D>
+template <int D, int KC>
 cudaError_t launch(DecodeKv4Params &p, long long units, cudaStream_t stream)
 {
-    const void *fn = reinterpret_cast<const void *>(&decode_kv4_kernel<D>);
+    const void *fn = reinterpret_cast<const void *>(&decode_kv4_kernel<D, KC>);
     cudaError_t e = prepare_kernel(fn, kSmem, 0);
     if (e != cudaSuccess) return e;
     const int nst = (p.L + 128 / D * kv4::kBlock - 1) / (128 / D * kv4::kBlock);
@@ -579,7 +590,7 @@ cudaError_t launch(DecodeKv4Params &p, long long units, cudaStream_t stream)
         e = cudaMemsetAsync(p.count, 0, cb, stream);
     }
     if (e == cudaSuccess) {
-        decode_kv4_kernel<D><<<static_cast<unsigned>(units * p.splits), kWarps * 32, kSmem, stream>>>(p);
+        decode_kv4_kernel<D, KC><<<static_cast<unsigned>(units * p.splits), kWarps * 32, kSmem, stream>>>(p);
         e = cudaGetLastError();
     }
     if (ws) {
@@ -633,11 +644,12 @@ extern "C" int alibi_attn_decode_kv4(const void *q, const void *cache, const int
     for (int h = 0; h < H; ++h) p.slopes.log2e[h] = s.log2e[h];
     const long long units = static_cast<long long>(B) * Hkv * p.chunks;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool few = p.rows <= kRows / 2;  // one row per lane
     cudaError_t e;
     switch (kv4::padded(d)) {
-        case 128: e = launch<128>(p, units, st); break;
-        case 64: e = launch<64>(p, units, st); break;
-        default: e = launch<32>(p, units, st); break;
+        case 128: e = few ? launch<128, 1>(p, units, st) : launch<128, 2>(p, units, st); break;
+        case 64: e = few ? launch<64, 1>(p, units, st) : launch<64, 2>(p, units, st); break;
+        default: e = few ? launch<32, 1>(p, units, st) : launch<32, 2>(p, units, st); break;
     }
     return e == cudaSuccess ? ALIBI_OK : ALIBI_ERR_CUDA;
 }
