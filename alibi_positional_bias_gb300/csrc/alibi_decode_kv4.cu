@@ -28,9 +28,13 @@
 //            rounding to 11 bits is the only one below fp32: off by at most 2^-11 of each
 //            product, a quarter of the bf16 output's own step.
 //
-// Warps, and then slices, are merged in fp32; the CTA that finishes a chunk last merges
-// its slices, so no CTA waits for another.
+// The work is dealt in stages: the chunks of all sequences, one after another, form one row of
+// stages, and each of the 2 x 152 resident CTAs takes an equal share of it, whatever the lengths (which
+// only the device knows). A share may end inside a chunk: such chunks leave a partial for each share,
+// and a second kernel, launched as a programmatic dependent, merges them in fp32. Where a
+// chunk is no more than one stage for each warp, a CTA takes one chunk and nothing is merged.
 
+#include <algorithm>
 #include <cfloat>
 #include <cmath>
 #include <cuda_bf16.h>
@@ -47,10 +51,22 @@ constexpr int kWarps = 8;
 constexpr int kStages = 3;          // ring depth of each warp
 constexpr int kStageBytes = 4608;   // 128 / D blocks of 36 D bytes
 constexpr int kRows = 8;            // query rows of a chunk, at most (the columns of an mma)
+constexpr int kMostShares = 512;   // CTAs that share the work (two per SM)
+constexpr int kMergeThreads = 256;
+constexpr int kWholeRounds = 4;
 constexpr int kSmem = kWarps * kStages * kStageBytes;
 
 struct HeadSlopes {
     float log2e[kMaxHeads];
+};
+
+// What a share leaves behind for the merge: the partial of a chunk that began in an earlier share (0) and of one that
+// goes on in a later one (1), each of kRows rows of D means and then (R, l) of each row.
+KV4_HD constexpr int part_floats(int D) { return kRows * (D + 2); }
+
+struct alignas(8) Header {
+    int unit;   // the chunk that ends in this share and began in an earlier one, or -1
+    int first;  // the share it began in
 };
 
 struct DecodeKv4Params {
@@ -59,13 +75,21 @@ struct DecodeKv4Params {
     const int *lens;         // [B] or null
     __nv_bfloat16 *out;      // [B, H, T, d]
     float *lse;              // [B, H, T] or null
-    float *part;             // [B H_kv chunks][splits][kRows][D + 2], used when splits > 1
-    unsigned *count;         // [B H_kv chunks] splits finished, zero at launch
+    float *part;             // [CTAs][2][part_floats], null: CTA i takes chunk i
+    Header *head;            // [CTAs]
     uint32_t *status;
-    int Hkv, T, L, blocks, d;  // blocks: C / 32
-    int rows, chunks, splits;  // G T, ceil(G T / 8)
-    float c1;                  // 2^-14 log2(e) / sqrt(d)
+    int B, Hkv, T, L, blocks, d;  // blocks: C / 32
+    int rows, chunks;             // G T, ceil(G T / 8)
+    float c1;                     // 2^-14 log2(e) / sqrt(d)
     HeadSlopes slopes;
+};
+
+struct MergeParams {
+    const float *part;
+    const Header *head;
+    __nv_bfloat16 *out;
+    float *lse;
+    int d, rows, chunks;
 };
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -366,37 +390,126 @@ __device__ __forceinline__ Merged merge(int n, RL rl, Mean mean)
 }
 
 // One row's result: 4 elements of out, and lse by the thread of element 0.
-__device__ __forceinline__ void finish(const DecodeKv4Params &p, size_t row, int e, const Merged &m, bool bad)
+__device__ __forceinline__ void finish(__nv_bfloat16 *out, float *lse, int d, size_t row, int e, const Merged &m, bool bad)
 {
     const float nan = __uint_as_float(0x7fc00000u);
-    if (e < p.d) {
+    if (e < d) {
         uint2 w;
         w.x = bad ? 0x7fc07fc0u : pack_bf16x2(m.o.x, m.o.y);
         w.y = bad ? 0x7fc07fc0u : pack_bf16x2(m.o.z, m.o.w);
-        *reinterpret_cast<uint2 *>(p.out + row * p.d + e) = w;
+        *reinterpret_cast<uint2 *>(out + row * d + e) = w;
     }
-    if (e == 0 && p.lse) p.lse[row] = bad ? nan : m.l == 0.0f ? -INFINITY : (m.R + log2f(m.l)) * 0.6931471805599453f;
+    if (e == 0 && lse) lse[row] = bad ? nan : m.l == 0.0f ? -INFINITY : (m.R + log2f(m.l)) * 0.6931471805599453f;
 }
 
-template <int D, int KC>
+// Length of sequence b; one outside [0, L] counts as 0.
+__device__ __forceinline__ int length_of(const DecodeKv4Params &p, int b, bool &bad)
+{
+    const int n = p.lens ? __ldg(p.lens + b) : p.L;
+    bad = n < 0 || n > p.L;
+    return bad ? 0 : n;
+}
+
+template <int SB>
+__device__ __forceinline__ int stages_of(int len)  // at least one, so that every chunk has a place in the row of stages
+{
+    return max(1, (len + SB * kv4::kBlock - 1) / (SB * kv4::kBlock));
+}
+
+// Where a share of the row of stages lies.
+struct Share {
+    long long left;  // stages of the share
+    int b, unit, at; // sequence, chunk of it and stage of that chunk that it begins with
+    long long row;   // stages in all
+    long long begin;
+    long long n;     // shares
+
+    // Share `i` is [i row / n, (i + 1) row / n), of as many shares as there are CTAs or, where these are fewer, stages.
+    __device__ __forceinline__ bool cut(int i, int ctas, long long stages)
+    {
+        row = stages;
+        n = min(static_cast<long long>(ctas), row);
+        left = 0;
+        if (i >= n) return false;
+        begin = i * row / n;
+        left = (i + 1) * row / n - begin;
+        return true;
+    }
+};
+
+// Share `i` of `ctas`. All threads of the CTA.
+template <int SB>
+__device__ Share share_of(const DecodeKv4Params &p, int i, int ctas)
+{
+    const long long U = static_cast<long long>(p.Hkv) * p.chunks;
+    Share s;
+    if (!p.lens) {
+        const int len = stages_of<SB>(p.L);
+        if (!s.cut(i, ctas, p.B * U * len)) return s;
+        s.b = static_cast<int>(s.begin / (U * len));
+        const long long rem = s.begin - s.b * (U * len);
+        s.unit = static_cast<int>(rem / len);
+        s.at = static_cast<int>(rem - static_cast<long long>(s.unit) * len);
+        return s;
+    }
+    // sum of the sequences' stages, a run of sequences per thread; then the run that holds the beginning
+    __shared__ long long warp_sum[kWarps];
+    __shared__ Share found;
+    const int run = (p.B + kWarps * 32 - 1) / (kWarps * 32), b0 = threadIdx.x * run, b1 = min(p.B, b0 + run);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    bool bad;
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) mine += stages_of<SB>(length_of(p, b, bad));
+    long long upto = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, upto, off);
+        if (lane >= off) upto += v;
+    }
+    if (lane == 31) warp_sum[warp] = upto;
+    __syncthreads();
+    long long before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += warp_sum[w];
+        all += warp_sum[w];
+    }
+    if (!s.cut(i, ctas, all * U)) return s;
+    before += upto - mine;
+    if (s.begin >= before * U && s.begin < (before + mine) * U) {
+        for (int b = b0; b < b1; ++b) {
+            const int len = stages_of<SB>(length_of(p, b, bad));
+            if (s.begin < (before + len) * U) {
+                const long long rem = s.begin - before * U;
+                found.b = b;
+                found.unit = static_cast<int>(rem / len);
+                found.at = static_cast<int>(rem % len);
+                break;
+            }
+            before += len;
+        }
+    }
+    __syncthreads();
+    s.b = found.b;
+    s.unit = found.unit;
+    s.at = found.at;
+    return s;
+}
+
+// SHARES: CTA i takes share i of the row of stages; otherwise it takes chunk i.
+template <int D, int KC, bool SHARES>
 __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid_constant__ DecodeKv4Params p)
 {
     constexpr int NG = D / 32, SB = 128 / D, kBlk = 36 * D;
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ __align__(8) uint64_t full[kWarps][kStages];
-    __shared__ bool last;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const int split = static_cast<int>(blockIdx.x % p.splits), unit = static_cast<int>(blockIdx.x / p.splits);
-    const int chunk = unit % p.chunks, bk = unit / p.chunks, hk = bk % p.Hkv, b = bk / p.Hkv;
-    const int row0 = chunk * kRows, nrows = min(kRows, p.rows - row0);
-    const int len_in = p.lens ? __ldg(p.lens + b) : p.L;
-    const bool bad = len_in < 0 || len_in > p.L;
-    const int len = bad ? 0 : len_in;
+    const int U = p.Hkv * p.chunks;
 
+    griddep_launch_dependents();
     if (threadIdx.x == 0) {
         cta_err_init(kWaitLimitNs);
         cta_check_init(p.status, ring, kSmem);
-        if (bad && split == 0) atomicOr(p.status, ALIBI_DEV_RANGE);
     }
     if (lane == 0) {
         for (int i = 0; i < kStages; ++i) mbar_init(&full[warp][i], 1);
@@ -404,200 +517,317 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
     }
     __syncthreads();
 
-    // This CTA's stages [s0, s1) of the sequence, dealt to its warps in turn from the newest to the oldest: the
-    // bias falls on the way, so the references R and M settle in the first tiles. (Oldest first, a
-    // steep head raises them at every tile.)
-    const int nblk = (len + kv4::kBlock - 1) / kv4::kBlock, nst = (nblk + SB - 1) / SB;
-    const int per = nst / p.splits, extra = nst % p.splits;
-    const int s0 = split * per + min(split, extra), s1 = s0 + per + (split < extra ? 1 : 0);
-    const uint8_t *src = p.cache + static_cast<size_t>(bk) * p.blocks * kBlk;
-    uint8_t *mine = ring + warp * (kStages * kStageBytes);
-    auto fetch = [&](int s, int slot) {
-        const uint32_t bytes = static_cast<uint32_t>(min(SB, nblk - s * SB)) * kBlk;
-        mbar_arrive_expect_tx(&full[warp][slot], bytes);
-        bulk_load(mine + slot * kStageBytes, src + static_cast<size_t>(s) * kStageBytes, bytes, &full[warp][slot]);
-    };
-    const int mine_end = s1 - 1 - warp;  // this warp's stages, newest first: mine_end, mine_end - kWarps, ...
-    if (lane == 0)
-        for (int i = 0; i < kStages; ++i)
-            if (mine_end - i * kWarps >= s0) fetch(mine_end - i * kWarps, i);
-
-    State<D, KC> st;
-    {
-        // this lane's slice of the row in column g: the 8 elements from 8 c of every group
-        uint32_t qw[NG][4], top = 0;
-        const int qr = KC == 2 ? g : g >> 1;
-        const bool in = qr < nrows && (KC == 2 || (g & 1) == 0);
-        const __nv_bfloat16 *qp = p.q + (static_cast<size_t>(bk) * p.rows + row0 + (in ? qr : 0)) * p.d;
-#pragma unroll
-        for (int n = 0; n < NG; ++n) {
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (in && 32 * n + 8 * c < p.d) w = *reinterpret_cast<const uint4 *>(qp + 32 * n + 8 * c);
-            qw[n][0] = w.x, qw[n][1] = w.y, qw[n][2] = w.z, qw[n][3] = w.w;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) top = __vmaxu2(top, qw[n][i] & 0x7fff7fffu);
-        }
-        top = max(top & 0xffffu, top >> 16);
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const uint32_t ex = max(top >> 7, 14u);
-        const float up = __uint_as_float((268u - ex) << 23);  // 2^14 over the largest element's power of two
-        const float kappa = __uint_as_float(ex << 23) * p.c1;
-#pragma unroll
-        for (int n = 0; n < NG; ++n) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                st.q[n][i] = (i & 1) ? pack_f16x2(bf16_hi(qw[n][i / 2]) * up, bf16_hi(qw[n][2 + i / 2]) * up)
-                                     : pack_f16x2(bf16_lo(qw[n][i / 2]) * up, bf16_lo(qw[n][2 + i / 2]) * up);
-                st.acc[n][0][i] = st.acc[n][1][i] = 0.0f;
+    // what is left of the share: kept in shared memory, out of the registers of the loop over blocks
+    __shared__ Share sh;
+    if constexpr (SHARES) {
+        const Share mine_ = share_of<SB>(p, blockIdx.x, gridDim.x);
+        if (threadIdx.x == 0) {
+            sh = mine_;
+            Header h = {-1, 0};
+            if (sh.left > 0 && sh.at > 0) {
+                bool bad;
+                const int n = stages_of<SB>(length_of(p, sh.b, bad));
+                if (sh.at + sh.left >= n) {
+                    h.unit = sh.b * U + sh.unit;
+                    // the last share that begins at or before the chunk's first stage
+                    const long long at = sh.begin - sh.at;
+                    h.first = static_cast<int>(((at + 1) * sh.n + sh.row - 1) / sh.row - 1);
+                }
             }
+            p.head[blockIdx.x] = h;
         }
-#pragma unroll
-        for (int k = 0; k < KC; ++k) {
-            const int r = min(row0 + KC * c + k, p.rows - 1);
-            const int G = p.rows / p.T;
-            st.kappa[k] = __shfl_sync(0xffffffffu, kappa, (2 * c + k) * 4);
-            st.slope[k] = p.slopes.log2e[hk * G + r / p.T];
-            st.pos[k] = static_cast<float>(len - p.T + r % p.T - g);
-            st.R[k] = st.M[k] = -FLT_MAX;
-            st.l[k] = 0.0f;
-        }
+        __syncthreads();
+        if (sh.left <= 0) return;
     }
 
+    uint8_t *mine = ring + warp * (kStages * kStageBytes);
     int slot = 0;
     uint32_t phase = 0;
-    bool ok = true;
-    int s = mine_end;
-    for (; s >= s0; s -= kWarps) {
-        ok = mbar_wait(&full[warp][slot], phase, p.status, 0x60);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        const uint8_t *stage = mine + slot * kStageBytes;
-#pragma unroll 1
-        for (int t = SB - 1; t >= 0; --t) {
-            const int j0 = (s * SB + t) * kv4::kBlock;
-            if (j0 >= len) continue;
-            if (j0 + kv4::kBlock > len - p.T + 1)
-                block32<D, KC, true>(st, stage + t * kBlk, j0, lane);
-            else
-                block32<D, KC, false>(st, stage + t * kBlk, j0, lane);
+
+    while (true) {
+        const int b = SHARES ? sh.b : blockIdx.x / U, unit = SHARES ? sh.unit : blockIdx.x % U, s0 = SHARES ? sh.at : 0;
+        bool bad;
+        const int len = length_of(p, b, bad), n = stages_of<SB>(len);
+        const int take = SHARES ? static_cast<int>(min(sh.left, static_cast<long long>(n - s0))) : n;
+        const int nblk = (len + kv4::kBlock - 1) / kv4::kBlock;
+        // This CTA's stages [s0, s1) of the chunk, dealt to its warps in turn from the newest to the oldest: the
+        // bias falls on the way, so the references R and M settle in the first tiles. (Oldest first, a
+        // steep head raises them at every tile.)
+        const int s1 = min(s0 + take, (nblk + SB - 1) / SB);
+        const int hk = unit / p.chunks, chunk = unit - hk * p.chunks;
+        const size_t bk = static_cast<size_t>(b) * p.Hkv + hk;
+        const int row0 = chunk * kRows, nrows = min(kRows, p.rows - row0);
+        const uint8_t *src = p.cache + bk * p.blocks * kBlk;
+        if (bad && unit == 0 && threadIdx.x == 0) atomicOr(p.status, ALIBI_DEV_RANGE);
+
+        auto fetch = [&](int s, int slot_) {
+            const uint32_t bytes = static_cast<uint32_t>(min(SB, nblk - s * SB)) * kBlk;
+            mbar_arrive_expect_tx(&full[warp][slot_], bytes);
+            bulk_load(mine + slot_ * kStageBytes, src + static_cast<size_t>(s) * kStageBytes, bytes, &full[warp][slot_]);
+        };
+        int s = s1 - 1 - warp;  // this warp's stages: s, s - kWarps, ...
+        if (lane == 0)
+            for (int i = 0, k = slot; i < kStages; ++i) {
+                if (s - i * kWarps >= s0) fetch(s - i * kWarps, k);
+                if (++k == kStages) k = 0;
+            }
+
+        State<D, KC> st;
+        {
+            // this lane's slice of the row in column g: the 8 elements from 8 c of every group
+            uint32_t qw[NG][4], top = 0;
+            const int qr = KC == 2 ? g : g >> 1;
+            const bool in = qr < nrows && (KC == 2 || (g & 1) == 0);
+            const __nv_bfloat16 *qp = p.q + (bk * p.rows + row0 + (in ? qr : 0)) * p.d;
+#pragma unroll
+            for (int i = 0; i < NG; ++i) {
+                uint4 w = make_uint4(0, 0, 0, 0);
+                if (in && 32 * i + 8 * c < p.d) w = *reinterpret_cast<const uint4 *>(qp + 32 * i + 8 * c);
+                qw[i][0] = w.x, qw[i][1] = w.y, qw[i][2] = w.z, qw[i][3] = w.w;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) top = __vmaxu2(top, qw[i][j] & 0x7fff7fffu);
+            }
+            top = max(top & 0xffffu, top >> 16);
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const uint32_t ex = max(top >> 7, 14u);
+            const float up = __uint_as_float((268u - ex) << 23);  // 2^14 over the largest element's power of two
+            const float kappa = __uint_as_float(ex << 23) * p.c1;
+#pragma unroll
+            for (int i = 0; i < NG; ++i) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    st.q[i][j] = (j & 1) ? pack_f16x2(bf16_hi(qw[i][j / 2]) * up, bf16_hi(qw[i][2 + j / 2]) * up)
+                                         : pack_f16x2(bf16_lo(qw[i][j / 2]) * up, bf16_lo(qw[i][2 + j / 2]) * up);
+                    st.acc[i][0][j] = st.acc[i][1][j] = 0.0f;
+                }
+            }
+            const int G = p.rows / p.T;
+#pragma unroll
+            for (int k = 0; k < KC; ++k) {
+                const int r = min(row0 + KC * c + k, p.rows - 1);
+                st.kappa[k] = __shfl_sync(0xffffffffu, kappa, (2 * c + k) * 4);
+                st.slope[k] = p.slopes.log2e[hk * G + r / p.T];
+                st.pos[k] = static_cast<float>(len - p.T + r % p.T - g);
+                st.R[k] = st.M[k] = -FLT_MAX;
+                st.l[k] = 0.0f;
+            }
         }
-        __syncwarp();
-        if (lane == 0 && s - kStages * kWarps >= s0) fetch(s - kStages * kWarps, slot);
-        if (++slot == kStages) slot = 0, phase ^= 1u;
-    }
-    if (s >= s0) {  // a wait ran out (recorded): let the copies in flight land before the ring is reused
+
+        for (; s >= s0; s -= kWarps) {
+            const bool ok = mbar_wait(&full[warp][slot], phase, p.status, 0x60);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            const uint8_t *stage = mine + slot * kStageBytes;
+#pragma unroll 1
+            for (int t = SB - 1; t >= 0; --t) {
+                const int j0 = (s * SB + t) * kv4::kBlock;
+                if (j0 >= len) continue;
+                if (j0 + kv4::kBlock > len - p.T + 1)
+                    block32<D, KC, true>(st, stage + t * kBlk, j0, lane);
+                else
+                    block32<D, KC, false>(st, stage + t * kBlk, j0, lane);
+            }
+            __syncwarp();
+            if (lane == 0 && s - kStages * kWarps >= s0) fetch(s - kStages * kWarps, slot);
+            if (++slot == kStages) slot = 0, phase ^= 1u;
+        }
+        // a wait ran out (recorded): let the copies in flight land before the ring is reused
         for (int i = 0; i < kStages && s >= s0; ++i, s -= kWarps) {
             mbar_wait(&full[warp][slot], phase, p.status, 0x61, true);
             if (++slot == kStages) slot = 0, phase ^= 1u;
         }
-    }
 
-    // the warp's partial: reference R, l = sum of p, and the mean of v (never beyond the largest |v|)
-    float *pw = reinterpret_cast<float *>(mine);  // [kRows][D + 4], then R and l of each row
-    constexpr int kRowStride = D + 4;
+        // the warp's partial: reference R, l = sum of p, and the mean of v (never beyond the largest |v|)
+        float *pw = reinterpret_cast<float *>(mine);  // [kRows][D + 4], then R and l of each row
+        constexpr int kRowStride = D + 4;
 #pragma unroll
-    for (int k = 0; k < KC; ++k) {
+        for (int k = 0; k < KC; ++k) {
 #pragma unroll
-        for (int off = 4; off < 32; off <<= 1) st.l[k] += __shfl_xor_sync(0xffffffffu, st.l[k], off);
-        const float f = ex2_approx(st.M[k] - st.R[k] - 7.0f) * (st.l[k] == 0.0f ? 0.0f : 1.0f / st.l[k]);
-        const int r = KC * c + k;
+            for (int off = 4; off < 32; off <<= 1) st.l[k] += __shfl_xor_sync(0xffffffffu, st.l[k], off);
+            const float f = ex2_approx(st.M[k] - st.R[k] - 7.0f) * (st.l[k] == 0.0f ? 0.0f : 1.0f / st.l[k]);
+            const int r = KC * c + k;
 #pragma unroll
-        for (int n = 0; n < NG; ++n) {
-            const float4 o = make_float4(st.acc[n][0][k] * f, st.acc[n][1][k] * f, st.acc[n][0][2 + k] * f,
-                                         st.acc[n][1][2 + k] * f);
-            *reinterpret_cast<float4 *>(pw + r * kRowStride + 32 * n + 4 * g) = o;
+            for (int i = 0; i < NG; ++i) {
+                const float4 o = make_float4(st.acc[i][0][k] * f, st.acc[i][1][k] * f, st.acc[i][0][2 + k] * f,
+                                             st.acc[i][1][2 + k] * f);
+                *reinterpret_cast<float4 *>(pw + r * kRowStride + 32 * i + 4 * g) = o;
+            }
+            if (g == 0)
+                *reinterpret_cast<float2 *>(pw + kRows * kRowStride + 2 * r) = make_float2(st.R[k], st.l[k]);
         }
-        if (g == 0) {
-            *reinterpret_cast<float2 *>(pw + kRows * kRowStride + 2 * r) = make_float2(st.R[k], st.l[k]);
-        }
-    }
-    __syncthreads();
+        __syncthreads();
 
-    const size_t out0 = static_cast<size_t>(bk) * p.rows + row0;
-    constexpr int kPart = kRows * (D + 2);  // floats of a split's partial: means, then (R, l) of each row
-    float *mypart = p.part + (static_cast<size_t>(unit) * p.splits + split) * kPart;
-    for (int i = threadIdx.x; i < nrows * (D / 4); i += kWarps * 32) {
-        const int r = i / (D / 4), e = i % (D / 4) * 4;
-        const float *base = reinterpret_cast<const float *>(ring);
-        constexpr int kStep = kStages * kStageBytes / 4;
-        const Merged m = merge(
-            kWarps, [&](int w) { return *reinterpret_cast<const float2 *>(base + w * kStep + kRows * kRowStride + 2 * r); },
-            [&](int w) { return *reinterpret_cast<const float4 *>(base + w * kStep + r * kRowStride + e); });
-        if (p.splits == 1) {
-            finish(p, out0 + r, e, m, bad);
-        } else {
-            *reinterpret_cast<float4 *>(mypart + r * D + e) = m.o;
-            if (e == 0) *reinterpret_cast<float2 *>(mypart + kRows * D + 2 * r) = make_float2(m.R, m.l);
+        bool whole = true;
+        float *to = nullptr;
+        if constexpr (SHARES) {
+            whole = sh.left >= n - sh.at && sh.at == 0;
+            to = p.part + (static_cast<size_t>(blockIdx.x) * 2 + (sh.at == 0)) * part_floats(D);
         }
-    }
-    if (p.splits == 1) return;
-    // Count this split as done once its partial is visible device-wide; the CTA that counts a
-    // chunk last merges it.
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) last = atomicAdd(p.count + unit, 1u) == static_cast<unsigned>(p.splits - 1);
-    __syncthreads();
-    if (!last) return;
-    __threadfence();
-    const float *parts = p.part + static_cast<size_t>(unit) * p.splits * kPart;
-    for (int i = threadIdx.x; i < nrows * (D / 4); i += kWarps * 32) {
-        const int r = i / (D / 4), e = i % (D / 4) * 4;
-        const Merged m = merge(
-            p.splits, [&](int k) { return __ldcg(reinterpret_cast<const float2 *>(parts + k * kPart + kRows * D + 2 * r)); },
-            [&](int k) { return __ldcg(reinterpret_cast<const float4 *>(parts + k * kPart + r * D + e)); });
-        finish(p, out0 + r, e, m, bad);
+        for (int i = threadIdx.x; i < nrows * (D / 4); i += kWarps * 32) {
+            const int r = i / (D / 4), e = i % (D / 4) * 4;
+            const float *base = reinterpret_cast<const float *>(ring);
+            constexpr int kStep = kStages * kStageBytes / 4;
+            const Merged m = merge(
+                kWarps,
+                [&](int w) { return *reinterpret_cast<const float2 *>(base + w * kStep + kRows * kRowStride + 2 * r); },
+                [&](int w) { return *reinterpret_cast<const float4 *>(base + w * kStep + r * kRowStride + e); });
+            if (whole) {
+                finish(p.out, p.lse, p.d, bk * p.rows + row0 + r, e, m, bad);
+            } else {
+                *reinterpret_cast<float4 *>(to + r * D + e) = m.o;
+                if (e == 0) *reinterpret_cast<float2 *>(to + kRows * D + 2 * r) = make_float2(m.R, m.l);
+            }
+        }
+        if constexpr (!SHARES) return;
+        fence_proxy_async_smem();  // the partials were written and read before the next copies overwrite them
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            sh.left -= take;
+            sh.at += take;
+            if (sh.at == n) {
+                sh.at = 0;
+                if (++sh.unit == U) sh.unit = 0, ++sh.b;
+            }
+        }
+        __syncthreads();
+        if (sh.left <= 0) return;
     }
 }
 
-// Slices per chunk: the number that minimises (waves of CTAs) x (stages per CTA + a fixed cost
-// of a CTA's start and merge, in stages) plus the merge over slices.
-int splits_for(long long units, int nst)
+// Merge of the chunks that several shares worked on: CTA (i, r) looks at row r of the chunk that ends in share i + 1. Its
+// partials are slot 1 of the share it began in and slot 0 of the shares up to this one. The loads of a thread are issued
+// together: with 76 partials the merge waits for three round trips to L2 and not for 76.
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) decode_kv4_merge_kernel(const __grid_constant__ MergeParams p)
 {
-    const long long slots = 2LL * num_sms();
-    int best = 1;
-    long long best_cost = -1;
-    const int most = (nst + kWarps - 1) / kWarps;  // a stage for every warp
-    for (int s = 1; s <= most && s <= 512; ++s) {
-        const long long waves = (units * s + slots - 1) / slots;
-        const long long cost = waves * ((nst + s - 1) / s + 12) * 8 + (s > 1 ? 64 + s : 0);
-        if (best_cost < 0 || cost < best_cost) {
-            best_cost = cost;
-            best = s;
+    constexpr int kPart = part_floats(D), kItems = D / 4, kGroups = kMergeThreads / kItems, kDepth = 8;
+    __shared__ float weight[kMostShares];
+    __shared__ float red[2][kMergeThreads / 32];
+    __shared__ float4 sum[kMergeThreads];
+    griddep_wait();
+    const int last = blockIdx.x + 1, r = blockIdx.y;
+    const int2 h = __ldcg(reinterpret_cast<const int2 *>(p.head + last));  // (unit, first)
+    if (h.x < 0) return;
+    const int n = last - h.y + 1;
+    const int bk = h.x / p.chunks, row0 = (h.x - bk * p.chunks) * kRows;
+    if (row0 + r >= p.rows) return;
+    const float *part0 = p.part + (static_cast<size_t>(h.y) * 2 + 1) * kPart;
+    const auto from = [&](int k) { return part0 + (k == 0 ? 0 : (2 * k - 1) * kPart); };
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, item = threadIdx.x % kItems, group = threadIdx.x / kItems;
+    // the first means are fetched while the weights are computed
+    float4 v[kDepth];
+#pragma unroll
+    for (int i = 0; i < kDepth; ++i) {
+        const int k = group + i * kGroups;
+        if (k < n) v[i] = __ldcg(reinterpret_cast<const float4 *>(from(k) + r * D + 4 * item));
+    }
+    // weights l 2^(R - max R)
+    float R = -FLT_MAX, l = 0.0f;
+    float2 x[kMostShares / kMergeThreads];
+#pragma unroll
+    for (int i = 0; i < kMostShares / kMergeThreads; ++i) {
+        const int k = threadIdx.x + i * kMergeThreads;
+        x[i] = k < n ? __ldcg(reinterpret_cast<const float2 *>(from(k) + kRows * D + 2 * r)) : make_float2(-FLT_MAX, 0.0f);
+        R = fmaxf(R, x[i].x);
+    }
+#pragma unroll
+    for (int off = 16; off; off >>= 1) R = fmaxf(R, __shfl_xor_sync(0xffffffffu, R, off));
+    if (lane == 0) red[0][warp] = R;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kMergeThreads / 32; ++w) R = fmaxf(R, red[0][w]);
+#pragma unroll
+    for (int i = 0; i < kMostShares / kMergeThreads; ++i) {
+        const int k = threadIdx.x + i * kMergeThreads;
+        const float w = x[i].y * ex2_approx(x[i].x - R);
+        if (k < n) weight[k] = w;
+        l += w;
+    }
+#pragma unroll
+    for (int off = 16; off; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+    if (lane == 0) red[1][warp] = l;
+    __syncthreads();
+    l = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kMergeThreads / 32; ++w) l += red[1][w];
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    Merged m = {R, l, make_float4(0.f, 0.f, 0.f, 0.f)};
+    for (int k0 = group; k0 < n; k0 += kDepth * kGroups) {
+#pragma unroll
+        for (int i = 0; i < kDepth; ++i) {
+            const int k = k0 + i * kGroups;
+            if (k < n) {
+                const float a = weight[k] * inv;
+                m.o.x = fmaf(v[i].x, a, m.o.x), m.o.y = fmaf(v[i].y, a, m.o.y);
+                m.o.z = fmaf(v[i].z, a, m.o.z), m.o.w = fmaf(v[i].w, a, m.o.w);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kDepth; ++i) {
+            const int k = k0 + (kDepth + i) * kGroups;
+            if (k < n) v[i] = __ldcg(reinterpret_cast<const float4 *>(from(k) + r * D + 4 * item));
         }
     }
-    return best;
+    sum[threadIdx.x] = m.o;
+    __syncthreads();
+    if (group != 0) return;
+#pragma unroll
+    for (int k = 1; k < kGroups; ++k) {
+        const float4 y = sum[k * kItems + item];
+        m.o.x += y.x, m.o.y += y.y, m.o.z += y.z, m.o.w += y.w;
+    }
+    finish(p.out, p.lse, p.d, static_cast<size_t>(bk) * p.rows + row0 + r, 4 * item, m, false);
 }
 
 bool aligned(const void *p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// Chunks that are dealt whole, one to a CTA: where they are no longer than a stage for each warp, and where there are
+// many rounds of them. (64 x 40 heads of 8192 tokens, 8.4 rounds: XX us whole, XX us in equal shares, which
+// wait for the SMs and heads that take longest.)
+bool whole_chunks(long long units, int per) { return per == 1 || units >= kWholeRounds * 2LL * num_sms(); }
+
 template <int D, int KC>
 cudaError_t launch(DecodeKv4Params &p, long long units, cudaStream_t stream)
 {
-    const void *fn = reinterpret_cast<const void *>(&decode_kv4_kernel<D, KC>);
-    cudaError_t e = prepare_kernel(fn, kSmem, 0);
-    if (e != cudaSuccess) return e;
-    const int nst = (p.L + 128 / D * kv4::kBlock - 1) / (128 / D * kv4::kBlock);
-    p.splits = splits_for(units, nst);
-    if (units * p.splits > 0x7fffffffLL) return cudaErrorInvalidValue;
-    char *ws = nullptr;
-    if (p.splits > 1) {
-        const size_t pb = (static_cast<size_t>(units) * p.splits * kRows * (D + 2) * sizeof(float) + 255) & ~size_t(255);
-        const size_t cb = static_cast<size_t>(units) * sizeof(unsigned);
-        e = cudaMallocFromPoolAsync(reinterpret_cast<void **>(&ws), pb + cb, decode_pool(), stream);
+    const auto whole = &decode_kv4_kernel<D, KC, false>;
+    const auto shared = &decode_kv4_kernel<D, KC, true>;
+    constexpr int kTokens = 128 / D * kv4::kBlock;  // of a stage
+    const int per = ((p.L + kTokens - 1) / kTokens + kWarps - 1) / kWarps;  // CTAs a chunk can keep busy
+    p.part = nullptr;
+    p.head = nullptr;
+    if (whole_chunks(units, per)) {
+        if (units > 0x7fffffffLL) return cudaErrorInvalidValue;
+        const cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(whole), kSmem, 0);
         if (e != cudaSuccess) return e;
-        p.part = reinterpret_cast<float *>(ws);
-        p.count = reinterpret_cast<unsigned *>(ws + pb);
-        e = cudaMemsetAsync(p.count, 0, cb, stream);
+        whole<<<static_cast<unsigned>(units), kWarps * 32, kSmem, stream>>>(p);
+        return cudaGetLastError();
     }
-    if (e == cudaSuccess) {
-        decode_kv4_kernel<D, KC><<<static_cast<unsigned>(units * p.splits), kWarps * 32, kSmem, stream>>>(p);
-        e = cudaGetLastError();
+    cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(shared), kSmem, 0);
+    if (e != cudaSuccess) return e;
+    const int shares = static_cast<int>(std::min<long long>(units * per, std::min(2 * num_sms(), kMostShares)));
+    const size_t bytes = static_cast<size_t>(shares) * 2 * part_floats(D) * sizeof(float);
+    char *ws = nullptr;
+    e = cudaMallocFromPoolAsync(reinterpret_cast<void **>(&ws), bytes + shares * sizeof(Header), decode_pool(), stream);
+    if (e != cudaSuccess) return e;
+    p.part = reinterpret_cast<float *>(ws);
+    p.head = reinterpret_cast<Header *>(ws + bytes);
+    shared<<<static_cast<unsigned>(shares), kWarps * 32, kSmem, stream>>>(p);
+    e = cudaGetLastError();
+    if (e == cudaSuccess && shares > 1) {
+        MergeParams m = {p.part, p.head, p.out, p.lse, p.d, p.rows, p.chunks};
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(shares - 1), static_cast<unsigned>(std::min(p.rows, kRows)));
+        cfg.blockDim = dim3(kMergeThreads);
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, decode_kv4_merge_kernel<D>, m);
     }
-    if (ws) {
-        const cudaError_t f = cudaFreeAsync(ws, stream);
-        if (e == cudaSuccess) e = f;
-    }
-    return e;
+    const cudaError_t f = cudaFreeAsync(ws, stream);
+    return e != cudaSuccess ? e : f;
 }
 
 }  // namespace
@@ -629,10 +859,9 @@ extern "C" int alibi_attn_decode_kv4(const void *q, const void *cache, const int
     p.lens = lens;
     p.out = static_cast<__nv_bfloat16 *>(out);
     p.lse = lse;
-    p.part = nullptr;
-    p.count = nullptr;
     p.status = device_status_word();
     if (!p.status) return ALIBI_ERR_CUDA;
+    p.B = B;
     p.Hkv = Hkv;
     p.T = T;
     p.L = L;
