@@ -63,6 +63,8 @@ def lib_path() -> str:
 def load(build_if_missing: bool = False):
     """Load the CUDA library (optionally building it first). Raises if it cannot be loaded."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -416,33 +418,63 @@ def alibi_kv4_cache(B: int, H: int, C: int, d: int, device=None):
                        device="cuda" if device is None else device)
 
 
-def _need_kv4(cache, B, H, d):
-    """Check a 4-bit cache of B sequences and (if given) H heads of size d; returns its (heads, capacity)."""
+def _is(t, dtype, shape, index) -> bool:
+    """Whether t is a contiguous CUDA tensor of this type, shape and device index: one pass over what _need checks and
+    explains, for calls whose latency counts."""
     import torch
-    _need(cache, torch.uint8, None, "cache")
-    if cache.dim() != 4 or cache.shape[0] != B or cache.shape[3] != 36 * max(d, 32) or H not in (None, cache.shape[1]):
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index
+            and index >= 0 and t.is_contiguous())
+
+
+def _need_on(t, dtype, shape, name, index):
+    """_need, and on CUDA device `index`."""
+    _need(t, dtype, shape, name)
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+
+
+def _need_kv4(cache, B, H, d, index):
+    """Check a 4-bit cache of B sequences and (if given) H heads of size d on a device; returns its (heads, capacity)."""
+    import torch
+    _need_on(cache, torch.uint8, None, "cache", index)
+    s = cache.shape
+    if len(s) != 4 or s[0] != B or s[3] != 36 * max(d, 32) or H not in (None, s[1]):
         raise ValueError(f"cache must have shape ({B}, {'heads' if H is None else H}, C / 32, {36 * max(d, 32)}), "
-                         f"got {tuple(cache.shape)}")
-    return cache.shape[1], cache.shape[2] * 32
+                         f"got {tuple(s)}")
+    return s[1], s[2] * 32
 
 
-def _need_same_device(first, *rest):
-    for t in rest:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"all tensors must be on one device, got {first.device} and {t.device}")
-
-
-def _on(device):
-    """The library launches on the current device: make it the tensors' own."""
+def _call_on(index, fn, stream, args, where):
+    """fn(*args, stream) with the tensors' device current, on `stream` (None: torch's current one)."""
     import torch
-    return torch.cuda.device(device)
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(index)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if torch.cuda.current_device() == index:
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, stream)
+    if status != ALIBI_OK:
+        raise AlibiError(status, where)
 
 
-def _kv4_span(pos, count, B):
+def _kv4_rows(k, v, dtype, cache, pos, count):
+    """Checks shared by alibi_kv4_write and _read; returns (device index, pointers of pos and count, B, H, T, C, d)."""
     import torch
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise (ValueError if isinstance(k, torch.Tensor) else TypeError)("k must be a torch tensor of shape (B, H, T, d)")
+    shape, index = k.shape, k.get_device()
+    if not (_is(k, dtype, shape, index) and _is(v, dtype, shape, index)):
+        _need(k, dtype, None, "k")
+        _need_on(v, dtype, shape, "v", index)
+    B, H, T, d = shape
+    _, C = _need_kv4(cache, B, H, d, index)
     for t, name in ((pos, "pos"), (count, "count")):
-        if t is not None:
-            _need(t, torch.int32, (B,), name)
+        if t is not None and not _is(t, torch.int32, (B,), index):
+            _need_on(t, torch.int32, (B,), name, index)
+    return (index, None if pos is None else pos.data_ptr(), None if count is None else count.data_ptr(), B, H, T, C, d)
 
 
 def alibi_kv4_write(k, v, cache, pos=None, count=None, stream=None) -> None:
@@ -451,17 +483,9 @@ def alibi_kv4_write(k, v, cache, pos=None, count=None, stream=None) -> None:
     CUDA tensors [B] (None: 0 and T). Sequences that do not fit are left out and reported by
     alibi_check_error."""
     import torch
-    _need(k, torch.bfloat16, None, "k")
-    if k.dim() != 4:
-        raise ValueError(f"k must have shape (B, H, T, d), got {tuple(k.shape)}")
-    B, H, T, d = k.shape
-    _need(v, torch.bfloat16, k.shape, "v")
-    _, C = _need_kv4(cache, B, H, d)
-    _kv4_span(pos, count, B)
-    _need_same_device(cache, k, v, pos, count)
-    with _on(cache.device):
-        _check(load().alibi_kv4_write(_ptr(k), _ptr(v), _ptr(cache), _ptr(pos), _ptr(count), B, H, T, C, d,
-                                      _stream(stream, cache.device)), "alibi_kv4_write")
+    index, pp, pc, *dims = _kv4_rows(k, v, torch.bfloat16, cache, pos, count)
+    _call_on(index, load().alibi_kv4_write, stream, (k.data_ptr(), v.data_ptr(), cache.data_ptr(), pp, pc, *dims),
+             "alibi_kv4_write")
 
 
 def alibi_kv4_read(cache, k, v, pos=None, count=None, stream=None):
@@ -469,17 +493,10 @@ def alibi_kv4_read(cache, k, v, pos=None, count=None, stream=None):
     held values exactly): row pos[b] + t of sequence b to token t < count[b]; other tokens of k and v
     are left as they were. pos and count as in alibi_kv4_write. Returns (k, v)."""
     import torch
-    _need(k, torch.float32 if getattr(k, "dtype", None) == torch.float32 else torch.bfloat16, None, "k")
-    if k.dim() != 4:
-        raise ValueError(f"k must have shape (B, H, T, d), got {tuple(k.shape)}")
-    B, H, T, d = k.shape
-    _need(v, k.dtype, k.shape, "v")
-    _, C = _need_kv4(cache, B, H, d)
-    _kv4_span(pos, count, B)
-    _need_same_device(cache, k, v, pos, count)
-    with _on(cache.device):
-        _check(load().alibi_kv4_read(_ptr(cache), _ptr(k), _ptr(v), _ptr(pos), _ptr(count), B, H, T, C, d,
-                                     int(k.dtype == torch.float32), _stream(stream, cache.device)), "alibi_kv4_read")
+    fp32 = getattr(k, "dtype", None) is torch.float32
+    index, pp, pc, *dims = _kv4_rows(k, v, torch.float32 if fp32 else torch.bfloat16, cache, pos, count)
+    _call_on(index, load().alibi_kv4_read, stream,
+             (cache.data_ptr(), k.data_ptr(), v.data_ptr(), pp, pc, *dims, int(fp32)), "alibi_kv4_read")
     return k, v
 
 
@@ -490,31 +507,34 @@ def alibi_attn_decode_kv4(q, cache, lens=None, L=None, out=None, lse=None, slope
     capacity C); slopes: H values (None: alibi_slopes(H)). Returns (out, lse): bf16 like q, fp32
     without the last dimension."""
     import torch
-    _need(q, torch.bfloat16, None, "q")
-    if q.dim() not in (3, 4):
-        raise ValueError(f"q must have shape (B, H, T, d) or (B, H, d), got {tuple(q.shape)}")
-    B, H, d = q.shape[0], q.shape[1], q.shape[-1]
-    T = q.shape[2] if q.dim() == 4 else 1
-    Hkv, C = _need_kv4(cache, B, None, d)
-    if lens is not None:
-        _need(lens, torch.int32, (B,), "lens")
+    if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
+        raise (ValueError if isinstance(q, torch.Tensor) else TypeError)(
+            "q must be a torch tensor of shape (B, H, T, d) or (B, H, d)")
+    shape, index = q.shape, q.get_device()
+    if not _is(q, torch.bfloat16, shape, index):
+        _need(q, torch.bfloat16, None, "q")
+    B, H, d = shape[0], shape[1], shape[-1]
+    T = shape[2] if len(shape) == 4 else 1
+    Hkv, C = _need_kv4(cache, B, None, d, index)
+    if lens is not None and not _is(lens, torch.int32, (B,), index):
+        _need_on(lens, torch.int32, (B,), "lens", index)
     if out is None:
         out = torch.empty_like(q)
+    elif not _is(out, torch.bfloat16, shape, index):
+        _need_on(out, torch.bfloat16, shape, "out", index)
     if lse is None:
-        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
-    _need(out, torch.bfloat16, q.shape, "out")
-    _need(lse, torch.float32, q.shape[:-1], "lse")
-    _need_same_device(cache, q, lens, out, lse)
+        lse = torch.empty(shape[:-1], dtype=torch.float32, device=q.device)
+    elif not _is(lse, torch.float32, shape[:-1], index):
+        _need_on(lse, torch.float32, shape[:-1], "lse", index)
     m = None
     if slopes is not None:
         m = np.ascontiguousarray(slopes, dtype=np.float32)
         if m.shape != (H,):
             raise ValueError(f"slopes: expected shape ({H},), got {m.shape}")
-    with _on(cache.device):
-        _check(load().alibi_attn_decode_kv4(_ptr(q), _ptr(cache), _ptr(lens), _ptr(out), _ptr(lse), B, H, Hkv, T,
-                                            C if L is None else int(L), C, d,
-                                            None if m is None else m.ctypes.data_as(ctypes.POINTER(ctypes.c_float)),
-                                            _stream(stream, cache.device)), "alibi_attn_decode_kv4")
+    _call_on(index, load().alibi_attn_decode_kv4, stream,
+             (q.data_ptr(), cache.data_ptr(), None if lens is None else lens.data_ptr(), out.data_ptr(), lse.data_ptr(),
+              B, H, Hkv, T, C if L is None else int(L), C, d,
+              None if m is None else m.ctypes.data_as(ctypes.POINTER(ctypes.c_float))), "alibi_attn_decode_kv4")
     return out, lse
 
 
