@@ -14,11 +14,12 @@
 //            q as fp16 operands, both exact: four bits under the exponent of 1024 are 1024 + u
 //            (or 1024 + 16 u), and one add or fma per pair leaves u - 8; q is scaled to
 //            [2^14, 2^15) per row, which holds elements down to 2^-32 of the row's largest.
-//            s_jn acc_n is the group's share of q.k_j: exact products summed in fp32. (Masked
-//            bits alone are operands too, the subnormals u 2^-24 and u 2^-20, without the add; but
-//            the tensor core aligns products by their nominal exponents, which cost 10 and 6
-//            bits of the sum, and the offset 8 then cancels against those: errors of
-//            2^-17 of 8 |s| were measured.)
+//            s_jn acc_n is the group's share of q.k_j: exact products summed in fp32.
+//            (Masked bits without the 1024 are operands too, the subnormals u 2^-24 and u 2^-20,
+//            but the tensor core aligns products by their nominal exponents, which costs 10 and 6
+//            bits of the sum: errors of 2^-17 of 8 |s| were measured. Keys as 1024 + 16 u, with the
+//            offset in the sum's start, save two operations in nine, but the start takes registers
+//            that the loop does not have: 426 -> 440 us at 64 x 40 heads of 8192 tokens.)
 //   softmax  in base 2: p_j = 2^(x_j - R), summed in fp32, with a reference R of each row that is
 //            raised when some x_j exceeds it by 8.
 //   values   O^T += (U - 8)^T P^T per group, P_jn = p_j s_jn as fp16, taken as
@@ -418,45 +419,59 @@ __device__ __forceinline__ int stages_of(int len)  // at least one, so that ever
 
 // Where a share of the row of stages lies.
 struct Share {
-    long long left;  // stages of the share
-    int b, unit, at; // sequence, chunk of it and stage of that chunk that it begins with
-    long long row;   // stages in all
-    long long begin;
-    long long n;     // shares
-
-    // Share `i` is [i row / n, (i + 1) row / n), of as many shares as there are CTAs or, where these are fewer, stages.
-    __device__ __forceinline__ bool cut(int i, int ctas, long long stages)
-    {
-        row = stages;
-        n = min(static_cast<long long>(ctas), row);
-        left = 0;
-        if (i >= n) return false;
-        begin = i * row / n;
-        left = (i + 1) * row / n - begin;
-        return true;
-    }
+    int left;         // stages of the share that are left
+    int b, unit, at;  // sequence, chunk of it and stage of that chunk that comes next
 };
 
-// Share `i` of `ctas`. All threads of the CTA.
-template <int SB>
-__device__ Share share_of(const DecodeKv4Params &p, int i, int ctas)
+// Share `i` of `ctas` of a row of `row` stages is [i row / n, (i + 1) row / n), n = min(ctas, row). Divisions in 32 bits
+// where the row allows it (all but sequences of many millions of tokens in all).
+struct Cut {
+    long long row;
+    int n;
+
+    __device__ __forceinline__ Cut(long long row_, int ctas) : row(row_), n(static_cast<int>(min(static_cast<long long>(ctas), row_)))
+    {
+    }
+    __device__ __forceinline__ long long begin(int i) const
+    {
+        if (row < (1LL << 32) / (kMostShares + 1)) return static_cast<uint32_t>(i) * static_cast<uint32_t>(row) / static_cast<uint32_t>(n);
+        return i * row / n;
+    }
+    // the last share that begins at or before stage `at`
+    __device__ __forceinline__ int holder(long long at) const { return static_cast<int>(((at + 1) * n + row - 1) / row - 1); }
+};
+
+__device__ __forceinline__ int divide(long long a, int b)
 {
-    const long long U = static_cast<long long>(p.Hkv) * p.chunks;
-    Share s;
+    return a < (1LL << 32) ? static_cast<int>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : static_cast<int>(a / b);
+}
+
+// Share blockIdx.x, into `sh`; returns the row. All threads of the CTA.
+template <int SB>
+__device__ __forceinline__ long long share_of(const DecodeKv4Params &p, Share &sh)
+{
+    const int U = p.Hkv * p.chunks, i = blockIdx.x;
+    __shared__ long long warp_sum[kWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (!p.lens) {
         const int len = stages_of<SB>(p.L);
-        if (!s.cut(i, ctas, p.B * U * len)) return s;
-        s.b = static_cast<int>(s.begin / (U * len));
-        const long long rem = s.begin - s.b * (U * len);
-        s.unit = static_cast<int>(rem / len);
-        s.at = static_cast<int>(rem - static_cast<long long>(s.unit) * len);
-        return s;
+        const Cut cut(static_cast<long long>(p.B) * U * len, gridDim.x);
+        if (threadIdx.x == 0) {
+            sh.left = 0;
+            if (i < cut.n) {
+                const long long begin = cut.begin(i);
+                const int unit = divide(begin, len);  // of all sequences
+                sh.left = static_cast<int>(cut.begin(i + 1) - begin);
+                sh.at = static_cast<int>(begin - static_cast<long long>(unit) * len);
+                sh.b = unit / U;
+                sh.unit = unit % U;
+            }
+        }
+        __syncthreads();
+        return cut.row;
     }
     // sum of the sequences' stages, a run of sequences per thread; then the run that holds the beginning
-    __shared__ long long warp_sum[kWarps];
-    __shared__ Share found;
     const int run = (p.B + kWarps * 32 - 1) / (kWarps * 32), b0 = threadIdx.x * run, b1 = min(p.B, b0 + run);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     bool bad;
     long long mine = 0;
     for (int b = b0; b < b1; ++b) mine += stages_of<SB>(length_of(p, b, bad));
@@ -474,26 +489,29 @@ __device__ Share share_of(const DecodeKv4Params &p, int i, int ctas)
         if (w < warp) before += warp_sum[w];
         all += warp_sum[w];
     }
-    if (!s.cut(i, ctas, all * U)) return s;
     before += upto - mine;
-    if (s.begin >= before * U && s.begin < (before + mine) * U) {
-        for (int b = b0; b < b1; ++b) {
-            const int len = stages_of<SB>(length_of(p, b, bad));
-            if (s.begin < (before + len) * U) {
-                const long long rem = s.begin - before * U;
-                found.b = b;
-                found.unit = static_cast<int>(rem / len);
-                found.at = static_cast<int>(rem % len);
-                break;
+    const Cut cut(all * U, gridDim.x);
+    if (i < cut.n) {
+        const long long begin = cut.begin(i);
+        if (begin >= before * U && begin < (before + mine) * U) {
+            for (int b = b0; b < b1; ++b) {
+                const int len = stages_of<SB>(length_of(p, b, bad));
+                if (begin < (before + len) * U) {
+                    const long long rem = begin - before * U;
+                    sh.left = static_cast<int>(cut.begin(i + 1) - begin);
+                    sh.b = b;
+                    sh.unit = divide(rem, len);
+                    sh.at = static_cast<int>(rem - static_cast<long long>(sh.unit) * len);
+                    break;
+                }
+                before += len;
             }
-            before += len;
         }
+    } else if (threadIdx.x == 0) {
+        sh.left = 0;
     }
     __syncthreads();
-    s.b = found.b;
-    s.unit = found.unit;
-    s.at = found.at;
-    return s;
+    return cut.row;
 }
 
 // SHARES: CTA i takes share i of the row of stages; otherwise it takes chunk i.
@@ -517,26 +535,17 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
     }
     __syncthreads();
 
+    griddep_wait();  // everything above overlaps the kernel before this one
+
     // what is left of the share: kept in shared memory, out of the registers of the loop over blocks
     __shared__ Share sh;
+    __shared__ long long row;
     if constexpr (SHARES) {
-        const Share mine_ = share_of<SB>(p, blockIdx.x, gridDim.x);
+        const long long all = share_of<SB>(p, sh);
         if (threadIdx.x == 0) {
-            sh = mine_;
-            Header h = {-1, 0};
-            if (sh.left > 0 && sh.at > 0) {
-                bool bad;
-                const int n = stages_of<SB>(length_of(p, sh.b, bad));
-                if (sh.at + sh.left >= n) {
-                    h.unit = sh.b * U + sh.unit;
-                    // the last share that begins at or before the chunk's first stage
-                    const long long at = sh.begin - sh.at;
-                    h.first = static_cast<int>(((at + 1) * sh.n + sh.row - 1) / sh.row - 1);
-                }
-            }
-            p.head[blockIdx.x] = h;
+            row = all;
+            p.head[blockIdx.x] = Header{-1, 0};  // until a chunk from an earlier share ends here
         }
-        __syncthreads();
         if (sh.left <= 0) return;
     }
 
@@ -548,7 +557,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
         const int b = SHARES ? sh.b : blockIdx.x / U, unit = SHARES ? sh.unit : blockIdx.x % U, s0 = SHARES ? sh.at : 0;
         bool bad;
         const int len = length_of(p, b, bad), n = stages_of<SB>(len);
-        const int take = SHARES ? static_cast<int>(min(sh.left, static_cast<long long>(n - s0))) : n;
+        const int take = SHARES ? min(sh.left, n - s0) : n;
         const int nblk = (len + kv4::kBlock - 1) / kv4::kBlock;
         // This CTA's stages [s0, s1) of the chunk, dealt to its warps in turn from the newest to the oldest: the
         // bias falls on the way, so the references R and M settle in the first tiles. (Oldest first, a
@@ -685,6 +694,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
             sh.left -= take;
             sh.at += take;
             if (sh.at == n) {
+                if (take < n) {  // the first chunk of this share: its first stage lies `take` before the share's end so far
+                    const Cut cut(row, gridDim.x);
+                    p.head[blockIdx.x] = Header{sh.b * U + sh.unit, cut.holder(cut.begin(blockIdx.x) + take - n)};
+                }
                 sh.at = 0;
                 if (++sh.unit == U) sh.unit = 0, ++sh.b;
             }
@@ -704,6 +717,7 @@ __global__ void __launch_bounds__(kMergeThreads) decode_kv4_merge_kernel(const _
     __shared__ float weight[kMostShares];
     __shared__ float red[2][kMergeThreads / 32];
     __shared__ float4 sum[kMergeThreads];
+    griddep_launch_dependents();
     griddep_wait();
     const int last = blockIdx.x + 1, r = blockIdx.y;
     const int2 h = __ldcg(reinterpret_cast<const int2 *>(p.head + last));  // (unit, first)
@@ -799,8 +813,7 @@ cudaError_t launch(DecodeKv4Params &p, long long units, cudaStream_t stream)
         if (units > 0x7fffffffLL) return cudaErrorInvalidValue;
         const cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(whole), kSmem, 0);
         if (e != cudaSuccess) return e;
-        whole<<<static_cast<unsigned>(units), kWarps * 32, kSmem, stream>>>(p);
-        return cudaGetLastError();
+        return launch_overlapped(whole, dim3(static_cast<unsigned>(units)), kWarps * 32, kSmem, stream, p);
     }
     cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(shared), kSmem, 0);
     if (e != cudaSuccess) return e;
@@ -811,20 +824,10 @@ cudaError_t launch(DecodeKv4Params &p, long long units, cudaStream_t stream)
     if (e != cudaSuccess) return e;
     p.part = reinterpret_cast<float *>(ws);
     p.head = reinterpret_cast<Header *>(ws + bytes);
-    shared<<<static_cast<unsigned>(shares), kWarps * 32, kSmem, stream>>>(p);
-    e = cudaGetLastError();
+    e = launch_overlapped(shared, dim3(static_cast<unsigned>(shares)), kWarps * 32, kSmem, stream, p);
     if (e == cudaSuccess && shares > 1) {
         MergeParams m = {p.part, p.head, p.out, p.lse, p.d, p.rows, p.chunks};
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(static_cast<unsigned>(shares - 1), static_cast<unsigned>(std::min(p.rows, kRows)));
-        cfg.blockDim = dim3(kMergeThreads);
-        cfg.stream = stream;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, decode_kv4_merge_kernel<D>, m);
+        e = launch_overlapped(decode_kv4_merge_kernel<D>, dim3(shares - 1, std::min(p.rows, kRows)), kMergeThreads, 0, stream, m);
     }
     const cudaError_t f = cudaFreeAsync(ws, stream);
     return e != cudaSuccess ? e : f;

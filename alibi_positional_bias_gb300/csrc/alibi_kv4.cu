@@ -12,8 +12,8 @@
 #include <cuda_bf16.h>
 
 #include "alibi.h"
-#include "internal.h"
 #include "kv4.h"
+#include "ptx.cuh"
 
 namespace alibi {
 namespace {
@@ -47,6 +47,8 @@ template <int D>
 __global__ void __launch_bounds__(256) kv4_write_kernel(const __grid_constant__ Kv4Params p)
 {
     constexpr int LPR = D / 8;  // lanes per row, 8 elements each
+    griddep_launch_dependents();
+    griddep_wait();
     const long long i = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / LPR;  // (row, key or value)
     const int l = threadIdx.x % LPR;
     const long long row = i >> 1;
@@ -102,6 +104,8 @@ template <int D, bool F32>
 __global__ void __launch_bounds__(256) kv4_read_kernel(const __grid_constant__ Kv4Params p)
 {
     constexpr int LPR = D / 8;
+    griddep_launch_dependents();
+    griddep_wait();
     const long long i = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / LPR;
     const int l = threadIdx.x % LPR;
     const long long row = i >> 1;
@@ -140,7 +144,7 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(const __grid_constant__ K
 
 bool aligned(const void *p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-int check(int B, int H, int T, int C, int d)
+int check_sizes(int B, int H, int T, int C, int d)
 {
     if (B < 1 || H < 1 || T < 1 || C < 1 || d < 1) return ALIBI_ERR_INVALID;
     if (C % kv4::kBlock != 0 || T > C) return ALIBI_ERR_INVALID;
@@ -154,13 +158,10 @@ template <int D>
 cudaError_t launch(const Kv4Params &p, int op, cudaStream_t stream)
 {
     const unsigned grid = static_cast<unsigned>((p.rows * 2 * (D / 8) + 255) / 256);
-    if (op == 0)
-        kv4_write_kernel<D><<<grid, 256, 0, stream>>>(p);
-    else if (op == 1)
-        kv4_read_kernel<D, false><<<grid, 256, 0, stream>>>(p);
-    else
-        kv4_read_kernel<D, true><<<grid, 256, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_overlapped(op == 0   ? kv4_write_kernel<D>
+                             : op == 1 ? kv4_read_kernel<D, false>
+                                       : kv4_read_kernel<D, true>,
+                             dim3(grid), 256, 0, stream, p);
 }
 
 int run(Kv4Params &p, int B, int op, void *stream)
@@ -196,7 +197,7 @@ extern "C" int alibi_kv4_write(const void *k, const void *v, void *cache, const 
     if (!k || !v || !cache) return ALIBI_ERR_INVALID;
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(cache, 16) || !aligned(pos, 4) || !aligned(count, 4))
         return ALIBI_ERR_INVALID;
-    const int st = check(B, H, T, C, d);
+    const int st = check_sizes(B, H, T, C, d);
     if (st != ALIBI_OK) return st;
     Kv4Params p = {};
     p.k = k;
@@ -218,7 +219,7 @@ extern "C" int alibi_kv4_read(const void *cache, void *k, void *v, const int *po
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(cache, 16) || !aligned(pos, 4) || !aligned(count, 4))
         return ALIBI_ERR_INVALID;
     if (fp32 != 0 && fp32 != 1) return ALIBI_ERR_INVALID;
-    const int st = check(B, H, T, C, d);
+    const int st = check_sizes(B, H, T, C, d);
     if (st != ALIBI_OK) return st;
     Kv4Params p = {};
     p.ko = k;

@@ -50,6 +50,25 @@ cudaMemPool_t decode_pool();     // library-owned stream-ordered pool of the cur
 bool encode_tmap_bf16_3d(CUtensorMap *map, const void *base, uint64_t dim0, uint64_t dim1, uint64_t dim2,
                          uint32_t box0, uint32_t box1, bool swizzle128 = true);
 
+// Launch with programmatic stream serialization: the grid may be scheduled while the previous kernel in the stream
+// drains. A kernel launched so executes griddepcontrol.wait in every thread that reads or writes memory, before it does.
+template <class Params>
+cudaError_t launch_overlapped(void (*kernel)(Params), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
+                              const Params &p)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 // Decode split plan (alibi_decode.cu): number of KV splits for B*H heads of length L.
 int decode_splits(int BH, int L);
 // Bytes of split-K partials the decode needs for that plan (0 when it does not split).
