@@ -65,9 +65,8 @@ struct HeadSlopes {
 // goes on in a later one (1), each of kRows rows of D means and then (R, l) of each row.
 KV4_HD constexpr int part_floats(int D) { return kRows * (D + 2); }
 
-struct alignas(8) Header {
-    int unit;   // the chunk that ends in this share and began in an earlier one, or -1
-    int first;  // the share it began in
+struct alignas(8) Header {  // of a chunk
+    int first, last;  // the shares it begins and ends in, or -1 where one share did all of it
 };
 
 struct DecodeKv4Params {
@@ -77,7 +76,7 @@ struct DecodeKv4Params {
     __nv_bfloat16 *out;      // [B, H, T, d]
     float *lse;              // [B, H, T] or null
     float *part;             // [CTAs][2][part_floats], null: CTA i takes chunk i
-    Header *head;            // [CTAs]
+    Header *head;            // [chunks of all sequences]
     uint32_t *status;
     int B, Hkv, T, L, blocks, d;  // blocks: C / 32
     int rows, chunks;             // G T, ceil(G T / 8)
@@ -446,33 +445,53 @@ __device__ __forceinline__ int divide(long long a, int b)
     return a < (1LL << 32) ? static_cast<int>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : static_cast<int>(a / b);
 }
 
-// Share blockIdx.x, into `sh`; returns the row. All threads of the CTA.
+// Share `i`, into `sh`; returns the row. All threads of the CTA.
 template <int SB>
-__device__ __forceinline__ long long share_of(const DecodeKv4Params &p, Share &sh)
+__device__ __forceinline__ long long share_of(const DecodeKv4Params &p, int i, Share &sh)
 {
-    const int U = p.Hkv * p.chunks, i = blockIdx.x;
-    __shared__ long long warp_sum[kWarps];
+    const int U = p.Hkv * p.chunks;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (!p.lens) {
-        const int len = stages_of<SB>(p.L);
-        const Cut cut(static_cast<long long>(p.B) * U * len, gridDim.x);
-        if (threadIdx.x == 0) {
-            sh.left = 0;
+    bool bad;
+    if (!p.lens || p.B <= 32) {
+        // one sequence per lane (or equal lengths), in every warp
+        const int len = !p.lens || lane < p.B ? stages_of<SB>(length_of(p, p.lens ? lane : 0, bad)) : 0;
+        int upto = len;
+        long long row = static_cast<long long>(p.B) * len;
+        if (p.lens) {
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, upto, off);
+                if (lane >= off) upto += v;
+            }
+            row = __shfl_sync(0xffffffffu, upto, 31);
+        }
+        const Cut cut(row * U, gridDim.x);
+        if (warp == 0) {
+            long long begin = 0;
+            int left = 0, b = 0, n = len;
             if (i < cut.n) {
-                const long long begin = cut.begin(i);
-                const int unit = divide(begin, len);  // of all sequences
-                sh.left = static_cast<int>(cut.begin(i + 1) - begin);
-                sh.at = static_cast<int>(begin - static_cast<long long>(unit) * len);
-                sh.b = unit / U;
-                sh.unit = unit % U;
+                begin = cut.begin(i);
+                left = static_cast<int>(cut.begin(i + 1) - begin);
+                if (p.lens) {
+                    b = __popc(__ballot_sync(0xffffffffu, static_cast<long long>(upto) * U <= begin));
+                    n = __shfl_sync(0xffffffffu, len, b);
+                    begin -= static_cast<long long>(__shfl_sync(0xffffffffu, upto, b) - n) * U;
+                }
+            }
+            if (lane == 0) {
+                const int unit = divide(begin, n);  // with equal lengths, of all sequences
+                sh.left = left;
+                sh.at = static_cast<int>(begin - static_cast<long long>(unit) * n);
+                sh.b = p.lens ? b : unit / U;
+                sh.unit = p.lens ? unit : unit % U;
             }
         }
         __syncthreads();
         return cut.row;
     }
     // sum of the sequences' stages, a run of sequences per thread; then the run that holds the beginning
+    __shared__ long long warp_sum[kWarps];
     const int run = (p.B + kWarps * 32 - 1) / (kWarps * 32), b0 = threadIdx.x * run, b1 = min(p.B, b0 + run);
-    bool bad;
     long long mine = 0;
     for (int b = b0; b < b1; ++b) mine += stages_of<SB>(length_of(p, b, bad));
     long long upto = mine;
@@ -540,12 +559,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
     // what is left of the share: kept in shared memory, out of the registers of the loop over blocks
     __shared__ Share sh;
     __shared__ long long row;
+    // The second half of the CTAs, which join the first on their SMs, take the shares from the end: with them an SM has heads
+    // from both ends of the row, steep slopes, whose far values are skipped, with flat ones.
+    const int half = gridDim.x / 2;
+    const int share = static_cast<int>(blockIdx.x) < half ? blockIdx.x : gridDim.x - 1 - (blockIdx.x - half);
     if constexpr (SHARES) {
-        const long long all = share_of<SB>(p, sh);
-        if (threadIdx.x == 0) {
-            row = all;
-            p.head[blockIdx.x] = Header{-1, 0};  // until a chunk from an earlier share ends here
-        }
+        const long long all = share_of<SB>(p, share, sh);
+        if (threadIdx.x == 0) row = all;
         if (sh.left <= 0) return;
     }
 
@@ -670,7 +690,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
         float *to = nullptr;
         if constexpr (SHARES) {
             whole = sh.left >= n - sh.at && sh.at == 0;
-            to = p.part + (static_cast<size_t>(blockIdx.x) * 2 + (sh.at == 0)) * part_floats(D);
+            to = p.part + (static_cast<size_t>(share) * 2 + (sh.at == 0)) * part_floats(D);
         }
         for (int i = threadIdx.x; i < nrows * (D / 4); i += kWarps * 32) {
             const int r = i / (D / 4), e = i % (D / 4) * 4;
@@ -694,10 +714,12 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
             sh.left -= take;
             sh.at += take;
             if (sh.at == n) {
-                if (take < n) {  // the first chunk of this share: its first stage lies `take` before the share's end so far
+                Header h = {-1, -1};
+                if (take < n) {  // this share's first chunk, whose first stage lies n - take before the share's beginning
                     const Cut cut(row, gridDim.x);
-                    p.head[blockIdx.x] = Header{sh.b * U + sh.unit, cut.holder(cut.begin(blockIdx.x) + take - n)};
+                    h = {cut.holder(cut.begin(share) + take - n), share};
                 }
+                p.head[static_cast<size_t>(sh.b) * U + sh.unit] = h;
                 sh.at = 0;
                 if (++sh.unit == U) sh.unit = 0, ++sh.b;
             }
@@ -707,8 +729,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
     }
 }
 
-// Merge of the chunks that several shares worked on: CTA (i, r) looks at row r of the chunk that ends in share i + 1. Its
-// partials are slot 1 of the share it began in and slot 0 of the shares up to this one. The loads of a thread are issued
+// Merge of the chunks that several shares worked on: CTA (i, r) looks at row r of chunk i. Its partials are slot 1 of the
+// share it began in and slot 0 of the shares up to the one it ends in. The loads of a thread are issued
 // together: with 76 partials the merge waits for three round trips to L2 and not for 76.
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) decode_kv4_merge_kernel(const __grid_constant__ MergeParams p)
@@ -719,13 +741,13 @@ __global__ void __launch_bounds__(kMergeThreads) decode_kv4_merge_kernel(const _
     __shared__ float4 sum[kMergeThreads];
     griddep_launch_dependents();
     griddep_wait();
-    const int last = blockIdx.x + 1, r = blockIdx.y;
-    const int2 h = __ldcg(reinterpret_cast<const int2 *>(p.head + last));  // (unit, first)
+    const int unit = blockIdx.x, r = blockIdx.y;
+    const int2 h = __ldcg(reinterpret_cast<const int2 *>(p.head + unit));  // (first, last)
     if (h.x < 0) return;
-    const int n = last - h.y + 1;
-    const int bk = h.x / p.chunks, row0 = (h.x - bk * p.chunks) * kRows;
+    const int n = h.y - h.x + 1;
+    const int bk = unit / p.chunks, row0 = (unit - bk * p.chunks) * kRows;
     if (row0 + r >= p.rows) return;
-    const float *part0 = p.part + (static_cast<size_t>(h.y) * 2 + 1) * kPart;
+    const float *part0 = p.part + (static_cast<size_t>(h.x) * 2 + 1) * kPart;
     const auto from = [&](int k) { return part0 + (k == 0 ? 0 : (2 * k - 1) * kPart); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, item = threadIdx.x % kItems, group = threadIdx.x / kItems;
     // the first means are fetched while the weights are computed
@@ -820,14 +842,14 @@ cudaError_t launch(DecodeKv4Params &p, long long units, cudaStream_t stream)
     const int shares = static_cast<int>(std::min<long long>(units * per, std::min(2 * num_sms(), kMostShares)));
     const size_t bytes = static_cast<size_t>(shares) * 2 * part_floats(D) * sizeof(float);
     char *ws = nullptr;
-    e = cudaMallocFromPoolAsync(reinterpret_cast<void **>(&ws), bytes + shares * sizeof(Header), decode_pool(), stream);
+    e = cudaMallocFromPoolAsync(reinterpret_cast<void **>(&ws), bytes + static_cast<size_t>(units) * sizeof(Header), decode_pool(), stream);
     if (e != cudaSuccess) return e;
     p.part = reinterpret_cast<float *>(ws);
     p.head = reinterpret_cast<Header *>(ws + bytes);
     e = launch_overlapped(shared, dim3(static_cast<unsigned>(shares)), kWarps * 32, kSmem, stream, p);
     if (e == cudaSuccess && shares > 1) {
         MergeParams m = {p.part, p.head, p.out, p.lse, p.d, p.rows, p.chunks};
-        e = launch_overlapped(decode_kv4_merge_kernel<D>, dim3(shares - 1, std::min(p.rows, kRows)), kMergeThreads, 0, stream, m);
+        e = launch_overlapped(decode_kv4_merge_kernel<D>, dim3(static_cast<unsigned>(units), std::min(p.rows, kRows)), kMergeThreads, 0, stream, m);
     }
     const cudaError_t f = cudaFreeAsync(ws, stream);
     return e != cudaSuccess ? e : f;
