@@ -29,11 +29,13 @@
 //            rounding to 11 bits is the only one below fp32: off by at most 2^-11 of each
 //            product, a quarter of the bf16 output's own step.
 //
-// The work is dealt in stages: the chunks of all sequences, one after another, form one row of
-// stages, and each of the 2 x 152 resident CTAs takes an equal share of it, whatever the lengths (which
-// only the device knows). A share may end inside a chunk: such chunks leave a partial for each share,
-// and a second kernel, launched as a programmatic dependent, merges them in fp32. Where a
-// chunk is no more than one stage for each warp, a CTA takes one chunk and nothing is merged.
+// The work is dealt in one of three ways (deal_of), by lengths that only the device knows:
+//   whole    a CTA takes one chunk: short sequences, and many chunks;
+//   slices   each of few chunks has several of the 2 x 152 resident CTAs, in proportion to its length;
+//   shares   the chunks of all sequences, one after another, form one row of stages, of which each resident
+//            CTA takes an equal share, whose ends may lie inside chunks.
+// A chunk that several CTAs worked on leaves a partial from each, and a second kernel, launched as a
+// programmatic dependent, merges them in fp32.
 
 #include <algorithm>
 #include <cfloat>
@@ -54,7 +56,6 @@ constexpr int kStageBytes = 4608;   // 128 / D blocks of 36 D bytes
 constexpr int kRows = 8;            // query rows of a chunk, at most (the columns of an mma)
 constexpr int kMostShares = 512;   // CTAs that share the work (two per SM)
 constexpr int kMergeThreads = 256;
-constexpr int kWholeRounds = 4;
 constexpr int kSmem = kWarps * kStages * kStageBytes;
 
 struct HeadSlopes {
@@ -80,6 +81,7 @@ struct DecodeKv4Params {
     uint32_t *status;
     int B, Hkv, T, L, blocks, d;  // blocks: C / 32
     int rows, chunks;             // G T, ceil(G T / 8)
+    bool slices;                  // every chunk has CTAs of its own; otherwise equal shares
     float c1;                     // 2^-14 log2(e) / sqrt(d)
     HeadSlopes slopes;
 };
@@ -416,14 +418,20 @@ __device__ __forceinline__ int stages_of(int len)  // at least one, so that ever
     return max(1, (len + SB * kv4::kBlock - 1) / (SB * kv4::kBlock));
 }
 
-// Where a share of the row of stages lies.
+// Where the work of a CTA lies.
 struct Share {
-    int left;         // stages of the share that are left
+    int left;         // stages that are left
     int b, unit, at;  // sequence, chunk of it and stage of that chunk that comes next
+    int first;        // slices: the CTA that has the chunk's first slice
 };
 
-// Share `i` of `ctas` of a row of `row` stages is [i row / n, (i + 1) row / n), n = min(ctas, row). Divisions in 32 bits
-// where the row allows it (all but sequences of many millions of tokens in all).
+__device__ __forceinline__ int divide(long long a, int b)
+{
+    return a < (1LL << 32) ? static_cast<int>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : static_cast<int>(a / b);
+}
+
+// Equal shares: share `i` of `ctas` of a row of `row` stages is [i row / n, (i + 1) row / n), n = min(ctas, row).
+// Divisions in 32 bits where the row allows it (all but sequences of many millions of tokens in all).
 struct Cut {
     long long row;
     int n;
@@ -440,100 +448,142 @@ struct Cut {
     __device__ __forceinline__ int holder(long long at) const { return static_cast<int>(((at + 1) * n + row - 1) / row - 1); }
 };
 
-__device__ __forceinline__ int divide(long long a, int b)
-{
-    return a < (1LL << 32) ? static_cast<int>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : static_cast<int>(a / b);
-}
+// Slices: every chunk has CTAs of its own, in proportion to its weight, its stages + `extra`, with `extra` just large enough
+// for the shortest chunk to have one. The chunk that begins at weight w of `all` has CTAs from floor(w ctas / all) on.
+struct Slices {
+    long long all;
+    int extra, ctas;
 
-// Share `i`, into `sh`; returns the row. All threads of the CTA.
+    __device__ __forceinline__ Slices(long long row, int units, int shortest, int ctas_) : ctas(ctas_)
+    {
+        const long long lack = row - static_cast<long long>(shortest) * ctas;
+        extra = lack > 0 ? divide(lack + ctas - units - 1, ctas - units) : 0;
+        all = row + static_cast<long long>(extra) * units;
+    }
+    __device__ __forceinline__ int cta(long long w) const
+    {
+        if (all < (1LL << 32) / (kMostShares + 1)) return static_cast<uint32_t>(w) * static_cast<uint32_t>(ctas) / static_cast<uint32_t>(all);
+        return static_cast<int>(w * ctas / all);
+    }
+    // the last weight whose CTA is i or before
+    __device__ __forceinline__ long long last(int i) const
+    {
+        if (all < (1LL << 32) / (kMostShares + 1))
+            return (static_cast<uint32_t>(i + 1) * static_cast<uint32_t>(all) + ctas - 1) / static_cast<uint32_t>(ctas) - 1;
+        return ((i + 1) * all + ctas - 1) / ctas - 1;
+    }
+    // slice i of the chunk of n stages that begins at weight w
+    __device__ __forceinline__ void place(int i, long long w, int n, Share &sh) const
+    {
+        const int c0 = cta(w), c1 = cta(w + n + extra), count = c1 - c0, k = i - c0;
+        const int per = n / count, more = n - per * count;
+        sh.first = c0;
+        sh.at = k * per + min(k, more);
+        sh.left = per + (k < more ? 1 : 0);
+    }
+};
+
+// Share or slice `i`, into `sh`; returns the row. All threads of the CTA.
 template <int SB>
 __device__ __forceinline__ long long share_of(const DecodeKv4Params &p, int i, Share &sh)
 {
-    const int U = p.Hkv * p.chunks;
+    const int U = p.Hkv * p.chunks, ctas = gridDim.x;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     bool bad;
-    if (!p.lens || p.B <= 32) {
-        // one sequence per lane (or equal lengths), in every warp
-        const int len = !p.lens || lane < p.B ? stages_of<SB>(length_of(p, p.lens ? lane : 0, bad)) : 0;
-        int upto = len;
-        long long row = static_cast<long long>(p.B) * len;
-        if (p.lens) {
+    if (p.B <= 32) {  // one sequence per lane, in every warp
+        const int n = lane < p.B ? stages_of<SB>(length_of(p, lane, bad)) : 0;
+        int upto = n;
 #pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, upto, off);
-                if (lane >= off) upto += v;
-            }
-            row = __shfl_sync(0xffffffffu, upto, 31);
+        for (int off = 1; off < 32; off <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, off);
+            if (lane >= off) upto += v;
         }
-        const Cut cut(row * U, gridDim.x);
+        const long long row = static_cast<long long>(__shfl_sync(0xffffffffu, upto, 31)) * U;
         if (warp == 0) {
-            long long begin = 0;
-            int left = 0, b = 0, n = len;
-            if (i < cut.n) {
-                begin = cut.begin(i);
-                left = static_cast<int>(cut.begin(i + 1) - begin);
-                if (p.lens) {
-                    b = __popc(__ballot_sync(0xffffffffu, static_cast<long long>(upto) * U <= begin));
-                    n = __shfl_sync(0xffffffffu, len, b);
-                    begin -= static_cast<long long>(__shfl_sync(0xffffffffu, upto, b) - n) * U;
-                }
-            }
+            const Cut cut(row, ctas);
+            const Slices sl(row, p.B * U, static_cast<int>(__reduce_min_sync(0xffffffffu, n ? n : 0x7fffffff)), ctas);
+            const long long weight = static_cast<long long>(upto) * U + static_cast<long long>(lane + 1) * U * sl.extra;
+            const long long at = p.slices ? sl.last(i) : i < cut.n ? cut.begin(i) : 0;
+            const int b = __popc(__ballot_sync(0xffffffffu, lane < p.B && (p.slices ? weight : static_cast<long long>(upto) * U) <= at));
+            const int nb = __shfl_sync(0xffffffffu, n, b), before = __shfl_sync(0xffffffffu, upto, b) - nb;
             if (lane == 0) {
-                const int unit = divide(begin, n);  // with equal lengths, of all sequences
-                sh.left = left;
-                sh.at = static_cast<int>(begin - static_cast<long long>(unit) * n);
-                sh.b = p.lens ? b : unit / U;
-                sh.unit = p.lens ? unit : unit % U;
+                sh.b = b;
+                if (p.slices) {
+                    const int step = nb + sl.extra;
+                    const long long w0 = (before + static_cast<long long>(b) * sl.extra) * U;
+                    sh.unit = min(U - 1, divide(at - w0, step));
+                    sl.place(i, w0 + static_cast<long long>(sh.unit) * step, nb, sh);
+                } else {
+                    const long long rem = at - static_cast<long long>(before) * U;
+                    sh.left = i < cut.n ? static_cast<int>(cut.begin(i + 1) - at) : 0;
+                    sh.unit = divide(rem, nb);
+                    sh.at = static_cast<int>(rem - static_cast<long long>(sh.unit) * nb);
+                }
             }
         }
         __syncthreads();
-        return cut.row;
+        return row;
     }
     // sum of the sequences' stages, a run of sequences per thread; then the run that holds the beginning
     __shared__ long long warp_sum[kWarps];
-    const int run = (p.B + kWarps * 32 - 1) / (kWarps * 32), b0 = threadIdx.x * run, b1 = min(p.B, b0 + run);
+    __shared__ int warp_min[kWarps];
+    const int run = (p.B + kWarps * 32 - 1) / (kWarps * 32), b0 = min(p.B, static_cast<int>(threadIdx.x) * run), b1 = min(p.B, b0 + run);
     long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += stages_of<SB>(length_of(p, b, bad));
+    int least = 0x7fffffff;
+    for (int b = b0; b < b1; ++b) {
+        const int n = stages_of<SB>(length_of(p, b, bad));
+        mine += n;
+        least = min(least, n);
+    }
     long long upto = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
         const long long v = __shfl_up_sync(0xffffffffu, upto, off);
         if (lane >= off) upto += v;
     }
-    if (lane == 31) warp_sum[warp] = upto;
+    least = __reduce_min_sync(0xffffffffu, least);
+    if (lane == 31) warp_sum[warp] = upto, warp_min[warp] = least;
     __syncthreads();
     long long before = 0, all = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
         if (w < warp) before += warp_sum[w];
         all += warp_sum[w];
+        least = min(least, warp_min[w]);
     }
     before += upto - mine;
-    const Cut cut(all * U, gridDim.x);
-    if (i < cut.n) {
-        const long long begin = cut.begin(i);
-        if (begin >= before * U && begin < (before + mine) * U) {
+    const Cut cut(all * U, ctas);
+    if (p.slices || i < cut.n) {
+        const Slices sl(all * U, p.B * U, least, ctas);
+        const int extra = p.slices ? sl.extra : 0;
+        const long long at = p.slices ? sl.last(i) : cut.begin(i);
+        long long w0 = (before + static_cast<long long>(b0) * extra) * U;
+        if (at >= w0 && at < w0 + (mine + static_cast<long long>(b1 - b0) * extra) * U) {
             for (int b = b0; b < b1; ++b) {
-                const int len = stages_of<SB>(length_of(p, b, bad));
-                if (begin < (before + len) * U) {
-                    const long long rem = begin - before * U;
-                    sh.left = static_cast<int>(cut.begin(i + 1) - begin);
+                const int n = stages_of<SB>(length_of(p, b, bad)), step = n + extra;
+                if (at < w0 + static_cast<long long>(step) * U) {
                     sh.b = b;
-                    sh.unit = divide(rem, len);
-                    sh.at = static_cast<int>(rem - static_cast<long long>(sh.unit) * len);
+                    sh.unit = divide(at - w0, step);
+                    w0 += static_cast<long long>(sh.unit) * step;
+                    if (p.slices) {
+                        sl.place(i, w0, n, sh);
+                    } else {
+                        sh.left = static_cast<int>(cut.begin(i + 1) - at);
+                        sh.at = static_cast<int>(at - w0);
+                    }
                     break;
                 }
-                before += len;
+                w0 += static_cast<long long>(step) * U;
             }
         }
     } else if (threadIdx.x == 0) {
         sh.left = 0;
     }
     __syncthreads();
-    return cut.row;
+    return all * U;
 }
 
-// SHARES: CTA i takes share i of the row of stages; otherwise it takes chunk i.
+// SHARES: CTA i takes share or slice i; otherwise it takes chunk i.
 template <int D, int KC, bool SHARES>
 __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid_constant__ DecodeKv4Params p)
 {
@@ -715,9 +765,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
             sh.at += take;
             if (sh.at == n) {
                 Header h = {-1, -1};
-                if (take < n) {  // this share's first chunk, whose first stage lies n - take before the share's beginning
+                if (take < n) {  // a share's first chunk, whose first stage lies n - take before the share's beginning
                     const Cut cut(row, gridDim.x);
-                    h = {cut.holder(cut.begin(share) + take - n), share};
+                    h = {p.slices ? sh.first : cut.holder(cut.begin(share) + take - n), share};
                 }
                 p.head[static_cast<size_t>(sh.b) * U + sh.unit] = h;
                 sh.at = 0;
@@ -817,10 +867,20 @@ __global__ void __launch_bounds__(kMergeThreads) decode_kv4_merge_kernel(const _
 
 bool aligned(const void *p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-// Chunks that are dealt whole, one to a CTA: where they are no longer than a stage for each warp, and where there are
-// many rounds of them. (64 x 40 heads of 8192 tokens, 8.4 rounds: XX us whole, XX us in equal shares, which
-// wait for the SMs and heads that take longest.)
-bool whole_chunks(long long units, int per) { return per == 1 || units >= kWholeRounds * 2LL * num_sms(); }
+enum class Deal { Whole, Slices, Shares };
+
+// The way with the least estimated time of its slowest CTA, in stages (a quarter of a microsecond each with two CTAs on
+// every SM): a chunk's start and end cost a CTA 18 more, unless the other CTA of its SM works on meanwhile, and
+// the merge kernel 12.
+Deal deal_of(long long units, int stages, int ctas)
+{
+    if (stages <= kWarps) return Deal::Whole;
+    const double rounds = static_cast<double>(units) / ctas;
+    const double whole = rounds > 1 ? std::ceil(rounds) * (stages + 4) : stages + 18;
+    const double slices = units <= ctas ? (stages + ctas / units - 1) / (ctas / units) + 18 + 12 : DBL_MAX;
+    const double shares = rounds * stages + 18 * (1 + rounds) + 18 + 12;
+    return whole <= slices && whole <= shares ? Deal::Whole : slices <= shares ? Deal::Slices : Deal::Shares;
+}
 
 template <int D, int KC>
 cudaError_t launch(DecodeKv4Params &p, long long units, cudaStream_t stream)
@@ -828,10 +888,12 @@ cudaError_t launch(DecodeKv4Params &p, long long units, cudaStream_t stream)
     const auto whole = &decode_kv4_kernel<D, KC, false>;
     const auto shared = &decode_kv4_kernel<D, KC, true>;
     constexpr int kTokens = 128 / D * kv4::kBlock;  // of a stage
-    const int per = ((p.L + kTokens - 1) / kTokens + kWarps - 1) / kWarps;  // CTAs a chunk can keep busy
+    const int stages = (p.L + kTokens - 1) / kTokens, ctas = std::min(2 * num_sms(), kMostShares);
+    const Deal deal = deal_of(units, stages, ctas);
     p.part = nullptr;
     p.head = nullptr;
-    if (whole_chunks(units, per)) {
+    p.slices = false;
+    if (deal == Deal::Whole) {
         if (units > 0x7fffffffLL) return cudaErrorInvalidValue;
         const cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(whole), kSmem, 0);
         if (e != cudaSuccess) return e;
@@ -839,7 +901,9 @@ cudaError_t launch(DecodeKv4Params &p, long long units, cudaStream_t stream)
     }
     cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(shared), kSmem, 0);
     if (e != cudaSuccess) return e;
-    const int shares = static_cast<int>(std::min<long long>(units * per, std::min(2 * num_sms(), kMostShares)));
+    const int per = (stages + kWarps - 1) / kWarps;  // CTAs that a chunk can keep busy
+    const int shares = static_cast<int>(std::min<long long>(units * per, ctas));
+    p.slices = deal == Deal::Slices;
     const size_t bytes = static_cast<size_t>(shares) * 2 * part_floats(D) * sizeof(float);
     char *ws = nullptr;
     e = cudaMallocFromPoolAsync(reinterpret_cast<void **>(&ws), bytes + static_cast<size_t>(units) * sizeof(Header), decode_pool(), stream);
