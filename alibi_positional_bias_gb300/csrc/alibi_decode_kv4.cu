@@ -31,7 +31,8 @@
 //
 // The work is dealt in one of three ways (deal_of), by lengths that only the device knows:
 //   whole    a CTA takes one chunk: short sequences, and many chunks;
-//   slices   each of few chunks has several of the 2 x 152 resident CTAs, in proportion to its length;
+//   slices   each of few chunks has several of the 2 x 152 resident CTAs, in proportion to its length, which take
+//            its stages in turn;
 //   shares   the chunks of all sequences, one after another, form one row of stages, of which each resident
 //            CTA takes an equal share, whose ends may lie inside chunks.
 // A chunk that several CTAs worked on leaves a partial from each, and a second kernel, launched as a
@@ -420,9 +421,9 @@ __device__ __forceinline__ int stages_of(int len)  // at least one, so that ever
 
 // Where the work of a CTA lies.
 struct Share {
-    int left;         // stages that are left
-    int b, unit, at;  // sequence, chunk of it and stage of that chunk that comes next
-    int first;        // slices: the CTA that has the chunk's first slice
+    int left;          // stages that are left (slices: of the whole chunk)
+    int b, unit, at;   // sequence, chunk of it and stage of that chunk that comes next (slices: number of the slice)
+    int first, count;  // slices: the CTA that has the chunk's first slice, and their number
 };
 
 __device__ __forceinline__ int divide(long long a, int b)
@@ -472,14 +473,15 @@ struct Slices {
             return (static_cast<uint32_t>(i + 1) * static_cast<uint32_t>(all) + ctas - 1) / static_cast<uint32_t>(ctas) - 1;
         return ((i + 1) * all + ctas - 1) / ctas - 1;
     }
-    // slice i of the chunk of n stages that begins at weight w
+    // CTA i's slice of the chunk of n stages that begins at weight w: of `count` slices, slice k has the stages k, k + count,
+    // ... counted from the newest, so that each has its part of the near tokens, whose values count, and of the far
+    // ones, whose values are skipped
     __device__ __forceinline__ void place(int i, long long w, int n, Share &sh) const
     {
-        const int c0 = cta(w), c1 = cta(w + n + extra), count = c1 - c0, k = i - c0;
-        const int per = n / count, more = n - per * count;
-        sh.first = c0;
-        sh.at = k * per + min(k, more);
-        sh.left = per + (k < more ? 1 : 0);
+        sh.first = cta(w);
+        sh.count = min(n, cta(w + n + extra) - sh.first);
+        sh.at = i - sh.first;
+        sh.left = sh.at < sh.count ? n : 0;
     }
 };
 
@@ -624,15 +626,17 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
     uint32_t phase = 0;
 
     while (true) {
-        const int b = SHARES ? sh.b : blockIdx.x / U, unit = SHARES ? sh.unit : blockIdx.x % U, s0 = SHARES ? sh.at : 0;
+        const int b = SHARES ? sh.b : blockIdx.x / U, unit = SHARES ? sh.unit : blockIdx.x % U, at = SHARES ? sh.at : 0;
         bool bad;
         const int len = length_of(p, b, bad), n = stages_of<SB>(len);
-        const int take = SHARES ? min(sh.left, n - s0) : n;
         const int nblk = (len + kv4::kBlock - 1) / kv4::kBlock;
-        // This CTA's stages [s0, s1) of the chunk, dealt to its warps in turn from the newest to the oldest: the
-        // bias falls on the way, so the references R and M settle in the first tiles. (Oldest first, a
-        // steep head raises them at every tile.)
-        const int s1 = min(s0 + take, (nblk + SB - 1) / SB);
+        const bool slices = SHARES && p.slices;
+        const int take = SHARES && !slices ? min(sh.left, n - at) : n;
+        // This CTA's stages [s0, s1) of the chunk (slices: every sh.count-th of all), dealt to its warps in turn from the
+        // newest to the oldest: the bias falls on the way, so the references R and M settle in the first
+        // tiles. (Oldest first, a steep head raises them at every tile.)
+        const int s0 = slices ? 0 : at, s1 = min(s0 + take, (nblk + SB - 1) / SB);
+        const int step = slices ? kWarps * sh.count : kWarps;
         const int hk = unit / p.chunks, chunk = unit - hk * p.chunks;
         const size_t bk = static_cast<size_t>(b) * p.Hkv + hk;
         const int row0 = chunk * kRows, nrows = min(kRows, p.rows - row0);
@@ -644,10 +648,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
             mbar_arrive_expect_tx(&full[warp][slot_], bytes);
             bulk_load(mine + slot_ * kStageBytes, src + static_cast<size_t>(s) * kStageBytes, bytes, &full[warp][slot_]);
         };
-        int s = s1 - 1 - warp;  // this warp's stages: s, s - kWarps, ...
+        int s = s1 - 1 - (slices ? at + warp * sh.count : warp);  // this warp's stages: s, s - step, ...
         if (lane == 0)
             for (int i = 0, k = slot; i < kStages; ++i) {
-                if (s - i * kWarps >= s0) fetch(s - i * kWarps, k);
+                if (s - i * step >= s0) fetch(s - i * step, k);
                 if (++k == kStages) k = 0;
             }
 
@@ -693,7 +697,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
             }
         }
 
-        for (; s >= s0; s -= kWarps) {
+        for (; s >= s0; s -= step) {
             const bool ok = mbar_wait(&full[warp][slot], phase, p.status, 0x60);
             if (!__all_sync(0xffffffffu, ok)) break;
             const uint8_t *stage = mine + slot * kStageBytes;
@@ -707,11 +711,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
                     block32<D, KC, false>(st, stage + t * kBlk, j0, lane);
             }
             __syncwarp();
-            if (lane == 0 && s - kStages * kWarps >= s0) fetch(s - kStages * kWarps, slot);
+            if (lane == 0 && s - kStages * step >= s0) fetch(s - kStages * step, slot);
             if (++slot == kStages) slot = 0, phase ^= 1u;
         }
         // a wait ran out (recorded): let the copies in flight land before the ring is reused
-        for (int i = 0; i < kStages && s >= s0; ++i, s -= kWarps) {
+        for (int i = 0; i < kStages && s >= s0; ++i, s -= step) {
             mbar_wait(&full[warp][slot], phase, p.status, 0x61, true);
             if (++slot == kStages) slot = 0, phase ^= 1u;
         }
@@ -739,7 +743,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
         bool whole = true;
         float *to = nullptr;
         if constexpr (SHARES) {
-            whole = sh.left >= n - sh.at && sh.at == 0;
+            whole = p.slices ? sh.count == 1 : take == n;
             to = p.part + (static_cast<size_t>(share) * 2 + (sh.at == 0)) * part_floats(D);
         }
         for (int i = threadIdx.x; i < nrows * (D / 4); i += kWarps * 32) {
@@ -758,6 +762,12 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
             }
         }
         if constexpr (!SHARES) return;
+        if (p.slices) {
+            if (threadIdx.x == 0 && sh.at == 0)
+                p.head[static_cast<size_t>(sh.b) * U + sh.unit] =
+                    sh.count == 1 ? Header{-1, -1} : Header{share, share + sh.count - 1};
+            return;
+        }
         fence_proxy_async_smem();  // the partials were written and read before the next copies overwrite them
         __syncthreads();
         if (threadIdx.x == 0) {
@@ -765,9 +775,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
             sh.at += take;
             if (sh.at == n) {
                 Header h = {-1, -1};
-                if (take < n) {  // a share's first chunk, whose first stage lies n - take before the share's beginning
+                if (take < n) {  // the share's first chunk, whose first stage lies n - take before the share's beginning
                     const Cut cut(row, gridDim.x);
-                    h = {p.slices ? sh.first : cut.holder(cut.begin(share) + take - n), share};
+                    h = {cut.holder(cut.begin(share) + take - n), share};
                 }
                 p.head[static_cast<size_t>(sh.b) * U + sh.unit] = h;
                 sh.at = 0;
@@ -869,16 +879,23 @@ bool aligned(const void *p, unsigned a) { return (reinterpret_cast<uintptr_t>(p)
 
 enum class Deal { Whole, Slices, Shares };
 
-// The way with the least estimated time of its slowest CTA, in stages (a quarter of a microsecond each with two CTAs on
-// every SM): a chunk's start and end cost a CTA 18 more, unless the other CTA of its SM works on meanwhile, and
-// the merge kernel 12.
+// The way with the least estimated time, in stages of a CTA that shares its SM (0.23 us for 32 tokens of d = 128; one that
+// has it to itself takes 0.56 of that). A launch is 27, the partials and their merge 26 more, and a
+// share that ends inside a chunk pays 20 to begin the next one. Measured, in us, whole / slices / shares:
+//   sequences x KV heads x tokens x d    1 x 40 x 8192 x 128    37.2 / 19.1 / 21.7
+//                                        8 x 8 x 32768 x 128     115 / 71.9 / 67.5
+//                                        1 x 4 x 131071 x 128    362 / 21.5 / 25.1
+//                                        16 x 8 x 4097 x 128    24.1 / 24.9 / 27.0
+//                                        8 x 16 x 2048 x 64     12.6 / 17.5 / 20.9
+//                                        16 x 40 x 4096 x 128   71.6 /    - / 74.3
+//                                        64 x 40 x 8192 x 128    427 /    - /  494
 Deal deal_of(long long units, int stages, int ctas)
 {
     if (stages <= kWarps) return Deal::Whole;
-    const double rounds = static_cast<double>(units) / ctas;
-    const double whole = rounds > 1 ? std::ceil(rounds) * (stages + 4) : stages + 18;
-    const double slices = units <= ctas ? (stages + ctas / units - 1) / (ctas / units) + 18 + 12 : DBL_MAX;
-    const double shares = rounds * stages + 18 * (1 + rounds) + 18 + 12;
+    const double rounds = static_cast<double>(units) / ctas, rest = rounds - std::floor(rounds);
+    const double whole = 27 + stages * (std::floor(rounds) + (rest == 0 ? 0 : rest <= 0.5 ? 0.56 : 1));
+    const double slices = 2 * units <= ctas ? 53 + std::ceil(stages / std::floor(ctas / static_cast<double>(units))) : DBL_MAX;
+    const double shares = 53 + stages * rounds + 20 * std::max(1.0, rounds);
     return whole <= slices && whole <= shares ? Deal::Whole : slices <= shares ? Deal::Slices : Deal::Shares;
 }
 

@@ -74,7 +74,9 @@ def check_read(ab, dev, k, v, pos, count):
 @pytest.mark.parametrize("B,H,T,C,pos,count", [
     (1, 1, 1, 32, None, None), (1, 2, 1, 64, [31], None), (1, 2, 1, 64, [32], None), (2, 3, 1, 96, [95, 0], [1, 0]),
     (1, 1, 32, 32, None, None), (2, 2, 33, 96, [31, 1], [33, 2]), (3, 2, 70, 160, [90, 0, 17], [70, 69, 0]),
-    (1, 3, 128, 128, None, None), (2, 1, 15, 32, [17, 16], [15, 15]), (1, 2, 200, 256, [56], [200])])
+    (1, 3, 128, 128, None, None), (2, 1, 15, 32, [17, 16], [15, 15]), (1, 2, 200, 256, [56], [200]),
+    (2, 3, 3, 64, [30, 61], None), (3, 1, 2, 64, [64, 62, 31], [0, 2, 1]), (4, 2, 4, 64, [0, 30, 60, 64], [4, 4, 4, 0]),
+    (3, 2, 40, 96, [96, 57, 8], [0, 39, 40])])
 def test_write_and_read(ab, d, B, H, T, C, pos, count):
     rng = np.random.default_rng(B + 10 * T + d)
     k, v = rng.standard_normal((B, H, T, d)) * 3, rng.standard_normal((B, H, T, d))
