@@ -41,10 +41,20 @@ __device__ __forceinline__ int2 span_of(const Kv4Params &p, int b, bool report)
     return make_int2(first, n);
 }
 
-// Two bf16 numbers in order of magnitude, each in 16 bits, a positive one before the negative one of its magnitude.
-__device__ __forceinline__ uint32_t order_keys(uint32_t w) { return ((w << 1) & 0xfffefffeu) | (~(w >> 15) & 0x00010001u); }
+// Two bf16 numbers in order of magnitude, each in 16 bits, a positive one before the negative one of its magnitude: the
+// sign, inverted, goes below the magnitude.
+__device__ __forceinline__ uint32_t order_keys(uint32_t w)
+{
+    uint32_t d;  // bits of 2 w where the mask has ones, of ~(w >> 15) elsewhere
+    asm("lop3.b32 %0, %1, %2, %3, 0xB1;" : "=r"(d) : "r"(w * 2u), "r"(w >> 15), "r"(0xfffefffeu));
+    return d;
+}
 
-// From the largest order key of a group: bf16 bits of the scale s, and 1 / s (0 where all codes are 8).
+// The larger of the two halves.
+__device__ __forceinline__ uint32_t fold(uint32_t keys) { return max(keys & 0xffffu, keys >> 16); }
+
+// From the largest order key of a group: bf16 bits of the scale s, and 1 / s (0 where nothing is to be scaled). The
+// reciprocal is the approximate one, good to 2^-23, as code_of allows for.
 struct Scale {
     uint32_t bits;
     float inverse;
@@ -53,27 +63,30 @@ struct Scale {
 __device__ __forceinline__ Scale scale_of(uint32_t key)
 {
     const uint32_t mag = key >> 1;
-    if (mag < 0x0d80u) return {0u, 0.0f};            // below 2^-100: zeros
-    if (mag >= 0x7f80u) return {0x7fc0u, 0.0f};      // an infinity or a NaN: the group is NaN
     const uint32_t bits = (mag - (3u << 7)) | ((key & 1u) << 15);  // -x_m / 8
-    return {bits, __frcp_rn(__uint_as_float(bits << 16))};
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__uint_as_float(bits << 16)));
+    const bool plain = mag - 0x0d80u < 0x7f80u - 0x0d80u;  // 2^-100 and above, and finite
+    return {plain ? bits : mag >= 0x7f80u ? 0x7fc0u : 0u, plain ? r : 0.0f};
 }
 
-// Code of x in the low four bits (and more above them).
+// floor(x / s + 8.5) in the low bits, up to 16: 2^-12 stands against the error of the product (at most 2^-19), and the sum
+// with 2^23, rounded down, leaves the floor in the low bits. A NaN leaves ones.
 __device__ __forceinline__ uint32_t code_of(float x, float inverse)
 {
-    // 8.5 + x / s, and 2^-12 against the error of the product; the sum with 2^23 leaves its floor in the low bits
-    return __float_as_uint(__fadd_rd(fminf(fmaf(x, inverse, 8.5f + 0x1p-12f), 15.5f), 8388608.0f));
+    return __float_as_uint(__fadd_rd(fmaf(x, inverse, 8.5f + 0x1p-12f), 8388608.0f));
 }
 
-// Codes of four bf16 numbers, 16 bits.
-__device__ __forceinline__ uint32_t codes4(uint2 w, float inverse)
+// A word of the cache: codes of four bf16 numbers in its low half, of four others in its high half.
+__device__ __forceinline__ uint32_t code_word(uint2 lo, uint2 hi, float inverse_lo, float inverse_hi)
 {
-    uint32_t c = code_of(__uint_as_float(w.y & 0xffff0000u), inverse);
-    c = c * 16 + code_of(__uint_as_float(w.y << 16), inverse);
-    c = c * 16 + code_of(__uint_as_float(w.x & 0xffff0000u), inverse);
-    c = c * 16 + code_of(__uint_as_float(w.x << 16), inverse);
-    return c - 0x4b000000u * (1u + 16u + 256u + 4096u);  // the exponents of the four sums
+    const auto pair = [&](uint32_t a, uint32_t b) {  // at most 15 each
+        const uint32_t x = code_of(__uint_as_float(a), inverse_lo), y = code_of(__uint_as_float(b), inverse_hi);
+        return __vminu2(__byte_perm(x, y, 0x5410), 0x000f000fu);
+    };
+    const uint32_t p0 = pair(lo.x << 16, hi.x << 16), p1 = pair(lo.x & 0xffff0000u, hi.x & 0xffff0000u);
+    const uint32_t p2 = pair(lo.y << 16, hi.y << 16), p3 = pair(lo.y & 0xffff0000u, hi.y & 0xffff0000u);
+    return ((p3 * 16u + p2) * 16u + p1) * 16u + p0;
 }
 
 // Values of four codes (the low 16 bits of w) times s.
@@ -136,15 +149,15 @@ __global__ void __launch_bounds__(256) kv4_write_rows_kernel(const __grid_consta
     top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
     if (!live) return;
-    const Scale s = scale_of(max(top & 0xffffu, top >> 16));
-    const uint32_t lo = codes4(make_uint2(w.x, w.y), s.inverse), hi = codes4(make_uint2(w.z, w.w), s.inverse);
+    const Scale s = scale_of(fold(top));
+    const uint32_t code = code_word(make_uint2(w.x, w.y), make_uint2(w.z, w.w), s.inverse, s.inverse);
     const int tok = sp.x + r.t, row = tok % kv4::kBlock;
     uint8_t *blk = p.cache + (static_cast<size_t>(r.bh) * p.blocks + tok / kv4::kBlock) * kv4::block_bytes(D);
     if (r.side == 0) {
-        *reinterpret_cast<uint32_t *>(blk + kv4::key_byte(D, row, e)) = lo | hi << 16;
+        *reinterpret_cast<uint32_t *>(blk + kv4::key_byte(D, row, e)) = code;
     } else {
-        *reinterpret_cast<uint16_t *>(blk + kv4::value_byte(D, row, e)) = static_cast<uint16_t>(lo);
-        *reinterpret_cast<uint16_t *>(blk + kv4::value_byte(D, row, e + 4)) = static_cast<uint16_t>(hi);
+        *reinterpret_cast<uint16_t *>(blk + kv4::value_byte(D, row, e)) = static_cast<uint16_t>(code);
+        *reinterpret_cast<uint16_t *>(blk + kv4::value_byte(D, row, e + 4)) = static_cast<uint16_t>(code >> 16);
     }
     if (r.l % 4 == 0)
         *reinterpret_cast<uint16_t *>(blk + kv4::scale_byte(D, row, r.side, r.l / 4)) = static_cast<uint16_t>(s.bits);
@@ -177,137 +190,171 @@ __global__ void __launch_bounds__(256) kv4_read_rows_kernel(const __grid_constan
 // together in the cache, 4 D / 32 bytes of a key row (8 elements of every group) or one lane's 16 bytes of a value tile
 // (4 elements of up to two groups, of 4 tokens), so that the cache is read and written in whole 16-byte
 // words without shared memory, and the rows in whole 64-byte segments.
+constexpr int kHalf = 128;  // threads for the keys, and for the values
+constexpr int kWriteCtas = 6, kReadCtas = 8;
+
 struct BlockItem {
-    int bh, first, n;  // head; token of the call in the block's row 0 (may be negative), tokens of the call
+    int first, n;       // token of the call in the block's row 0 (may be negative), tokens of the call
+    size_t row0;        // row of the call's tensors that is the block's row 0 (may wrap below the first one)
     uint8_t *blk;
 };
 
 template <int D>
 __device__ __forceinline__ bool block_item(const Kv4Params &p, BlockItem &it)
 {
-    it.bh = blockIdx.x / p.span;
-    const int i = blockIdx.x - it.bh * p.span, b = it.bh / p.H;
-    const int2 sp = span_of(p, b, threadIdx.x == 0 && i == 0 && it.bh == b * p.H);
+    const int bh = blockIdx.x / p.span, i = blockIdx.x - bh * p.span, b = bh / p.H;
+    const int2 sp = span_of(p, b, threadIdx.x == 0 && i == 0 && bh == b * p.H);
     const int block = sp.x / kv4::kBlock + i;
     it.first = block * kv4::kBlock - sp.x;
     it.n = sp.y;
-    it.blk = p.cache + (static_cast<size_t>(it.bh) * p.blocks + block) * kv4::block_bytes(D);
+    it.row0 = static_cast<size_t>(bh) * p.T + it.first;
+    it.blk = p.cache + (static_cast<size_t>(bh) * p.blocks + block) * kv4::block_bytes(D);
     return it.first < it.n;  // the block has tokens of the call (it is inside the cache then)
 }
 
-constexpr int kHalf = 128;  // threads for the keys, and for the values
-constexpr int kWriteCtas = 5, kReadCtas = 6;
-
-template <int D>
-__global__ void __launch_bounds__(2 * kHalf, kWriteCtas) kv4_write_block_kernel(const __grid_constant__ Kv4Params p)
+// ALL: every row of the block is a token of the call.
+template <bool ALL>
+__device__ __forceinline__ bool live(const BlockItem &it, int row)
 {
-    constexpr int NG = D / 32;
-    griddep_launch_dependents();
-    griddep_wait();
-    BlockItem it;
-    if (!block_item<D>(p, it)) return;
-    const auto live = [&](int row) { return static_cast<unsigned>(it.first + row) < static_cast<unsigned>(it.n); };
-    const auto at = [&](const char *x, int row) { return x + (static_cast<size_t>(it.bh) * p.T + it.first + row) * p.d * 2; };
-    if (threadIdx.x < kHalf) {
-        const int row = threadIdx.x / 4, c = threadIdx.x % 4;
-        uint4 w[NG];
+    return ALL || static_cast<unsigned>(it.first + row) < static_cast<unsigned>(it.n);
+}
+
+// Pieces of a value tile: groups per lane, and 512-byte runs of lanes.
+template <int D>
+struct ValuePiece {
+    static constexpr int kGroups = D < 64 ? 1 : 2, kRuns = D < 64 ? 1 : D / 64;
+    int g, c, tile, run;
+
+    __device__ __forceinline__ explicit ValuePiece(int i) : g(i % 32 / 4), c(i % 4), tile(i / 32 % 2), run(i / 64) {}
+    __device__ __forceinline__ int row() const { return 16 * tile + 2 * c; }  // and row + 1, + 8, + 9
+    static __device__ __forceinline__ constexpr int step(int z) { return 8 * (z / 2) + z % 2; }
+    __device__ __forceinline__ int element() const { return 64 * run + 4 * g; }
+    __device__ __forceinline__ uint8_t *in(uint8_t *blk) const { return blk + kv4::value_byte(D, row(), element()); }
+};
+
+template <int d, bool ALL>
+__device__ __forceinline__ void write_keys(const Kv4Params &p, const BlockItem &it, int i)
+{
+    constexpr int D = kv4::padded(d), NG = D / 32;
+    const int row = i / 4, c = i % 4;
+    const char *src = p.k + (it.row0 + row) * (2 * d) + 16 * c;
+    uint4 w[NG];
 #pragma unroll
-        for (int n = 0; n < NG; ++n) {
-            w[n] = make_uint4(0, 0, 0, 0);
-            if (live(row) && 32 * n + 8 * c < p.d) w[n] = *reinterpret_cast<const uint4 *>(at(p.k, row) + (32 * n + 8 * c) * 2);
-        }
-        uint32_t code[NG], bits[NG];
+    for (int n = 0; n < NG; ++n) {
+        w[n] = make_uint4(0, 0, 0, 0);
+        if (live<ALL>(it, row) && (d >= 32 || 8 * c < d)) w[n] = *reinterpret_cast<const uint4 *>(src + 64 * n);
+    }
+    // lane c makes the scale of group c
+    uint32_t code[NG], mine = 0;
 #pragma unroll
-        for (int n = 0; n < NG; ++n) {
-            uint32_t top = __vmaxu2(__vmaxu2(order_keys(w[n].x), order_keys(w[n].y)),
-                                    __vmaxu2(order_keys(w[n].z), order_keys(w[n].w)));
-            top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const Scale s = scale_of(max(top & 0xffffu, top >> 16));
-            code[n] = codes4(make_uint2(w[n].x, w[n].y), s.inverse) | codes4(make_uint2(w[n].z, w[n].w), s.inverse) << 16;
-            bits[n] = s.bits;
+    for (int n = 0; n < NG; ++n) {
+        uint32_t top = __vmaxu2(__vmaxu2(order_keys(w[n].x), order_keys(w[n].y)),
+                                __vmaxu2(order_keys(w[n].z), order_keys(w[n].w)));
+        top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        if (c == n) mine = top;
+    }
+    const Scale s = scale_of(fold(mine));
+#pragma unroll
+    for (int n = 0; n < NG; ++n) {
+        const float inverse = __shfl_sync(0xffffffffu, s.inverse, n, 4);
+        code[n] = code_word(make_uint2(w[n].x, w[n].y), make_uint2(w[n].z, w[n].w), inverse, inverse);
+    }
+    if (!live<ALL>(it, row)) return;
+    uint8_t *dst = it.blk + kv4::key_byte(D, row, 8 * c);
+    if constexpr (NG == 4)
+        *reinterpret_cast<uint4 *>(dst) = make_uint4(code[0], code[1], code[2], code[3]);
+    else if constexpr (NG == 2)
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(code[0], code[1]);
+    else
+        *reinterpret_cast<uint32_t *>(dst) = code[0];
+    if (c < NG) *reinterpret_cast<uint16_t *>(it.blk + kv4::scale_byte(D, row, 0, c)) = static_cast<uint16_t>(s.bits);
+}
+
+template <int d, bool ALL>
+__device__ __forceinline__ void write_values(const Kv4Params &p, const BlockItem &it, int i)
+{
+    constexpr int D = kv4::padded(d), NL = ValuePiece<D>::kGroups;
+    const ValuePiece<D> v(i);
+    if (v.run >= ValuePiece<D>::kRuns) return;  // whole warps
+    const char *src = p.v + (it.row0 + v.row()) * (2 * d) + 2 * v.element();
+    uint32_t code[NL][2], mine = 0;
+    uint2 w[NL][4];  // of the piece's four tokens
+#pragma unroll
+    for (int m = 0; m < NL; ++m)
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+            w[m][z] = make_uint2(0, 0);
+            if (live<ALL>(it, v.row() + v.step(z)) && (d >= 32 || v.element() < d))
+                w[m][z] = *reinterpret_cast<const uint2 *>(src + v.step(z) * (2 * d) + 64 * m);
         }
-        if (!live(row)) return;
-        uint8_t *dst = it.blk + kv4::key_byte(D, row, 8 * c);
-        if constexpr (NG == 4)
-            *reinterpret_cast<uint4 *>(dst) = make_uint4(code[0], code[1], code[2], code[3]);
-        else if constexpr (NG == 2)
-            *reinterpret_cast<uint2 *>(dst) = make_uint2(code[0], code[1]);
+    // largest keys of the tokens of a word; lane g makes the scale of group g / 4 and token g % 4
+#pragma unroll
+    for (int m = 0; m < NL; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint2 *x = w[m] + 2 * h;
+            uint32_t pair = fold(__vmaxu2(order_keys(x[0].x), order_keys(x[0].y))) |
+                            fold(__vmaxu2(order_keys(x[1].x), order_keys(x[1].y))) << 16;
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) pair = __vmaxu2(pair, __shfl_xor_sync(0xffffffffu, pair, off));
+            if (v.g / 2 == 2 * m + h) mine = pair;
+        }
+    const Scale s = scale_of(v.g % 2 ? mine >> 16 : mine & 0xffffu);
+    const int own = v.row() + v.step(v.g % 4);
+    if (v.g < 4 * NL && live<ALL>(it, own))
+        *reinterpret_cast<uint16_t *>(it.blk + kv4::scale_byte(D, own, 1, 2 * v.run + v.g / 4)) = static_cast<uint16_t>(s.bits);
+#pragma unroll
+    for (int m = 0; m < NL; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int from = (4 * m + 2 * h) * 4 + v.c;
+            code[m][h] = code_word(w[m][2 * h], w[m][2 * h + 1], __shfl_sync(0xffffffffu, s.inverse, from),
+                                   __shfl_sync(0xffffffffu, s.inverse, from + 4));
+        }
+    uint8_t *dst = v.in(it.blk);
+    if (live<ALL>(it, v.row()) && live<ALL>(it, v.row() + 9)) {  // and the tokens between
+        if constexpr (NL == 2)
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(code[0][0], code[0][1], code[1][0], code[1][1]);
         else
-            *reinterpret_cast<uint32_t *>(dst) = code[0];
-#pragma unroll
-        for (int n = 0; n < NG; ++n)
-            if (c == n) *reinterpret_cast<uint16_t *>(it.blk + kv4::scale_byte(D, row, 0, n)) = static_cast<uint16_t>(bits[n]);
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(code[0][0], code[0][1]);
     } else {
-        constexpr int kChunks = NG > 2 ? NG / 2 : 1, NL = NG < 2 ? NG : 2;  // groups of a lane's piece
-        const int i = threadIdx.x - kHalf, lane = i % 32, g = lane / 4, c = lane % 4;
-        const int tile = i / 32 % 2, chunk = i / 64;
-        if (chunk >= kChunks) return;  // whole warps
-        uint32_t code[NL][2];
-        uint2 w[NL][4];  // of the tokens 2c, 2c + 1, 2c + 8, 2c + 9 of the tile
 #pragma unroll
         for (int m = 0; m < NL; ++m)
 #pragma unroll
-            for (int z = 0; z < 4; ++z) {
-                const int row = 16 * tile + 8 * (z / 2) + 2 * c + z % 2, e = 64 * chunk + 32 * m + 4 * g;
-                w[m][z] = make_uint2(0, 0);
-                if (live(row) && e < p.d) w[m][z] = *reinterpret_cast<const uint2 *>(at(p.v, row) + e * 2);
-            }
-#pragma unroll
-        for (int m = 0; m < NL; ++m) {
-            uint32_t top[4];
-#pragma unroll
-            for (int z = 0; z < 4; ++z) {
-                const uint32_t t = __vmaxu2(order_keys(w[m][z].x), order_keys(w[m][z].y));
-                top[z] = max(t & 0xffffu, t >> 16);
-            }
-            uint32_t pair[2] = {top[0] | top[1] << 16, top[2] | top[3] << 16};
-#pragma unroll
-            for (int off = 4; off < 32; off <<= 1) {
-                pair[0] = __vmaxu2(pair[0], __shfl_xor_sync(0xffffffffu, pair[0], off));
-                pair[1] = __vmaxu2(pair[1], __shfl_xor_sync(0xffffffffu, pair[1], off));
-            }
-#pragma unroll
-            for (int z = 0; z < 4; ++z) {
-                const int row = 16 * tile + 8 * (z / 2) + 2 * c + z % 2;
-                const Scale s = scale_of(z % 2 ? pair[z / 2] >> 16 : pair[z / 2] & 0xffffu);
-                const uint32_t u = codes4(w[m][z], s.inverse);
-                code[m][z / 2] = z % 2 ? code[m][z / 2] | u << 16 : u;
-                if (g == z && live(row))
-                    *reinterpret_cast<uint16_t *>(it.blk + kv4::scale_byte(D, row, 1, 2 * chunk + m)) = static_cast<uint16_t>(s.bits);
-            }
-        }
-        uint8_t *dst = it.blk + kv4::value_byte(D, 16 * tile + 2 * c, 64 * chunk + 4 * g);
-        const int row = 16 * tile + 2 * c;
-        if (live(row) && live(row + 9)) {  // and the tokens between
-            if constexpr (NL == 2)
-                *reinterpret_cast<uint4 *>(dst) = make_uint4(code[0][0], code[0][1], code[1][0], code[1][1]);
-            else
-                *reinterpret_cast<uint2 *>(dst) = make_uint2(code[0][0], code[0][1]);
-        } else {
-#pragma unroll
-            for (int m = 0; m < NL; ++m)
-#pragma unroll
-                for (int z = 0; z < 4; ++z)
-                    if (live(row + 8 * (z / 2) + z % 2))
-                        *reinterpret_cast<uint16_t *>(dst + 8 * m + 2 * z) = static_cast<uint16_t>(code[m][z / 2] >> (16 * (z % 2)));
-        }
+            for (int z = 0; z < 4; ++z)
+                if (live<ALL>(it, v.row() + v.step(z)))
+                    *reinterpret_cast<uint16_t *>(dst + 8 * m + 2 * z) = static_cast<uint16_t>(code[m][z / 2] >> (16 * (z % 2)));
     }
 }
 
-template <int D, bool F32>
+template <int d>
+__global__ void __launch_bounds__(2 * kHalf, kWriteCtas) kv4_write_block_kernel(const __grid_constant__ Kv4Params p)
+{
+    griddep_launch_dependents();
+    griddep_wait();
+    BlockItem it;
+    if (!block_item<kv4::padded(d)>(p, it)) return;
+    const bool all = it.first >= 0 && it.first + kv4::kBlock <= it.n;
+    const int i = threadIdx.x % kHalf;
+    if (threadIdx.x < kHalf)
+        all ? write_keys<d, true>(p, it, i) : write_keys<d, false>(p, it, i);
+    else
+        all ? write_values<d, true>(p, it, i) : write_values<d, false>(p, it, i);
+}
+
+template <int d, bool F32>
 __global__ void __launch_bounds__(2 * kHalf, kReadCtas) kv4_read_block_kernel(const __grid_constant__ Kv4Params p)
 {
-    constexpr int NG = D / 32;
+    constexpr int D = kv4::padded(d), NG = D / 32, kSize = F32 ? 4 : 2;
     griddep_launch_dependents();
     griddep_wait();
     BlockItem it;
     if (!block_item<D>(p, it)) return;
-    const auto live = [&](int row) { return static_cast<unsigned>(it.first + row) < static_cast<unsigned>(it.n); };
-    const auto at = [&](char *x, int row) { return x + (static_cast<size_t>(it.bh) * p.T + it.first + row) * p.d * (F32 ? 4 : 2); };
+    const int i = threadIdx.x % kHalf;
     if (threadIdx.x < kHalf) {
-        const int row = threadIdx.x / 4, c = threadIdx.x % 4;
-        if (!live(row)) return;
+        const int row = i / 4, c = i % 4;
+        if (!live<false>(it, row) || (d < 32 && 8 * c >= d)) return;
         uint32_t code[NG];
         const uint8_t *src = it.blk + kv4::key_byte(D, row, 8 * c);
         if constexpr (NG == 4) {
@@ -319,11 +366,10 @@ __global__ void __launch_bounds__(2 * kHalf, kReadCtas) kv4_read_block_kernel(co
         } else {
             code[0] = *reinterpret_cast<const uint32_t *>(src);
         }
-        char *out = at(p.ko, row);
+        char *out = p.ko + (it.row0 + row) * (kSize * d);
 #pragma unroll
         for (int n = 0; n < NG; ++n) {
             const int e = 32 * n + 8 * c;
-            if (e >= p.d) continue;
             const float s = bf16_at(it.blk + kv4::scale_byte(D, row, 0, n));
             const float4 x = values4(code[n], s), y = values4(code[n] >> 16, s);
             if (F32) {
@@ -336,30 +382,27 @@ __global__ void __launch_bounds__(2 * kHalf, kReadCtas) kv4_read_block_kernel(co
             }
         }
     } else {
-        constexpr int kChunks = NG > 2 ? NG / 2 : 1, NL = NG < 2 ? NG : 2;
-        const int i = threadIdx.x - kHalf, lane = i % 32, g = lane / 4, c = lane % 4;
-        const int tile = i / 32 % 2, chunk = i / 64, row0 = 16 * tile + 2 * c;
-        if (chunk >= kChunks) return;
+        constexpr int NL = ValuePiece<D>::kGroups;
+        const ValuePiece<D> v(i);
+        if (v.run >= ValuePiece<D>::kRuns || (d < 32 && v.element() >= d)) return;
         uint32_t code[NL][2];
-        const uint8_t *src = it.blk + kv4::value_byte(D, row0, 64 * chunk + 4 * g);
         if constexpr (NL == 2) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(src);
+            const uint4 x = *reinterpret_cast<const uint4 *>(v.in(it.blk));
             code[0][0] = x.x, code[0][1] = x.y, code[1][0] = x.z, code[1][1] = x.w;
         } else {
-            const uint2 x = *reinterpret_cast<const uint2 *>(src);
+            const uint2 x = *reinterpret_cast<const uint2 *>(v.in(it.blk));
             code[0][0] = x.x, code[0][1] = x.y;
         }
+        char *out = p.vo + (it.row0 + v.row()) * (kSize * d);
 #pragma unroll
         for (int z = 0; z < 4; ++z) {
-            const int row = row0 + 8 * (z / 2) + z % 2;
-            if (live(row)) {
-                char *out = at(p.vo, row);
+            const int row = v.row() + v.step(z);
+            if (live<false>(it, row)) {
 #pragma unroll
-                for (int m = 0; m < NL; ++m) {
-                    const int n = 2 * chunk + m, e = 32 * n + 4 * g;
-                    if (e < p.d)
-                        put4<F32>(out, e, values4(code[m][z / 2] >> (16 * (z % 2)), bf16_at(it.blk + kv4::scale_byte(D, row, 1, n))));
-                }
+                for (int m = 0; m < NL; ++m)
+                    put4<F32>(out + v.step(z) * (kSize * d), v.element() + 32 * m,
+                              values4(code[m][z / 2] >> (16 * (z % 2)),
+                                      bf16_at(it.blk + kv4::scale_byte(D, row, 1, 2 * v.run + m))));
             }
         }
     }
@@ -380,9 +423,10 @@ int check_sizes(int B, int H, int T, int C, int d)
 // Tokens per sequence from which a CTA takes a block and not single rows.
 constexpr int kBlockTokens = 16;
 
-template <int D>
+template <int d>
 cudaError_t launch(Kv4Params &p, int op, cudaStream_t stream)
 {
+    constexpr int D = kv4::padded(d);
     const long long rows = static_cast<long long>(p.BH) * p.T;
     if (p.T < kBlockTokens && rows < (1LL << 31)) {
         constexpr int kRowsPerCta = 256 / (D / 8) / 2;
@@ -394,9 +438,9 @@ cudaError_t launch(Kv4Params &p, int op, cudaStream_t stream)
     p.span = std::min(p.blocks, (p.T + 2 * kv4::kBlock - 2) / kv4::kBlock);
     const long long ctas = static_cast<long long>(p.BH) * p.span;
     if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
-    return launch_overlapped(op == 0   ? kv4_write_block_kernel<D>
-                             : op == 1 ? kv4_read_block_kernel<D, false>
-                                       : kv4_read_block_kernel<D, true>,
+    return launch_overlapped(op == 0   ? kv4_write_block_kernel<d>
+                             : op == 1 ? kv4_read_block_kernel<d, false>
+                                       : kv4_read_block_kernel<d, true>,
                              dim3(static_cast<unsigned>(ctas)), 2 * kHalf, 0, stream, p);
 }
 
@@ -407,10 +451,11 @@ int run(Kv4Params p, int op, void *stream)
     if (!p.status) return ALIBI_ERR_CUDA;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
-    switch (kv4::padded(p.d)) {
+    switch (p.d) {
         case 128: e = launch<128>(p, op, s); break;
         case 64: e = launch<64>(p, op, s); break;
-        default: e = launch<32>(p, op, s); break;
+        case 32: e = launch<32>(p, op, s); break;
+        default: e = launch<16>(p, op, s); break;
     }
     return e == cudaSuccess ? ALIBI_OK : ALIBI_ERR_CUDA;
 }
