@@ -365,6 +365,82 @@ def test_offsets_beyond_32_bits(ab):
     torch.cuda.empty_cache()
 
 
+def run_picked(ab, seed, B, Hkv, G, T, N, d, lens, L, picks, steep=None):
+    """A case too large for a whole reference: keys and values are made and written on the GPU, and the rows of some
+    (sequence, KV head) pairs are compared; all outputs have to be finite, and empty where no token is."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    C = -(-N // 32) * 32
+    k, v, q = rand(B, Hkv, N, d), rand(B, Hkv, N, d), rand(B, Hkv * G, T, d)
+    cache = ab.alibi_kv4_cache(B, Hkv, C, d)
+    cache.fill_(0xFF)
+    true = [N] * B if lens is None else lens
+    ab.alibi_kv4_write(k, v, cache, count=ints(true))
+    m = None if steep is None else np.full(Hkv * G, steep, dtype=np.float32)
+    out, lse = ab.alibi_attn_decode_kv4(q, cache, lens=None if lens is None else ints(lens), L=L, slopes=m)
+    ab.alibi_check_error()
+    assert bool(torch.isfinite(out).all())
+    empty = torch.tensor([[n - T + t < 0 for t in range(T)] for n in true], device="cuda")[:, None]
+    assert torch.equal(torch.isinf(lse), empty.expand_as(lse)) and bool((out.transpose(2, 3)[empty[:, :, None].expand(
+        B, Hkv * G, d, T)] == 0).all())
+    slopes = oracle.slopes(Hkv * G) if m is None else m.astype(np.float64)
+    for b, h in picks:
+        n, rows = true[b], slice(h * G, (h + 1) * G)
+        x = [host64(t) for t in (q[b:b + 1, rows], k[b:b + 1, h:h + 1, :max(n, 1)], v[b:b + 1, h:h + 1, :max(n, 1)])]
+        ro, rl, eo, el = ref.decode(x[0], ref.held(x[1]), ref.held(x[2]), [n], slopes[rows])
+        go, gl = host64(out[b:b + 1, rows]), host64(lse[b:b + 1, rows])
+        assert (np.abs(go - ro) <= eo + half_ulp_bf16(ro) * (1 + 2.0 ** -6)).all(), (b, h)
+        seen = ~np.isinf(rl)
+        assert (np.abs(gl - rl)[seen] <= el[seen]).all(), (b, h)
+
+
+# (on 152 SMs) whole chunks, slices and equal shares; more and fewer than 32 sequences; very unequal lengths; lengths far
+# below the bound that the work was planned for
+@pytest.mark.parametrize("B,Hkv,G,T,N,d,kind,L", [
+    (24, 7, 1, 1, 14336, 32, "ragged", None),      # shares
+    (40, 5, 8, 1, 16384, 64, "ragged", None),      # shares, two columns per lane
+    (40, 5, 8, 1, 16384, 64, None, 16384),         # shares, one length for all
+    (8, 38, 1, 1, 4096, 128, "ragged", None),      # whole, one round
+    (40, 2, 1, 1, 8192, 128, "ragged", None),      # slices, more than 32 sequences
+    (40, 2, 2, 3, 8192, 64, "one long", 8192),     # one sequence of 8192 among sequences of one token
+    (3, 2, 1, 1, 16384, 128, "one long", 16384),
+    (24, 7, 1, 1, 14336, 32, "one long", 14336),
+    (6, 4, 2, 2, 16384, 64, "short", 16384),       # planned for 16384, a few tokens each
+    (40, 4, 1, 1, 20000, 32, "short", 20000),
+    (24, 9, 1, 1, 14000, 32, "short", 14000),
+    (1, 2, 64, 2, 4096, 64, None, 4096),           # 16 chunks of a head
+    (1, 1, 1, 1, 300000, 32, None, 300000),
+])
+def test_ways_of_dealing(ab, B, Hkv, G, T, N, d, kind, L):
+    lens = {None: None, "ragged": [max(0, N - 1 - (N * 7 * b // 11) % N) if b % 5 else b % 3 for b in range(B)],
+            "one long": [N if b == B // 2 else 1 for b in range(B)], "short": [(7 * b) % 40 for b in range(B)]}[kind]
+    picks = sorted({(0, 0), (B - 1, Hkv - 1), (B // 2, 0), (B // 3, Hkv // 2), (B // 2, Hkv - 1)})
+    run_picked(ab, 1000 + B + N, B, Hkv, G, T, N, d, lens, L, picks)
+
+
+@pytest.mark.parametrize("B,Hkv,G,T,N,d", [(24, 7, 1, 1, 14336, 32), (3, 4, 8, 1, 8192, 128), (40, 5, 2, 4, 1000, 64)])
+def test_ways_of_dealing_without_bias(ab, B, Hkv, G, T, N, d):
+    # no bias: no block's weights vanish, long sums of small weights
+    lens = [N - 17 * b for b in range(B)]
+    run_picked(ab, 77, B, Hkv, G, T, N, d, lens, None, [(0, 0), (B - 1, Hkv - 1)], steep=0.0)
+
+
+def test_repeated_calls_of_every_way_give_the_same_bits(ab):
+    import torch
+    for B, Hkv, N, d in ((24, 7, 14336, 32), (4, 2, 8192, 128), (8, 38, 600, 64)):
+        k = torch.randn(B, Hkv, N, d, device="cuda", dtype=torch.bfloat16)
+        cache = ab.alibi_kv4_cache(B, Hkv, -(-N // 32) * 32, d)
+        ab.alibi_kv4_write(k, torch.flip(k, dims=[2]).contiguous(), cache)
+        q = torch.randn(B, Hkv, 1, d, device="cuda", dtype=torch.bfloat16)
+        lens = ints([N - 31 * b for b in range(B)])
+        first = ab.alibi_attn_decode_kv4(q, cache, lens=lens)
+        for _ in range(10):
+            again = ab.alibi_attn_decode_kv4(q, cache, lens=lens)
+            assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    ab.alibi_check_error()
+
+
 def test_binding_refusals(ab):
     import torch
     q = torch.zeros(2, 4, 1, 64, dtype=torch.bfloat16, device="cuda")
