@@ -29,13 +29,14 @@
 //            rounding to 11 bits is the only one below fp32: off by at most 2^-11 of each
 //            product, a quarter of the bf16 output's own step.
 //
-// The work is dealt in one of three ways (deal_of), by lengths that only the device knows:
+// The work is dealt in one of four ways (deal_of), by lengths that only the device knows:
 //   whole    a CTA takes one chunk: short sequences, and many chunks;
+//   clusters a chunk's stages are dealt to the CTAs of a cluster, which merge through each other's shared memory;
 //   slices   each of few chunks has several of the 2 x 152 resident CTAs, in proportion to its length, which take
 //            its stages in turn;
 //   shares   the chunks of all sequences, one after another, form one row of stages, of which each resident
 //            CTA takes an equal share, whose ends may lie inside chunks.
-// A chunk that several CTAs worked on leaves a partial from each, and a second kernel, launched as a
+// A chunk that slices or shares worked on leaves a partial from each, and a second kernel, launched as a
 // programmatic dependent, merges them in fp32.
 
 #include <algorithm>
@@ -45,17 +46,17 @@
 #include <cuda_fp16.h>
 
 #include "alibi.h"
-#include "kv4.h"
+#include "kv4_deal.h"
 #include "ptx.cuh"
 
 namespace alibi {
 namespace {
 
-constexpr int kWarps = 8;
+using namespace kv4;
+
 constexpr int kStages = 3;          // ring depth of each warp
 constexpr int kStageBytes = 4608;   // 128 / D blocks of 36 D bytes
 constexpr int kRows = 8;            // query rows of a chunk, at most (the columns of an mma)
-constexpr int kMostShares = 512;   // CTAs that share the work (two per SM)
 constexpr int kMergeThreads = 256;
 constexpr int kSmem = kWarps * kStages * kStageBytes;
 
@@ -82,7 +83,8 @@ struct DecodeKv4Params {
     uint32_t *status;
     int B, Hkv, T, L, blocks, d;  // blocks: C / 32
     int rows, chunks;             // G T, ceil(G T / 8)
-    bool slices;                  // every chunk has CTAs of its own; otherwise equal shares
+    bool slices;                  // Shares: every chunk has CTAs of its own; otherwise equal shares
+    int count;                    // Cluster: CTAs of a cluster
     float c1;                     // 2^-14 log2(e) / sqrt(d)
     HeadSlopes slopes;
 };
@@ -102,6 +104,32 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// Floats at shared-memory address `a` of CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t map_cluster(uint32_t a, int rank)
+{
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float2 ld_cluster2(uint32_t a, int rank)
+{
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(map_cluster(a, rank)) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t a, int rank)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(map_cluster(a, rank))
+                 : "memory");
+    return v;
 }
 
 // Transpose of an 8 x 8 matrix of halves spread over the warp (lane 4 i + c: row i, columns 2c, 2c + 1).
@@ -419,72 +447,6 @@ __device__ __forceinline__ int stages_of(int len)  // at least one, so that ever
     return max(1, (len + SB * kv4::kBlock - 1) / (SB * kv4::kBlock));
 }
 
-// Where the work of a CTA lies.
-struct Share {
-    int left;          // stages that are left (slices: of the whole chunk)
-    int b, unit, at;   // sequence, chunk of it and stage of that chunk that comes next (slices: number of the slice)
-    int first, count;  // slices: the CTA that has the chunk's first slice, and their number
-};
-
-__device__ __forceinline__ int divide(long long a, int b)
-{
-    return a < (1LL << 32) ? static_cast<int>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : static_cast<int>(a / b);
-}
-
-// Equal shares: share `i` of `ctas` of a row of `row` stages is [i row / n, (i + 1) row / n), n = min(ctas, row).
-// Divisions in 32 bits where the row allows it (all but sequences of many millions of tokens in all).
-struct Cut {
-    long long row;
-    int n;
-
-    __device__ __forceinline__ Cut(long long row_, int ctas) : row(row_), n(static_cast<int>(min(static_cast<long long>(ctas), row_)))
-    {
-    }
-    __device__ __forceinline__ long long begin(int i) const
-    {
-        if (row < (1LL << 32) / (kMostShares + 1)) return static_cast<uint32_t>(i) * static_cast<uint32_t>(row) / static_cast<uint32_t>(n);
-        return i * row / n;
-    }
-    // the last share that begins at or before stage `at`
-    __device__ __forceinline__ int holder(long long at) const { return static_cast<int>(((at + 1) * n + row - 1) / row - 1); }
-};
-
-// Slices: every chunk has CTAs of its own, in proportion to its weight, its stages + `extra`, with `extra` just large enough
-// for the shortest chunk to have one. The chunk that begins at weight w of `all` has CTAs from floor(w ctas / all) on.
-struct Slices {
-    long long all;
-    int extra, ctas;
-
-    __device__ __forceinline__ Slices(long long row, int units, int shortest, int ctas_) : ctas(ctas_)
-    {
-        const long long lack = row - static_cast<long long>(shortest) * ctas;
-        extra = lack > 0 ? divide(lack + ctas - units - 1, ctas - units) : 0;
-        all = row + static_cast<long long>(extra) * units;
-    }
-    __device__ __forceinline__ int cta(long long w) const
-    {
-        if (all < (1LL << 32) / (kMostShares + 1)) return static_cast<uint32_t>(w) * static_cast<uint32_t>(ctas) / static_cast<uint32_t>(all);
-        return static_cast<int>(w * ctas / all);
-    }
-    // the last weight whose CTA is i or before
-    __device__ __forceinline__ long long last(int i) const
-    {
-        if (all < (1LL << 32) / (kMostShares + 1))
-            return (static_cast<uint32_t>(i + 1) * static_cast<uint32_t>(all) + ctas - 1) / static_cast<uint32_t>(ctas) - 1;
-        return ((i + 1) * all + ctas - 1) / ctas - 1;
-    }
-    // CTA i's slice of the chunk of n stages that begins at weight w: of `count` slices, slice k has the stages k, k + count,
-    // ... counted from the newest, so that each has its part of the near tokens, whose values count, and of the far
-    // ones, whose values are skipped
-    __device__ __forceinline__ void place(int i, long long w, int n, Share &sh) const
-    {
-        sh.first = cta(w);
-        sh.count = min(n, cta(w + n + extra) - sh.first);
-        sh.at = i - sh.first;
-        sh.left = sh.at < sh.count ? n : 0;
-    }
-};
-
 // Share or slice `i`, into `sh`; returns the row. All threads of the CTA.
 template <int SB>
 __device__ __forceinline__ long long share_of(const DecodeKv4Params &p, int i, Share &sh)
@@ -585,11 +547,14 @@ __device__ __forceinline__ long long share_of(const DecodeKv4Params &p, int i, S
     return all * U;
 }
 
-// SHARES: CTA i takes share or slice i; otherwise it takes chunk i.
-template <int D, int KC, bool SHARES>
+// What a CTA takes: a chunk, a slice of a cluster's chunk, or share (or slice) i of the row of all stages.
+enum class Mode { Chunk, Cluster, Shares };
+
+template <int D, int KC, Mode MODE>
 __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid_constant__ DecodeKv4Params p)
 {
     constexpr int NG = D / 32, SB = 128 / D, kBlk = 36 * D;
+    constexpr bool SHARES = MODE == Mode::Shares, CLUSTER = MODE == Mode::Cluster;
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ __align__(8) uint64_t full[kWarps][kStages];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
@@ -626,17 +591,20 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
     uint32_t phase = 0;
 
     while (true) {
-        const int b = SHARES ? sh.b : blockIdx.x / U, unit = SHARES ? sh.unit : blockIdx.x % U, at = SHARES ? sh.at : 0;
+        const int all = CLUSTER ? blockIdx.x / p.count : blockIdx.x;  // chunk of all sequences
+        const int b = SHARES ? sh.b : all / U, unit = SHARES ? sh.unit : all % U;
+        const int at = SHARES ? sh.at : CLUSTER ? blockIdx.x - all * p.count : 0;
         bool bad;
         const int len = length_of(p, b, bad), n = stages_of<SB>(len);
         const int nblk = (len + kv4::kBlock - 1) / kv4::kBlock;
-        const bool slices = SHARES && p.slices;
+        const bool slices = CLUSTER || (SHARES && p.slices);
+        const int count = CLUSTER ? p.count : slices ? sh.count : 1;  // slices of the chunk
         const int take = SHARES && !slices ? min(sh.left, n - at) : n;
-        // This CTA's stages [s0, s1) of the chunk (slices: every sh.count-th of all), dealt to its warps in turn from the
+        // This CTA's stages [s0, s1) of the chunk (slices: every count-th of all), dealt to its warps in turn from the
         // newest to the oldest: the bias falls on the way, so the references R and M settle in the first
         // tiles. (Oldest first, a steep head raises them at every tile.)
         const int s0 = slices ? 0 : at, s1 = min(s0 + take, (nblk + SB - 1) / SB);
-        const int step = slices ? kWarps * sh.count : kWarps;
+        const int step = kWarps * count;
         const int hk = unit / p.chunks, chunk = unit - hk * p.chunks;
         const size_t bk = static_cast<size_t>(b) * p.Hkv + hk;
         const int row0 = chunk * kRows, nrows = min(kRows, p.rows - row0);
@@ -648,7 +616,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
             mbar_arrive_expect_tx(&full[warp][slot_], bytes);
             bulk_load(mine + slot_ * kStageBytes, src + static_cast<size_t>(s) * kStageBytes, bytes, &full[warp][slot_]);
         };
-        int s = s1 - 1 - (slices ? at + warp * sh.count : warp);  // this warp's stages: s, s - step, ...
+        int s = s1 - 1 - (slices ? at + warp * count : warp);  // this warp's stages: s, s - step, ...
         if (lane == 0)
             for (int i = 0, k = slot; i < kStages; ++i) {
                 if (s - i * step >= s0) fetch(s - i * step, k);
@@ -742,7 +710,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
 
         bool whole = true;
         float *to = nullptr;
-        if constexpr (SHARES) {
+        if constexpr (CLUSTER) {
+            // into the second stage of the first warp's ring, which no partial lies in
+            static_assert(part_floats(D) * sizeof(float) <= kStageBytes && kRows * (kRowStride + 2) * sizeof(float) <= kStageBytes,
+                          "a warp's partial and the CTA's take a stage each");
+            whole = false;
+            to = reinterpret_cast<float *>(ring + kStageBytes);
+        } else if constexpr (SHARES) {
             whole = p.slices ? sh.count == 1 : take == n;
             to = p.part + (static_cast<size_t>(share) * 2 + (sh.at == 0)) * part_floats(D);
         }
@@ -760,6 +734,21 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
                 *reinterpret_cast<float4 *>(to + r * D + e) = m.o;
                 if (e == 0) *reinterpret_cast<float2 *>(to + kRows * D + 2 * r) = make_float2(m.R, m.l);
             }
+        }
+        if constexpr (CLUSTER) {
+            cluster_arrive();
+            cluster_wait();
+            const int items = nrows * (D / 4), per = (items + count - 1) / count;  // elements that this CTA merges
+            const uint32_t base = smem_u32(to);
+            for (int i = at * per + threadIdx.x; i < min(items, (at + 1) * per); i += kWarps * 32) {
+                const int r = i / (D / 4), e = i % (D / 4) * 4;
+                const Merged m = merge(
+                    count, [&](int k) { return ld_cluster2(base + (kRows * D + 2 * r) * 4, k); },
+                    [&](int k) { return ld_cluster4(base + (r * D + e) * 4, k); });
+                finish(p.out, p.lse, p.d, bk * p.rows + row0 + r, e, m, bad);
+            }
+            cluster_arrive();  // the other CTAs may still read this one's partial
+            cluster_wait();
         }
         if constexpr (!SHARES) return;
         if (p.slices) {
@@ -877,50 +866,32 @@ __global__ void __launch_bounds__(kMergeThreads) decode_kv4_merge_kernel(const _
 
 bool aligned(const void *p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-enum class Deal { Whole, Slices, Shares };
-
-// The way with the least estimated time, in stages of a CTA that shares its SM (0.23 us for 32 tokens of d = 128; one that
-// has it to itself takes 0.56 of that). A launch is 27, the partials and their merge 26 more, and a
-// share that ends inside a chunk pays 20 to begin the next one. Measured, in us, whole / slices / shares:
-//   sequences x KV heads x tokens x d    1 x 40 x 8192 x 128    37.2 / 19.1 / 21.7
-//                                        8 x 8 x 32768 x 128     115 / 71.9 / 67.5
-//                                        1 x 4 x 131071 x 128    362 / 21.5 / 25.1
-//                                        16 x 8 x 4097 x 128    24.1 / 24.9 / 27.0
-//                                        8 x 16 x 2048 x 64     12.6 / 17.5 / 20.9
-//                                        16 x 40 x 4096 x 128   71.6 /    - / 74.3
-//                                        64 x 40 x 8192 x 128    427 /    - /  494
-Deal deal_of(long long units, int stages, int ctas)
-{
-    if (stages <= kWarps) return Deal::Whole;
-    const double rounds = static_cast<double>(units) / ctas, rest = rounds - std::floor(rounds);
-    const double whole = 27 + stages * (std::floor(rounds) + (rest == 0 ? 0 : rest <= 0.5 ? 0.56 : 1));
-    const double slices = 2 * units <= ctas ? 53 + std::ceil(stages / std::floor(ctas / static_cast<double>(units))) : DBL_MAX;
-    const double shares = 53 + stages * rounds + 20 * std::max(1.0, rounds);
-    return whole <= slices && whole <= shares ? Deal::Whole : slices <= shares ? Deal::Slices : Deal::Shares;
-}
-
 template <int D, int KC>
 cudaError_t launch(DecodeKv4Params &p, long long units, cudaStream_t stream)
 {
-    const auto whole = &decode_kv4_kernel<D, KC, false>;
-    const auto shared = &decode_kv4_kernel<D, KC, true>;
+    const auto whole = &decode_kv4_kernel<D, KC, Mode::Chunk>;
+    const auto clusters = &decode_kv4_kernel<D, KC, Mode::Cluster>;
+    const auto shared = &decode_kv4_kernel<D, KC, Mode::Shares>;
     constexpr int kTokens = 128 / D * kv4::kBlock;  // of a stage
     const int stages = (p.L + kTokens - 1) / kTokens, ctas = std::min(2 * num_sms(), kMostShares);
-    const Deal deal = deal_of(units, stages, ctas);
+    const Plan plan = deal_of(units, stages, ctas);
     p.part = nullptr;
     p.head = nullptr;
     p.slices = false;
-    if (deal == Deal::Whole) {
-        if (units > 0x7fffffffLL) return cudaErrorInvalidValue;
-        const cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(whole), kSmem, 0);
+    p.count = plan.count;
+    if (plan.deal == Deal::Whole || plan.deal == Deal::Clusters) {
+        if (units * plan.count > 0x7fffffffLL) return cudaErrorInvalidValue;
+        const auto kernel = plan.count > 1 ? clusters : whole;
+        const cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(kernel), kSmem, 0, plan.count > 1);
         if (e != cudaSuccess) return e;
-        return launch_overlapped(whole, dim3(static_cast<unsigned>(units)), kWarps * 32, kSmem, stream, p);
+        return launch_overlapped(kernel, dim3(static_cast<unsigned>(units * plan.count)), kWarps * 32, kSmem, stream, p,
+                                 plan.count);
     }
     cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(shared), kSmem, 0);
     if (e != cudaSuccess) return e;
     const int per = (stages + kWarps - 1) / kWarps;  // CTAs that a chunk can keep busy
     const int shares = static_cast<int>(std::min<long long>(units * per, ctas));
-    p.slices = deal == Deal::Slices;
+    p.slices = plan.deal == Deal::Slices;
     const size_t bytes = static_cast<size_t>(shares) * 2 * part_floats(D) * sizeof(float);
     char *ws = nullptr;
     e = cudaMallocFromPoolAsync(reinterpret_cast<void **>(&ws), bytes + static_cast<size_t>(units) * sizeof(Header), decode_pool(), stream);

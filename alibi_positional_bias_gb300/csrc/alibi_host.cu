@@ -207,7 +207,7 @@ const int2 *work_order(OrderKind kind, int causal, int BH, int N, int dr, cudaSt
     return d;
 }
 
-cudaError_t prepare_kernel(const void *func, int smem, uint32_t regs)
+cudaError_t prepare_kernel(const void *func, int smem, uint32_t regs, bool big_clusters)
 {
     struct Prepared {
         int dev;
@@ -226,6 +226,10 @@ cudaError_t prepare_kernel(const void *func, int smem, uint32_t regs)
     if (regs != 0 && fa.numRegs != static_cast<int>(regs)) return cudaErrorInvalidConfiguration;
     e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
+    if (big_clusters) {
+        e = cudaFuncSetAttribute(func, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
     if (ndone < 256) done[ndone++] = {dev, func};  // a full table only repeats the (idempotent) set-up
     return cudaSuccess;
 }

@@ -40,9 +40,9 @@ enum class OrderKind { Prefill = 0, BwdDkDv = 1, BwdDq = 2 };
 const int2 *work_order(OrderKind kind, int causal, int BH, int N, int dr, cudaStream_t stream);
 // Once per (current device, kernel): check that `func` compiled to `regs` registers
 // per thread (0: any count) and raise its dynamic shared-memory limit to `smem`
-// bytes. Function attributes belong to each device's context, so a process that
+// bytes; `big_clusters` allows more than 8 CTAs in a cluster. Function attributes belong to each device's context, so a process that
 // runs on several devices prepares each one.
-cudaError_t prepare_kernel(const void *func, int smem, uint32_t regs);
+cudaError_t prepare_kernel(const void *func, int smem, uint32_t regs, bool big_clusters = false);
 cudaMemPool_t decode_pool();     // library-owned stream-ordered pool of the current device
 // 3-D TMA map over a [dim2, dim1, dim0] bf16 tensor (dim0 fastest), box {box0, box1, 1},
 // zero fill out of bounds; 128-byte swizzle, or none (plain row-major boxes, as the
@@ -50,22 +50,26 @@ cudaMemPool_t decode_pool();     // library-owned stream-ordered pool of the cur
 bool encode_tmap_bf16_3d(CUtensorMap *map, const void *base, uint64_t dim0, uint64_t dim1, uint64_t dim2,
                          uint32_t box0, uint32_t box1, bool swizzle128 = true);
 
-// Launch with programmatic stream serialization: the grid may be scheduled while the previous kernel in the stream
+// Launch with programmatic stream serialization, in clusters of `cluster` CTAs: the grid may be scheduled while the previous kernel in the stream
 // drains. A kernel launched so executes griddepcontrol.wait in every thread that reads or writes memory, before it does.
 template <class Params>
 cudaError_t launch_overlapped(void (*kernel)(Params), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
-                              const Params &p)
+                              const Params &p, int cluster = 1)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
