@@ -422,8 +422,8 @@ def _is(t, dtype, shape, index) -> bool:
     """Whether t is a contiguous CUDA tensor of this type, shape and device index: one pass over what _need checks and
     explains, for calls whose latency counts."""
     import torch
-    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index
-            and index >= 0 and t.is_contiguous())
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index >= 0 and t.shape == shape
+            and t.is_contiguous())
 
 
 def _need_on(t, dtype, shape, name, index):
@@ -436,8 +436,9 @@ def _need_on(t, dtype, shape, name, index):
 def _need_kv4(cache, B, H, d, index):
     """Check a 4-bit cache of B sequences and (if given) H heads of size d on a device; returns its (heads, capacity)."""
     import torch
-    _need_on(cache, torch.uint8, None, "cache", index)
-    s = cache.shape
+    s = getattr(cache, "shape", None)
+    if not _is(cache, torch.uint8, s, index):
+        _need_on(cache, torch.uint8, None, "cache", index)
     if len(s) != 4 or s[0] != B or s[3] != 36 * max(d, 32) or H not in (None, s[1]):
         raise ValueError(f"cache must have shape ({B}, {'heads' if H is None else H}, C / 32, {36 * max(d, 32)}), "
                          f"got {tuple(s)}")
@@ -451,7 +452,7 @@ def _call_on(index, fn, stream, args, where):
         stream = torch._C._cuda_getCurrentRawStream(index)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:
         status = fn(*args, stream)
     else:
         with torch.cuda.device(index):
