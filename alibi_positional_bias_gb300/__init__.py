@@ -418,13 +418,8 @@ def alibi_kv4_cache(B: int, H: int, C: int, d: int, device=None):
                        device="cuda" if device is None else device)
 
 
-def _is(t, dtype, shape, index) -> bool:
-    """Whether t is a contiguous CUDA tensor of this type, shape and device index: one pass over what _need checks and
-    explains, for calls whose latency counts."""
-    import torch
-    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index >= 0 and t.shape == shape
-            and t.is_contiguous())
-
+# The 4-bit cache's calls are made once per layer and token, so they check their arguments in one expression and leave it to
+# _explain_kv4 to say what is wrong.
 
 def _need_on(t, dtype, shape, name, index):
     """_need, and on CUDA device `index`."""
@@ -433,19 +428,27 @@ def _need_on(t, dtype, shape, name, index):
         raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
 
 
-def _need_kv4(cache, B, H, d, index):
-    """Check a 4-bit cache of B sequences and (if given) H heads of size d on a device; returns its (heads, capacity)."""
+def _explain_kv4(dtype, first, others, cache, H, ints):
+    """Raise what is wrong with a call on the 4-bit cache. first: (tensor, name, dimensions); others: (tensor, name, dtype,
+    shape) like it; ints: (tensor or None, name) of int32 [B]."""
     import torch
-    s = getattr(cache, "shape", None)
-    if not _is(cache, torch.uint8, s, index):
-        _need_on(cache, torch.uint8, None, "cache", index)
+    t, name, dims = first
+    _need(t, dtype, None, name)
+    if t.dim() not in dims:
+        raise ValueError(f"{name} must have {' or '.join(map(str, dims))} dimensions, got shape {tuple(t.shape)}")
+    B, d, index = t.shape[0], t.shape[-1], t.get_device()
+    for o, oname, odtype, shape in others:
+        _need_on(o, odtype, shape, oname, index)
+    _need_on(cache, torch.uint8, None, "cache", index)
+    s = tuple(cache.shape)
     if len(s) != 4 or s[0] != B or s[3] != 36 * max(d, 32) or H not in (None, s[1]):
-        raise ValueError(f"cache must have shape ({B}, {'heads' if H is None else H}, C / 32, {36 * max(d, 32)}), "
-                         f"got {tuple(s)}")
-    return s[1], s[2] * 32
+        raise ValueError(f"cache must have shape ({B}, {'heads' if H is None else H}, C / 32, {36 * max(d, 32)}), got {s}")
+    for o, oname in ints:
+        if o is not None:
+            _need_on(o, torch.int32, (B,), oname, index)
 
 
-def _call_on(index, fn, stream, args, where):
+def _call_kv4(index, fn, where, stream, *args):
     """fn(*args, stream) with the tensors' device current, on `stream` (None: torch's current one)."""
     import torch
     if stream is None:
@@ -461,21 +464,21 @@ def _call_on(index, fn, stream, args, where):
         raise AlibiError(status, where)
 
 
-def _kv4_rows(k, v, dtype, cache, pos, count):
-    """Checks shared by alibi_kv4_write and _read; returns (device index, pointers of pos and count, B, H, T, C, d)."""
+def _kv4_rows_ok(k, v, dtype, cache, pos, count) -> bool:
     import torch
-    if not isinstance(k, torch.Tensor) or k.dim() != 4:
-        raise (ValueError if isinstance(k, torch.Tensor) else TypeError)("k must be a torch tensor of shape (B, H, T, d)")
-    shape, index = k.shape, k.get_device()
-    if not (_is(k, dtype, shape, index) and _is(v, dtype, shape, index)):
-        _need(k, dtype, None, "k")
-        _need_on(v, dtype, shape, "v", index)
-    B, H, T, d = shape
-    _, C = _need_kv4(cache, B, H, d, index)
-    for t, name in ((pos, "pos"), (count, "count")):
-        if t is not None and not _is(t, torch.int32, (B,), index):
-            _need_on(t, torch.int32, (B,), name, index)
-    return (index, None if pos is None else pos.data_ptr(), None if count is None else count.data_ptr(), B, H, T, C, d)
+    try:
+        shape, c, index = k.shape, cache.shape, k.get_device()
+        B, H, _, d = shape
+        return (k.dtype is dtype and v.dtype is dtype and cache.dtype is torch.uint8
+                and index == v.get_device() == cache.get_device() >= 0 and v.shape == shape
+                and len(c) == 4 and c[0] == B and c[1] == H and c[3] == (36 * d if d > 32 else 1152)
+                and k.is_contiguous() and v.is_contiguous() and cache.is_contiguous()
+                and (pos is None or (pos.dtype is torch.int32 and pos.shape == (B,) and pos.get_device() == index
+                                     and pos.is_contiguous()))
+                and (count is None or (count.dtype is torch.int32 and count.shape == (B,)
+                                       and count.get_device() == index and count.is_contiguous())))
+    except (AttributeError, TypeError, ValueError):
+        return False
 
 
 def alibi_kv4_write(k, v, cache, pos=None, count=None, stream=None) -> None:
@@ -484,9 +487,13 @@ def alibi_kv4_write(k, v, cache, pos=None, count=None, stream=None) -> None:
     CUDA tensors [B] (None: 0 and T). Sequences that do not fit are left out and reported by
     alibi_check_error."""
     import torch
-    index, pp, pc, *dims = _kv4_rows(k, v, torch.bfloat16, cache, pos, count)
-    _call_on(index, load().alibi_kv4_write, stream, (k.data_ptr(), v.data_ptr(), cache.data_ptr(), pp, pc, *dims),
-             "alibi_kv4_write")
+    if not _kv4_rows_ok(k, v, torch.bfloat16, cache, pos, count):
+        _explain_kv4(torch.bfloat16, (k, "k", (4,)), [(v, "v", torch.bfloat16, getattr(k, "shape", None))], cache,
+                     k.shape[1] if hasattr(k, "shape") and len(k.shape) == 4 else None, [(pos, "pos"), (count, "count")])
+    B, H, T, d = k.shape
+    _call_kv4(k.get_device(), load().alibi_kv4_write, "alibi_kv4_write", stream, k.data_ptr(), v.data_ptr(),
+              cache.data_ptr(), None if pos is None else pos.data_ptr(), None if count is None else count.data_ptr(),
+              B, H, T, cache.shape[2] * 32, d)
 
 
 def alibi_kv4_read(cache, k, v, pos=None, count=None, stream=None):
@@ -494,10 +501,14 @@ def alibi_kv4_read(cache, k, v, pos=None, count=None, stream=None):
     held values exactly): row pos[b] + t of sequence b to token t < count[b]; other tokens of k and v
     are left as they were. pos and count as in alibi_kv4_write. Returns (k, v)."""
     import torch
-    fp32 = getattr(k, "dtype", None) is torch.float32
-    index, pp, pc, *dims = _kv4_rows(k, v, torch.float32 if fp32 else torch.bfloat16, cache, pos, count)
-    _call_on(index, load().alibi_kv4_read, stream,
-             (cache.data_ptr(), k.data_ptr(), v.data_ptr(), pp, pc, *dims, int(fp32)), "alibi_kv4_read")
+    dtype = torch.float32 if getattr(k, "dtype", None) is torch.float32 else torch.bfloat16
+    if not _kv4_rows_ok(k, v, dtype, cache, pos, count):
+        _explain_kv4(dtype, (k, "k", (4,)), [(v, "v", dtype, getattr(k, "shape", None))], cache,
+                     k.shape[1] if hasattr(k, "shape") and len(k.shape) == 4 else None, [(pos, "pos"), (count, "count")])
+    B, H, T, d = k.shape
+    _call_kv4(k.get_device(), load().alibi_kv4_read, "alibi_kv4_read", stream, cache.data_ptr(), k.data_ptr(),
+              v.data_ptr(), None if pos is None else pos.data_ptr(), None if count is None else count.data_ptr(),
+              B, H, T, cache.shape[2] * 32, d, int(dtype is torch.float32))
     return k, v
 
 
@@ -508,34 +519,38 @@ def alibi_attn_decode_kv4(q, cache, lens=None, L=None, out=None, lse=None, slope
     capacity C); slopes: H values (None: alibi_slopes(H)). Returns (out, lse): bf16 like q, fp32
     without the last dimension."""
     import torch
-    if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
-        raise (ValueError if isinstance(q, torch.Tensor) else TypeError)(
-            "q must be a torch tensor of shape (B, H, T, d) or (B, H, d)")
-    shape, index = q.shape, q.get_device()
-    if not _is(q, torch.bfloat16, shape, index):
-        _need(q, torch.bfloat16, None, "q")
-    B, H, d = shape[0], shape[1], shape[-1]
-    T = shape[2] if len(shape) == 4 else 1
-    Hkv, C = _need_kv4(cache, B, None, d, index)
-    if lens is not None and not _is(lens, torch.int32, (B,), index):
-        _need_on(lens, torch.int32, (B,), "lens", index)
+    try:
+        shape, c, index = q.shape, cache.shape, q.get_device()
+        B, H, d = shape[0], shape[1], shape[-1]
+        good = (3 <= len(shape) <= 4 and q.dtype is torch.bfloat16 and cache.dtype is torch.uint8
+                and index == cache.get_device() >= 0 and len(c) == 4 and c[0] == B and c[3] == (36 * d if d > 32 else 1152)
+                and q.is_contiguous() and cache.is_contiguous()
+                and (lens is None or (lens.dtype is torch.int32 and lens.shape == (B,) and lens.get_device() == index
+                                      and lens.is_contiguous()))
+                and (out is None or (out.dtype is torch.bfloat16 and out.shape == shape and out.get_device() == index
+                                     and out.is_contiguous()))
+                and (lse is None or (lse.dtype is torch.float32 and lse.shape == shape[:-1] and lse.get_device() == index
+                                     and lse.is_contiguous())))
+    except (AttributeError, IndexError, TypeError, ValueError):
+        good = False
+    if not good:
+        given = [(out, "out", torch.bfloat16, getattr(q, "shape", None))] if out is not None else []
+        given += [(lse, "lse", torch.float32, getattr(q, "shape", (0,))[:-1])] if lse is not None else []
+        _explain_kv4(torch.bfloat16, (q, "q", (3, 4)), given, cache, None, [(lens, "lens")])
     if out is None:
         out = torch.empty_like(q)
-    elif not _is(out, torch.bfloat16, shape, index):
-        _need_on(out, torch.bfloat16, shape, "out", index)
     if lse is None:
         lse = torch.empty(shape[:-1], dtype=torch.float32, device=q.device)
-    elif not _is(lse, torch.float32, shape[:-1], index):
-        _need_on(lse, torch.float32, shape[:-1], "lse", index)
     m = None
     if slopes is not None:
         m = np.ascontiguousarray(slopes, dtype=np.float32)
         if m.shape != (H,):
             raise ValueError(f"slopes: expected shape ({H},), got {m.shape}")
-    _call_on(index, load().alibi_attn_decode_kv4, stream,
-             (q.data_ptr(), cache.data_ptr(), None if lens is None else lens.data_ptr(), out.data_ptr(), lse.data_ptr(),
-              B, H, Hkv, T, C if L is None else int(L), C, d,
-              None if m is None else m.ctypes.data_as(ctypes.POINTER(ctypes.c_float))), "alibi_attn_decode_kv4")
+    C = c[2] * 32
+    _call_kv4(index, load().alibi_attn_decode_kv4, "alibi_attn_decode_kv4", stream, q.data_ptr(), cache.data_ptr(),
+              None if lens is None else lens.data_ptr(), out.data_ptr(), lse.data_ptr(), B, H, c[1],
+              shape[2] if len(shape) == 4 else 1, C if L is None else int(L), C, d,
+              None if m is None else m.ctypes.data_as(ctypes.POINTER(ctypes.c_float)))
     return out, lse
 
 
