@@ -341,9 +341,10 @@ __device__ __forceinline__ void block32(State<D, KC> &st, const uint8_t *blk, in
             st.l[k] += ex2_approx(a[i][k]);
             b[i][k] = ex2_approx(b[i][k]);
         }
-    // Every P_jn of the block rounds to zero (2^(b + 7) below 2^-25): nothing to add. With ALiBi most of a long
-    // sequence ends here.
-    if (!__any_sync(0xffffffffu, !(topb <= -33.0f))) return;
+    // Every P_jn of the block rounds to zero (2^(b + 7) below 2^-25), and no scale is NaN: nothing to add. With ALiBi most
+    // of a long sequence ends here.
+    const uint32_t largest = max(max(big[0], big[1]), max(big[2], big[3]));
+    if (!__any_sync(0xffffffffu, !(topb <= -33.0f) || largest == 255u)) return;
 
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -560,7 +561,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const int U = p.Hkv * p.chunks;
 
-    griddep_launch_dependents();
+    if (MODE == Mode::Shares) griddep_launch_dependents();  // the merge kernel
     if (threadIdx.x == 0) {
         cta_err_init(kWaitLimitNs);
         cta_check_init(p.status, ring, kSmem);
@@ -570,8 +571,6 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
         fence_mbar_init();
     }
     __syncthreads();
-
-    griddep_wait();  // everything above overlaps the kernel before this one
 
     // what is left of the share: kept in shared memory, out of the registers of the loop over blocks
     __shared__ Share sh;
@@ -788,7 +787,6 @@ __global__ void __launch_bounds__(kMergeThreads) decode_kv4_merge_kernel(const _
     __shared__ float weight[kMostShares];
     __shared__ float red[2][kMergeThreads / 32];
     __shared__ float4 sum[kMergeThreads];
-    griddep_launch_dependents();
     griddep_wait();
     const int unit = blockIdx.x, r = blockIdx.y;
     const int2 h = __ldcg(reinterpret_cast<const int2 *>(p.head + unit));  // (first, last)
@@ -884,8 +882,7 @@ cudaError_t launch(DecodeKv4Params &p, long long units, cudaStream_t stream)
         const auto kernel = plan.count > 1 ? clusters : whole;
         const cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(kernel), kSmem, 0, plan.count > 1);
         if (e != cudaSuccess) return e;
-        return launch_overlapped(kernel, dim3(static_cast<unsigned>(units * plan.count)), kWarps * 32, kSmem, stream, p,
-                                 plan.count);
+        return launch_kernel(kernel, dim3(static_cast<unsigned>(units * plan.count)), kWarps * 32, kSmem, stream, p, plan.count);
     }
     cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(shared), kSmem, 0);
     if (e != cudaSuccess) return e;
@@ -898,10 +895,11 @@ cudaError_t launch(DecodeKv4Params &p, long long units, cudaStream_t stream)
     if (e != cudaSuccess) return e;
     p.part = reinterpret_cast<float *>(ws);
     p.head = reinterpret_cast<Header *>(ws + bytes);
-    e = launch_overlapped(shared, dim3(static_cast<unsigned>(shares)), kWarps * 32, kSmem, stream, p);
+    e = launch_kernel(shared, dim3(static_cast<unsigned>(shares)), kWarps * 32, kSmem, stream, p);
     if (e == cudaSuccess && shares > 1) {
         MergeParams m = {p.part, p.head, p.out, p.lse, p.d, p.rows, p.chunks};
-        e = launch_overlapped(decode_kv4_merge_kernel<D>, dim3(static_cast<unsigned>(units), std::min(p.rows, kRows)), kMergeThreads, 0, stream, m);
+        e = launch_kernel(decode_kv4_merge_kernel<D>, dim3(static_cast<unsigned>(units), std::min(p.rows, kRows)), kMergeThreads, 0, stream,
+                          m, 1, true);
     }
     const cudaError_t f = cudaFreeAsync(ws, stream);
     return e != cudaSuccess ? e : f;
@@ -947,7 +945,8 @@ extern "C" int alibi_attn_decode_kv4(const void *q, const void *cache, const int
     p.rows = H / Hkv * T;
     p.chunks = (p.rows + kRows - 1) / kRows;
     p.c1 = 0x1p-14f * 1.4426950408889634f / sqrtf(static_cast<float>(d));
-    for (int h = 0; h < H; ++h) p.slopes.log2e[h] = s.log2e[h];
+    // A slope beyond 1e30 is 1e30: the bias of the next token is out of reach already, and its multiples stay finite.
+    for (int h = 0; h < H; ++h) p.slopes.log2e[h] = std::min(s.log2e[h], 1e30f);
     const long long units = static_cast<long long>(B) * Hkv * p.chunks;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool few = p.rows <= kRows / 2;  // one row per lane

@@ -94,7 +94,8 @@ struct Plan {
 // The way with the least estimated time of its slowest CTA, in stages of a CTA that shares its SM (0.23 us for 32 tokens of
 // d = 128; one that has it to itself takes 0.58 of that). A launch is 27, the merge of a cluster 8 more (18 above
 // 8 CTAs), the partials and their merge kernel 20 (slices) or 26 (shares), and a share that ends inside a chunk pays
-// 20 to begin the next one. Clusters fit into groups of SMs, the smallest of which has 16 (40 clusters of 7 CTAs
+// 20 to begin the next one. Several rounds of whole chunks run at 0.85 of that, as fast as memory goes, with a tail of
+// 0.3. Clusters fit into groups of SMs, the smallest of which has 16 (40 clusters of 7 CTAs
 // take a second round, 40 of 6 do not). Measured, in us, whole / clusters of / slices / shares:
 //   sequences x KV heads (x G) x tokens x d   1 x 40 x 8192 x 128        35.2 / 18.7 (6) / 18.8 / 21.5
 //                                             1 x 32 x 2048 x 128        14.6 / 10.6 (8) / 12.7 /    -
@@ -105,14 +106,16 @@ struct Plan {
 //                                             16 x 8 (x 4) x 4097 x 128  22.9 / 21.0 (2) / 25.0 / 27.1
 //                                             8 x 8 (x 4) x 16384 x 128  57.6 / 33.1 (4) / 37.9 / 42.9
 //                                             8 x 8 (x 8) x 32768 x 128   115 /    -     / 71.9 / 67.5
+//                                             9 x 37 x 16384 x 128        152 /    -     /    - /  134
+//                                             13 x 38 (x 4) x 16384 x 128 178 /    -     /    - /  199
 //                                             16 x 40 x 4096 x 128       71.6 /    -     /    - / 74.3
 //                                             64 x 40 x 8192 x 128        424 /    -     /    - /  494
 inline Plan deal_of(long long units, int stages, int ctas)
 {
     if (stages <= kWarps) return {Deal::Whole, 1};
-    const double rounds = static_cast<double>(units) / ctas, rest = rounds - std::floor(rounds), alone = 0.58;
+    const double rounds = static_cast<double>(units) / ctas, alone = 0.58;
     Plan best = {Deal::Whole, 1};
-    double cost = 27 + stages * (std::floor(rounds) + (rest == 0 ? 0 : rest <= 0.5 ? alone : 1));
+    double cost = 27 + stages * (rounds <= 0.5 ? alone : rounds <= 1 ? 1 : 0.85 * rounds + 0.3);
     const auto consider = [&](Deal deal, int count, double c) {
         if (c < cost) cost = c, best = {deal, count};
     };
@@ -121,7 +124,7 @@ inline Plan deal_of(long long units, int stages, int ctas)
             consider(Deal::Clusters, c,
                      27 + (c > 8 ? 18 : 8) + std::ceil(stages / static_cast<double>(c)) * (2 * units * c <= ctas ? alone : 1));
     if (2 * units <= ctas) consider(Deal::Slices, 1, 47 + std::ceil(stages / std::floor(ctas / static_cast<double>(units))));
-    consider(Deal::Shares, 1, 53 + stages * rounds + 20 * (rounds > 1 ? rounds : 1));
+    consider(Deal::Shares, 1, 53 + stages * rounds + 20);
     return best;
 }
 

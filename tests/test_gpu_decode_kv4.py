@@ -325,6 +325,66 @@ def test_two_streams_and_two_graphs_at_once(ab):
     ab.alibi_check_error()
 
 
+@pytest.mark.parametrize("B,Hkv,G,N,d", [(2, 5, 1, 300, 64), (1, 32, 2, 2048, 128), (1, 2, 8, 30000, 128),
+                                         (24, 7, 1, 14336, 32)])
+def test_graph_of_every_way_follows_lengths_on_the_device(ab, B, Hkv, G, N, d):
+    # captured once for the capacity, replayed while the lengths change (whole chunks, clusters, slices, shares)
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(N)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    cache = ab.alibi_kv4_cache(B, Hkv, -(-N // 32) * 32, d)
+    ab.alibi_kv4_write(rand(B, Hkv, N, d), rand(B, Hkv, N, d), cache)
+    q, lens = rand(B, Hkv * G, 1, d), ints([N] * B)
+    ab.alibi_attn_decode_kv4(q, cache, lens=lens)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = ab.alibi_attn_decode_kv4(q, cache, lens=lens)
+    for new in ([N] * B, [1 + b for b in range(B)], [N - 13 * b for b in range(B)], [0] * B, [(N * b) // B for b in range(B)]):
+        lens.copy_(ints(new))
+        out.fill_(7.0)
+        lse.fill_(7.0)
+        graph.replay()
+        want, wl = ab.alibi_attn_decode_kv4(q, cache, lens=lens)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(lse, wl)
+        assert bool((lse[[b for b in range(B) if new[b] == 0]] == -np.inf).all())
+    ab.alibi_check_error()
+
+
+def test_every_way_with_a_nan_far_back(ab):
+    # a NaN value whose weight has long vanished still reaches its group, as 0 x NaN does in the bf16 decode; NaN rows past
+    # the length do not
+    import torch
+    for B, Hkv, N, d in ((1, 3, 200, 128), (1, 32, 4096, 128), (1, 2, 20000, 64), (24, 7, 14336, 32)):
+        k = torch.randn(B, Hkv, N, d, device="cuda", dtype=torch.bfloat16)
+        v = torch.randn(B, Hkv, N, d, device="cuda", dtype=torch.bfloat16)
+        v[:, 1, 3, 2] = float("nan")
+        v[:, 0, N - 1, 2] = float("nan")
+        k[:, 0, N - 1, 2] = float("nan")
+        cache = ab.alibi_kv4_cache(B, Hkv, -(-N // 32) * 32, d)
+        ab.alibi_kv4_write(k, v, cache)
+        q = torch.randn(B, Hkv, 1, d, device="cuda", dtype=torch.bfloat16)
+        out, lse = ab.alibi_attn_decode_kv4(q, cache, lens=ints([N - 1] * B), slopes=[1.0] * Hkv)
+        ab.alibi_check_error()
+        nan = torch.isnan(out)
+        assert bool(nan[:, 1, 0, :32].all()) and not bool(nan[:, 1, 0, 32:].any())
+        assert not bool(nan[:, [0] + list(range(2, Hkv))].any()) and not bool(torch.isnan(lse).any())
+
+
+def test_very_large_slopes(ab):
+    # only the query's own token is left, whatever the slope
+    import torch
+    q, k, v = case(40, 1, 4, 1, 1, 300, 64)
+    cache = up(ref.pack(k, v))
+    out, lse = ab.alibi_attn_decode_kv4(bf16(q)[1], cache, lens=ints([300]), slopes=[1e20, 1e30, 3e38, 3.4e38])
+    ab.alibi_check_error()
+    want = torch.from_numpy(ref.held(v)[:, :, 299].astype(np.float32)).to(torch.bfloat16)
+    assert torch.equal(out[:, :, 0].cpu(), want)
+    x = (q[:, :, 0] * ref.held(k)[:, :, 299]).sum(-1) / 8.0
+    assert np.abs(host64(lse)[:, :, 0] - x).max() <= 1e-5
+
+
 def test_more_heads_than_grid_rows(ab):
     # 71680 (b, head) pairs
     import torch
