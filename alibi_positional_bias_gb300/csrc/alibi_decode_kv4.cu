@@ -27,7 +27,19 @@
 //            2^(e_j - 1) <= max_n |s_jn| < 2^e_j and a second reference M for x_j + e_j, so
 //            it neither overflows nor vanishes whatever the magnitude of the values. Its
 //            rounding to 11 bits is the only one below fp32: off by at most 2^-11 of each
-//            product, a quarter of the bf16 output's own step.
+//            product, a quarter of the bf16 output's own step. (bf16 weights would be off by as
+//            much as the output itself.) A block whose P all round to zero adds nothing and its
+//            values are not multiplied.
+//
+// mma.sync and not tcgen05.mma: the operands are made in registers, where tcgen05 would have to be
+// fed through shared or tensor memory, and at 8 columns the tensor pipe is 19% busy.
+//
+// What has to move: 1.125 d bytes per key and KV head, once. 64 x 40 heads of 8192 tokens, d = 128
+// (3.0 GB): 424 us, 7.1 TB/s, 105% of the measured copy (which also writes). With fewer CTAs than
+// SMs' room a warp's own chain bounds a block of 32 tokens (1100 cycles for the keys, 1800 with the values,
+// at 2 warps per scheduler), and about 10 us of launch, first loads and merge come on
+// top: 1 x 40 x 8192, 47 MB, 17.9 us. 16 warps per SM are what 128 registers allow; the ring of 3 stages
+// per warp keeps 147 KB in flight.
 //
 // The work is dealt in one of four ways (deal_of), by lengths that only the device knows:
 //   whole    a CTA takes one chunk: short sequences, and many chunks;

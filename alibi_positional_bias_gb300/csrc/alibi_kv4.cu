@@ -6,8 +6,17 @@
 // so x_m itself is code 0 and is held exactly, and all 16 codes are used. x is bf16,
 // so s is a bf16 number exactly (below 2^-100 the group is stored as zeros), and the
 // quotient of two 8-bit significands either is a multiple of 1/2 or is at least 2^-10
-// away from one: x (1/s) in fp32, off by at most 2^-20, with 2^-12 added before the
+// away from one: x (1/s) in fp32, off by at most 2^-19, with 2^-12 added before the
 // floor, decides every element as exact arithmetic does.
+//
+// What has to move: 4 d bytes of a token's key and value and 1.125 d of the cache. Prompts
+// go a block per CTA, the cache in whole 16-byte words of a thread, the rows in 64-byte
+// segments, no shared memory. Written and read, d = 128: 4 x 32 heads x 2048 tokens 33.1 and
+// 29.7 us (172 MB each: 5.2 and 5.8 TB/s), 8 x 32 x 2048 59.2 and 54.6 us (5.8 and
+// 6.3 TB/s, 86 and 93% of the measured copy). The write is bound by the logic pipe (66% busy, 73% of issue slots):
+// 12 operations per element, of which ordering the group's elements takes 2, the codes 4;
+// one thread per 8 elements with 16-bit stores of the values took 161 us for both. A step's new
+// token of 64 x 40 heads takes 4.6 us, a launch's time.
 
 #include <algorithm>
 #include <cuda_bf16.h>
@@ -53,7 +62,7 @@ __device__ __forceinline__ uint32_t order_keys(uint32_t w)
 // The larger of the two halves.
 __device__ __forceinline__ uint32_t fold(uint32_t keys) { return max(keys & 0xffffu, keys >> 16); }
 
-// From the largest order key of a group: bf16 bits of the scale s, and 1 / s (0 where nothing is to be scaled). The
+// From the largest order key of a group: bf16 bits of the scale s, and 1 / (16 s) (0 where nothing is to be scaled). The
 // reciprocal is the approximate one, good to 2^-23, as code_of allows for.
 struct Scale {
     uint32_t bits;
@@ -67,22 +76,23 @@ __device__ __forceinline__ Scale scale_of(uint32_t key)
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__uint_as_float(bits << 16)));
     const bool plain = mag - 0x0d80u < 0x7f80u - 0x0d80u;  // 2^-100 and above, and finite
-    return {plain ? bits : mag >= 0x7f80u ? 0x7fc0u : 0u, plain ? r : 0.0f};
+    return {plain ? bits : mag >= 0x7f80u ? 0x7fc0u : 0u, plain ? r * 0.0625f : 0.0f};
 }
 
-// floor(x / s + 8.5) in the low bits, up to 16: 2^-12 stands against the error of the product (at most 2^-19), and the sum
-// with 2^23, rounded down, leaves the floor in the low bits. A NaN leaves ones.
+// min(15, floor(x / s + 8.5)) in the low bits, `inverse` being 1 / (16 s). The sum of a sixteenth, clamped to [0, 1], is off by
+// 2^-23 at most; 2^-12 (in units of a code) stands against that and keeps ties above their integer, and the product with 16 (1 - 2^-22), added
+// to 2^23 and rounded down, leaves the floor in the low bits, 15 for the clamped ones. Both are fma, on the pipe
+// that has room: minimum, and, or, shift and permute share the other one, which bounds the kernel.
 __device__ __forceinline__ uint32_t code_of(float x, float inverse)
 {
-    return __float_as_uint(__fadd_rd(fmaf(x, inverse, 8.5f + 0x1p-12f), 8388608.0f));
+    return __float_as_uint(__fmaf_rd(__saturatef(fmaf(x, inverse, (8.5f + 0x1p-12f) / 16.0f)), 16.0f - 0x1p-18f, 8388608.0f));
 }
 
 // A word of the cache: codes of four bf16 numbers in its low half, of four others in its high half.
 __device__ __forceinline__ uint32_t code_word(uint2 lo, uint2 hi, float inverse_lo, float inverse_hi)
 {
-    const auto pair = [&](uint32_t a, uint32_t b) {  // at most 15 each
-        const uint32_t x = code_of(__uint_as_float(a), inverse_lo), y = code_of(__uint_as_float(b), inverse_hi);
-        return __vminu2(__byte_perm(x, y, 0x5410), 0x000f000fu);
+    const auto pair = [&](uint32_t a, uint32_t b) {
+        return __byte_perm(code_of(__uint_as_float(a), inverse_lo), code_of(__uint_as_float(b), inverse_hi), 0x5410);
     };
     const uint32_t p0 = pair(lo.x << 16, hi.x << 16), p1 = pair(lo.x & 0xffff0000u, hi.x & 0xffff0000u);
     const uint32_t p2 = pair(lo.y << 16, hi.y << 16), p3 = pair(lo.y & 0xffff0000u, hi.y & 0xffff0000u);
@@ -187,7 +197,7 @@ __global__ void __launch_bounds__(256) kv4_read_rows_kernel(const __grid_constan
 // (4 elements of up to two groups, of 4 tokens), so that the cache is read and written in whole 16-byte
 // words without shared memory, and the rows in whole 64-byte segments.
 constexpr int kHalf = 128;  // threads for the keys, and for the values
-constexpr int kWriteCtas = 6, kReadCtas = 8;
+constexpr int kWriteCtas = 8, kReadCtas = 8;
 
 struct BlockItem {
     int first, n;       // token of the call in the block's row 0 (may be negative), tokens of the call

@@ -363,7 +363,11 @@ ALIBI_API int alibi_kv4_read(const void *cache, void *k, void *v, const int *pos
  * with lens[b] outside [0, L] gets NaN in out and lse, and alibi_check_error returns
  * ALIBI_ERR_RANGE. slopes: optional HOST array of H slopes as in
  * alibi_fwd_options (NULL: alibi_slopes(H)).
- * Rows past a sequence's length are not used, whatever they hold.
+ * Rows past a sequence's length are not used, whatever they hold; a NaN in a key
+ * that a query sees makes its out and lse NaN, one in a value its group of 32
+ * elements of out. out and lse are the same bits for the same arguments. A call takes up
+ * to 2.6 MB of scratch from the library's stream-ordered pool where it splits sequences over
+ * several CTAs and merges them in a second kernel (few long sequences).
  */
 ALIBI_API int alibi_attn_decode_kv4(const void *q, const void *cache, const int *lens, void *out, float *lse, int B,
                                     int H, int Hkv, int T, int L, int C, int d, const float *slopes, void *stream);
