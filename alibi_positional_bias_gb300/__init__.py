@@ -448,13 +448,29 @@ def _explain_kv4(dtype, first, others, cache, H, ints):
             _need_on(o, torch.int32, (B,), oname, index)
 
 
+def _raw_stream(stream, index) -> int:
+    """Handle of a stream of device `index` (None: torch's current one)."""
+    import torch
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _empty_on(stream, index, shape, dtype):
+    """An uninitialised tensor whose memory belongs to the stream that will write it: memory of another stream may still
+    be in use there."""
+    import torch
+    device = torch.device("cuda", index)
+    if stream is None or _raw_stream(stream, index) == _raw_stream(None, index):
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(_raw_stream(stream, index), device=device)):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _call_kv4(index, fn, where, stream, *args):
     """fn(*args, stream) with the tensors' device current, on `stream` (None: torch's current one)."""
     import torch
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(index)
-    elif not isinstance(stream, int):
-        stream = stream.cuda_stream
+    stream = _raw_stream(stream, index)
     if torch._C._cuda_getDevice() == index:
         status = fn(*args, stream)
     else:
@@ -517,7 +533,7 @@ def alibi_attn_decode_kv4(q, cache, lens=None, L=None, out=None, lse=None, slope
     q: bf16 [B, H, T, d], or [B, H, d] for one token; cache: uint8 [B, H_kv, C / 32, bytes], H a multiple
     of H_kv; lens: int32 CUDA tensor [B] of lengths (None: all L); L: a bound on them (None: the
     capacity C); slopes: H values (None: alibi_slopes(H)). Returns (out, lse): bf16 like q, fp32
-    without the last dimension."""
+    without the last dimension; those made here belong to `stream`."""
     import torch
     try:
         shape, c, index = q.shape, cache.shape, q.get_device()
@@ -538,9 +554,10 @@ def alibi_attn_decode_kv4(q, cache, lens=None, L=None, out=None, lse=None, slope
         given += [(lse, "lse", torch.float32, getattr(q, "shape", (0,))[:-1])] if lse is not None else []
         _explain_kv4(torch.bfloat16, (q, "q", (3, 4)), given, cache, None, [(lens, "lens")])
     if out is None:
-        out = torch.empty_like(q)
+        out = torch.empty_like(q) if stream is None else _empty_on(stream, index, shape, torch.bfloat16)
     if lse is None:
-        lse = torch.empty(shape[:-1], dtype=torch.float32, device=q.device)
+        lse = (torch.empty(shape[:-1], dtype=torch.float32, device=q.device) if stream is None
+               else _empty_on(stream, index, shape[:-1], torch.float32))
     m = None
     if slopes is not None:
         m = np.ascontiguousarray(slopes, dtype=np.float32)

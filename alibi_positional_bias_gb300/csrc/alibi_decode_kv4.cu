@@ -403,8 +403,8 @@ __device__ __forceinline__ void block32(State<D, KC> &st, const uint8_t *blk, in
     }
 }
 
-// Merge of n partials of 4 elements of a row: `at(i)` gives partial i's R, l and mean. The weights l 2^(R - max R)
-// are normalised before they meet the means, so nothing overflows.
+// Merge of n partials of 4 elements of a row: `rl(i)` gives partial i's R and l, `mean(i)` its mean. The weights
+// l 2^(R - max R) are normalised before they meet the means, so nothing overflows.
 struct Merged {
     float R, l;
     float4 o;
@@ -465,6 +465,7 @@ template <int SB>
 __device__ __forceinline__ long long share_of(const DecodeKv4Params &p, int i, Share &sh)
 {
     const int U = p.Hkv * p.chunks, ctas = gridDim.x;
+    const int units = p.slices ? p.B * U : 0;  // of shares there may be fewer than chunks, which `Slices` cannot take
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     bool bad;
     if (p.B <= 32) {  // one sequence per lane, in every warp
@@ -478,7 +479,7 @@ __device__ __forceinline__ long long share_of(const DecodeKv4Params &p, int i, S
         const long long row = static_cast<long long>(__shfl_sync(0xffffffffu, upto, 31)) * U;
         if (warp == 0) {
             const Cut cut(row, ctas);
-            const Slices sl(row, p.B * U, static_cast<int>(__reduce_min_sync(0xffffffffu, n ? n : 0x7fffffff)), ctas);
+            const Slices sl(row, units, static_cast<int>(__reduce_min_sync(0xffffffffu, n ? n : 0x7fffffff)), ctas);
             const long long weight = static_cast<long long>(upto) * U + static_cast<long long>(lane + 1) * U * sl.extra;
             const long long at = p.slices ? sl.last(i) : i < cut.n ? cut.begin(i) : 0;
             const int b = __popc(__ballot_sync(0xffffffffu, lane < p.B && (p.slices ? weight : static_cast<long long>(upto) * U) <= at));
@@ -531,7 +532,7 @@ __device__ __forceinline__ long long share_of(const DecodeKv4Params &p, int i, S
     before += upto - mine;
     const Cut cut(all * U, ctas);
     if (p.slices || i < cut.n) {
-        const Slices sl(all * U, p.B * U, least, ctas);
+        const Slices sl(all * U, units, least, ctas);
         const int extra = p.slices ? sl.extra : 0;
         const long long at = p.slices ? sl.last(i) : cut.begin(i);
         long long w0 = (before + static_cast<long long>(b0) * extra) * U;

@@ -325,6 +325,34 @@ def test_two_streams_and_two_graphs_at_once(ab):
     ab.alibi_check_error()
 
 
+@pytest.mark.parametrize("handle", [False, True])
+def test_outputs_made_for_another_stream_belong_to_it(ab, handle):
+    # Memory that the current stream has just let go of may still be in use there, so a call on another stream must
+    # not get its outputs from it; and memory that it writes is handed out again behind it.
+    import torch
+    q, k, v = case(24, 2, 2, 2, 1, 96, 128)
+    qd, cache = bf16(q)[1], up(ref.pack(k, v))
+    want, want_lse = ab.alibi_attn_decode_kv4(qd, cache)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    gone = [torch.empty_like(want), torch.empty_like(want_lse)]
+    was = {t.data_ptr() for t in gone}
+    del gone
+    out, lse = ab.alibi_attn_decode_kv4(qd, cache, stream=side.cuda_stream if handle else side)
+    side.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    assert out.data_ptr() not in was and lse.data_ptr() not in was
+    assert torch.cuda.current_stream() != side
+    mine = {out.data_ptr(), lse.data_ptr()}
+    del out, lse
+    with torch.cuda.stream(side):
+        assert {torch.empty_like(want).data_ptr(), torch.empty_like(want_lse).data_ptr()} & mine
+    same = ab.alibi_attn_decode_kv4(qd, cache, stream=torch.cuda.current_stream())[0]
+    torch.cuda.synchronize()
+    assert torch.equal(same, want)
+    ab.alibi_check_error()
+
+
 @pytest.mark.parametrize("B,Hkv,G,N,d", [(2, 5, 1, 300, 64), (1, 32, 2, 2048, 128), (1, 2, 8, 30000, 128),
                                          (24, 7, 1, 14336, 32)])
 def test_graph_of_every_way_follows_lengths_on_the_device(ab, B, Hkv, G, N, d):
