@@ -93,8 +93,9 @@ struct DecodeKv4Params {
     float *part;             // [CTAs][2][part_floats], null: CTA i takes chunk i
     Header *head;            // [chunks of all sequences]
     uint32_t *status;
-    int B, Hkv, T, L, blocks, d;  // blocks: C / 32
+    int B, Hkv, G, T, L, blocks, d;  // G: H / H_kv, blocks: C / 32
     int rows, chunks;             // G T, ceil(G T / 8)
+    kv4::Divisor by_chunks, by_U, by_T, by_count;  // U: chunks of a sequence
     bool slices;                  // Shares: every chunk has CTAs of its own; otherwise equal shares
     int count;                    // Cluster: CTAs of a cluster
     float c1;                     // 2^-14 log2(e) / sqrt(d)
@@ -608,10 +609,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
     uint32_t phase = 0;
 
     while (true) {
-        const int all = CLUSTER ? blockIdx.x / p.count : blockIdx.x;  // chunk of all sequences
-        const int b = SHARES ? sh.b : all / U, unit = SHARES ? sh.unit : all % U;
+        const int all = CLUSTER ? p.by_count.of(blockIdx.x) : blockIdx.x;  // chunk of all sequences
+        const int b = SHARES ? sh.b : p.by_U.of(all), unit = SHARES ? sh.unit : all - b * U;
         const int at = SHARES ? sh.at : CLUSTER ? blockIdx.x - all * p.count : 0;
-        const int hk = unit / p.chunks, chunk = unit - hk * p.chunks;
+        const int hk = p.by_chunks.of(unit), chunk = unit - hk * p.chunks;
         const size_t bk = static_cast<size_t>(b) * p.Hkv + hk;
         const int row0 = chunk * kRows, nrows = min(kRows, p.rows - row0);
         // This lane's slice of the row in column g: the 8 elements from 8 c of every group. Asked for before the first copies
@@ -677,13 +678,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
                     st.acc[i][0][j] = st.acc[i][1][j] = 0.0f;
                 }
             }
-            const int G = p.rows / p.T;
 #pragma unroll
             for (int k = 0; k < KC; ++k) {
                 const int r = min(row0 + KC * c + k, p.rows - 1);
                 st.kappa[k] = __shfl_sync(0xffffffffu, kappa, (2 * c + k) * 4);
-                st.slope[k] = p.slopes.log2e[hk * G + r / p.T];
-                st.pos[k] = static_cast<float>(len - p.T + r % p.T - g);
+                const int h = p.by_T.of(r);
+                st.slope[k] = p.slopes.log2e[hk * p.G + h];
+                st.pos[k] = static_cast<float>(len - p.T + r - h * p.T - g);
                 st.R[k] = st.M[k] = -FLT_MAX;
                 st.l[k] = 0.0f;
             }
@@ -762,16 +763,19 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
         if constexpr (CLUSTER) {
             cluster_arrive();
             cluster_wait();
-            const int items = nrows * (D / 4), per = (items + count - 1) / count;  // elements that this CTA merges
+            // This CTA merges `per` of the rows' elements, fewer than it has threads.
+            const int items = nrows * (D / 4), per = p.by_count.of(items + count - 1);
             const uint32_t base = smem_u32(to);
-            for (int i = at * per + threadIdx.x; i < min(items, (at + 1) * per); i += kWarps * 32) {
-                const int r = i / (D / 4), e = i % (D / 4) * 4;
+            const int i = at * per + threadIdx.x, r = i / (D / 4), e = i % (D / 4) * 4;
+            const bool in = i < min(items, (at + 1) * per);
+            Merged m;
+            if (in) {
                 const auto rl = [&](int k) { return ld_cluster2(base + (kRows * D + 2 * r) * 4, k); };
                 const auto mean = [&](int k) { return ld_cluster4(base + (r * D + e) * 4, k); };
-                const Merged m = count <= 8 ? merge<8>(count, rl, mean) : merge<kv4::kMostCluster>(count, rl, mean);
-                finish(p.out, p.lse, p.d, bk * p.rows + row0 + r, e, m, bad);
+                m = count <= 8 ? merge<8>(count, rl, mean) : merge<kv4::kMostCluster>(count, rl, mean);
             }
             cluster_arrive();  // the other CTAs may still read this one's partial
+            if (in) finish(p.out, p.lse, p.d, bk * p.rows + row0 + r, e, m, bad);
             cluster_wait();
         }
         if constexpr (!SHARES) return;
@@ -902,6 +906,7 @@ cudaError_t launch(DecodeKv4Params &p, long long units, cudaStream_t stream)
     p.head = nullptr;
     p.slices = false;
     p.count = plan.count;
+    p.by_count = kv4::Divisor(plan.count);
     if (plan.deal == Deal::Whole || plan.deal == Deal::Clusters) {
         if (units * plan.count > 0x7fffffffLL) return cudaErrorInvalidValue;
         const auto kernel = plan.count > 1 ? clusters : whole;
@@ -964,11 +969,15 @@ extern "C" int alibi_attn_decode_kv4(const void *q, const void *cache, const int
     p.B = B;
     p.Hkv = Hkv;
     p.T = T;
+    p.G = H / Hkv;
     p.L = L;
     p.blocks = C / kv4::kBlock;
     p.d = d;
-    p.rows = H / Hkv * T;
+    p.rows = p.G * T;
     p.chunks = (p.rows + kRows - 1) / kRows;
+    p.by_chunks = kv4::Divisor(p.chunks);
+    p.by_U = kv4::Divisor(Hkv * p.chunks);
+    p.by_T = kv4::Divisor(T);
     p.c1 = 0x1p-14f * 1.4426950408889634f / sqrtf(static_cast<float>(d));
     // A slope beyond 1e30 is 1e30: the bias of the next token is out of reach already, and its multiples stay finite.
     for (int h = 0; h < H; ++h) p.slopes.log2e[h] = std::min(s.log2e[h], 1e30f);

@@ -7,6 +7,7 @@ one, very unequal ones, row counts beyond 32-bit arithmetic, fewer stages than C
   began earlier and one of a chunk that goes on, and holder() names the share a chunk began in;
 * slices: every chunk has a slice of its own at least, the CTAs of a chunk follow each other, no slice within the
   count is empty, and last() inverts cta();
+* divisions by multiplication give the quotient;
 * the plan: whole chunks for short sequences, clusters only as many as fit, slices only where every chunk can have two
   CTAs. No GPU involved."""
 import os
@@ -84,8 +85,20 @@ static void slices(const std::vector<ll> &n, int ctas)
     }
 }
 
+static void divisor(uint32_t d)
+{
+    const Divisor by(d);
+    const auto check = [&](ll n) { if (n >= 0 && n < (1ll << 31)) EXPECT(by.of(static_cast<int>(n)) == n / d); };
+    for (ll n = 0; n < 5000; ++n) check(n);
+    for (ll k : {1ll, 2ll, 3ll, 1000ll, 65535ll, 1ll << 20, ((1ll << 31) - 1) / d})
+        for (ll off : {-1ll, 0ll, 1ll}) check(k * d + off);
+    check((1ll << 31) - 1);
+}
+
 int main()
 {
+    for (uint32_t d = 1; d < 5000; ++d) divisor(d);
+    for (uint32_t d : {65535u, 65536u, 65537u, 131072u, (1u << 30) - 1, 1u << 30, (1u << 30) + 1, (1u << 31) - 1}) divisor(d);
     std::mt19937_64 rng(7);
     const auto pick = [&](ll lo, ll hi) { return lo + static_cast<ll>(rng() % static_cast<unsigned long long>(hi - lo + 1)); };
     for (int t = 0; t < 4000; ++t) {
