@@ -56,6 +56,7 @@
 #include <cmath>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <mutex>
 
 #include "alibi.h"
 #include "kv4_deal.h"
@@ -893,6 +894,46 @@ __global__ void __launch_bounds__(kMergeThreads) decode_kv4_merge_kernel(const _
 
 bool aligned(const void *p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// What the current device holds of clusters of 8-warp CTAs with kSmem, asked for once; kAlone bytes are more than half of an
+// SM's shared memory.
+constexpr int kAlone = 120 << 10;
+
+template <class Kernel>
+cudaError_t cluster_fit(Kernel kernel, kv4::ClusterFit *fit)
+{
+    constexpr int kDevices = 64;  // a device beyond is asked every time
+    static std::mutex mu;
+    static kv4::ClusterFit known[kDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> g(mu);
+    if (dev < kDevices && known[dev].two[0] != 0) {
+        *fit = known[dev];
+        return cudaSuccess;
+    }
+    kv4::ClusterFit f = {};
+    for (int c = 2; c <= kv4::kMostCluster; ++c)
+        for (int smem : {kSmem, kAlone}) {
+            cudaLaunchAttribute attr = {};
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = static_cast<unsigned>(c);
+            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(static_cast<unsigned>(c));
+            cfg.blockDim = dim3(kWarps * 32);
+            cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            e = cudaOccupancyMaxActiveClusters(smem == kSmem ? &f.two[c] : &f.one[c], kernel, &cfg);
+            if (e != cudaSuccess) return e;
+        }
+    f.two[0] = 1;
+    if (dev < kDevices) known[dev] = f;
+    *fit = f;
+    return cudaSuccess;
+}
+
 template <int D, int KC>
 cudaError_t launch(DecodeKv4Params &p, long long units, cudaStream_t stream)
 {
@@ -901,7 +942,12 @@ cudaError_t launch(DecodeKv4Params &p, long long units, cudaStream_t stream)
     const auto shared = &decode_kv4_kernel<D, KC, Mode::Shares>;
     constexpr int kTokens = 128 / D * kv4::kBlock;  // of a stage
     const int stages = (p.L + kTokens - 1) / kTokens, ctas = std::min(2 * num_sms(), kMostShares);
-    const Plan plan = deal_of(units, stages, ctas);
+    cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(clusters), kAlone, 0, true);
+    if (e != cudaSuccess) return e;
+    kv4::ClusterFit fit;
+    e = cluster_fit(clusters, &fit);
+    if (e != cudaSuccess) return e;
+    const Plan plan = deal_of(units, stages, ctas, fit);
     p.part = nullptr;
     p.head = nullptr;
     p.slices = false;
@@ -909,12 +955,11 @@ cudaError_t launch(DecodeKv4Params &p, long long units, cudaStream_t stream)
     p.by_count = kv4::Divisor(plan.count);
     if (plan.deal == Deal::Whole || plan.deal == Deal::Clusters) {
         if (units * plan.count > 0x7fffffffLL) return cudaErrorInvalidValue;
-        const auto kernel = plan.count > 1 ? clusters : whole;
-        const cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(kernel), kSmem, 0, plan.count > 1);
+        if (plan.count == 1) e = prepare_kernel(reinterpret_cast<const void *>(whole), kSmem, 0);
         if (e != cudaSuccess) return e;
-        return launch_kernel(kernel, dim3(static_cast<unsigned>(units * plan.count)), kWarps * 32, kSmem, stream, p, plan.count);
+        return launch_kernel(plan.count > 1 ? clusters : whole, dim3(static_cast<unsigned>(units * plan.count)), kWarps * 32, kSmem, stream, p, plan.count);
     }
-    cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(shared), kSmem, 0);
+    e = prepare_kernel(reinterpret_cast<const void *>(shared), kSmem, 0);
     if (e != cudaSuccess) return e;
     const int per = (stages + kWarps - 1) / kWarps;  // CTAs that a chunk can keep busy
     const int shares = static_cast<int>(std::min<long long>(units * per, ctas));

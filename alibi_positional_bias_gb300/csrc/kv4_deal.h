@@ -16,7 +16,6 @@ namespace kv4 {
 constexpr int kWarps = 8;         // of a CTA
 constexpr int kMostShares = 512;  // CTAs that share the work (two per SM)
 constexpr int kMostCluster = 16;
-constexpr int kGroups = 8, kGroupCtas = 32;  // groups of SMs that hold a cluster, and resident CTAs of the smallest
 
 KV4_HD constexpr int least(int a, int b) { return a < b ? a : b; }
 
@@ -108,40 +107,49 @@ struct Plan {
     int count;  // Clusters: CTAs of a cluster
 };
 
-// The way with the least estimated time of its slowest CTA, in stages of a CTA that shares its SM (0.23 us for 32 tokens of
-// d = 128; one that has it to itself takes 0.58 of that). A launch is 27, the merge of a cluster 8 more (18 above
-// 8 CTAs), the partials and their merge kernel 20 (slices) or 26 (shares), and a share that ends inside a chunk pays
-// 20 to begin the next one. Several rounds of whole chunks run at 0.85 of that, as fast as memory goes, with a tail of
-// 0.3. Clusters fit into groups of SMs, the smallest of which has 16 (40 clusters of 7 CTAs
-// take a second round, 40 of 6 do not). Measured, in us, whole / clusters of / slices / shares:
-//   sequences x KV heads (x G) x tokens x d   1 x 40 x 8192 x 128        35.2 / 18.7 (6) / 18.8 / 21.5
-//                                             1 x 32 x 2048 x 128        14.6 / 10.6 (8) / 12.7 /    -
-//                                             1 x 8 (x 4) x 8192 x 128   35.1 / 12.5 (8) / 12.8 /    -
-//                                             1 x 8 (x 4) x 32768 x 128     - / 20.7 (8) / 16.9 / 18.9
-//                                             1 x 4 (x 4) x 131071 x 128    - / 32.9 (16) / 21.5 / 25.1
-//                                             4 x 8 (x 8) x 8192 x 128   39.3 / 16.7 (8) / 18.8 / 23.0
-//                                             16 x 8 (x 4) x 4097 x 128  22.9 / 21.0 (2) / 25.0 / 27.1
-//                                             8 x 8 (x 4) x 16384 x 128  57.6 / 33.1 (4) / 37.9 / 42.9
-//                                             8 x 8 (x 8) x 32768 x 128   115 /    -     / 71.9 / 67.5
-//                                             9 x 37 x 16384 x 128        152 /    -     /    - /  134
-//                                             13 x 38 (x 4) x 16384 x 128 178 /    -     /    - /  199
-//                                             16 x 40 x 4096 x 128       71.6 /    -     /    - / 74.3
-//                                             64 x 40 x 8192 x 128        424 /    -     /    - /  494
-inline Plan deal_of(long long units, int stages, int ctas)
+// Clusters of c CTAs that the device holds at once, at two CTAs per SM and at one. A cluster lies within a group of SMs, so
+// that 152 SMs hold 38 clusters of 7 but 46 of 6.
+struct ClusterFit {
+    int two[kMostCluster + 1], one[kMostCluster + 1];
+};
+
+// The way with the least estimated time, in us. A CTA that has its SM to itself takes 0.113 for a stage (32 tokens of d =
+// 128), two that share one 0.15 to 0.2 each, the more the fuller the device; several rounds of whole chunks, and slices and
+// shares, which fill it, run as fast as memory goes, whole chunks with a tail of the last round. A launch takes 4.2, the merge of a
+// cluster 1.6 more, the partials and their merge kernel 4.1 (slices) or, with what a share pays to begin its next chunk, 8.8
+// (shares). Measured, in us, caches colder than L2, whole / clusters of / slices / shares:
+//   sequences x KV heads (x G) x tokens x d   1 x 32 x 2048 x 128        11.6 / 7.3 (8) 8.2 (5) 7.4 (4) / 9.5 / 9.7
+//                                             1 x 40 x 8192 x 128        33.2 / 13.9 (6) 17.6 (7) 16.3 (3) / 15.9 / 19.5
+//                                             1 x 8 (x 4) x 8192 x 128   32.6 / 7.7 (12) 8.9 (16) 8.7 (8) / 9.7 / 9.9
+//                                             1 x 8 (x 4) x 32768 x 128  95.9 / 13.8 (12) 16.2 (16) 17.7 (8) / 14.2 / 15.3
+//                                             1 x 4 (x 4) x 131071 x 128  349 / 28.9 (16) / 21.3 / 22.4
+//                                             4 x 8 (x 8) x 8192 x 128   38.2 / 13.4 (8) / 16.3 / 21.0
+//                                             2 x 40 x 8192 x 128        33.8 / 22.1 (3) 24.8 (2) / 25.6 / 27.5
+//                                             2 x 40 x 1024 x 128         7.9 / 8.1 (2) 8.4 (3) / 11.0 / 13.2
+//                                             4 x 40 x 4096 x 128        23.2 / 24.8 (2) /    - / 27.2
+//                                             16 x 8 (x 4) x 4097 x 128  21.5 / 18.9 (2) / 21.6 / 24.2
+//                                             8 x 8 (x 4) x 16384 x 128  55.3 / 27.7 (4) 38.8 (5) / 34.0 / 38.3
+//                                             8 x 8 (x 8) x 32768 x 128   113 / 51.1 (4) / 60.8 / 65.2
+//                                             9 x 37 x 16384 x 128        158 /    - /    - / 129
+//                                             16 x 40 x 4096 x 128       67.1 /    - /    - / 69.6
+//                                             64 x 40 x 8192 x 128        418 /    - /    - / 494
+inline Plan deal_of(long long units, int stages, int ctas, const ClusterFit &fit)
 {
     if (stages <= kWarps) return {Deal::Whole, 1};
-    const double rounds = static_cast<double>(units) / ctas, alone = 0.58;
+    const double rounds = static_cast<double>(units) / ctas, last = rounds - std::ceil(rounds) + 1, alone = 0.113;
     Plan best = {Deal::Whole, 1};
-    double cost = 27 + stages * (rounds <= 0.5 ? alone : rounds <= 1 ? 1 : 0.85 * rounds + 0.3);
+    double cost = 4.2 + stages * (rounds <= 0.5 ? alone : rounds <= 1 ? 0.148 + 0.1 * (rounds - 0.5) : 0.195 * rounds + 0.09 * (1 - last));
     const auto consider = [&](Deal deal, int count, double c) {
         if (c < cost) cost = c, best = {deal, count};
     };
     for (int c = 2; c <= kMostCluster; ++c)
-        if (units <= kGroups * (kGroupCtas / c))
-            consider(Deal::Clusters, c,
-                     27 + (c > 8 ? 18 : 8) + std::ceil(stages / static_cast<double>(c)) * (2 * units * c <= ctas ? alone : 1));
-    if (2 * units <= ctas) consider(Deal::Slices, 1, 47 + std::ceil(stages / std::floor(ctas / static_cast<double>(units))));
-    consider(Deal::Shares, 1, 53 + stages * rounds + 20);
+        if (units <= fit.two[c]) {
+            const double full = rounds * c;  // of the places for CTAs
+            const double shared = 0.17 + 0.06 * (full > 0.5 ? full - 0.5 : 0);
+            consider(Deal::Clusters, c, 5.8 + std::ceil(stages / static_cast<double>(c)) * (units <= fit.one[c] ? alone : shared));
+        }
+    if (2 * units <= ctas) consider(Deal::Slices, 1, 8.3 + std::ceil(stages / std::floor(ctas / static_cast<double>(units))) * 0.2);
+    consider(Deal::Shares, 1, 13 + stages * rounds * 0.21);
     return best;
 }
 

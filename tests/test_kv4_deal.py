@@ -113,13 +113,17 @@ int main()
         shares(n, ctas[t % 7]);
         slices(n, ctas[(t / 7) % 7]);
     }
+    // 152 SMs in groups of 20 and 12, and a device that holds no cluster
+    ClusterFit some = {}, none = {};
+    for (int c = 2; c <= kMostCluster; ++c) some.two[c] = 7 * (40 / c) + 24 / c, some.one[c] = 7 * (20 / c) + 12 / c;
     for (ll units : {1ll, 2ll, 8ll, 19ll, 32ll, 40ll, 64ll, 100ll, 152ll, 153ll, 304ll, 305ll, 2560ll, 71680ll})
         for (int stages = 1; stages <= 20000; stages = stages < 40 ? stages + 1 : stages * 5 / 4)
             for (int ctas : {2, 264, 304}) {
-                const Plan p = deal_of(units, stages, ctas);
+                EXPECT(deal_of(units, stages, ctas, none).deal != Deal::Clusters);
+                const Plan p = deal_of(units, stages, ctas, some);
                 if (stages <= kWarps) EXPECT(p.deal == Deal::Whole);
                 EXPECT(p.deal == Deal::Clusters ? p.count >= 2 && p.count <= kMostCluster : p.count == 1);
-                if (p.deal == Deal::Clusters) EXPECT(units <= kGroups * (kGroupCtas / p.count));
+                if (p.deal == Deal::Clusters) EXPECT(units <= some.two[p.count]);
                 if (p.deal == Deal::Slices) EXPECT(2 * units <= ctas);
             }
     std::printf(fails ? "%d failures\n" : "ok\n", fails);
