@@ -354,7 +354,7 @@ def test_outputs_made_for_another_stream_belong_to_it(ab, handle):
 
 
 @pytest.mark.parametrize("B,Hkv,G,N,d", [(2, 5, 1, 300, 64), (1, 32, 2, 2048, 128), (1, 2, 8, 30000, 128),
-                                         (24, 7, 1, 14336, 32)])
+                                         (24, 7, 1, 14336, 32), (24, 7, 1, 40000, 32)])
 def test_graph_of_every_way_follows_lengths_on_the_device(ab, B, Hkv, G, N, d):
     # captured once for the capacity, replayed while the lengths change (whole chunks, clusters, slices, shares)
     import torch
@@ -384,7 +384,8 @@ def test_every_way_with_a_nan_far_back(ab):
     # a NaN value whose weight has long vanished still reaches its group, as 0 x NaN does in the bf16 decode; NaN rows past
     # the length do not
     import torch
-    for B, Hkv, N, d in ((1, 3, 200, 128), (1, 32, 4096, 128), (1, 2, 20000, 64), (24, 7, 14336, 32)):
+    for B, Hkv, N, d in ((1, 3, 200, 128), (1, 32, 4096, 128), (1, 2, 20000, 64), (24, 7, 14336, 32), (1, 2, 130000, 64),
+                         (24, 7, 40000, 32)):
         k = torch.randn(B, Hkv, N, d, device="cuda", dtype=torch.bfloat16)
         v = torch.randn(B, Hkv, N, d, device="cuda", dtype=torch.bfloat16)
         v[:, 1, 3, 2] = float("nan")
@@ -483,14 +484,23 @@ def run_picked(ab, seed, B, Hkv, G, T, N, d, lens, L, picks, steep=None):
         assert (np.abs(gl[seen] - rl[seen]) <= el[seen]).all(), (b, h)
 
 
-# (on 152 SMs) whole chunks, slices and equal shares; more and fewer than 32 sequences; very unequal lengths; lengths far
-# below the bound that the work was planned for
+# Whole chunks, clusters, slices and equal shares (the ways on 152 SMs: tests/test_kv4_deal.py); more and fewer than 32
+# sequences; very unequal lengths; lengths far below the bound that the work was planned for
 @pytest.mark.parametrize("B,Hkv,G,T,N,d,kind,L", [
-    (24, 7, 1, 1, 14336, 32, "ragged", None),      # shares
-    (40, 5, 8, 1, 16384, 64, "ragged", None),      # shares, two columns per lane
-    (40, 5, 8, 1, 16384, 64, None, 16384),         # shares, one length for all
+    (24, 7, 1, 1, 14336, 32, "ragged", None),      # whole, more CTAs than SMs
+    (40, 5, 8, 1, 16384, 64, "ragged", None),      # two columns per lane
+    (40, 5, 8, 1, 16384, 64, None, 16384),         # one length for all
     (8, 38, 1, 1, 4096, 128, "ragged", None),      # whole, one round
-    (40, 2, 1, 1, 8192, 128, "ragged", None),      # slices, more than 32 sequences
+    (40, 2, 1, 1, 8192, 128, "ragged", None),      # clusters
+    (24, 7, 1, 1, 40000, 32, "ragged", None),      # shares
+    (24, 7, 1, 1, 40000, 32, "one long", 40000),
+    (24, 7, 1, 1, 40000, 32, "short", 40000),
+    (40, 4, 8, 1, 30000, 64, "ragged", None),      # shares, two columns per lane, more than 32 sequences
+    (40, 4, 8, 1, 30000, 64, None, 30000),         # one length for all
+    (50, 1, 1, 1, 128000, 32, "ragged", None),     # slices, more than 32 sequences
+    (50, 1, 2, 3, 64000, 64, "one long", 64000),
+    (50, 1, 2, 3, 64000, 64, "short", 64000),
+    (2, 1, 4, 2, 80000, 64, "ragged", None),       # slices
     (40, 2, 2, 3, 8192, 64, "one long", 8192),     # one sequence of 8192 among sequences of one token
     (3, 2, 1, 1, 16384, 128, "one long", 16384),
     (24, 7, 1, 1, 14336, 32, "one long", 14336),
@@ -507,7 +517,8 @@ def test_ways_of_dealing(ab, B, Hkv, G, T, N, d, kind, L):
     run_picked(ab, 1000 + B + N, B, Hkv, G, T, N, d, lens, L, picks)
 
 
-@pytest.mark.parametrize("B,Hkv,G,T,N,d", [(24, 7, 1, 1, 14336, 32), (3, 4, 8, 1, 8192, 128), (40, 5, 2, 4, 1000, 64)])
+@pytest.mark.parametrize("B,Hkv,G,T,N,d", [(24, 7, 1, 1, 14336, 32), (3, 4, 8, 1, 8192, 128), (40, 5, 2, 4, 1000, 64),
+                                             (24, 7, 1, 1, 40000, 32), (1, 1, 1, 1, 80000, 64)])
 def test_ways_of_dealing_without_bias(ab, B, Hkv, G, T, N, d):
     # no bias: no block's weights vanish, long sums of small weights
     lens = [N - 17 * b for b in range(B)]
@@ -516,7 +527,7 @@ def test_ways_of_dealing_without_bias(ab, B, Hkv, G, T, N, d):
 
 def test_repeated_calls_of_every_way_give_the_same_bits(ab):
     import torch
-    for B, Hkv, N, d in ((24, 7, 14336, 32), (4, 2, 8192, 128), (8, 38, 600, 64)):
+    for B, Hkv, N, d in ((24, 7, 14336, 32), (4, 2, 8192, 128), (8, 38, 600, 64), (24, 7, 40000, 32), (1, 1, 80000, 64)):
         k = torch.randn(B, Hkv, N, d, device="cuda", dtype=torch.bfloat16)
         cache = ab.alibi_kv4_cache(B, Hkv, -(-N // 32) * 32, d)
         ab.alibi_kv4_write(k, torch.flip(k, dims=[2]).contiguous(), cache)

@@ -126,6 +126,13 @@ int main()
                 if (p.deal == Deal::Clusters) EXPECT(units <= some.two[p.count]);
                 if (p.deal == Deal::Slices) EXPECT(2 * units <= ctas);
             }
+    // the sizes of the GPU tests take every way
+    for (ll stages : {313ll, 1024ll}) EXPECT(deal_of(168, static_cast<int>(stages), 304, some).deal == Deal::Shares);
+    EXPECT(deal_of(160, 469, 304, some).deal == Deal::Shares);
+    EXPECT(deal_of(50, 1000, 304, some).deal == Deal::Slices && deal_of(2, 1250, 304, some).deal == Deal::Slices);
+    EXPECT(deal_of(1, 1250, 304, some).deal == Deal::Slices && deal_of(2, 938, 304, some).deal == Deal::Slices);
+    EXPECT(deal_of(32, 64, 304, some).deal == Deal::Clusters && deal_of(8, 256, 304, some).deal == Deal::Clusters);
+    EXPECT(deal_of(304, 128, 304, some).deal == Deal::Whole && deal_of(168, 112, 304, some).deal == Deal::Whole);
     std::printf(fails ? "%d failures\n" : "ok\n", fails);
     return fails != 0;
 }
