@@ -35,10 +35,10 @@
 // fed through shared or tensor memory, and at 8 columns the tensor pipe is 19% busy.
 //
 // What has to move: 1.125 d bytes per key and KV head, once. 64 x 40 heads of 8192 tokens, d = 128
-// (3.0 GB): 424 us, 7.1 TB/s, 105% of the measured copy (which also writes). With fewer CTAs than
+// (3.0 GB): 412 us, 7.3 TB/s, 108% of the measured copy (which also writes). With fewer CTAs than
 // SMs' room a warp's own chain bounds a block of 32 tokens (1100 cycles for the keys, 1800 with the values,
-// at 2 warps per scheduler), and about 10 us of launch, first loads and merge come on
-// top: 1 x 40 x 8192, 47 MB, 17.9 us. 16 warps per SM are what 128 registers allow; the ring of 3 stages
+// at 2 warps per scheduler), and about 6 us of first loads and merge come on
+// top: 1 x 40 x 8192, 47 MB, 13.0 us. 16 warps per SM are what 128 registers allow; the ring of 3 stages
 // per warp keeps 147 KB in flight.
 //
 // The work is dealt in one of four ways (deal_of), by lengths that only the device knows:
@@ -48,8 +48,8 @@
 //            its stages in turn;
 //   shares   the chunks of all sequences, one after another, form one row of stages, of which each resident
 //            CTA takes an equal share, whose ends may lie inside chunks.
-// A chunk that slices or shares worked on leaves a partial from each, and a second kernel, launched as a
-// programmatic dependent, merges them in fp32.
+// A chunk that slices or shares worked on leaves a partial from each, and a second kernel merges them in
+// fp32. Each kernel begins while the one before it ends (16 x 8 (x 4) x 4097 tokens: 20.5 -> 18.0 us per call).
 
 #include <algorithm>
 #include <cfloat>
@@ -591,6 +591,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
         fence_mbar_init();
     }
     __syncthreads();
+    griddep_wait();  // the kernel before, which may have written what this one reads, is done
 
     // what is left of the share: kept in shared memory, out of the registers of the loop over blocks
     __shared__ Share sh;
@@ -974,7 +975,7 @@ cudaError_t launch(DecodeKv4Params &p, long long units, cudaStream_t stream)
     if (e == cudaSuccess && shares > 1) {
         MergeParams m = {p.part, p.head, p.out, p.lse, p.d, p.rows, p.chunks};
         e = launch_kernel(decode_kv4_merge_kernel<D>, dim3(static_cast<unsigned>(units), std::min(p.rows, kRows)), kMergeThreads, 0, stream,
-                          m, 1, true);
+                          m);
     }
     const cudaError_t f = cudaFreeAsync(ws, stream);
     return e != cudaSuccess ? e : f;

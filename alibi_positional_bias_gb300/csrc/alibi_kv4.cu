@@ -16,7 +16,9 @@
 // 6.3 TB/s, 86 and 93% of the measured copy). The write is bound by the logic pipe (66% busy, 73% of issue slots):
 // 12 operations per element, of which ordering the group's elements takes 2, the codes 4;
 // one thread per 8 elements with 16-bit stores of the values took 161 us for both. A step's new
-// token of 64 x 40 heads takes 4.6 us, a launch's time.
+// token of 64 x 40 heads takes 3.1 us, a launch's time. Every launch overlaps the end of the kernel before it (each kernel
+// waits for that before it touches memory): a call after another takes 3.1 and not 4.1 us, large ones written and read in
+// turn 59.1 and not 64.1 us.
 
 #include <algorithm>
 #include <cuda_bf16.h>
@@ -146,6 +148,8 @@ __device__ __forceinline__ RowItem row_item(const Kv4Params &p)
 template <int D>
 __global__ void __launch_bounds__(256) kv4_write_rows_kernel(const __grid_constant__ Kv4Params p)
 {
+    griddep_launch_dependents();
+    griddep_wait();
     const RowItem r = row_item<D>(p);
     const int b = r.bh / p.H, e = 8 * r.l;
     const int2 sp = span_of(p, b, r.in && r.t == 0 && threadIdx.x % (2 * (D / 8)) == 0 && r.bh == b * p.H);
@@ -174,6 +178,8 @@ __global__ void __launch_bounds__(256) kv4_write_rows_kernel(const __grid_consta
 template <int D, bool F32>
 __global__ void __launch_bounds__(256) kv4_read_rows_kernel(const __grid_constant__ Kv4Params p)
 {
+    griddep_launch_dependents();
+    griddep_wait();
     const RowItem r = row_item<D>(p);
     const int b = r.bh / p.H, e = 8 * r.l;
     const int2 sp = span_of(p, b, r.in && r.t == 0 && threadIdx.x % (2 * (D / 8)) == 0 && r.bh == b * p.H);
@@ -429,9 +435,6 @@ int check_sizes(int B, int H, int T, int C, int d)
 // Tokens per sequence from which a CTA takes a block and not single rows. (64 x 40 heads, d = 128, write / read in us: 8
 // tokens 10.4 / 8.7 as rows, 14.7 / 10.5 as blocks; 16 tokens 16.6 / 12.1 as rows, 14.6 / 10.5 as blocks.)
 constexpr int kBlockTokens = 16;
-// CTAs per SM from which a launch overlaps the kernel before it (4 x 32 heads x 2048 tokens written and read: 64.1 -> 59.1
-// us); for small launches the attribute costs the host more (1.5 us) than it gains.
-constexpr int kOverlapRounds = 16;
 
 template <int d>
 cudaError_t launch(Kv4Params &p, int op, cudaStream_t stream)
@@ -451,7 +454,7 @@ cudaError_t launch(Kv4Params &p, int op, cudaStream_t stream)
     return launch_kernel(op == 0   ? kv4_write_block_kernel<d>
                              : op == 1 ? kv4_read_block_kernel<d, false>
                                        : kv4_read_block_kernel<d, true>,
-                             dim3(static_cast<unsigned>(ctas)), 2 * kHalf, 0, stream, p, 1, ctas >= kOverlapRounds * num_sms());
+                             dim3(static_cast<unsigned>(ctas)), 2 * kHalf, 0, stream, p);
 }
 
 // op: 0 write, 1 read as bf16, 2 read as fp32

@@ -50,11 +50,11 @@ cudaMemPool_t decode_pool();     // library-owned stream-ordered pool of the cur
 bool encode_tmap_bf16_3d(CUtensorMap *map, const void *base, uint64_t dim0, uint64_t dim1, uint64_t dim2,
                          uint32_t box0, uint32_t box1, bool swizzle128 = true);
 
-// Launch in clusters of `cluster` CTAs. `overlapped`: with programmatic stream serialization, so that the grid may be
-// scheduled while the kernel before it drains; it executes griddepcontrol.wait in every thread before it touches memory.
+// Launch in clusters of `cluster` CTAs with programmatic stream serialization: the grid may be scheduled while the kernel
+// before it drains, and executes griddepcontrol.wait in every thread before it touches memory.
 template <class Params>
 cudaError_t launch_kernel(void (*kernel)(Params), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
-                          const Params &p, int cluster = 1, bool overlapped = false)
+                          const Params &p, int cluster = 1)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
@@ -62,17 +62,14 @@ cudaError_t launch_kernel(void (*kernel)(Params), dim3 grid, unsigned threads, s
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    if (cluster > 1) {
-        attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
-        attr[cfg.numAttrs].val.clusterDim.x = static_cast<unsigned>(cluster);
-        attr[cfg.numAttrs].val.clusterDim.y = 1;
-        attr[cfg.numAttrs++].val.clusterDim.z = 1;
-    }
-    if (overlapped) {
-        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
-    }
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 

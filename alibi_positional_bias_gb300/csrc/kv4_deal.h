@@ -113,40 +113,42 @@ struct ClusterFit {
     int two[kMostCluster + 1], one[kMostCluster + 1];
 };
 
-// The way with the least estimated time, in us. A CTA that has its SM to itself takes 0.113 for a stage (32 tokens of d =
-// 128), two that share one 0.15 to 0.2 each, the more the fuller the device; several rounds of whole chunks, and slices and
-// shares, which fill it, run as fast as memory goes, whole chunks with a tail of the last round. A launch takes 4.2, the merge of a
-// cluster 1.6 more, the partials and their merge kernel 4.1 (slices) or, with what a share pays to begin its next chunk, 8.8
-// (shares). Measured, in us, caches colder than L2, whole / clusters of / slices / shares:
-//   sequences x KV heads (x G) x tokens x d   1 x 32 x 2048 x 128        11.6 / 7.3 (8) 8.2 (5) 7.4 (4) / 9.5 / 9.7
-//                                             1 x 40 x 8192 x 128        33.2 / 13.9 (6) 17.6 (7) 16.3 (3) / 15.9 / 19.5
-//                                             1 x 8 (x 4) x 8192 x 128   32.6 / 7.7 (12) 8.9 (16) 8.7 (8) / 9.7 / 9.9
-//                                             1 x 8 (x 4) x 32768 x 128  95.9 / 13.8 (12) 16.2 (16) 17.7 (8) / 14.2 / 15.3
-//                                             1 x 4 (x 4) x 131071 x 128  349 / 28.9 (16) / 21.3 / 22.4
-//                                             4 x 8 (x 8) x 8192 x 128   38.2 / 13.4 (8) / 16.3 / 21.0
-//                                             2 x 40 x 8192 x 128        33.8 / 22.1 (3) 24.8 (2) / 25.6 / 27.5
-//                                             2 x 40 x 1024 x 128         7.9 / 8.1 (2) 8.4 (3) / 11.0 / 13.2
-//                                             4 x 40 x 4096 x 128        23.2 / 24.8 (2) /    - / 27.2
-//                                             16 x 8 (x 4) x 4097 x 128  21.5 / 18.9 (2) / 21.6 / 24.2
-//                                             8 x 8 (x 4) x 16384 x 128  55.3 / 27.7 (4) 38.8 (5) / 34.0 / 38.3
-//                                             8 x 8 (x 8) x 32768 x 128   113 / 51.1 (4) / 60.8 / 65.2
-//                                             9 x 37 x 16384 x 128        158 /    - /    - / 129
-//                                             16 x 40 x 4096 x 128       67.1 /    - /    - / 69.6
-//                                             64 x 40 x 8192 x 128        418 /    - /    - / 494
+// The way with the least estimated time, in us. A CTA that has its SM to itself takes 0.11 for a stage (32 tokens of d =
+// 128) of 8192 tokens, less of more, whose far values are skipped, and no less than memory gives it; two that share one take 0.15 to 0.2 each, the more the
+// fuller the device; several rounds of whole chunks, and slices and shares, which fill it, run as fast as memory goes, whole chunks
+// with a tail of the last round. A launch takes 3.4, the merge of a cluster 1.6 more, the partials and their merge kernel
+// 4.9 (slices) or, with what a share pays to begin its next chunk, 9.6 (shares). Measured, in us, launches in one
+// graph, caches colder than L2, whole / clusters of / slices / shares:
+//   sequences x KV heads (x G) x tokens x d   1 x 32 x 2048 x 128        10.5 / 6.5 (8) 7.6 (5) 6.6 (4) / 9.5 / 9.7
+//                                             1 x 40 x 8192 x 128        31.6 / 13.1 (6) 16.6 (7) 14.9 (3) / 16.0 / 19.2
+//                                             1 x 8 (x 4) x 8192 x 128   31.0 / 7.1 (12) 8.4 (16) 7.9 (8) / 9.5 / 9.7
+//                                             1 x 8 (x 4) x 32768 x 128  90.7 / 12.7 (12) 15.2 (16) 16.5 (8) / 14.1 / 15.2
+//                                             1 x 4 (x 4) x 131071 x 128  331 / 27.7 (16) / 21.6 / 22.5
+//                                             4 x 8 (x 8) x 8192 x 128   35.1 / 12.5 (8) / 16.5 / 20.6
+//                                             2 x 40 x 8192 x 128        31.7 / 20.6 (3) 23.1 (2) / 25.3 / 27.5
+//                                             2 x 40 x 1024 x 128         7.2 / 7.9 (2) 7.6 (3) / 10.6 / 13.1
+//                                             4 x 40 x 4096 x 128        21.0 / 23.9 (2) /    - / 27.4
+//                                             16 x 8 (x 4) x 4097 x 128  19.9 / 17.8 (2) / 21.3 / 23.7
+//                                             8 x 8 (x 4) x 16384 x 128  52.7 / 27.8 (4) 36.6 (5) / 33.8 / 37.8
+//                                             8 x 8 (x 8) x 32768 x 128   105 / 50.9 (4) / 61.0 / 65.8
+//                                             9 x 37 x 16384 x 128        153 /    - /    - / 130
+//                                             16 x 40 x 4096 x 128       64.8 /    - /    - / 68.8
+//                                             64 x 40 x 8192 x 128        412 /    - /    - / 494
 inline Plan deal_of(long long units, int stages, int ctas, const ClusterFit &fit)
 {
     if (stages <= kWarps) return {Deal::Whole, 1};
-    const double rounds = static_cast<double>(units) / ctas, last = rounds - std::ceil(rounds) + 1, alone = 0.113;
+    const double rounds = static_cast<double>(units) / ctas, last = rounds - std::ceil(rounds) + 1;
+    const double far = stages < 256 ? 0.11 : 0.08 + 0.03 * 256 / stages;
+    const auto alone = [&](double full) { return far > 0.25 * full ? far : 0.25 * full; };  // full: of the places for CTAs
     Plan best = {Deal::Whole, 1};
-    double cost = 4.2 + stages * (rounds <= 0.5 ? alone : rounds <= 1 ? 0.148 + 0.1 * (rounds - 0.5) : 0.195 * rounds + 0.09 * (1 - last));
+    double cost = 3.4 + stages * (rounds <= 0.5 ? alone(rounds) : rounds <= 1 ? 0.148 + 0.1 * (rounds - 0.5) : 0.195 * rounds + 0.09 * (1 - last));
     const auto consider = [&](Deal deal, int count, double c) {
         if (c < cost) cost = c, best = {deal, count};
     };
     for (int c = 2; c <= kMostCluster; ++c)
         if (units <= fit.two[c]) {
-            const double full = rounds * c;  // of the places for CTAs
-            const double shared = 0.17 + 0.06 * (full > 0.5 ? full - 0.5 : 0);
-            consider(Deal::Clusters, c, 5.8 + std::ceil(stages / static_cast<double>(c)) * (units <= fit.one[c] ? alone : shared));
+            const double full = rounds * c, shared = 0.17 + 0.06 * (full > 0.5 ? full - 0.5 : 0);
+            consider(Deal::Clusters, c, 5 + std::ceil(stages / static_cast<double>(c)) * (units <= fit.one[c] ? alone(full) : shared));
         }
     if (2 * units <= ctas) consider(Deal::Slices, 1, 8.3 + std::ceil(stages / std::floor(ctas / static_cast<double>(units))) * 0.2);
     consider(Deal::Shares, 1, 13 + stages * rounds * 0.21);
