@@ -263,6 +263,58 @@ def test_serving_steps_prompt_write_then_decode_in_a_graph(ab):
     ab.alibi_check_error()
 
 
+@pytest.mark.parametrize("B,Hkv,G,N,d,T", [(2, 6, 2, 300, 64, 1), (1, 2, 4, 30000, 128, 1), (64, 8, 1, 2000, 128, 20),
+                                           (1, 32, 1, 6000, 64, 3), (24, 7, 1, 40000, 32, 1)])
+def test_calls_one_after_another_wait_for_each_other(ab, B, Hkv, G, N, d, T):
+    # Every kernel begins while the one before it ends: write, decode, read back and torch's own kernels on the same
+    # rows, positions and outputs give the same bits with and without a wait between any two of them.
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(N)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    C, steps, D = -(-(N + 13 * T) // 32) * 32, 12, min(T, 16)
+    k, v, new = rand(B, Hkv, N, d), rand(B, Hkv, N, d), rand(steps, 3, B, Hkv, T, d)
+    q = rand(steps, B, Hkv * G, D, d)
+    results = []
+    for wait in (True, False):
+        sync = torch.cuda.synchronize if wait else lambda: None
+        cache = ab.alibi_kv4_cache(B, Hkv, C, d)
+        cache.fill_(0xFF)
+        ab.alibi_kv4_write(k, v, cache)
+        pos, lens = ints([N] * B), ints([N + T] * B)
+        row, kr, vr, qx = torch.empty_like(new[0, 0]), torch.empty_like(new[0, 0]), torch.empty_like(new[0, 0]), q[0].clone()
+        got = []
+        for i in range(steps):
+            row.copy_(new[i, 0])
+            sync()
+            ab.alibi_kv4_write(row, new[i, 1], cache, pos=pos)
+            sync()
+            qx.copy_(q[i])
+            sync()
+            out, lse = ab.alibi_attn_decode_kv4(qx, cache, lens=lens, L=C)
+            sync()
+            qx.zero_()
+            row.fill_(float("nan"))
+            sync()
+            ab.alibi_kv4_read(cache, kr, vr, pos=pos)
+            sync()
+            again = ab.alibi_attn_decode_kv4(q[i], cache, lens=lens, L=C)
+            sync()
+            ab.alibi_kv4_write(new[i, 2], kr, cache, pos=pos)  # over what the decode before it reads
+            sync()
+            got += [out, lse, again[0], again[1], kr.clone(), vr.clone()]
+            pos += T
+            lens += T
+            sync()
+        torch.cuda.synchronize()
+        got.append(cache)
+        results.append(got)
+    ab.alibi_check_error()
+    for i, (a, b) in enumerate(zip(*results)):
+        assert torch.equal(a, b), i
+    for out, again in zip(results[0][0:-1:6], results[0][2:-1:6]):
+        assert torch.equal(out, again)
+
+
 def test_drafted_tokens_equal_single_steps(ab):
     # four new tokens at once see what four single calls with growing lengths see
     q, k, v = case(16, 2, 2, 2, 4, 352, 128)
