@@ -24,7 +24,7 @@
 #include <cuda_bf16.h>
 
 #include "alibi.h"
-#include "kv4.h"
+#include "kv4_deal.h"
 #include "ptx.cuh"
 
 namespace alibi {
@@ -38,6 +38,7 @@ struct Kv4Params {
     uint32_t *status;
     int BH, H, T, blocks, d;  // blocks: C / 32
     int span;                 // blocks that T tokens can touch, from any row on
+    kv4::Divisor by_span, by_H, by_T;
 };
 
 // The rows of sequence b: first row and number, or 0 rows after recording a span
@@ -138,8 +139,8 @@ __device__ __forceinline__ RowItem row_item(const Kv4Params &p)
     const unsigned i = blockIdx.x * (kRowsPerCta / 2) + threadIdx.x / (2 * (D / 8));
     RowItem r;
     r.in = i < static_cast<unsigned>(p.BH) * static_cast<unsigned>(p.T);
-    r.bh = r.in ? static_cast<int>(i / static_cast<unsigned>(p.T)) : 0;
-    r.t = r.in ? static_cast<int>(i - static_cast<unsigned>(r.bh) * static_cast<unsigned>(p.T)) : 0;
+    r.bh = r.in ? p.by_T.of(static_cast<int>(i)) : 0;
+    r.t = r.in ? static_cast<int>(i) - r.bh * p.T : 0;
     r.side = threadIdx.x / (D / 8) % 2;
     r.l = threadIdx.x % (D / 8);
     return r;
@@ -151,7 +152,7 @@ __global__ void __launch_bounds__(256) kv4_write_rows_kernel(const __grid_consta
     griddep_launch_dependents();
     griddep_wait();
     const RowItem r = row_item<D>(p);
-    const int b = r.bh / p.H, e = 8 * r.l;
+    const int b = p.by_H.of(r.bh), e = 8 * r.l;
     const int2 sp = span_of(p, b, r.in && r.t == 0 && threadIdx.x % (2 * (D / 8)) == 0 && r.bh == b * p.H);
     const bool live = r.in && r.t < sp.y;
     uint4 w = make_uint4(0, 0, 0, 0);
@@ -181,7 +182,7 @@ __global__ void __launch_bounds__(256) kv4_read_rows_kernel(const __grid_constan
     griddep_launch_dependents();
     griddep_wait();
     const RowItem r = row_item<D>(p);
-    const int b = r.bh / p.H, e = 8 * r.l;
+    const int b = p.by_H.of(r.bh), e = 8 * r.l;
     const int2 sp = span_of(p, b, r.in && r.t == 0 && threadIdx.x % (2 * (D / 8)) == 0 && r.bh == b * p.H);
     if (!r.in || r.t >= sp.y || e >= p.d) return;
     const int tok = sp.x + r.t, row = tok % kv4::kBlock;
@@ -214,7 +215,7 @@ struct BlockItem {
 template <int D>
 __device__ __forceinline__ bool block_item(const Kv4Params &p, BlockItem &it)
 {
-    const int bh = blockIdx.x / p.span, i = blockIdx.x - bh * p.span, b = bh / p.H;
+    const int bh = p.by_span.of(blockIdx.x), i = blockIdx.x - bh * p.span, b = p.by_H.of(bh);
     const int2 sp = span_of(p, b, threadIdx.x == 0 && i == 0 && bh == b * p.H);
     const int block = sp.x / kv4::kBlock + i;
     it.first = block * kv4::kBlock - sp.x;
@@ -449,6 +450,7 @@ cudaError_t launch(Kv4Params &p, int op, cudaStream_t stream)
                                  dim3(static_cast<unsigned>((rows + kRowsPerCta - 1) / kRowsPerCta)), 256, 0, stream, p);
     }
     p.span = std::min(p.blocks, (p.T + 2 * kv4::kBlock - 2) / kv4::kBlock);
+    p.by_span = kv4::Divisor(p.span);
     const long long ctas = static_cast<long long>(p.BH) * p.span;
     if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
     return launch_kernel(op == 0   ? kv4_write_block_kernel<d>
@@ -482,6 +484,8 @@ Kv4Params params(const void *cache, const int *pos, const int *count, int B, int
     p.BH = B * H;
     p.H = H;
     p.T = T;
+    p.by_H = kv4::Divisor(H);
+    p.by_T = kv4::Divisor(T);
     p.blocks = C / kv4::kBlock;
     p.d = d;
     return p;
