@@ -53,13 +53,16 @@ __device__ __forceinline__ int2 span_of(const Kv4Params &p, int b, bool report)
     return make_int2(first, n);
 }
 
-// Two bf16 numbers in order of magnitude, each in 16 bits, a positive one before the negative one of its magnitude: the
-// sign, inverted, goes below the magnitude.
-__device__ __forceinline__ uint32_t order_keys(uint32_t w)
+// The largest element of each half of N words of two bf16 numbers, as keys in order of magnitude, a positive one before the
+// negative one of its magnitude: the magnitude, and below it the sign, inverted. As signed 16-bit numbers the largest
+// positive one comes first, as unsigned ones the largest negative one: one operation per word and sign.
+template <int N>
+__device__ __forceinline__ uint32_t top_keys(const uint32_t (&w)[N])
 {
-    uint32_t d;  // bits of 2 w where the mask has ones, of ~(w >> 15) elsewhere
-    asm("lop3.b32 %0, %1, %2, %3, 0xB1;" : "=r"(d) : "r"(w * 2u), "r"(w >> 15), "r"(0xfffefffeu));
-    return d;
+    uint32_t above = w[0], below = w[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) above = __vmaxs2(above, w[i]), below = __vmaxu2(below, w[i]);
+    return __vmaxu2(__vmaxs2(above, 0u) * 2u + 0x00010001u, (below & 0x7fff7fffu) * 2u);
 }
 
 // The larger of the two halves.
@@ -158,7 +161,7 @@ __global__ void __launch_bounds__(256) kv4_write_rows_kernel(const __grid_consta
     uint4 w = make_uint4(0, 0, 0, 0);
     if (live && e < p.d)
         w = *reinterpret_cast<const uint4 *>((r.side ? p.v : p.k) + ((static_cast<size_t>(r.bh) * p.T + r.t) * p.d + e) * 2);
-    uint32_t top = __vmaxu2(__vmaxu2(order_keys(w.x), order_keys(w.y)), __vmaxu2(order_keys(w.z), order_keys(w.w)));
+    uint32_t top = top_keys<4>({w.x, w.y, w.z, w.w});
     top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
     if (!live) return;
@@ -261,8 +264,7 @@ __device__ __forceinline__ void write_keys(const Kv4Params &p, const BlockItem &
     uint32_t code[NG], mine = 0;
 #pragma unroll
     for (int n = 0; n < NG; ++n) {
-        uint32_t top = __vmaxu2(__vmaxu2(order_keys(w[n].x), order_keys(w[n].y)),
-                                __vmaxu2(order_keys(w[n].z), order_keys(w[n].w)));
+        uint32_t top = top_keys<4>({w[n].x, w[n].y, w[n].z, w[n].w});
         top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
         if (c == n) mine = top;
@@ -307,8 +309,9 @@ __device__ __forceinline__ void write_values(const Kv4Params &p, const BlockItem
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const uint2 *x = w[m] + 2 * h;
-            uint32_t pair = fold(__vmaxu2(order_keys(x[0].x), order_keys(x[0].y))) |
-                            fold(__vmaxu2(order_keys(x[1].x), order_keys(x[1].y))) << 16;
+            // the first token in the low halves, the second one in the high halves
+            uint32_t pair = top_keys<4>({__byte_perm(x[0].x, x[1].x, 0x5410), __byte_perm(x[0].x, x[1].x, 0x7632),
+                                         __byte_perm(x[0].y, x[1].y, 0x5410), __byte_perm(x[0].y, x[1].y, 0x7632)});
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) pair = __vmaxu2(pair, __shfl_xor_sync(0xffffffffu, pair, off));
             if (v.g / 2 == 2 * m + h) mine = pair;
