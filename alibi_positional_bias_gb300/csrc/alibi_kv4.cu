@@ -37,8 +37,8 @@ struct Kv4Params {
     const int *pos, *count;
     uint32_t *status;
     int BH, H, T, blocks, d;  // blocks: C / 32
-    int span;                 // blocks that T tokens can touch, from any row on
-    kv4::Divisor by_span, by_H, by_T;
+    int run, runs;            // blocks of a CTA, and runs of so many that T tokens can touch from any row on
+    kv4::Divisor by_runs, by_H, by_T;
 };
 
 // The rows of sequence b: first row and number, or 0 rows after recording a span
@@ -215,17 +215,34 @@ struct BlockItem {
     uint8_t *blk;
 };
 
+// Blocks of a CTA: one of the larger head sizes, whose kernels are the faster without a loop.
 template <int D>
-__device__ __forceinline__ bool block_item(const Kv4Params &p, BlockItem &it)
+__device__ __forceinline__ int run_of(const Kv4Params &p)
 {
-    const int bh = p.by_span.of(blockIdx.x), i = blockIdx.x - bh * p.span, b = p.by_H.of(bh);
+    return D < 64 ? p.run : 1;
+}
+
+// The first block of this CTA's run.
+template <int D>
+__device__ __forceinline__ BlockItem first_block(const Kv4Params &p)
+{
+    const int bh = p.by_runs.of(blockIdx.x), i = blockIdx.x - bh * p.runs, b = p.by_H.of(bh);
     const int2 sp = span_of(p, b, threadIdx.x == 0 && i == 0 && bh == b * p.H);
-    const int block = sp.x / kv4::kBlock + i;
+    const int block = sp.x / kv4::kBlock + i * run_of<D>(p);
+    BlockItem it;
     it.first = block * kv4::kBlock - sp.x;
     it.n = sp.y;
     it.row0 = static_cast<size_t>(bh) * p.T + it.first;
     it.blk = p.cache + (static_cast<size_t>(bh) * p.blocks + block) * kv4::block_bytes(D);
-    return it.first < it.n;  // the block has tokens of the call (it is inside the cache then)
+    return it;
+}
+
+template <int D>
+__device__ __forceinline__ void next_block(BlockItem &it)
+{
+    it.first += kv4::kBlock;
+    it.row0 += kv4::kBlock;
+    it.blk += kv4::block_bytes(D);
 }
 
 // ALL: every row of the block is a token of the call.
@@ -349,25 +366,24 @@ __global__ void __launch_bounds__(2 * kHalf, kWriteCtas) kv4_write_block_kernel(
 {
     griddep_launch_dependents();
     griddep_wait();
-    BlockItem it;
-    if (!block_item<kv4::padded(d)>(p, it)) return;
-    const bool all = it.first >= 0 && it.first + kv4::kBlock <= it.n;
-    const int i = threadIdx.x % kHalf;
-    if (threadIdx.x < kHalf)
-        all ? write_keys<d, true>(p, it, i) : write_keys<d, false>(p, it, i);
-    else
-        all ? write_values<d, true>(p, it, i) : write_values<d, false>(p, it, i);
+    constexpr int D = kv4::padded(d);
+    BlockItem it = first_block<D>(p);
+#pragma unroll 1
+    for (int k = 0; k < run_of<D>(p); ++k, next_block<D>(it)) {
+        if (it.first >= it.n) return;  // no tokens of the call here (others are inside the cache)
+        const bool all = it.first >= 0 && it.first + kv4::kBlock <= it.n;
+        const int i = threadIdx.x % kHalf;
+        if (threadIdx.x < kHalf)
+            all ? write_keys<d, true>(p, it, i) : write_keys<d, false>(p, it, i);
+        else
+            all ? write_values<d, true>(p, it, i) : write_values<d, false>(p, it, i);
+    }
 }
 
 template <int d, bool F32>
-__global__ void __launch_bounds__(2 * kHalf, kReadCtas) kv4_read_block_kernel(const __grid_constant__ Kv4Params p)
+__device__ __forceinline__ void read_block(const Kv4Params &p, const BlockItem &it, int i)
 {
     constexpr int D = kv4::padded(d), NG = D / 32, kSize = F32 ? 4 : 2;
-    griddep_launch_dependents();
-    griddep_wait();
-    BlockItem it;
-    if (!block_item<D>(p, it)) return;
-    const int i = threadIdx.x % kHalf;
     if (threadIdx.x < kHalf) {
         const int row = i / 4, c = i % 4;
         if (!live<false>(it, row) || (d < 32 && 8 * c >= d)) return;
@@ -424,6 +440,20 @@ __global__ void __launch_bounds__(2 * kHalf, kReadCtas) kv4_read_block_kernel(co
     }
 }
 
+template <int d, bool F32>
+__global__ void __launch_bounds__(2 * kHalf, kReadCtas) kv4_read_block_kernel(const __grid_constant__ Kv4Params p)
+{
+    griddep_launch_dependents();
+    griddep_wait();
+    constexpr int D = kv4::padded(d);
+    BlockItem it = first_block<D>(p);
+#pragma unroll 1
+    for (int k = 0; k < run_of<D>(p); ++k, next_block<D>(it)) {
+        if (it.first >= it.n) return;
+        read_block<d, F32>(p, it, threadIdx.x % kHalf);
+    }
+}
+
 bool aligned(const void *p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 int check_sizes(int B, int H, int T, int C, int d)
@@ -439,6 +469,10 @@ int check_sizes(int B, int H, int T, int C, int d)
 // Tokens per sequence from which a CTA takes a block and not single rows. (64 x 40 heads, d = 128, write / read in us: 8
 // tokens 10.4 / 8.7 as rows, 14.7 / 10.5 as blocks; 16 tokens 16.6 / 12.1 as rows, 14.6 / 10.5 as blocks.)
 constexpr int kBlockTokens = 16;
+// Blocks of a head that a CTA takes one after another where there are more than a CTA each that is resident: of d = 32 (and
+// 16), where beginning a CTA costs as much as a block, 4 (8 x 32 x 8192 tokens written and read in 68 and 64 us, with one
+// each in 82 and 77); of d = 64 one (8 x 32 x 4096 tokens written in 59.6 us, with two in 61.8).
+constexpr int kRun = 4;
 
 template <int d>
 cudaError_t launch(Kv4Params &p, int op, cudaStream_t stream)
@@ -452,9 +486,12 @@ cudaError_t launch(Kv4Params &p, int op, cudaStream_t stream)
                                            : kv4_read_rows_kernel<D, true>,
                                  dim3(static_cast<unsigned>((rows + kRowsPerCta - 1) / kRowsPerCta)), 256, 0, stream, p);
     }
-    p.span = std::min(p.blocks, (p.T + 2 * kv4::kBlock - 2) / kv4::kBlock);
-    p.by_span = kv4::Divisor(p.span);
-    const long long ctas = static_cast<long long>(p.BH) * p.span;
+    const int blocks = std::min(p.blocks, (p.T + 2 * kv4::kBlock - 2) / kv4::kBlock);
+    const bool full = static_cast<long long>(p.BH) * blocks > kWriteCtas * num_sms();
+    p.run = D < 64 && full ? kRun : 1;
+    p.runs = (blocks + p.run - 1) / p.run;
+    p.by_runs = kv4::Divisor(p.runs);
+    const long long ctas = static_cast<long long>(p.BH) * p.runs;
     if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
     return launch_kernel(op == 0   ? kv4_write_block_kernel<d>
                              : op == 1 ? kv4_read_block_kernel<d, false>

@@ -84,6 +84,33 @@ def test_write_and_read(ab, d, B, H, T, C, pos, count):
     check_read(ab, dev, kf, vf, pos, count)
 
 
+@pytest.mark.parametrize("d", [16, 32])
+@pytest.mark.parametrize("T,start", [(1000, 0), (1000, 31), (97, 64), (16, 120), (33, 1)])
+def test_runs_of_blocks_equal_single_ones(ab, d, T, start):
+    # many heads, so that a CTA takes a run of blocks, against the same rows of few heads, a block each
+    import torch
+    B, H, C = 40, 60, 1056
+    k = torch.randn(B, H, T, d, device="cuda", dtype=torch.bfloat16)
+    v = torch.randn(B, H, T, d, device="cuda", dtype=torch.bfloat16)
+    pos = ints([start + (3 * b if start + 3 * (B - 1) + T <= C else b % 2) for b in range(B)])
+    count = ints([T - b % 7 for b in range(B)])
+    cache = ab.alibi_kv4_cache(B, H, C, d)
+    cache.fill_(0xA5)
+    ab.alibi_kv4_write(k, v, cache, pos=pos, count=count)
+    kr, vr = torch.full_like(k, 7.0), torch.full_like(v, 7.0)
+    ab.alibi_kv4_read(cache, kr, vr, pos=pos, count=count)
+    for b, h in ((0, 0), (1, 59), (17, 30), (39, 59), (6, 1)):
+        one = ab.alibi_kv4_cache(1, 1, C, d)
+        one.fill_(0xA5)
+        rows = [x[b:b + 1, h:h + 1].contiguous() for x in (k, v)]
+        ab.alibi_kv4_write(*rows, one, pos=pos[b:b + 1].clone(), count=count[b:b + 1].clone())
+        assert torch.equal(one, cache[b:b + 1, h:h + 1])
+        got = [torch.full_like(x, 7.0) for x in rows]
+        ab.alibi_kv4_read(one, *got, pos=pos[b:b + 1].clone(), count=count[b:b + 1].clone())
+        assert torch.equal(got[0], kr[b:b + 1, h:h + 1]) and torch.equal(got[1], vr[b:b + 1, h:h + 1])
+    ab.alibi_check_error()
+
+
 def test_appending_tokens_equals_writing_them_at_once(ab):
     import torch
     rng = np.random.default_rng(3)
