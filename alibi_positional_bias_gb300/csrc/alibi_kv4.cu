@@ -11,14 +11,14 @@
 //
 // What has to move: 4 d bytes of a token's key and value and 1.125 d of the cache. Prompts
 // go a block per CTA, the cache in whole 16-byte words of a thread, the rows in 64-byte
-// segments, no shared memory. Written and read, d = 128: 4 x 32 heads x 2048 tokens 33.1 and
-// 29.7 us (172 MB each: 5.2 and 5.8 TB/s), 8 x 32 x 2048 59.2 and 54.6 us (5.8 and
-// 6.3 TB/s, 86 and 93% of the measured copy). The write is bound by the logic pipe (66% busy, 73% of issue slots):
-// 12 operations per element, of which ordering the group's elements takes 2, the codes 4;
+// segments, no shared memory. Written and read, d = 128: 4 x 32 heads x 2048 tokens 31.1 and
+// 29.6 us (172 MB each: 5.5 and 5.8 TB/s), 8 x 32 x 2048 56.2 and 54.2 us (6.1 and
+// 6.3 TB/s, 90 and 93% of the measured copy). The write is bound by memory's latency and the logic pipe (59% busy, 68% of
+// issue slots): 10 operations per element, of which the group's largest takes 1, the codes 4;
 // one thread per 8 elements with 16-bit stores of the values took 161 us for both. A step's new
 // token of 64 x 40 heads takes 3.1 us, a launch's time. Every launch overlaps the end of the kernel before it (each kernel
 // waits for that before it touches memory): a call after another takes 3.1 and not 4.1 us, large ones written and read in
-// turn 59.1 and not 64.1 us.
+// turn 52.9 and not 58 us.
 
 #include <algorithm>
 #include <cuda_bf16.h>
@@ -466,9 +466,10 @@ int check_sizes(int B, int H, int T, int C, int d)
     return ALIBI_OK;
 }
 
-// Tokens per sequence from which a CTA takes a block and not single rows. (64 x 40 heads, d = 128, write / read in us: 8
-// tokens 10.4 / 8.7 as rows, 14.7 / 10.5 as blocks; 16 tokens 16.6 / 12.1 as rows, 14.6 / 10.5 as blocks.)
-constexpr int kBlockTokens = 16;
+// Tokens per sequence from which a CTA takes a block and not single rows. (In us, rows / blocks: 64 x 40 heads of d = 128, 8
+// tokens written 5.9 / 11.2, read 5.8 / 6.7; 12 tokens 8.4 / 11.8 and 8.1 / 7.3; 16 tokens 10.8 / 12.5 and 10.3 / 8.0; 24 tokens 15.6 /
+// 13.6 and 14.8 / 9.3. 64 x 8 heads of d = 64: 16 tokens 2.7 / 3.1 and 2.7 / 2.3, 24 tokens 3.2 / 3.1 and 3.1 / 2.4.)
+constexpr int kWriteBlocks = 20, kReadBlocks = 10;
 // Blocks of a head that a CTA takes one after another where there are more than a CTA each that is resident: of d = 32 (and
 // 16), where beginning a CTA costs as much as a block, 4 (8 x 32 x 8192 tokens written and read in 68 and 64 us, with one
 // each in 82 and 77); of d = 64 one (8 x 32 x 4096 tokens written in 59.6 us, with two in 61.8).
@@ -479,7 +480,7 @@ cudaError_t launch(Kv4Params &p, int op, cudaStream_t stream)
 {
     constexpr int D = kv4::padded(d);
     const long long rows = static_cast<long long>(p.BH) * p.T;
-    if (p.T < kBlockTokens && rows < (1LL << 31)) {
+    if (p.T < (op == 0 ? kWriteBlocks : kReadBlocks) && rows < (1LL << 31)) {
         constexpr int kRowsPerCta = 256 / (D / 8) / 2;
         return launch_kernel(op == 0   ? kv4_write_rows_kernel<D>
                                  : op == 1 ? kv4_read_rows_kernel<D, false>
