@@ -566,7 +566,8 @@ def alibi_attn_decode_kv4(q, cache, lens=None, L=None, out=None, lse=None, slope
         given += [(lse, "lse", float32, getattr(q, "shape", (0,))[:-1])] if lse is not None else []
         _explain_kv4(bfloat16, (q, "q", (3, 4)), given, cache, None, [(lens, "lens")])
     if out is None:
-        out = torch.empty_like(q) if stream is None else _empty_on(stream, index, shape, bfloat16)
+        out = (torch.empty(shape, dtype=bfloat16, device=q.device) if stream is None
+               else _empty_on(stream, index, shape, bfloat16))
     if lse is None:
         lse = (torch.empty(shape[:-1], dtype=float32, device=q.device) if stream is None
                else _empty_on(stream, index, shape[:-1], float32))
