@@ -958,7 +958,8 @@ cudaError_t launch(DecodeKv4Params &p, long long units, cudaStream_t stream)
         if (units * plan.count > 0x7fffffffLL) return cudaErrorInvalidValue;
         if (plan.count == 1) e = prepare_kernel(reinterpret_cast<const void *>(whole), kSmem, 0);
         if (e != cudaSuccess) return e;
-        return launch_kernel(plan.count > 1 ? clusters : whole, dim3(static_cast<unsigned>(units * plan.count)), kWarps * 32, kSmem, stream, p, plan.count);
+        return launch_kernel(plan.count > 1 ? clusters : whole, dim3(static_cast<unsigned>(units * plan.count)),
+                             kWarps * 32, kSmem, stream, p, plan.count);
     }
     e = prepare_kernel(reinterpret_cast<const void *>(shared), kSmem, 0);
     if (e != cudaSuccess) return e;
@@ -974,8 +975,8 @@ cudaError_t launch(DecodeKv4Params &p, long long units, cudaStream_t stream)
     e = launch_kernel(shared, dim3(static_cast<unsigned>(shares)), kWarps * 32, kSmem, stream, p);
     if (e == cudaSuccess && shares > 1) {
         MergeParams m = {p.part, p.head, p.out, p.lse, p.d, p.rows, p.chunks};
-        e = launch_kernel(decode_kv4_merge_kernel<D>, dim3(static_cast<unsigned>(units), std::min(p.rows, kRows)), kMergeThreads, 0, stream,
-                          m);
+        e = launch_kernel(decode_kv4_merge_kernel<D>, dim3(static_cast<unsigned>(units), std::min(p.rows, kRows)),
+                          kMergeThreads, 0, stream, m);
     }
     const cudaError_t f = cudaFreeAsync(ws, stream);
     return e != cudaSuccess ? e : f;

@@ -86,8 +86,8 @@ __device__ __forceinline__ Scale scale_of(uint32_t key)
 }
 
 // min(15, floor(x / s + 8.5)) in the low bits, `inverse` being 1 / (16 s). The sum of a sixteenth, clamped to [0, 1], is off by
-// 2^-23 at most; 2^-12 (in units of a code) stands against that and keeps ties above their integer, and the product with 16 (1 - 2^-22), added
-// to 2^23 and rounded down, leaves the floor in the low bits, 15 for the clamped ones. Both are fma, on the pipe
+// 2^-23 at most; 2^-12 (in units of a code) stands against that and keeps ties above their integer, and the product with
+// 16 (1 - 2^-22), added to 2^23 and rounded down, leaves the floor in the low bits, 15 for the clamped ones. Both are fma, on the pipe
 // that has room: minimum, and, or, shift and permute share the other one, which bounds the kernel.
 __device__ __forceinline__ uint32_t code_of(float x, float inverse)
 {
@@ -466,9 +466,10 @@ int check_sizes(int B, int H, int T, int C, int d)
     return ALIBI_OK;
 }
 
-// Tokens per sequence from which a CTA takes a block and not single rows. (In us, rows / blocks: 64 x 40 heads of d = 128, 8
-// tokens written 5.9 / 11.2, read 5.8 / 6.7; 12 tokens 8.4 / 11.8 and 8.1 / 7.3; 16 tokens 10.8 / 12.5 and 10.3 / 8.0; 24 tokens 15.6 /
-// 13.6 and 14.8 / 9.3. 64 x 8 heads of d = 64: 16 tokens 2.7 / 3.1 and 2.7 / 2.3, 24 tokens 3.2 / 3.1 and 3.1 / 2.4.)
+// Tokens per sequence from which a CTA takes a block and not single rows. (In us, rows / blocks: 64 x 40 heads of d = 128,
+// 8 tokens written 5.9 / 11.2, read 5.8 / 6.7; 12 tokens 8.4 / 11.8 and 8.1 / 7.3; 16 tokens 10.8 / 12.5 and 10.3 / 8.0;
+// 24 tokens 15.6 / 13.6 and 14.8 / 9.3. 64 x 8 heads of d = 64: 16 tokens 2.7 / 3.1 and 2.7 / 2.3, 24 tokens 3.2 / 3.1 and
+// 3.1 / 2.4.)
 constexpr int kWriteBlocks = 20, kReadBlocks = 10;
 // Blocks of a head that a CTA takes one after another where there are more than a CTA each that is resident: of d = 32 (and
 // 16), where beginning a CTA costs as much as a block, 4 (8 x 32 x 8192 tokens written and read in 68 and 64 us, with one

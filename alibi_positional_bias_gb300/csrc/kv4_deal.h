@@ -114,11 +114,11 @@ struct ClusterFit {
 };
 
 // The way with the least estimated time, in us. A CTA that has its SM to itself takes 0.11 for a stage (32 tokens of d =
-// 128) of 8192 tokens, less of more, whose far values are skipped, and no less than memory gives it; two that share one take 0.15 to 0.2 each, the more the
-// fuller the device; several rounds of whole chunks, and slices and shares, which fill it, run as fast as memory goes, whole chunks
-// with a tail of the last round. A launch takes 3.4, the merge of a cluster 1.6 more, the partials and their merge kernel
-// 4.9 (slices) or, with what a share pays to begin its next chunk, 9.6 (shares). Measured, in us, launches in one
-// graph, caches colder than L2, whole / clusters of / slices / shares:
+// 128) of up to 8192 tokens, less of more, whose far values are skipped, and no less than memory gives it; two that share
+// one take 0.15 to 0.2 each, the more the fuller the device; several rounds of whole chunks, and slices and shares, which
+// fill it, run as fast as memory goes, whole chunks with a tail of the last round. A launch takes 3.4, the merge of a
+// cluster 1.6 more, the partials and their merge kernel 4.9 (slices) or, with what a share pays to begin its next chunk,
+// 9.6 (shares). Measured, in us, launches in one graph, caches colder than L2, whole / clusters of / slices / shares:
 //   sequences x KV heads (x G) x tokens x d   1 x 32 x 2048 x 128        10.5 / 6.5 (8) 7.6 (5) 6.6 (4) / 9.5 / 9.7
 //                                             1 x 40 x 8192 x 128        31.6 / 13.1 (6) 16.6 (7) 14.9 (3) / 16.0 / 19.2
 //                                             1 x 8 (x 4) x 8192 x 128   31.0 / 7.1 (12) 8.4 (16) 7.9 (8) / 9.5 / 9.7
@@ -141,16 +141,20 @@ inline Plan deal_of(long long units, int stages, int ctas, const ClusterFit &fit
     const double far = stages < 256 ? 0.11 : 0.08 + 0.03 * 256 / stages;
     const auto alone = [&](double full) { return far > 0.25 * full ? far : 0.25 * full; };  // full: of the places for CTAs
     Plan best = {Deal::Whole, 1};
-    double cost = 3.4 + stages * (rounds <= 0.5 ? alone(rounds) : rounds <= 1 ? 0.148 + 0.1 * (rounds - 0.5) : 0.195 * rounds + 0.09 * (1 - last));
+    double cost = 3.4 + stages * (rounds <= 0.5 ? alone(rounds)
+                                  : rounds <= 1 ? 0.148 + 0.1 * (rounds - 0.5)
+                                                : 0.195 * rounds + 0.09 * (1 - last));
     const auto consider = [&](Deal deal, int count, double c) {
         if (c < cost) cost = c, best = {deal, count};
     };
     for (int c = 2; c <= kMostCluster; ++c)
         if (units <= fit.two[c]) {
             const double full = rounds * c, shared = 0.17 + 0.06 * (full > 0.5 ? full - 0.5 : 0);
-            consider(Deal::Clusters, c, 5 + std::ceil(stages / static_cast<double>(c)) * (units <= fit.one[c] ? alone(full) : shared));
+            const double longest = std::ceil(stages / static_cast<double>(c));
+            consider(Deal::Clusters, c, 5 + longest * (units <= fit.one[c] ? alone(full) : shared));
         }
-    if (2 * units <= ctas) consider(Deal::Slices, 1, 8.3 + std::ceil(stages / std::floor(ctas / static_cast<double>(units))) * 0.2);
+    if (2 * units <= ctas)
+        consider(Deal::Slices, 1, 8.3 + std::ceil(stages / std::floor(ctas / static_cast<double>(units))) * 0.2);
     consider(Deal::Shares, 1, 13 + stages * rounds * 0.21);
     return best;
 }
