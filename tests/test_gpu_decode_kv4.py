@@ -377,6 +377,46 @@ def test_two_streams_and_two_graphs_at_once(ab):
     ab.alibi_check_error()
 
 
+def test_calls_from_several_host_threads(ab):
+    # the library's calls release the interpreter's lock: four threads, each on a stream of its own, give what one gives
+    import threading
+
+    import torch
+    jobs, failed = [], []
+    for i, (B, Hkv, G, N, d) in enumerate([(1, 2, 2, 20000, 128), (1, 32, 1, 3000, 64), (3, 4, 8, 100, 32), (2, 40, 1, 5000, 128)]):
+        g = torch.Generator(device="cuda").manual_seed(i)
+        k, v = (torch.randn(B, Hkv, N, d, generator=g, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+        q = torch.randn(B, Hkv * G, 1, d, generator=g, device="cuda", dtype=torch.bfloat16)
+        cache = ab.alibi_kv4_cache(B, Hkv, -(-N // 32) * 32, d)
+        ab.alibi_kv4_write(k, v, cache)
+        jobs.append((k, v, q, cache, ab.alibi_attn_decode_kv4(q, cache, L=N)))
+    torch.cuda.synchronize()
+
+    def work(k, v, q, cache, want):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                for _ in range(20):
+                    mine = torch.full_like(cache, 0xFF)
+                    ab.alibi_kv4_write(k, v, mine)
+                    out, lse = ab.alibi_attn_decode_kv4(q, mine, L=k.shape[2])
+                    kr, vr = ab.alibi_kv4_read(mine, torch.empty_like(k), torch.empty_like(v))
+                    k2, v2 = ab.alibi_kv4_read(cache, torch.empty_like(k), torch.empty_like(v))
+                    stream.synchronize()
+                    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+                    assert torch.equal(kr, k2) and torch.equal(vr, v2)
+        except BaseException as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=job) for job in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+    ab.alibi_check_error()
+
+
 @pytest.mark.parametrize("handle", [False, True])
 def test_outputs_made_for_another_stream_belong_to_it(ab, handle):
     # Memory that the current stream has just let go of may still be in use there, so a call on another stream must
