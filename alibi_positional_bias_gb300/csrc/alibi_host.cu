@@ -246,10 +246,16 @@ cudaMemPool_t decode_pool()
         props.location.type = cudaMemLocationTypeDevice;
         props.location.id = dev;
         cudaMemPool_t pool = nullptr;
-        if (cudaMemPoolCreate(&pool, &props) != cudaSuccess) return nullptr;
+        // The first call may be one that is captured into a graph, and making a pool or setting its attributes would end
+        // the capture in a thread of the default mode.
+        cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+        if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return nullptr;
+        const cudaError_t e = cudaMemPoolCreate(&pool, &props);
         // keep freed blocks in this pool: the partials buffer is reused call after call
         uint64_t keep = UINT64_MAX;
-        cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep);
+        if (e == cudaSuccess) cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep);
+        cudaThreadExchangeStreamCaptureMode(&mode);
+        if (e != cudaSuccess) return nullptr;
         g_pool[dev] = pool;
     }
     return g_pool[dev];

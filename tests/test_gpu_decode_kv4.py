@@ -472,6 +472,39 @@ def test_graph_of_every_way_follows_lengths_on_the_device(ab, B, Hkv, G, N, d):
     ab.alibi_check_error()
 
 
+FIRST_CALL = """
+import torch
+import alibi_positional_bias_gb300 as ab
+B, H, N, d = {0}
+k = torch.randn(B, H, N, d, device="cuda", dtype=torch.bfloat16)
+v, q = torch.randn_like(k), torch.randn(B, H, 1, d, device="cuda", dtype=torch.bfloat16)
+cache = torch.full((B, H, -(-N // 32), 36 * max(d, 32)), 255, dtype=torch.uint8, device="cuda")
+kr, vr = torch.empty_like(k), torch.empty_like(v)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    ab.alibi_kv4_write(k, v, cache)
+    out, lse = ab.alibi_attn_decode_kv4(q, cache, L=N)
+    ab.alibi_kv4_read(cache, kr, vr)
+graph.replay()
+want, wl = ab.alibi_attn_decode_kv4(q, cache, L=N)
+torch.cuda.synchronize()
+assert torch.equal(out, want) and torch.equal(lse, wl) and bool(torch.isfinite(out).all())
+ab.alibi_check_error()
+"""
+
+
+@pytest.mark.parametrize("shape", [(1, 6, 100, 64), (1, 32, 3000, 128), (1, 2, 60000, 128), (24, 7, 40000, 32)])
+def test_first_calls_of_a_process_in_a_graph(shape):
+    # whole chunks, clusters, slices and shares, captured before the library has made any call on the device
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL.format(shape)], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
 def test_every_way_with_a_nan_far_back(ab):
     # a NaN value whose weight has long vanished still reaches its group, as 0 x NaN does in the bf16 decode; NaN rows past
     # the length do not
