@@ -20,16 +20,18 @@
 //            bits of the sum: errors of 2^-17 of 8 |s| were measured. Keys as 1024 + 16 u, with the
 //            offset in the sum's start, save two operations in nine, but the start takes registers
 //            that the loop does not have: 426 -> 440 us at 64 x 40 heads of 8192 tokens.)
-//   softmax  in base 2: p_j = 2^(x_j - R), summed in fp32, with a reference R of each row that is
-//            raised when some x_j exceeds it by 8.
-//   values   O^T += (U - 8)^T P^T per group, P_jn = p_j s_jn as fp16, taken as
-//            2^(x_j + e_j - M) (s_jn 2^-e_j), with
-//            2^(e_j - 1) <= max_n |s_jn| < 2^e_j and a second reference M for x_j + e_j, so
-//            it neither overflows nor vanishes whatever the magnitude of the values. Its
-//            rounding to 11 bits is the only one below fp32: off by at most 2^-11 of each
-//            product, a quarter of the bf16 output's own step. (bf16 weights would be off by as
-//            much as the output itself.) A block whose P all round to zero adds nothing and its
-//            values are not multiplied.
+//   softmax  in base 2: p_j = 2^(x_j - R), summed in fp32, with a reference R of each row, its first block's largest
+//            x_j (so that a row that sees one token has its value exactly), which is raised by a whole number when some
+//            x_j exceeds it by 8. A weight below 2^-126 of the row's largest counts as zero.
+//   values   O^T += (U - 8)^T P^T per group, P_jn = p_j s_jn F_n as fp16, with a power of two F_n of each row
+//            and group that puts the largest |p_j s_jn| so far at 2^7 or more and is lowered when one leaves
+//            fp16's range then: a group's products are held relative to the largest of that group, however large
+//            or small the other groups' values are (with one reference for all groups, those of 2^-32 of the
+//            largest vanished). The rounding of P is the only one below fp32: off by at most 2^-11 of a product,
+//            a quarter of the bf16 output's own step, or, below fp16's normal numbers, by 2^-32 of the
+//            group's largest product. (bf16 weights would be off by as much as the output itself.) F_n is a
+//            bf16 number, so that it multiplies two scales at once, exactly. A block whose P all round to zero adds
+//            nothing and its values are not multiplied.
 //
 // mma.sync and not tcgen05.mma: the operands are made in registers, where tcgen05 would have to be
 // fed through shared or tensor memory, and at 8 columns the tensor pipe is 19% busy.
@@ -57,6 +59,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <mutex>
+#include <type_traits>
 
 #include "alibi.h"
 #include "kv4_deal.h"
@@ -72,6 +75,7 @@ constexpr int kStageBytes = 4608;   // 128 / D blocks of 36 D bytes
 constexpr int kRows = 8;            // query rows of a chunk, at most (the columns of an mma)
 constexpr int kMergeThreads = 256;
 constexpr int kSmem = kWarps * kStages * kStageBytes;
+constexpr uint32_t kMostF = 253;    // exponent field of a value factor F_n, at most: 1 / F_n is a normal number too
 
 struct HeadSlopes {
     float log2e[kMaxHeads];
@@ -160,6 +164,25 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+// Products of two bf16 pairs, rounded to bf16 (exact where one is a power of two and the product is in range).
+__device__ __forceinline__ uint32_t bmul2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// The largest of |a|, |b| and |c|, NaN if one is.
+__device__ __forceinline__ float max_abs3(float a, float b, float c)
+{
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// 2^n for n <= 127, 0 below the normal numbers.
+__device__ __forceinline__ float pow2(int n) { return n < -126 ? 0.0f : __uint_as_float(static_cast<uint32_t>(n + 127) << 23); }
+
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
@@ -220,7 +243,8 @@ struct State {
     float kappa[KC];        // from s acc to base-2 logits
     float slope[KC];        // m log2(e)
     float pos[KC];          // position less lane / 4
-    float R[KC], M[KC], l[KC];
+    float R[KC], l[KC];
+    uint32_t F[KC][NG > 1 ? NG / 2 : 1];  // bf16 pairs, as the value scales lie (D = 32: in the high half)
     float acc[NG][2][4];    // elements 32 n + 4 g + (0, 2) in [0], + (1, 3) in [1]; columns 2c, 2c + 1
 };
 
@@ -273,92 +297,110 @@ __device__ __forceinline__ void block32(State<D, KC> &st, const uint8_t *blk, in
         }
     }
 
-    // e_j from the largest exponent of the value scales. A NaN scale counts as 2^129 here, which either sends the
-    // warp to the slow path, where it is left out, or is below M anyway.
-    float e[4];
-    uint32_t big[4];
+    const auto seen = [&](int i, int k) { return !MASK || !(jf + 8.0f * i > st.pos[k]); };
+    // scale of group n of token i: the word it lies in, and itself from that word (or the word's multiple)
+    const auto scales = [&](int i, int n) { return sv[i][NG == 1 ? 0 : NG / 2 + n / 2]; };
+    const auto scale = [](uint32_t word, int n) { return NG == 1 || (n & 1) ? bf16_hi(word) : bf16_lo(word); };
+    // p_j and P_jn; of a token that the row does not see zero, whatever its scale. Two rows' P are packed at once, which
+    // holds them in half the registers.
+    using Product = std::conditional_t<KC == 1, float, uint32_t>;
+    const auto product = [](const float (&f)[KC]) -> Product {
+        if constexpr (KC == 1)
+            return f[0];
+        else
+            return pack_f16x2(f[0], f[1]);
+    };
+    float p[4][KC], top = -INFINITY, most = 0.0f;
+    Product pr[4][NG];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        uint32_t m;
-        if constexpr (NG == 1)
-            m = sv[i][0] >> 16 & 0x7fffu;
-        else if constexpr (NG == 2)
-            m = max(sv[i][1] & 0x7fffu, sv[i][1] >> 16 & 0x7fffu);
-        else {
-            m = __vmaxu2(sv[i][2] & 0x7fff7fffu, sv[i][3] & 0x7fff7fffu);
-            m = max(m & 0xffffu, m >> 16);
-        }
-        big[i] = m >> 7;
-        e[i] = __uint_as_float(0x4b000000u | big[i]) - (8388608.0f + 126.0f);
-    }
-    float a[4][KC], b[4][KC], top = -INFINITY, topb = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int k = 0; k < KC; ++k) {
-            a[i][k] = x[i][k] - st.R[k];
-            b[i][k] = x[i][k] + e[i] - st.M[k];
-            top = fmaxf(top, a[i][k]);
-            topb = fmaxf(topb, b[i][k]);
+            const float a = x[i][k] - st.R[k];
+            top = fmaxf(top, a);
+            p[i][k] = ex2_approx(a);
         }
-    if (__any_sync(0xffffffffu, fmaxf(top, topb) > 8.0f)) {
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+            float f[KC];
+#pragma unroll
+            for (int k = 0; k < KC; ++k)
+                f[k] = seen(i, k) ? p[i][k] * scale(bmul2(scales(i, n), st.F[k][n / 2]), n) : 0.0f;
+            most = max_abs3(most, f[0], f[KC - 1]);
+            pr[i][n] = product(f);
+        }
+    }
+    const auto sum = [&] {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (big[i] == 255u) {  // leave the NaN groups out
-                uint32_t m = 0;
 #pragma unroll
-                for (int n = 0; n < NG; ++n) {
-                    const uint32_t w = NG == 1 ? sv[i][0] >> 16 : sv[i][NG / 2 + n / 2] >> (16 * (n & 1));
-                    if ((w & 0x7f80u) != 0x7f80u) m = max(m, w >> 7 & 0xffu);
-                }
-                big[i] = m;
-                e[i] = static_cast<float>(static_cast<int>(m) - 126);
-            }
+            for (int k = 0; k < KC; ++k) st.l[k] += p[i][k];
+    };
+    // Every P_jn of the block rounds to zero, and no scale is NaN: nothing to add. With ALiBi most of a long sequence
+    // ends here.
+    if (!__any_sync(0xffffffffu, top > 8.0f || !(most <= 0x1p-25f))) return sum();
+    // References are moved where a P_jn leaves fp16's range; also where F_n times a scale overflows although the product
+    // would not, and where a scale is NaN. With R at the largest x_j or above it p_j <= 1, and p_j s_jn is finite.
+    if (__any_sync(0xffffffffu, top > 8.0f || !(most <= 65408.0f))) {
+        constexpr int NW = NG > 1 ? NG / 2 : 1;
 #pragma unroll
         for (int k = 0; k < KC; ++k) {
-            float mx = -INFINITY, my = -INFINITY;
+            float mx = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                mx = fmaxf(mx, x[i][k]);
-                my = fmaxf(my, x[i][k] + e[i]);
-            }
+            for (int i = 0; i < 4; ++i) mx = fmaxf(mx, x[i][k]);
 #pragma unroll
-            for (int off = 4; off < 32; off <<= 1) {
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-                my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, off));
-            }
-            const float r = fmaxf(st.R[k], mx), m = fmaxf(st.M[k], my);
-            st.l[k] *= ex2_approx(st.R[k] - r);
-            const float be = ex2_approx(st.M[k] - m);
+            for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+            const float was = st.R[k], r = fmaxf(was, was == -FLT_MAX ? mx : was + ceilf(mx - was));
+            const float up = fminf(r - was, 1000.0f);
+            st.l[k] *= ex2_approx(-up);
             st.R[k] = r;
-            st.M[k] = m;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[i][k] = ex2_approx(x[i][k] - r);
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                // the largest |p_j s_jn| of each group, NaN left out: its exponent, in the upper bits of its half
+                uint32_t tops = 0;
+#pragma unroll
+                for (int n = 2 * w; n < 2 * w + 2 && n < NG; ++n) {
+                    float my = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (seen(i, k)) my = fmaxf(my, fabsf(p[i][k] * scale(scales(i, n), n)));
+                    tops |= NG == 1 || (n & 1) ? __float_as_uint(my) & 0xffff0000u : __float_as_uint(my) >> 16;
+                }
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) tops = __vmaxu2(tops, __shfl_xor_sync(0xffffffffu, tops, off));
+                // the exponent fields of F_n: with R raised they grow by as much, and the sums stay, unless that is too large
+                uint32_t F = 0;
+#pragma unroll
+                for (int n = 2 * w; n < 2 * w + 2 && n < NG; ++n) {
+                    const int half = NG == 1 || (n & 1) ? 16 : 0;
+                    const int old = static_cast<int>(st.F[k][w] >> (half + 7) & 0xffu);
+                    const int e = static_cast<int>(tops >> (half + 7) & 0xffu);  // 2^(e - 127) F_n is 2^7
+                    const int f = min(min(old + __float2int_rn(up), 261 - e), static_cast<int>(kMostF));
+                    F |= static_cast<uint32_t>(f) << (half + 7);
+                    const float down = ex2_approx(static_cast<float>(f - old) - up);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        st.acc[n][i][k] *= down;
+                        st.acc[n][i][2 + k] *= down;
+                    }
+                }
+                st.F[k][w] = F;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int n = 0; n < NG; ++n) {
+                float f[KC];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    st.acc[n][i][k] *= be;
-                    st.acc[n][i][2 + k] *= be;
-                }
+                for (int k = 0; k < KC; ++k)
+                    f[k] = seen(i, k) ? p[i][k] * scale(scales(i, n), n) * scale(st.F[k][n / 2], n) : 0.0f;
+                pr[i][n] = product(f);
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                a[i][k] = x[i][k] - r;
-                b[i][k] = x[i][k] + e[i] - m;
-            }
-        }
-        topb = 0.0f;
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int k = 0; k < KC; ++k) {
-            st.l[k] += ex2_approx(a[i][k]);
-            b[i][k] = ex2_approx(b[i][k]);
-        }
-    // Every P_jn of the block rounds to zero (2^(b + 7) below 2^-25), and no scale is NaN: nothing to add. With ALiBi most
-    // of a long sequence ends here.
-    const uint32_t largest = max(max(big[0], big[1]), max(big[2], big[3]));
-    if (!__any_sync(0xffffffffu, !(topb <= -33.0f) || largest == 255u)) return;
+    sum();
 
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -374,27 +416,15 @@ __device__ __forceinline__ void block32(State<D, KC> &st, const uint8_t *blk, in
                 vw[n][0] = w[0], vw[n][1] = w[1], vw[n + 1][0] = w[2], vw[n + 1][1] = w[3];
             }
         }
-        // P <= 2^8 2^7: the 2^7 keeps small weights off fp16's subnormals. (No scale: the shift overflows, and meets
-        // zeros.)
-        float down[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) down[h] = __uint_as_float((260u - big[2 * t + h]) << 23);  // 2^(7 - e)
 #pragma unroll
         for (int n = 0; n < NG; ++n) {
             uint32_t pb[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int i = 2 * t + h;
-                const uint32_t word = sv[i][NG == 1 ? 0 : NG / 2 + n / 2];
-                const float s = ((NG == 1 || (n & 1)) ? bf16_hi(word) : bf16_lo(word)) * down[h];
-                float pr[2] = {0.0f, 0.0f};
-#pragma unroll
-                for (int k = 0; k < KC; ++k) {
-                    pr[k] = b[i][k] * s;
-                    // a NaN scale of a token that the query does not see stays out
-                    if (MASK && jf + 8.0f * i > st.pos[k]) pr[k] = 0.0f;
-                }
-                pb[h] = transpose8(pack_f16x2(pr[0], pr[1]));
+                if constexpr (KC == 1)
+                    pb[h] = transpose8(pack_f16x2(pr[2 * t + h][n], 0.0f));
+                else
+                    pb[h] = transpose8(pr[2 * t + h][n]);
             }
             uint32_t v0[4], v1[4];
             unpack(vw[n][0], v0);
@@ -639,7 +669,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
         const int count = CLUSTER ? p.count : slices ? sh.count : 1;  // slices of the chunk
         const int take = SHARES && !slices ? min(sh.left, n - at) : n;
         // This CTA's stages [s0, s1) of the chunk (slices: every count-th of all), dealt to its warps in turn from the
-        // newest to the oldest: the bias falls on the way, so the references R and M settle in the first
+        // newest to the oldest: the bias falls on the way, so the references R and F_n settle in the first
         // tiles. (Oldest first, a steep head raises them at every tile.)
         const int s0 = slices ? 0 : at, s1 = min(s0 + take, (nblk + SB - 1) / SB);
         const int step = kWarps * count;
@@ -687,8 +717,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
                 const int h = p.by_T.of(r);
                 st.slope[k] = p.slopes.log2e[hk * p.G + h];
                 st.pos[k] = static_cast<float>(len - p.T + r - h * p.T - g);
-                st.R[k] = st.M[k] = -FLT_MAX;
+                st.R[k] = -FLT_MAX;
                 st.l[k] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < (NG > 1 ? NG / 2 : 1); ++i) st.F[k][i] = kMostF << 23 | kMostF << 7;
             }
         }
 
@@ -722,12 +754,15 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
         for (int k = 0; k < KC; ++k) {
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) st.l[k] += __shfl_xor_sync(0xffffffffu, st.l[k], off);
-            const float f = ex2_approx(st.M[k] - st.R[k] - 7.0f) * (st.l[k] == 0.0f ? 0.0f : 1.0f / st.l[k]);
+            const float inv = st.l[k] == 0.0f ? 0.0f : 1.0f / st.l[k];
             const int r = KC * c + k;
 #pragma unroll
             for (int i = 0; i < NG; ++i) {
-                const float4 o = make_float4(st.acc[i][0][k] * f, st.acc[i][1][k] * f, st.acc[i][0][2 + k] * f,
-                                             st.acc[i][1][2 + k] * f);
+                // 1 / F_n, after the division by l: a mean is in range, the sum may not be
+                const uint32_t F = st.F[k][i / 2] >> (NG == 1 || (i & 1) ? 23 : 7) & 0xffu;
+                const float up = pow2(127 - static_cast<int>(F));
+                const float4 o = make_float4(st.acc[i][0][k] * inv * up, st.acc[i][1][k] * inv * up,
+                                             st.acc[i][0][2 + k] * inv * up, st.acc[i][1][2 + k] * inv * up);
                 *reinterpret_cast<float4 *>(pw + r * kRowStride + 32 * i + 4 * g) = o;
             }
             if (g == 0)

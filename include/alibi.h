@@ -365,7 +365,10 @@ ALIBI_API int alibi_kv4_read(const void *cache, void *k, void *v, const int *pos
  * alibi_fwd_options (NULL: alibi_slopes(H)).
  * Rows past a sequence's length are not used, whatever they hold; a NaN in a key
  * that a query sees makes its out and lse NaN, one in a value its group of 32
- * elements of out. out and lse are the same bits for the same arguments. A call takes up
+ * elements of out. Weights are fp32 numbers (one below 2^-126 of the row's largest counts as
+ * zero). A weight's product with the scale of a group of 32 value elements is rounded to 11 bits, or
+ * to 2^-32 of the largest such product of that row and group, whatever other groups hold.
+ * out and lse are the same bits for the same arguments. A call takes up
  * to 2.6 MB of scratch from the library's stream-ordered pool where it splits sequences over
  * several CTAs and merges them in a second kernel (few long sequences).
  */

@@ -149,3 +149,36 @@ def decode(q, kh, vh, lens, m):
                     2.0 ** -31 * (W[:, None] * tv).max() * (i + 1)
                 e_lse[b, h, t] = D + 2.0 ** -20 * (1 + np.abs(lse[b, h, t]))
     return out, lse, e_out, e_lse
+
+
+def decode_by_group(q, kh, vh, lens, m):
+    """As `decode`, with bounds that hold group by group of 32 elements, whatever the other groups of the
+    same rows hold: the 16-bit products of weight and scale are relative to the largest product of THEIR value
+    group, so 2^-31 N max_j,n becomes 2^-31 N max_j of the element's own group n. Weights are fp32 numbers: one
+    below 2^-126 of the row's largest may count as zero."""
+    B, H, T, d = q.shape
+    G = H // kh.shape[1]
+    out, lse = np.zeros(q.shape), np.full(q.shape[:-1], -np.inf)
+    e_out, e_lse = np.zeros(q.shape), np.zeros(q.shape[:-1])
+    for b in range(B):
+        for h in range(H):
+            for t in range(T):
+                i = int(lens[b]) - T + t
+                if i < 0:
+                    continue
+                K, V = kh[b, h // G, : i + 1], vh[b, h // G, : i + 1]
+                Q = q[b, h, t]
+                dist = m[h] * (i - np.arange(i + 1))
+                x = K @ Q / np.sqrt(d) - dist
+                M = x.max()
+                w = np.exp(x - M)
+                W = w / w.sum()
+                out[b, h, t], lse[b, h, t] = W @ V, M + np.log(w.sum())
+                tk, tv = _largest(K), _largest(V)
+                dx = 2.0 ** -18 * (tk @ np.abs(Q)) / np.sqrt(d) + 2.0 ** -21 * (dist + np.abs(x)) + \
+                    2.0 ** -34 * np.abs(Q).max() * tk.sum(-1) / np.sqrt(d)
+                E = W @ dx
+                e_out[b, h, t] = (W * (2.0 ** -11 + dx + E)) @ np.abs(V) + 2.0 ** -19 * (W @ tv) + \
+                    2.0 ** -31 * (W[:, None] * tv).max(0) * (i + 1) + 2.0 ** -126 * tv.sum(0)
+                e_lse[b, h, t] = E + 2.0 ** -20 * (1 + np.abs(lse[b, h, t]))
+    return out, lse, e_out, e_lse

@@ -1,0 +1,84 @@
+"""Decode over the 4-bit KV cache where the groups of 32 elements of a row differ widely in magnitude:
+against attention in 64 bits over the held values, within bounds
+that hold for each group by itself (kv4_ref.decode_by_group)."""
+import numpy as np
+import pytest
+
+import alibi_inputs as gen
+import kv4_ref as ref
+import oracle
+from gpu_helpers import half_ulp_bf16, host64
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ab():
+    import alibi_positional_bias_gb300 as ab
+    ab.load()
+    return ab
+
+
+def exact_bf16(x):
+    return gen.make_tensor(np.asarray(x, dtype=np.float32), np.shape(x), "bf16").f32.astype(np.float64)
+
+
+def compare(ab, q, k, v, lens, m=None, what=""):
+    """q, k, v: exact bf16 values; the whole of out and lse against the bounds of each group."""
+    import torch
+    B, H = q.shape[:2]
+    C = -(-k.shape[2] // 32) * 32
+    cache = torch.from_numpy(np.concatenate([ref.pack(k[b:b + 1, :, :n], v[b:b + 1, :, :n], C)
+                                             for b, n in enumerate(lens)])).cuda()
+    qd = torch.from_numpy(gen.make_tensor(q.astype(np.float32), q.shape, "bf16").bf16.view(np.int16)).view(torch.bfloat16).cuda()
+    slopes = None if m is None else np.asarray(m, dtype=np.float32)
+    out, lse = ab.alibi_attn_decode_kv4(qd, cache, lens=torch.tensor(lens, dtype=torch.int32, device="cuda"), slopes=slopes)
+    ab.alibi_check_error()
+    ro, rl, eo, el = ref.decode_by_group(q, ref.held(k), ref.held(v), lens,
+                                         oracle.slopes(H) if m is None else slopes.astype(np.float64))
+    go, gl = host64(out), host64(lse)
+    assert np.isfinite(go).all() and np.isfinite(gl).all(), what
+    lim = eo + half_ulp_bf16(ro) * (1 + 2.0 ** -6) + 2.0 ** -133
+    assert (np.abs(go - ro) <= lim).all(), (what, (np.abs(go - ro) / lim).max())
+    assert (np.abs(gl - rl) <= el).all(), (what, (np.abs(gl - rl) / el).max())
+
+
+def case(seed, B, Hkv, G, T, N, d):
+    rng = np.random.default_rng(seed)
+    return (exact_bf16(rng.standard_normal(s)) for s in ((B, Hkv * G, T, d), (B, Hkv, N, d), (B, Hkv, N, d)))
+
+
+# Whole chunks (the first two), clusters, and slices with a merge kernel; one row per lane and two
+SHAPES = [(2, 2, 1, 1, 96, 64), (1, 2, 3, 2, 200, 128), (1, 8, 1, 1, 3000, 128), (1, 1, 1, 1, 20000, 64), (1, 2, 8, 1, 3000, 64)]
+
+
+@pytest.mark.parametrize("power", [16, 24, 32, 40, 100, -40])
+@pytest.mark.parametrize("B,Hkv,G,T,N,d", SHAPES)
+def test_a_value_group_far_larger_or_smaller_than_the_others(ab, B, Hkv, G, T, N, d, power):
+    q, k, v = case(power + N, B, Hkv, G, T, N, d)
+    v[..., :32] *= 2.0 ** power
+    lens = [N - 5 * b for b in range(B)]
+    compare(ab, q, k, exact_bf16(v), lens, what="default slopes")
+    compare(ab, q, k, exact_bf16(v), lens, m=np.zeros(Hkv * G), what="flat")
+    compare(ab, q * 0, k, exact_bf16(v), lens, m=np.zeros(Hkv * G), what="equal weights")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("apart", [10, 20, 50])
+def test_groups_apart_by_powers_of_two_in_turn(ab, apart, d):
+    # group n of token j has values about 2^(apart (n + j) mod 3): the largest group changes from token to token
+    q, k, v = case(apart, 1, 2, 2, 1, 320, d)
+    n, j = np.arange(d) // 32, np.arange(320)
+    v = exact_bf16(v * 2.0 ** (apart * ((n[None, :] + j[:, None]) % 3 - 1)))
+    for m in (None, np.zeros(4)):
+        compare(ab, q, k, v, [317], m=m)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_group_that_only_far_tokens_fill(ab, d):
+    # the newest tokens have zeros in group 1 and large values in group 0; the far ones, whose weights are 2^-30 of the
+    # newest ones', alone fill group 1
+    q, k, v = case(3, 1, 1, 1, 1, 256, d)
+    v[..., 224:, 32:64] = 0.0
+    v[..., 224:, :32] *= 2.0 ** 30
+    compare(ab, q, k, exact_bf16(v), [256], m=np.full(1, 30 * np.log(2) / 64))
