@@ -12,9 +12,12 @@
 //
 //   scores   acc_n = (U_n - 8) Q_n^T per group n of 32 elements, mma.m16n8k16 with u - 8 and
 //            q as fp16 operands, both exact: four bits under the exponent of 1024 are 1024 + u
-//            (or 1024 + 16 u), and one add or fma per pair leaves u - 8; q is scaled to
-//            [2^14, 2^15) per row, which holds elements down to 2^-32 of the row's largest.
-//            s_jn acc_n is the group's share of q.k_j: exact products summed in fp32.
+//            (or 1024 + 16 u), and one add or fma per pair leaves u - 8; each group of
+//            q is scaled to [2^14, 2^15), which holds elements down to 2^-32 of the group's largest.
+//            kappa (s_jn 2^e_n) acc_n is the group's share of the logit: exact products summed in fp32, the
+//            powers of two taking the scaling of q back. 2^e_n, a bf16 number of at most 2^-23 (2^-13 for rows of 2^117
+//            and more), meets the scale first, exactly, so that the sum over n stays in range; kappa is
+//            the row's: s_jn acc_n alone leaves fp32 from keys of 2^113 on.
 //            (Masked bits without the 1024 are operands too, the subnormals u 2^-24 and u 2^-20,
 //            but the tensor core aligns products by their nominal exponents, which costs 10 and 6
 //            bits of the sum: errors of 2^-17 of 8 |s| were measured. Keys as 1024 + 16 u, with the
@@ -29,8 +32,8 @@
 //            or small the other groups' values are (with one reference for all groups, those of 2^-32 of the
 //            largest vanished). The rounding of P is the only one below fp32: off by at most 2^-11 of a product,
 //            a quarter of the bf16 output's own step, or, below fp16's normal numbers, by 2^-32 of the
-//            group's largest product. (bf16 weights would be off by as much as the output itself.) F_n is a
-//            bf16 number, so that it multiplies two scales at once, exactly. A block whose P all round to zero adds
+//            group's largest product. (bf16 weights would be off by as much as the output itself.) F_n is held
+//            as a bf16 number, as the scale that it multiplies first, exactly. A block whose P all round to zero adds
 //            nothing and its values are not multiplied.
 //
 // mma.sync and not tcgen05.mma: the operands are made in registers, where tcgen05 would have to be
@@ -103,7 +106,7 @@ struct DecodeKv4Params {
     kv4::Divisor by_chunks, by_U, by_T, by_count;  // U: chunks of a sequence
     bool slices;                  // Shares: every chunk has CTAs of its own; otherwise equal shares
     int count;                    // Cluster: CTAs of a cluster
-    float c1;                     // 2^-14 log2(e) / sqrt(d)
+    float c1;                     // log2(e) / sqrt(d)
     HeadSlopes slopes;
 };
 
@@ -164,11 +167,25 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// Products of two bf16 pairs, rounded to bf16 (exact where one is a power of two and the product is in range).
-__device__ __forceinline__ uint32_t bmul2(uint32_t a, uint32_t b)
+// Product of the low halves of two bf16 pairs, or of the high ones, in fp32: exact, and in one operation of the fma pipe. (A
+// product of pairs in bf16 and taking it apart takes half an operation there and one of the logic pipe, which has less
+// room: 24 x 7 x 14336 tokens of d = 32 28.3 -> 27.1 us, 8 x 8 (x 8) x 32768 55.1 -> 52.7.)
+template <int HALF>
+__device__ __forceinline__ float bf16_product(uint32_t a, uint32_t b)
 {
-    uint32_t d;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    float d;
+    if constexpr (HALF == 0)
+        asm("{\n\t.reg .b16 a0, a1, b0, b1;\n\t"
+            "mov.b32 {a0, a1}, %1;\n\t"
+            "mov.b32 {b0, b1}, %2;\n\t"
+            "fma.rn.f32.bf16 %0, a0, b0, %3;\n\t}"
+            : "=f"(d) : "r"(a), "r"(b), "f"(0.0f));
+    else
+        asm("{\n\t.reg .b16 a0, a1, b0, b1;\n\t"
+            "mov.b32 {a0, a1}, %1;\n\t"
+            "mov.b32 {b0, b1}, %2;\n\t"
+            "fma.rn.f32.bf16 %0, a1, b1, %3;\n\t}"
+            : "=f"(d) : "r"(a), "r"(b), "f"(0.0f));
     return d;
 }
 
@@ -240,7 +257,8 @@ template <int D, int KC>
 struct State {
     static constexpr int NG = D / 32;
     uint32_t q[NG][4];      // B operands: column lane / 4, elements 32 n + 8 c + (i, i + 4)
-    float kappa[KC];        // from s acc to base-2 logits
+    uint32_t unq[KC][NG > 1 ? NG / 2 : 1];  // bf16 pairs 2^e_n, as the key scales lie (D = 32: in the low half)
+    float kappa[KC];        // from their sum to base-2 logits
     float slope[KC];        // m log2(e)
     float pos[KC];          // position less lane / 4
     float R[KC], l[KC];
@@ -278,11 +296,12 @@ __device__ __forceinline__ void block32(State<D, KC> &st, const uint8_t *blk, in
             mma16816(s, k0[2], k1[2], k0[3], k1[3], st.q[n][2], st.q[n][3]);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const uint32_t w = sv[2 * t + h][n / 2];
-                const float sk = (n & 1) ? bf16_hi(w) : bf16_lo(w);
 #pragma unroll
-                for (int k = 0; k < KC; ++k)
+                for (int k = 0; k < KC; ++k) {
+                    const uint32_t w = sv[2 * t + h][n / 2];
+                    const float sk = (n & 1) ? bf16_product<1>(w, st.unq[k][n / 2]) : bf16_product<0>(w, st.unq[k][n / 2]);
                     x[2 * t + h][k] = n == 0 ? sk * s[2 * h + k] : fmaf(sk, s[2 * h + k], x[2 * t + h][k]);
+                }
             }
         }
     }
@@ -310,39 +329,43 @@ __device__ __forceinline__ void block32(State<D, KC> &st, const uint8_t *blk, in
         else
             return pack_f16x2(f[0], f[1]);
     };
-    float p[4][KC], top = -INFINITY, most = 0.0f;
+    float sum[KC] = {}, top = -INFINITY, most = 0.0f;
     Product pr[4][NG];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+        float p[KC];
 #pragma unroll
         for (int k = 0; k < KC; ++k) {
             const float a = x[i][k] - st.R[k];
             top = fmaxf(top, a);
-            p[i][k] = ex2_approx(a);
+            p[k] = ex2_approx(a);
+            sum[k] += p[k];
         }
 #pragma unroll
         for (int n = 0; n < NG; ++n) {
             float f[KC];
 #pragma unroll
-            for (int k = 0; k < KC; ++k)
-                f[k] = seen(i, k) ? p[i][k] * scale(bmul2(scales(i, n), st.F[k][n / 2]), n) : 0.0f;
+            for (int k = 0; k < KC; ++k) {
+                const uint32_t w = scales(i, n), F = st.F[k][n / 2];
+                const float sF = NG == 1 || (n & 1) ? bf16_product<1>(w, F) : bf16_product<0>(w, F);
+                f[k] = seen(i, k) ? p[k] * sF : 0.0f;
+            }
             most = max_abs3(most, f[0], f[KC - 1]);
             pr[i][n] = product(f);
         }
     }
-    const auto sum = [&] {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int k = 0; k < KC; ++k) st.l[k] += p[i][k];
-    };
     // Every P_jn of the block rounds to zero, and no scale is NaN: nothing to add. With ALiBi most of a long sequence
     // ends here.
-    if (!__any_sync(0xffffffffu, top > 8.0f || !(most <= 0x1p-25f))) return sum();
+    if (!__any_sync(0xffffffffu, top > 8.0f || !(most <= 0x1p-25f))) {
+#pragma unroll
+        for (int k = 0; k < KC; ++k) st.l[k] += sum[k];
+        return;
+    }
     // References are moved where a P_jn leaves fp16's range; also where F_n times a scale overflows although the product
     // would not, and where a scale is NaN. With R at the largest x_j or above it p_j <= 1, and p_j s_jn is finite.
     if (__any_sync(0xffffffffu, top > 8.0f || !(most <= 65408.0f))) {
         constexpr int NW = NG > 1 ? NG / 2 : 1;
+        float p[4][KC];
 #pragma unroll
         for (int k = 0; k < KC; ++k) {
             float mx = -INFINITY;
@@ -356,6 +379,7 @@ __device__ __forceinline__ void block32(State<D, KC> &st, const uint8_t *blk, in
             st.R[k] = r;
 #pragma unroll
             for (int i = 0; i < 4; ++i) p[i][k] = ex2_approx(x[i][k] - r);
+            sum[k] = (p[0][k] + p[1][k]) + (p[2][k] + p[3][k]);
 #pragma unroll
             for (int w = 0; w < NW; ++w) {
                 // the largest |p_j s_jn| of each group, NaN left out: its exponent, in the upper bits of its half
@@ -400,7 +424,8 @@ __device__ __forceinline__ void block32(State<D, KC> &st, const uint8_t *blk, in
                 pr[i][n] = product(f);
             }
     }
-    sum();
+#pragma unroll
+    for (int k = 0; k < KC; ++k) st.l[k] += sum[k];
 
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -690,19 +715,27 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
 
         State<D, KC> st;
         {
-            uint32_t top = 0;
-#pragma unroll
-            for (int i = 0; i < NG; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) top = __vmaxu2(top, qw[i][j] & 0x7fff7fffu);
-            top = max(top & 0xffffu, top >> 16);
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const uint32_t ex = max(top >> 7, 14u);
-            const float up = __uint_as_float((268u - ex) << 23);  // 2^14 over the largest element's power of two
-            const float kappa = __uint_as_float(ex << 23) * p.c1;
+            uint32_t ex[NG], most = 14u;  // exponents of the groups' largest elements, and of the row's
 #pragma unroll
             for (int i = 0; i < NG; ++i) {
+                uint32_t top = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) top = __vmaxu2(top, qw[i][j] & 0x7fff7fffu);
+                top = max(top & 0xffffu, top >> 16);
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                ex[i] = top >> 7;
+                most = max(most, ex[i]);
+            }
+            const uint32_t m = min(most, 244u);  // kappa stays finite
+            const float kappa = __uint_as_float((m + 9u) << 23) * p.c1;
+            uint32_t unq[NG > 1 ? NG / 2 : 1] = {};
+#pragma unroll
+            for (int i = 0; i < NG; ++i) {
+                // a group of less than 2^-103 of the row's largest element is scaled up less, so that 2^e_n is a normal number
+                const uint32_t e = max(ex[i], max(m, 103u + 14u) - 103u);
+                const float up = __uint_as_float((268u - e) << 23);  // 2^14 over the largest element's power of two
+                unq[i / 2] |= (104u + e - m) << (i & 1 ? 23 : 7);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     st.q[i][j] = (j & 1) ? pack_f16x2(bf16_hi(qw[i][j / 2]) * up, bf16_hi(qw[i][2 + j / 2]) * up)
@@ -714,6 +747,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
             for (int k = 0; k < KC; ++k) {
                 const int r = min(row0 + KC * c + k, p.rows - 1);
                 st.kappa[k] = __shfl_sync(0xffffffffu, kappa, (2 * c + k) * 4);
+#pragma unroll
+                for (int i = 0; i < (NG > 1 ? NG / 2 : 1); ++i) st.unq[k][i] = __shfl_sync(0xffffffffu, unq[i], (2 * c + k) * 4);
                 const int h = p.by_T.of(r);
                 st.slope[k] = p.slopes.log2e[hk * p.G + h];
                 st.pos[k] = static_cast<float>(len - p.T + r - h * p.T - g);
@@ -1060,7 +1095,7 @@ extern "C" int alibi_attn_decode_kv4(const void *q, const void *cache, const int
     p.by_chunks = kv4::Divisor(p.chunks);
     p.by_U = kv4::Divisor(Hkv * p.chunks);
     p.by_T = kv4::Divisor(T);
-    p.c1 = 0x1p-14f * 1.4426950408889634f / sqrtf(static_cast<float>(d));
+    p.c1 = 1.4426950408889634f / sqrtf(static_cast<float>(d));
     // A slope beyond 1e30 is 1e30: the bias of the next token is out of reach already, and its multiples stay finite.
     for (int h = 0; h < H; ++h) p.slopes.log2e[h] = std::min(s.log2e[h], 1e30f);
     const long long units = static_cast<long long>(B) * Hkv * p.chunks;

@@ -366,7 +366,8 @@ ALIBI_API int alibi_kv4_read(const void *cache, void *k, void *v, const int *pos
  * Rows past a sequence's length are not used, whatever they hold; a NaN in a key
  * that a query sees makes its out and lse NaN, one in a value its group of 32
  * elements of out. Weights are fp32 numbers (one below 2^-126 of the row's largest counts as
- * zero). A weight's product with the scale of a group of 32 value elements is rounded to 11 bits, or
+ * zero). Elements of q are exact down to 2^-32 of the largest of their 32; keys and queries may have
+ * any magnitude as long as the logits are fp32 numbers. A weight's product with the scale of a group of 32 value elements is rounded to 11 bits, or
  * to 2^-32 of the largest such product of that row and group, whatever other groups hold.
  * out and lse are the same bits for the same arguments. A call takes up
  * to 2.6 MB of scratch from the library's stream-ordered pool where it splits sequences over

@@ -153,11 +153,13 @@ def decode(q, kh, vh, lens, m):
 
 def decode_by_group(q, kh, vh, lens, m):
     """As `decode`, with bounds that hold group by group of 32 elements, whatever the other groups of the
-    same rows hold: the 16-bit products of weight and scale are relative to the largest product of THEIR value
-    group, so 2^-31 N max_j,n becomes 2^-31 N max_j of the element's own group n. Weights are fp32 numbers: one
+    same rows hold: elements of q are inexact below 2^-32 of the largest of THEIR group of 32, and the 16-bit
+    products of weight and scale are relative to the largest product of THEIR value group. So the term
+    2^-34 max|q| sum_e 16 |s_je| becomes its sum over the groups, each with its own maximum, and
+    2^-31 N max_j,n becomes 2^-31 N max_j of the element's own group n. Weights are fp32 numbers: one
     below 2^-126 of the row's largest may count as zero."""
     B, H, T, d = q.shape
-    G = H // kh.shape[1]
+    G, D = H // kh.shape[1], padded(d)
     out, lse = np.zeros(q.shape), np.full(q.shape[:-1], -np.inf)
     e_out, e_lse = np.zeros(q.shape), np.zeros(q.shape[:-1])
     for b in range(B):
@@ -175,8 +177,9 @@ def decode_by_group(q, kh, vh, lens, m):
                 W = w / w.sum()
                 out[b, h, t], lse[b, h, t] = W @ V, M + np.log(w.sum())
                 tk, tv = _largest(K), _largest(V)
-                dx = 2.0 ** -18 * (tk @ np.abs(Q)) / np.sqrt(d) + 2.0 ** -21 * (dist + np.abs(x)) + \
-                    2.0 ** -34 * np.abs(Q).max() * tk.sum(-1) / np.sqrt(d)
+                q_top = np.repeat(np.abs(np.pad(Q, (0, D - d))).reshape(-1, 32).max(-1), 32)[:d]
+                dx = (2.0 ** -18 * (tk @ np.abs(Q)) + 2.0 ** -34 * (tk @ q_top)) / np.sqrt(d) + \
+                    2.0 ** -21 * (dist + np.abs(x))
                 E = W @ dx
                 e_out[b, h, t] = (W * (2.0 ** -11 + dx + E)) @ np.abs(V) + 2.0 ** -19 * (W @ tv) + \
                     2.0 ** -31 * (W[:, None] * tv).max(0) * (i + 1) + 2.0 ** -126 * tv.sum(0)

@@ -1,5 +1,5 @@
-"""Decode over the 4-bit KV cache where the groups of 32 elements of a row differ widely in magnitude:
-against attention in 64 bits over the held values, within bounds
+"""Decode over the 4-bit KV cache where the groups of 32 elements of a row differ widely in magnitude, and where
+queries and keys lie at the ends of bf16's range: against attention in 64 bits over the held values, within bounds
 that hold for each group by itself (kv4_ref.decode_by_group)."""
 import numpy as np
 import pytest
@@ -82,3 +82,44 @@ def test_a_group_that_only_far_tokens_fill(ab, d):
     v[..., 224:, 32:64] = 0.0
     v[..., 224:, :32] *= 2.0 ** 30
     compare(ab, q, k, exact_bf16(v), [256], m=np.full(1, 30 * np.log(2) / 64))
+
+
+@pytest.mark.parametrize("B,Hkv,G,T,N,d", SHAPES)
+@pytest.mark.parametrize("sk,sq", [(1e34, 1e-34), (7e37, 1e-37), (2.0 ** 112, 2.0 ** -112), (1e37, 1e-38), (1e20, 1e-20)])
+def test_keys_at_the_upper_end_of_the_range(ab, B, Hkv, G, T, N, d, sk, sq):
+    q, k, v = case(N, B, Hkv, G, T, N, d)
+    lens = [N - 5 * b for b in range(B)]
+    big = 255 * 2.0 ** 120  # bf16's largest number
+    compare(ab, exact_bf16(q * sq), exact_bf16(np.clip(k * sk, -big, big)), v, lens)
+
+
+@pytest.mark.parametrize("d", [16, 32, 64, 128])
+def test_the_largest_keys(ab, d):
+    # keys of +-bf16's largest number; queries of 2^-126 to 2^-120, whose logits are some tens
+    rng = np.random.default_rng(d)
+    big = 255 * 2.0 ** 120
+    k = exact_bf16(rng.choice([-big, big], size=(1, 2, 160, d)))
+    q = exact_bf16(rng.standard_normal((1, 4, 1, d)) * 2.0 ** -126)
+    v = exact_bf16(rng.standard_normal((1, 2, 160, d)))
+    compare(ab, q, k, v, [150])
+    compare(ab, exact_bf16(q * 32), k, v, [150])
+
+
+@pytest.mark.parametrize("power", [12, 30, 45, 90])
+@pytest.mark.parametrize("d", [64, 128])
+def test_query_groups_of_very_different_magnitude(ab, d, power):
+    # group 0 of the query is 2^power larger and that of the keys as much smaller: every group has its part of the logits
+    q, k, v = case(power, 2, 2, 2, 2, 320, d)
+    q[..., :32] *= 2.0 ** power
+    k[..., :32] *= 2.0 ** -power
+    compare(ab, exact_bf16(q), exact_bf16(k), v, [320, 77])
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("sk,sq", [(1e38, 1e6), (1e38, 1e38), (1e30, 1e20)])
+def test_large_keys_that_large_queries_do_not_meet(ab, d, sk, sq):
+    # q.k = 0 although the largest of both are out of range together: where one has values the other has zeros
+    q, k, v = case(d, 1, 2, 2, 1, 128, d)
+    q[..., ::2] = 0.0
+    k[..., 1::2] = 0.0
+    compare(ab, exact_bf16(np.clip(q, -3, 3) * sq), exact_bf16(np.clip(k, -3, 3) * sk), v, [120])
