@@ -320,6 +320,10 @@ __device__ __forceinline__ void block32(State<D, KC> &st, const uint8_t *blk, in
     // scale of group n of token i: the word it lies in, and itself from that word (or the word's multiple)
     const auto scales = [&](int i, int n) { return sv[i][NG == 1 ? 0 : NG / 2 + n / 2]; };
     const auto scale = [](uint32_t word, int n) { return NG == 1 || (n & 1) ? bf16_hi(word) : bf16_lo(word); };
+    const auto scaleF = [&](int i, int n, int k) {
+        const uint32_t w = scales(i, n), F = st.F[k][n / 2];
+        return NG == 1 || (n & 1) ? bf16_product<1>(w, F) : bf16_product<0>(w, F);
+    };
     // p_j and P_jn; of a token that the row does not see zero, whatever its scale. Two rows' P are packed at once, which
     // holds them in half the registers.
     using Product = std::conditional_t<KC == 1, float, uint32_t>;
@@ -345,11 +349,7 @@ __device__ __forceinline__ void block32(State<D, KC> &st, const uint8_t *blk, in
         for (int n = 0; n < NG; ++n) {
             float f[KC];
 #pragma unroll
-            for (int k = 0; k < KC; ++k) {
-                const uint32_t w = scales(i, n), F = st.F[k][n / 2];
-                const float sF = NG == 1 || (n & 1) ? bf16_product<1>(w, F) : bf16_product<0>(w, F);
-                f[k] = seen(i, k) ? p[k] * sF : 0.0f;
-            }
+            for (int k = 0; k < KC; ++k) f[k] = seen(i, k) ? p[k] * scaleF(i, n, k) : 0.0f;
             most = max_abs3(most, f[0], f[KC - 1]);
             pr[i][n] = product(f);
         }
@@ -763,11 +763,15 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
             const bool ok = mbar_wait(&full[warp][slot], phase, p.status, 0x60);
             if (!__all_sync(0xffffffffu, ok)) break;
             const uint8_t *stage = mine + slot * kStageBytes;
+            // Of one row per lane and d = 128 the masked form takes every block: a second copy of the loop's body costs more
+            // there than the masks (64 x 40 x 8192 tokens 424 us with two copies, 413 with one; d = 32 27.1 and 28.0 at
+            // 24 x 7 x 14336, two rows per lane 55.1 and 58.0 at 8 x 8 (x 8) x 32768; d = 64 the same at 8 x 38 x 16384).
+            constexpr bool kOneForm = KC == 1 && D == 128;
 #pragma unroll 1
             for (int t = SB - 1; t >= 0; --t) {
                 const int j0 = (s * SB + t) * kv4::kBlock;
                 if (j0 >= len) continue;
-                if (j0 + kv4::kBlock > len - p.T + 1)
+                if (kOneForm || j0 + kv4::kBlock > len - p.T + 1)
                     block32<D, KC, true>(st, stage + t * kBlk, j0, lane);
                 else
                     block32<D, KC, false>(st, stage + t * kBlk, j0, lane);
