@@ -508,10 +508,11 @@ __device__ __forceinline__ void finish(__nv_bfloat16 *out, float *lse, int d, si
     if (e == 0 && lse) lse[row] = bad ? nan : m.l == 0.0f ? -INFINITY : (m.R + log2f(m.l)) * 0.6931471805599453f;
 }
 
-// Length of sequence b; one outside [0, L] counts as 0.
+// Length of sequence b; one outside [0, L] counts as 0. Not by the read-only path: this kernel's life begins while the one
+// that writes the lengths may still run.
 __device__ __forceinline__ int length_of(const DecodeKv4Params &p, int b, bool &bad)
 {
-    const int n = p.lens ? __ldg(p.lens + b) : p.L;
+    const int n = p.lens ? __ldcg(p.lens + b) : p.L;
     bad = n < 0 || n > p.L;
     return bad ? 0 : n;
 }
