@@ -542,7 +542,7 @@ def alibi_kv4_read(cache, k, v, pos=None, count=None, stream=None):
 def alibi_attn_decode_kv4(q, cache, lens=None, L=None, out=None, lse=None, slopes=None, stream=None):
     """ALiBi attention of the newest T tokens of each sequence over the 4-bit cache that holds them.
     q: bf16 [B, H, T, d], or [B, H, d] for one token; cache: uint8 [B, H_kv, C / 32, bytes], H a multiple
-    of H_kv; lens: int32 CUDA tensor [B] of lengths (None: all L); L: a bound on them (None: the
+    of H_kv and at most 384; lens: int32 CUDA tensor [B] of lengths (None: all L); L: a bound on them (None: the
     capacity C); slopes: H values (None: alibi_slopes(H)). Returns (out, lse): bf16 like q, fp32
     without the last dimension; those made here belong to `stream`."""
     bfloat16, uint8, int32, float32, raw_stream, current, lib = _kv4_names()

@@ -81,7 +81,7 @@ constexpr int kSmem = kWarps * kStages * kStageBytes;
 constexpr uint32_t kMostF = 253;    // exponent field of a value factor F_n, at most: 1 / F_n is a normal number too
 
 struct HeadSlopes {
-    float log2e[kMaxHeads];
+    float log2e[kMaxQueryHeads];
 };
 
 // What a share leaves behind for the merge: the partial of a chunk that began in an earlier share (0) and of one that
@@ -1070,17 +1070,16 @@ extern "C" int alibi_attn_decode_kv4(const void *q, const void *cache, const int
         return ALIBI_ERR_INVALID;
     if (B < 1 || H < 1 || Hkv < 1 || T < 1 || L < 1 || C < 1 || d < 1) return ALIBI_ERR_INVALID;
     if (H % Hkv != 0 || C % kv4::kBlock != 0 || L > C) return ALIBI_ERR_INVALID;
-    if (!decode_supports(d) || H > kMaxHeads || T > 16 || C > (1 << 24)) return ALIBI_ERR_UNSUPPORTED;
+    if (!decode_supports(d) || H > kMaxQueryHeads || T > 16 || C > (1 << 24)) return ALIBI_ERR_UNSUPPORTED;
     if (static_cast<long long>(B) * H * T > (1LL << 31) - 1) return ALIBI_ERR_UNSUPPORTED;
     if (slopes)
         for (int h = 0; h < H; ++h)
             if (!std::isfinite(slopes[h]) || slopes[h] < 0.0f) return ALIBI_ERR_INVALID;
-    Slopes s;
-    if (slopes)
-        fill_slopes_from(H, slopes, &s);
-    else
-        fill_slopes(H, &s);
     DecodeKv4Params p;
+    if (slopes)
+        for (int h = 0; h < H; ++h) p.slopes.log2e[h] = static_cast<float>(static_cast<double>(slopes[h]) * 1.4426950408889634);
+    else
+        fill_slopes_log2e(H, p.slopes.log2e);
     p.q = static_cast<const __nv_bfloat16 *>(q);
     p.cache = static_cast<const uint8_t *>(cache);
     p.lens = lens;
@@ -1102,7 +1101,7 @@ extern "C" int alibi_attn_decode_kv4(const void *q, const void *cache, const int
     p.by_T = kv4::Divisor(T);
     p.c1 = 1.4426950408889634f / sqrtf(static_cast<float>(d));
     // A slope beyond 1e30 is 1e30: the bias of the next token is out of reach already, and its multiples stay finite.
-    for (int h = 0; h < H; ++h) p.slopes.log2e[h] = std::min(s.log2e[h], 1e30f);
+    for (int h = 0; h < H; ++h) p.slopes.log2e[h] = std::min(p.slopes.log2e[h], 1e30f);
     const long long units = static_cast<long long>(B) * Hkv * p.chunks;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool few = p.rows <= kRows / 2;  // one row per lane

@@ -297,6 +297,28 @@ void fill_slopes(int H, Slopes *s)
     std::memcpy(s->log2e, c->log2e, sizeof(float) * static_cast<size_t>(H));
 }
 
+void fill_slopes_log2e(int H, float *log2e)
+{
+    static std::atomic<const float *> cache[kMaxQueryHeads + 1];
+    const float *c = cache[H].load(std::memory_order_acquire);
+    if (!c) {
+        float *fresh = new float[static_cast<size_t>(H)];
+        for (int h = 0; h < H; ++h) {
+            int num, den;
+            slope_exponent(H, h, &num, &den);
+            fresh[h] = static_cast<float>(static_cast<double>(slope_value(num, den)) * 1.4426950408889634);
+        }
+        const float *expected = nullptr;
+        if (cache[H].compare_exchange_strong(expected, fresh, std::memory_order_acq_rel)) {
+            c = fresh;
+        } else {  // another thread published the same table first
+            delete[] fresh;
+            c = expected;
+        }
+    }
+    std::memcpy(log2e, c, sizeof(float) * static_cast<size_t>(H));
+}
+
 void fill_slopes_from(int H, const float *nat, Slopes *s)
 {
     for (int h = 0; h < H && h < kMaxHeads; ++h) {

@@ -19,6 +19,8 @@ constexpr uint64_t kWaitLimitNs = 1000000000ull;
 
 // Largest head count the kernels accept (slopes travel as kernel parameters).
 constexpr int kMaxHeads = 256;
+// Of the 4-bit decode, whose query heads may be eight to each of 48 KV heads.
+constexpr int kMaxQueryHeads = 384;
 
 struct Slopes {
     float log2e[kMaxHeads];  // m_h * log2(e): the bias in base-2 exponent units
@@ -29,6 +31,7 @@ struct Slopes {
 uint32_t *device_status_word();  // per current device, 2 words
 void fill_slopes(int H, Slopes *s);
 void fill_slopes_from(int H, const float *nat, Slopes *s);  // caller-chosen slopes (natural-log units)
+void fill_slopes_log2e(int H, float *log2e);                // the first alone, for up to kMaxQueryHeads heads
 int num_sms();                   // of the current device
 int l2_bytes();                  // L2 size of the current device
 // Blocked work order (work_order.h) of a dense launch over B*H heads of N rows,

@@ -330,7 +330,7 @@ ALIBI_API int alibi_kv4_block_bytes(int d);
 /*
  * Quantise new tokens and write them into the cache: token t < count[b] of
  * sequence b goes to row pos[b] + t. k, v: device bf16 [B, H, T, d] (H the KV
- * heads); pos, count: device int32 [B], or NULL for 0 and T. Other rows of the
+ * heads, at most 256); pos, count: device int32 [B], or NULL for 0 and T. Other rows of the
  * cache, and tokens from count[b] on, are left as they were. A sequence with
  * pos[b] < 0, count[b] < 0, count[b] > T or pos[b] + count[b] > C is left out
  * whole, and alibi_check_error returns ALIBI_ERR_RANGE. T in [1, C].
@@ -354,7 +354,7 @@ ALIBI_API int alibi_kv4_read(const void *cache, void *k, void *v, const int *pos
  *   x_j = q.k_j / sqrt(d) - m_h (i - j),  out = sum_j softmax_j(x) v_j,
  * k and v the values the cache holds. q, out: device bf16 [B, H, T, d]; lse:
  * device fp32 [B, H, T] = ln sum_j exp(x_j), or NULL. H query heads share
- * Hkv KV heads, H / Hkv consecutive ones each (H a multiple of Hkv). T in [1, 16]:
+ * Hkv KV heads, H / Hkv consecutive ones each (H a multiple of Hkv, at most 384). T in [1, 16]:
  * one token, or a few drafted ones checked at once. lens: device int32 [B], the
  * lengths with the T tokens included, or NULL (every sequence has L); 0 <=
  * lens[b] <= L <= C. L bounds the work that is planned: pass the largest length
@@ -365,10 +365,11 @@ ALIBI_API int alibi_kv4_read(const void *cache, void *k, void *v, const int *pos
  * alibi_fwd_options (NULL: alibi_slopes(H)).
  * Rows past a sequence's length are not used, whatever they hold; a NaN in a key
  * that a query sees makes its out and lse NaN, one in a value its group of 32
- * elements of out. Weights are fp32 numbers (one below 2^-126 of the row's largest counts as
- * zero). Elements of q are exact down to 2^-32 of the largest of their 32; keys and queries may have
- * any magnitude as long as the logits are fp32 numbers. A weight's product with the scale of a group of 32 value elements is rounded to 11 bits, or
- * to 2^-32 of the largest such product of that row and group, whatever other groups hold.
+ * elements of out. Elements of q are exact down to 2^-32 of the largest of their group of 32;
+ * keys and queries may have any magnitude as long as the logits are fp32 numbers. Weights are
+ * fp32 numbers (one below 2^-126 of the row's largest counts as zero); a weight's product with
+ * the scale of a group of 32 value elements is rounded to 11 bits, or to 2^-32 of the largest
+ * such product of that row and group, whatever other groups hold.
  * out and lse are the same bits for the same arguments. A call takes up
  * to 2.6 MB of scratch from the library's stream-ordered pool where it splits sequences over
  * several CTAs and merges them in a second kernel (few long sequences).

@@ -1,4 +1,4 @@
-"""Decode over the 4-bit KV cache where the groups of 32 elements of a row differ widely in magnitude, and where
+"""Decode over the 4-bit KV cache with more than 256 query heads, where the groups of 32 elements of a row differ widely in magnitude, and where
 queries and keys lie at the ends of bf16's range: against attention in 64 bits over the held values, within bounds
 that hold for each group by itself (kv4_ref.decode_by_group)."""
 import numpy as np
@@ -123,3 +123,10 @@ def test_large_keys_that_large_queries_do_not_meet(ab, d, sk, sq):
     q[..., ::2] = 0.0
     k[..., 1::2] = 0.0
     compare(ab, exact_bf16(np.clip(q, -3, 3) * sq), exact_bf16(np.clip(k, -3, 3) * sk), v, [120])
+
+
+@pytest.mark.parametrize("Hkv,G,T,d", [(40, 8, 1, 64), (37, 7, 2, 32), (48, 8, 1, 128), (1, 384, 1, 64), (43, 6, 5, 16)])
+def test_more_than_256_query_heads(ab, Hkv, G, T, d):
+    q, k, v = case(Hkv, 2, Hkv, G, T, 64, d)
+    compare(ab, q, k, v, [64, 37])
+    compare(ab, q, k, v, [50, 64], m=np.linspace(0.0, 1.5, Hkv * G))

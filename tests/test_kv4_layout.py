@@ -158,6 +158,11 @@ def test_decode_argument_errors(lib):
         assert f(P, P, None, P, P, *ok, m, None) == I
 
 
+def test_decode_refuses_more_than_384_query_heads(lib):
+    for H, Hkv in ((385, 385), (385, 1), (386, 193), (400, 50)):
+        assert lib.alibi_attn_decode_kv4(P, P, None, P, P, 1, H, Hkv, 1, 32, 32, 64, None, None) == ab.ALIBI_ERR_UNSUPPORTED
+
+
 def test_binding_refuses_host_tensors():
     import torch
     z = torch.zeros(1, 1, 1, 32, dtype=torch.bfloat16)
