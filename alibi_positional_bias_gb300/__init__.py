@@ -402,7 +402,7 @@ def alibi_attn_decode_noalloc(q, kcache, vcache, out, stream=None):
 
 def alibi_kv4_block_bytes(d: int) -> int:
     """Bytes of one 32-token block of the 4-bit KV cache for head size d."""
-    n = load().alibi_kv4_block_bytes(int(d))
+    n = load().alibi_kv4_block_bytes(max(-1, min(int(d), 1 << 30)))
     if n < 0:
         raise AlibiError(n, "alibi_kv4_block_bytes")
     return n
@@ -491,6 +491,14 @@ def _call_kv4(index, fn, where, stream, *args):
         raise AlibiError(status, where)
 
 
+def _kv4_sizes(n, C, where):
+    """What the library refuses of n tokens and a capacity of C, here, where a number beyond 32 bits is still itself."""
+    if not 0 < n <= C:
+        raise AlibiError(ALIBI_ERR_INVALID, where)
+    if C > 1 << 24:
+        raise AlibiError(ALIBI_ERR_UNSUPPORTED, where)
+
+
 def _kv4_rows_ok(k, v, dtype, cache, pos, count) -> bool:
     _, uint8, int32, _, _, _, _ = _kv4_names()
     try:
@@ -518,9 +526,12 @@ def alibi_kv4_write(k, v, cache, pos=None, count=None, stream=None) -> None:
         _explain_kv4(bfloat16, (k, "k", (4,)), [(v, "v", bfloat16, getattr(k, "shape", None))], cache,
                      k.shape[1] if hasattr(k, "shape") and len(k.shape) == 4 else None, [(pos, "pos"), (count, "count")])
     B, H, T, d = k.shape
+    C = cache.shape[2] * 32
+    if not 0 < T <= C <= 1 << 24:
+        _kv4_sizes(T, C, "alibi_kv4_write")
     _call_kv4(k.get_device(), lib.alibi_kv4_write, "alibi_kv4_write", stream, k.data_ptr(), v.data_ptr(),
               cache.data_ptr(), None if pos is None else pos.data_ptr(), None if count is None else count.data_ptr(),
-              B, H, T, cache.shape[2] * 32, d)
+              B, H, T, C, d)
 
 
 def alibi_kv4_read(cache, k, v, pos=None, count=None, stream=None):
@@ -533,9 +544,12 @@ def alibi_kv4_read(cache, k, v, pos=None, count=None, stream=None):
         _explain_kv4(dtype, (k, "k", (4,)), [(v, "v", dtype, getattr(k, "shape", None))], cache,
                      k.shape[1] if hasattr(k, "shape") and len(k.shape) == 4 else None, [(pos, "pos"), (count, "count")])
     B, H, T, d = k.shape
+    C = cache.shape[2] * 32
+    if not 0 < T <= C <= 1 << 24:
+        _kv4_sizes(T, C, "alibi_kv4_read")
     _call_kv4(k.get_device(), lib.alibi_kv4_read, "alibi_kv4_read", stream, cache.data_ptr(), k.data_ptr(),
               v.data_ptr(), None if pos is None else pos.data_ptr(), None if count is None else count.data_ptr(),
-              B, H, T, cache.shape[2] * 32, d, int(dtype is float32))
+              B, H, T, C, d, int(dtype is float32))
     return k, v
 
 
@@ -577,8 +591,11 @@ def alibi_attn_decode_kv4(q, cache, lens=None, L=None, out=None, lse=None, slope
         if m.shape != (H,):
             raise ValueError(f"slopes: expected shape ({H},), got {m.shape}")
     C = c[2] * 32
+    L = C if L is None else int(L)
+    if not 0 < L <= C <= 1 << 24:
+        _kv4_sizes(L, C, "alibi_attn_decode_kv4")
     args = (q.data_ptr(), cache.data_ptr(), None if lens is None else lens.data_ptr(), out.data_ptr(), lse.data_ptr(), B, H,
-            c[1], shape[2] if dims == 4 else 1, C if L is None else int(L), C, d,
+            c[1], shape[2] if dims == 4 else 1, L, C, d,
             None if m is None else m.ctypes.data_as(ctypes.POINTER(ctypes.c_float)))
     if stream is None and current() == index:  # as _call_kv4 does it, without its 0.6 us
         status = lib.alibi_attn_decode_kv4(*args, raw_stream(index))
