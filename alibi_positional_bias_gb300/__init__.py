@@ -424,13 +424,20 @@ def alibi_kv4_cache(B: int, H: int, C: int, d: int, device=None):
 _names = None
 
 
+def _current_stream_handle(index: int) -> int:
+    import torch
+    return torch.cuda.current_stream(index).cuda_stream
+
+
 def _kv4_names():
     """(bfloat16, uint8, int32, float32, handle of a device's current stream, current device, the library)"""
     global _names
     if _names is None:
         import torch
-        _names = (torch.bfloat16, torch.uint8, torch.int32, torch.float32, torch._C._cuda_getCurrentRawStream,
-                  torch._C._cuda_getDevice, load())
+        # torch's own shortcuts, where it has them, take 0.06 and 0.1 us; its documented calls, 1.1 and 0.2 us, do the same
+        raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or _current_stream_handle
+        current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        _names = (torch.bfloat16, torch.uint8, torch.int32, torch.float32, raw_stream, current, load())
     return _names
 
 

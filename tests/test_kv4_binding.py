@@ -1,5 +1,6 @@
 """The binding of the 4-bit cache without a GPU: sizes that a C int does not hold, against a library that records its
-arguments and tensors that have a shape and an address only."""
+arguments and tensors that have a shape and an address only; and a torch without the private names that it shortens
+the way with."""
 import numpy as np
 import pytest
 import torch
@@ -90,3 +91,17 @@ def test_head_sizes_that_no_int_holds():
     for d in (BIG + 64, 2 ** 31, -BIG + 64):
         with pytest.raises(ab.AlibiError):
             ab.alibi_kv4_block_bytes(d)
+
+
+def test_a_torch_without_its_private_shortcuts(monkeypatch):
+    for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"):
+        monkeypatch.delattr(torch._C, name, raising=False)
+
+    class Stream:
+        cuda_stream = 77
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda index: Stream if index == 1 else None)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(ab, "load", lambda: "library")
+    monkeypatch.setattr(ab, "_names", None)
+    names = ab._kv4_names()
+    assert names[4](1) == 77 and names[5]() == 1 and names[6] == "library"
