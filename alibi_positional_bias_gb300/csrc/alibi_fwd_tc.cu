@@ -41,6 +41,7 @@
 
 #include <type_traits>
 
+#include "divide.h"
 #include "ptx.cuh"
 
 namespace alibi {
@@ -89,7 +90,7 @@ struct FwdParams {
     uint64_t wait_ns;  // limit of every bounded wait
     int test_skip_q0;  // failure-path self-test (mitigation kernels only): the producer leaves out the first item's Q tiles
     int N, BH, H, NQB, NQT, num_items;
-    FastDiv div_bh, div_h, div_nqb;  // by B*H, H and NQB
+    Divisor div_bh, div_h, div_nqb;  // by B*H, H and NQB
     int dr;  // the tensors' head size (<= D: the D = 64 kernel also serves d = 16 and 32)
     int causal;  // 1: keys j <= i only; 0: every key, distance |i - j|
     float c1;  // log2(e) / sqrt(d)
@@ -175,11 +176,11 @@ __device__ __forceinline__ Item decode_item(const FwdParams &p, int idx, bool ca
     int first = 0;
     if (p.plan) {
         const int2 e = p.plan[idx];
-        it.bh = fdiv(e.x, p.div_nqb);
+        it.bh = p.div_nqb.of(e.x);
         it.qb = e.x - it.bh * p.NQB;
         first = e.y;
     } else {
-        const int round = fdiv(idx, p.div_bh);
+        const int round = p.div_bh.of(idx);
         it.bh = idx - round * p.BH;
         it.qb = p.NQB - 1 - round;
     }
@@ -451,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(const __grid_consta
                     const int wn = item_index(kk);
                     if (wn >= p.num_items) return;
                     const Item tn = decode_item(p, wn, CAUSAL);
-                    const float bv = p.slopes.log2e[fmod_(tn.bh, p.div_h)] * static_cast<float>(r) / p.c1;
+                    const float bv = p.slopes.log2e[p.div_h.rest(tn.bh)] * static_cast<float>(r) / p.c1;
                     write_bias_row(smem + C::kAux, r, kk & 1, bv);
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -463,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(const __grid_consta
             if (s == 1 && !t.q1valid) continue;
             const int qt = 2 * t.qb + s;
             const int i = qt * BM + r;
-            const float sl2 = p.slopes.log2e[fmod_(t.bh, p.div_h)];
+            const float sl2 = p.slopes.log2e[p.div_h.rest(t.bh)];
             const int it0 = (s == 0 && t.q1valid && CAUSAL) ? 1 : 0;
             float M = -INFINITY, l = 0.f;
             for (int it = it0; it < t.n; ++it) {
@@ -498,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(const __grid_consta
                     //            -m log2(D + 1) in base 2), clamped from below.
                     const bool cap = p.variant & kFwdSoftcap, logd = p.variant & kFwdLogDist,
                                clamp = p.variant & kFwdClamp;
-                    const float mnat = p.slopes.nat[fmod_(t.bh, p.div_h)];
+                    const float mnat = p.slopes.nat[p.div_h.rest(t.bh)];
                     const float di = static_cast<float>(i - j * BN);  // exact: |i - k0| < 2^24
 #pragma unroll
                     for (int c = 0; c < BN; ++c) {
@@ -699,9 +700,9 @@ static cudaError_t launch_fwd_tc_d(const void *q, const void *k, const void *v, 
     p.NQT = (N + BM - 1) / BM;
     p.NQB = (p.NQT + 1) / 2;
     p.num_items = p.NQB * p.BH;
-    p.div_bh = make_fastdiv(static_cast<uint32_t>(p.BH));
-    p.div_h = make_fastdiv(static_cast<uint32_t>(H));
-    p.div_nqb = make_fastdiv(static_cast<uint32_t>(p.NQB));
+    p.div_bh = Divisor(static_cast<uint32_t>(p.BH));
+    p.div_h = Divisor(static_cast<uint32_t>(H));
+    p.div_nqb = Divisor(static_cast<uint32_t>(p.NQB));
     p.causal = causal;
     p.c1 = 1.4426950408889634f / sqrtf(static_cast<float>(dr));
     p.slopes = slopes;

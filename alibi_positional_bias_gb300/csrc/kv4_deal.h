@@ -8,6 +8,7 @@
 #include <cfloat>
 #include <cmath>
 
+#include "divide.h"
 #include "kv4.h"
 
 namespace alibi {
@@ -31,22 +32,7 @@ KV4_HD int divide(long long a, int b)
     return a < (1LL << 32) ? static_cast<int>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : static_cast<int>(a / b);
 }
 
-// Division of 0 <= n < 2^31 by a number that the host knows, by multiplication (Granlund and Montgomery, 1994).
-struct Divisor {
-    uint32_t magic, shift;
-
-    Divisor() = default;
-    explicit Divisor(uint32_t d)
-    {
-        for (shift = 0; (1u << shift) < d;) ++shift;
-        magic = static_cast<uint32_t>(((1ull << 32) * ((1ull << shift) - d)) / d + 1);
-    }
-    KV4_HD int of(int n) const
-    {
-        const uint32_t x = static_cast<uint32_t>(n);
-        return static_cast<int>((static_cast<uint32_t>(static_cast<uint64_t>(x) * magic >> 32) + x) >> shift);
-    }
-};
+using alibi::Divisor;
 
 // Equal shares: share `i` of `ctas` of a row of `row` stages is [i row / n, (i + 1) row / n), n = least(ctas, row).
 // Divisions in 32 bits where the row allows it (all but sequences of many millions of tokens in all).
