@@ -113,6 +113,15 @@ def test_reference_properties():
     assert off[~near].max() <= 0.5 and off.max() <= 1.0
 
 
+def test_the_smoke_check_has_the_definition_of_its_own():
+    import __graft_entry__ as entry
+    rng = np.random.default_rng(8)
+    x = gen.make_tensor(rng.standard_normal((50, 64)), (50, 64), "bf16").f32
+    x[:8, 5] *= 2.0 ** np.arange(-4, 4)  # ties and clamped codes too
+    x[9], x[10, 32:], x[11, 3], x[11, 4] = 0.0, 2.0 ** -101, 4.0, -4.0
+    assert np.array_equal(entry.held_in_4_bits(x), ref.held(x.astype(np.float64)).astype(np.float32))
+
+
 P = ctypes.c_void_p(0x10000)  # never dereferenced: arguments are checked before any CUDA call
 MIS = ctypes.c_void_p(0x10008)
 ODD = ctypes.c_void_p(0x10002)
