@@ -373,7 +373,8 @@ __device__ __forceinline__ void block32(State<D, KC> &st, const uint8_t *blk, in
             for (int i = 0; i < 4; ++i) mx = fmaxf(mx, x[i][k]);
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-            const float was = st.R[k], r = fmaxf(was, was == -FLT_MAX ? mx : was + ceilf(mx - was));
+            // the sum may round below mx, from 2^24 on
+            const float was = st.R[k], r = fmaxf(was == -FLT_MAX ? was : was + ceilf(fmaxf(mx - was, 0.0f)), mx);
             const float up = fminf(r - was, 1000.0f);
             st.l[k] *= ex2_approx(-up);
             st.R[k] = r;

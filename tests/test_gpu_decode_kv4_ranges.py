@@ -130,3 +130,25 @@ def test_more_than_256_query_heads(ab, Hkv, G, T, d):
     q, k, v = case(Hkv, 2, Hkv, G, T, 64, d)
     compare(ab, q, k, v, [64, 37])
     compare(ab, q, k, v, [50, 64], m=np.linspace(0.0, 1.5, Hkv * G))
+
+
+@pytest.mark.parametrize("G,d", [(1, 64), (8, 64), (2, 128), (8, 128), (1, 32)])
+@pytest.mark.parametrize("step", [2.0 ** 18, 3e8, 7e9, 1e15, 1e33])
+def test_logits_far_beyond_whole_numbers_in_fp32(ab, G, d, step):
+    # logits that grow towards the oldest token, up to some 25 `step`: the reference moves in nearly every block, by numbers
+    # that fp32 rounds to more than one. Only the oldest tokens, whose keys are equal in bf16, have a weight: two products off
+    # by 2^-11 at most, a mean and a rounding of 2^-9
+    rng = np.random.default_rng(d)
+    N = 700
+    q = np.ones((1, G, 1, d))
+    k = exact_bf16(np.broadcast_to(3.0 * step * np.linspace(1.0, 1.0 / 400.0, N)[:, None], (1, 1, N, d)))
+    v = exact_bf16(rng.standard_normal((1, 1, N, d)) * 2.0 ** 100)
+    compare(ab, q, k, v, [N], m=np.zeros(G))
+    import torch
+    cache = torch.from_numpy(ref.pack(k, v, 704)).cuda()
+    qd = torch.ones(1, G, 1, d, dtype=torch.bfloat16, device="cuda")
+    out, _ = ab.alibi_attn_decode_kv4(qd, cache, lens=torch.tensor([N], dtype=torch.int32, device="cuda"),
+                                      slopes=np.zeros(G, dtype=np.float32))
+    logits = ref.held(k)[0, 0].sum(-1)
+    first = ref.held(v)[0, 0, logits == logits.max()]
+    assert np.abs(host64(out)[0, :, 0] - first.mean(0)).max() <= (2.0 ** -9 + 2.0 ** -10) * np.abs(first).max()
