@@ -513,7 +513,7 @@ __device__ __forceinline__ void finish(__nv_bfloat16 *out, float *lse, int d, si
 // that writes the lengths may still run.
 __device__ __forceinline__ int length_of(const DecodeKv4Params &p, int b, bool &bad)
 {
-    const int n = p.lens ? __ldcg(p.lens + b) : p.L;
+    const int n = p.lens ? p.lens[b] : p.L;
     bad = n < 0 || n > p.L;
     return bad ? 0 : n;
 }
