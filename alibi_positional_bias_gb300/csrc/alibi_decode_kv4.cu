@@ -37,14 +37,17 @@
 //            nothing and its values are not multiplied.
 //
 // mma.sync and not tcgen05.mma: the operands are made in registers, where tcgen05 would have to be
-// fed through shared or tensor memory, and at 8 columns the tensor pipe is 19% busy.
+// fed through shared or tensor memory, and at 8 columns the tensor pipe is 20% busy.
 //
 // What has to move: 1.125 d bytes per key and KV head, once. 64 x 40 heads of 8192 tokens, d = 128
-// (3.0 GB): 412 us, 7.3 TB/s, 108% of the measured copy (which also writes). With fewer CTAs than
-// SMs' room a warp's own chain bounds a block of 32 tokens (1100 cycles for the keys, 1800 with the values,
-// at 2 warps per scheduler), and about 6 us of first loads and merge come on
-// top: 1 x 40 x 8192, 47 MB, 13.0 us. 16 warps per SM are what 128 registers allow; the ring of 3 stages
-// per warp keeps 147 KB in flight.
+// (3.0 GB): 413 us, 7.3 TB/s, 109% of the measured copy (which also writes); 565 instructions of a warp per block of 32
+// tokens at 1 x 40 x 8192, start and merge included. With fewer CTAs than
+// SMs' room a warp's own chain bounds a block (about 1300 cycles where the values are skipped and 1900 with them,
+// at 2 warps per scheduler: 1 x 8 (x 4) x 8192 and 32768 tokens with a CTA each 30 and 89 us, 1 x 40 x 8192 without bias 33),
+// and about 6 us of first loads, merge and an uneven last round of stages come on
+// top: 1 x 40 x 8192, 47 MB, 13.0 us. 16 warps per SM are what 128 registers allow (of d = 128 the kernels of clusters and
+// shares with one row per lane keep 16 and 32 bytes of a thread in local memory, that of shares with two 4); the ring of 3
+// stages per warp keeps 147 KB in flight.
 //
 // The work is dealt in one of four ways (deal_of), by lengths that only the device knows:
 //   whole    a CTA takes one chunk: short sequences, and many chunks;
@@ -240,7 +243,10 @@ __device__ __forceinline__ uint32_t under1024(uint32_t w, uint32_t mask)
     return d;
 }
 
-// The codes of a word as four fp16 pairs: r[i] = (u_i - 8, u_{i+4} - 8).
+// The codes of a word as four fp16 pairs: r[i] = (u_i - 8, u_{i+4} - 8). Bits under the exponent of 1024, or of 1024 over
+// their place, as a number whose offset one operation takes off: the conversion published by Kim, Henry, Fahim and Hassan
+// Awadalla, "Who Says Elephants Can't Run: Bringing Large Scale MoE Models into Cloud Scale Production" (2022). The order
+// of the codes in a word is this cache's own (kv4.h).
 __device__ __forceinline__ void unpack(uint32_t w, uint32_t (&r)[4])
 {
     constexpr uint32_t k1032 = 0x64086408u, kSixteenth = 0x2c002c00u, kMinus72 = 0xd480d480u;

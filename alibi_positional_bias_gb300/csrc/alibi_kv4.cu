@@ -11,14 +11,19 @@
 //
 // What has to move: 4 d bytes of a token's key and value and 1.125 d of the cache. Prompts
 // go a block per CTA, the cache in whole 16-byte words of a thread, the rows in 64-byte
-// segments, no shared memory. Written and read, d = 128: 4 x 32 heads x 2048 tokens 31.1 and
-// 29.6 us (172 MB each: 5.5 and 5.8 TB/s), 8 x 32 x 2048 56.2 and 54.2 us (6.1 and
-// 6.3 TB/s, 90 and 93% of the measured copy). The write is bound by memory's latency and the logic pipe (59% busy, 68% of
+// segments, no shared memory. Written and read back, calls in one graph over sets of tensors that together are larger
+// than L2, in us and TB/s (the measured copy: 6.7):
+//   4 x 32 heads x 2048 tokens, d = 128    28.2 (6.1)   26.4 (6.5)   as fp32 47.5 (6.5)
+//   8 x 32 x 2048, d = 128                 53.0 (6.5)   50.3 (6.8)   91.5 (6.7)
+//   8 x 32 x 4096, d = 64                  56.0 (6.1)   52.9 (6.5)   90.7 (6.7)
+//   8 x 32 x 8192, d = 32                  66.2 (5.2)   61.3 (5.6)   93.3 (6.6)
+//   64 x 40 x 1, d = 128                    3.0          3.3          3.4
+// The write is bound by memory's latency and the logic pipe (59% busy, 68% of
 // issue slots): 10 operations per element, of which the group's largest takes 1, the codes 4;
-// one thread per 8 elements with 16-bit stores of the values took 161 us for both. A step's new
-// token of 64 x 40 heads takes 3.1 us, a launch's time. Every launch overlaps the end of the kernel before it (each kernel
-// waits for that before it touches memory): a call after another takes 3.1 and not 4.1 us, large ones written and read in
-// turn 52.9 and not 58 us.
+// one thread per 8 elements with 16-bit stores of the values took 161 us for the first case's two calls. A step's new
+// token takes a launch's time. Every launch overlaps the end of the kernel before it (each kernel
+// waits for that before it touches memory): the first case written and read in turn takes 54.3 and not 55.7 us, 64 x 40 x 16
+// tokens 18.0 and not 19.3; a single token's two calls, 6.8 us, take 6.5 without.
 
 #include <algorithm>
 #include <cuda_bf16.h>
@@ -466,14 +471,14 @@ int check_sizes(int B, int H, int T, int C, int d)
     return ALIBI_OK;
 }
 
-// Tokens per sequence from which a CTA takes a block and not single rows. (In us, rows / blocks: 64 x 40 heads of d = 128,
-// 8 tokens written 5.9 / 11.2, read 5.8 / 6.7; 12 tokens 8.4 / 11.8 and 8.1 / 7.3; 16 tokens 10.8 / 12.5 and 10.3 / 8.0;
-// 24 tokens 15.6 / 13.6 and 14.8 / 9.3. 64 x 8 heads of d = 64: 16 tokens 2.7 / 3.1 and 2.7 / 2.3, 24 tokens 3.2 / 3.1 and
-// 3.1 / 2.4.)
+// Tokens per sequence from which a CTA takes a block and not single rows. (In us, rows / blocks, at odd rows of a cache of
+// 2048 tokens, which touch two blocks: 64 x 40 heads of d = 128, 8 tokens written 7.5 / 11.7, read 7.4 / 7.6; 12 tokens
+// 10.1 / 12.4 and 9.7 / 8.4; 16 tokens 12.6 / 13.1 and 12.2 / 9.2; 20 tokens 15.1 / 13.7 and 14.3 / 9.8; 24 tokens
+// 17.5 / 14.4 and 16.7 / 10.6. 64 x 8 heads of d = 64: 16 tokens 2.8 / 3.2 and 2.7 / 2.5, 24 tokens 3.2 / 3.2 and 3.2 / 2.6.)
 constexpr int kWriteBlocks = 20, kReadBlocks = 10;
 // Blocks of a head that a CTA takes one after another where there are more than a CTA each that is resident: of d = 32 (and
-// 16), where beginning a CTA costs as much as a block, 4 (8 x 32 x 8192 tokens written and read in 68 and 64 us, with one
-// each in 82 and 77); of d = 64 one (8 x 32 x 4096 tokens written in 59.6 us, with two in 61.8).
+// 16), where beginning a CTA costs as much as a block, 4 (8 x 32 x 8192 tokens written and read in 66 and 62 us, with one
+// each in 92 and 81); of d = 64 one (8 x 32 x 4096 tokens written and read in 56.3 and 53.2 us, with two in 58.6 and 52.0).
 constexpr int kRun = 4;
 
 template <int d>

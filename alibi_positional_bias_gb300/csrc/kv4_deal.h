@@ -104,22 +104,39 @@ struct ClusterFit {
 // one take 0.15 to 0.2 each, the more the fuller the device; several rounds of whole chunks, and slices and shares, which
 // fill it, run as fast as memory goes, whole chunks with a tail of the last round. A launch takes 3.4, the merge of a
 // cluster 1.6 more, the partials and their merge kernel 4.9 (slices) or, with what a share pays to begin its next chunk,
-// 9.6 (shares). Measured, in us, launches in one graph, caches colder than L2, whole / clusters of / slices / shares:
-//   sequences x KV heads (x G) x tokens x d   1 x 32 x 2048 x 128        10.5 / 6.5 (8) 7.6 (5) 6.6 (4) / 9.5 / 9.7
-//                                             1 x 40 x 8192 x 128        31.6 / 13.1 (6) 16.6 (7) 14.9 (3) / 16.0 / 19.2
-//                                             1 x 8 (x 4) x 8192 x 128   31.0 / 7.1 (12) 8.4 (16) 7.9 (8) / 9.5 / 9.7
-//                                             1 x 8 (x 4) x 32768 x 128  90.7 / 12.7 (12) 15.2 (16) 16.5 (8) / 14.1 / 15.2
-//                                             1 x 4 (x 4) x 131071 x 128  331 / 27.7 (16) / 21.6 / 22.5
-//                                             4 x 8 (x 8) x 8192 x 128   35.1 / 12.5 (8) / 16.5 / 20.6
-//                                             2 x 40 x 8192 x 128        31.7 / 20.6 (3) 23.1 (2) / 25.3 / 27.5
-//                                             2 x 40 x 1024 x 128         7.2 / 7.9 (2) 7.6 (3) / 10.6 / 13.1
-//                                             4 x 40 x 4096 x 128        21.0 / 23.9 (2) /    - / 27.4
-//                                             16 x 8 (x 4) x 4097 x 128  19.9 / 17.8 (2) / 21.3 / 23.7
-//                                             8 x 8 (x 4) x 16384 x 128  52.7 / 27.8 (4) 36.6 (5) / 33.8 / 37.8
-//                                             8 x 8 (x 8) x 32768 x 128   105 / 50.9 (4) / 61.0 / 65.8
-//                                             9 x 37 x 16384 x 128        153 /    - /    - / 130
-//                                             16 x 40 x 4096 x 128       64.8 /    - /    - / 68.8
-//                                             64 x 40 x 8192 x 128        412 /    - /    - / 494
+// 9.6 (shares). The estimate was fitted at d = 128 with default slopes and knows neither the head size, the rows of a
+// chunk nor the slopes; of all cases measured it takes the fastest way or one within 6% of it. Measured, in us, launches in
+// one graph, caches colder than L2, whole / clusters of / slices / shares, the way taken first in brackets:
+//   sequences x KV heads (x G) x tokens x d
+//   1 x 32 x 2048 x 128        [8]   10.2 / 6.9 (8) 6.7 (4) 7.8 (5) / 9.6 / 9.8
+//   1 x 40 x 8192 x 128        [6]   30.7 / 13.2 (6) 14.5 (3) / 15.8 / 19.6
+//   1 x 8 (x 4) x 8192 x 128   [12]  29.9 / 7.0 (12) 7.8 (8) 8.4 (16) / 9.8 / 9.9
+//   1 x 8 (x 4) x 32768 x 128  [12]  88.6 / 12.6 (12) 15.9 (8) 15.2 (16) / 14.2 / 15.4
+//   1 x 4 (x 4) x 131071 x 128 [S]   323 / 26.5 (16) / 21.7 / 21.8
+//   4 x 8 (x 8) x 8192 x 128   [8]   37.6 / 13.5 (8) 14.2 (4) / 16.8 / 21.3
+//   2 x 40 x 8192 x 128        [3]   30.6 / 20.0 (3) 22.5 (2) / 25.5 / 27.4
+//   2 x 40 x 1024 x 128        [W]   7.2 / 7.9 (2) 7.9 (3) / 10.7 / 13.4
+//   4 x 40 x 4096 x 128        [W]   21.3 /    - /    - / 27.1
+//   16 x 8 (x 4) x 4097 x 128  [2]   19.5 / 17.6 (2) / 21.4 / 24.4
+//   8 x 8 (x 4) x 16384 x 128  [4]   50.5 / 28.1 (4) 30.3 (2) / 34.0 / 38.3
+//   8 x 8 (x 8) x 32768 x 128  [4]   119.5 / 52.8 (4) / 61.3 / 61.9
+//   9 x 37 x 16384 x 128       [E]   154 /    - /    - / 129.6
+//   16 x 40 x 4096 x 128       [W]   64.6 /    - /    - / 68.4
+//   64 x 40 x 8192 x 128       [W]   413 /    - /    - / 494 (of an earlier kernel)
+//   1 x 32 x 8192 x 64         [8]   19.0 / 8.6 (8) 8.8 (4) / 11.4 / 14.1
+//   8 x 16 (x 2) x 4 new, 2048 x 64  [W]  8.9 / 10.0 (2) / 15.3 / 18.1
+//   1 x 8 (x 8) x 16384 x 64   [12]  35.9 / 7.9 (12) 8.6 (8) / 10.3 / 10.5
+//   4 x 16 x 16384 x 64        [4]   32.1 / 16.6 (4) / 21.1 / 23.3
+//   1 x 2 (x 4) x 131071 x 64  [S]   200 / 16.5 (16) / 12.9 / 13.5
+//   1 x 32 x 16384 x 32        [8]   20.5 / 8.9 (8) / 11.8 / 14.2
+//   8 x 8 (x 4) x 16384 x 32   [4]   21.4 / 12.9 (4) / 15.9 / 18.9
+//   24 x 7 x 14336 x 32        [W]   27.3 /    - /    - / 27.1
+//   1 x 4 (x 8) x 65536 x 32   [16]  80.1 / 9.6 (16) / 10.2 / 10.4
+//   no bias:
+//   1 x 40 x 8192 x 128        [6]   33.5 / 15.3 (6) 15.8 (3) / 17.2 / 19.9
+//   2 x 40 x 8192 x 128        [3]   33.8 / 24.1 (3) / 27.4 / 27.4
+//   16 x 8 (x 4) x 4097 x 128  [2]   19.8 / 20.0 (2) / 24.4 / 25.5
+//   1 x 8 (x 8) x 32768 x 128  [12]  148 / 18.3 (12) / 17.4 / 17.6
 inline Plan deal_of(long long units, int stages, int ctas, const ClusterFit &fit)
 {
     if (stages <= kWarps) return {Deal::Whole, 1};
