@@ -46,8 +46,8 @@
 // at 2 warps per scheduler: 1 x 8 (x 4) x 8192 and 32768 tokens with a CTA each 30 and 89 us, 1 x 40 x 8192 without bias 33),
 // and about 6 us of first loads, merge and an uneven last round of stages come on
 // top: 1 x 40 x 8192, 47 MB, 13.0 us. 16 warps per SM are what 128 registers allow (of d = 128 the kernels of clusters and
-// shares with one row per lane keep 16 and 32 bytes of a thread in local memory, that of shares with two 4); the ring of 3
-// stages per warp keeps 147 KB in flight.
+// shares keep 4 to 32 bytes of a thread in local memory, that of whole chunks none); the ring of 3 stages
+// per warp keeps 147 KB in flight.
 //
 // The work is dealt in one of four ways (deal_of), by lengths that only the device knows:
 //   whole    a CTA takes one chunk: short sequences, and many chunks;
@@ -311,18 +311,22 @@ __device__ __forceinline__ void block32(State<D, KC> &st, const uint8_t *blk, in
             }
         }
     }
-    const float jf = static_cast<float>(j0);
+    // token less position, in whole numbers below 2^24: exact
+    const auto behind = [&](int i, int k) { return static_cast<float>(j0 + 8 * i) - st.pos[k]; };  // pos is less g
+    const auto seen = [&](int i, int k) { return !MASK || behind(i, k) <= 0.0f; };
 #pragma unroll
     for (int k = 0; k < KC; ++k) {
-        const float bias = st.slope[k] * (jf - st.pos[k]);  // whole numbers below 2^24: exact; pos is less g
+        // Where all tokens are seen, from the nearest one on, so that no bias is off by more than two roundings of its own
+        // size; else each by itself, so that the nearest one's is exact wherever it stands.
+        const float nearest = st.slope[k] * behind(3, k);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[i][k] = fmaf(st.kappa[k], x[i][k], i == 0 ? bias : fmaf(8.0f * i, st.slope[k], bias));
-            if (MASK && jf + 8.0f * i > st.pos[k]) x[i][k] = -INFINITY;
-        }
+        for (int i = 0; i < 4; ++i)
+            if constexpr (MASK)
+                x[i][k] = seen(i, k) ? fmaf(st.kappa[k], x[i][k], st.slope[k] * behind(i, k)) : -INFINITY;
+            else
+                x[i][k] = fmaf(st.kappa[k], x[i][k], i == 3 ? nearest : fmaf(8.0f * (i - 3), st.slope[k], nearest));
     }
 
-    const auto seen = [&](int i, int k) { return !MASK || !(jf + 8.0f * i > st.pos[k]); };
     // scale of group n of token i: the word it lies in, and itself from that word (or the word's multiple)
     const auto scales = [&](int i, int n) { return sv[i][NG == 1 ? 0 : NG / 2 + n / 2]; };
     const auto scale = [](uint32_t word, int n) { return NG == 1 || (n & 1) ? bf16_hi(word) : bf16_lo(word); };

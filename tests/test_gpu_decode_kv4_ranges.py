@@ -152,3 +152,45 @@ def test_logits_far_beyond_whole_numbers_in_fp32(ab, G, d, step):
     logits = ref.held(k)[0, 0].sum(-1)
     first = ref.held(v)[0, 0, logits == logits.max()]
     assert np.abs(host64(out)[0, :, 0] - first.mean(0)).max() <= (2.0 ** -9 + 2.0 ** -10) * np.abs(first).max()
+
+
+@pytest.mark.parametrize("T,d", [(1, 64), (3, 128), (1, 32)])
+def test_large_slopes_at_every_length_of_a_block(ab, T, d):
+    # the bias of the query's own token is 0 wherever in a block it stands, and that of the one before it the slope
+    B = 33
+    q, k, v = case(T, B, 1, 6, T, 320, d)
+    compare(ab, q, k, v, list(range(288, 288 + B)), m=[0.0, 3.0, 1e3, 1e4, 1e10, 1e30])
+
+
+def magnitudes(rng, x, lo, hi):
+    """x times powers of two: none, one for all, one per group of 32, one per token, or with most elements zero."""
+    d, kind = x.shape[-1], rng.integers(0, 5)
+    if kind == 1:
+        return x * 2.0 ** rng.integers(lo, hi)
+    if kind == 2:
+        return x * np.repeat(2.0 ** rng.integers(lo // 2, hi // 2, size=max(1, d // 32)), min(32, d))
+    if kind == 3:
+        return x * 2.0 ** rng.integers(lo // 3, hi // 3, size=x.shape[:-1] + (1,))
+    return x * (rng.random(x.shape) < 0.2) if kind == 4 else x
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_random_calls(ab, seed):
+    rng = np.random.default_rng(1000 + seed)
+    d = int(rng.choice([16, 32, 64, 128]))
+    B, Hkv, N = int(rng.integers(1, 5)), int(rng.integers(1, 4)), max(1, int(np.exp(rng.uniform(0.0, np.log(3000.0)))))
+    G, T = int(rng.choice([1, 1, 2, 3, 5, 8, 11])), int(rng.choice([1, 1, 1, 2, 4, 7, 16]))
+    q, k, v = (rng.standard_normal(s) for s in ((B, Hkv * G, T, d), (B, Hkv, N, d), (B, Hkv, N, d)))
+    s = int(rng.integers(-60, 110)) if seed % 2 else 0
+    k, q, v = k * 2.0 ** s, q * 2.0 ** max(-120, -s), magnitudes(rng, v, -90, 110)
+    if seed % 3 == 0:
+        g = np.repeat(2.0 ** rng.integers(-40, 40, size=max(1, d // 32)), min(32, d))
+        q, k = q * g, k / g
+    big = 255 * 2.0 ** 120
+    q, k, v = (exact_bf16(np.clip(x, -big, big)) for x in (q, k, v))
+    lens = [int(rng.choice([N, rng.integers(1, N + 1), min(N, int(rng.integers(1, 4)))])) for _ in range(B)]
+    lens = [max(n, T) for n in lens] if N >= T else [N] * B
+    if N < T:
+        q, T = q[:, :, :1], 1
+    m = None if seed % 5 < 2 else rng.choice([0.0, 1e-3, 0.3, 5.0, 1e4]) * rng.random(Hkv * G)
+    compare(ab, q, k, v, lens, m=m, what=(B, Hkv, G, T, N, d, lens))
