@@ -40,12 +40,12 @@
 // fed through shared or tensor memory, and at 8 columns the tensor pipe is 20% busy.
 //
 // What has to move: 1.125 d bytes per key and KV head, once. 64 x 40 heads of 8192 tokens, d = 128
-// (3.0 GB): 413 us, 7.3 TB/s, 109% of the measured copy (which also writes); 565 instructions of a warp per block of 32
+// (3.0 GB): 408 to 413 us, 7.3 to 7.4 TB/s, 109 to 111% of the measured copy (which also writes); 565 instructions of a warp per block of 32
 // tokens at 1 x 40 x 8192, start and merge included. With fewer CTAs than
 // SMs' room a warp's own chain bounds a block (about 1300 cycles where the values are skipped and 1900 with them,
-// at 2 warps per scheduler: 1 x 8 (x 4) x 8192 and 32768 tokens with a CTA each 30 and 89 us, 1 x 40 x 8192 without bias 33),
+// at 2 warps per scheduler: 1 x 8 (x 4) x 8192 and 32768 tokens with a CTA each 30 and 88 us, 1 x 40 x 8192 without bias 34),
 // and about 6 us of first loads, merge and an uneven last round of stages come on
-// top: 1 x 40 x 8192, 47 MB, 13.0 us. 16 warps per SM are what 128 registers allow (of d = 128 the kernels of clusters and
+// top: 1 x 40 x 8192, 47 MB, 13.2 us. 16 warps per SM are what 128 registers allow (of d = 128 the kernels of clusters and
 // shares keep 4 to 32 bytes of a thread in local memory, that of whole chunks none); the ring of 3 stages
 // per warp keeps 147 KB in flight.
 //
@@ -776,8 +776,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kv4_kernel(const __grid
             if (!__all_sync(0xffffffffu, ok)) break;
             const uint8_t *stage = mine + slot * kStageBytes;
             // Of one row per lane and d = 128 the masked form takes every block: a second copy of the loop's body costs more
-            // there than the masks (64 x 40 x 8192 tokens 424 us with two copies, 413 with one; d = 32 27.1 and 28.0 at
-            // 24 x 7 x 14336, two rows per lane 55.1 and 58.0 at 8 x 8 (x 8) x 32768; d = 64 the same at 8 x 38 x 16384).
+            // there than the masks (64 x 40 x 8192 tokens 419 us with two copies, 412 with one; d = 32 28.0 and 29.2 at
+            // 24 x 7 x 14336, two rows per lane 53.1 and 55.5 at 8 x 8 (x 8) x 32768; d = 64 57.4 and 57.6 at 8 x 38 x 16384).
             constexpr bool kOneForm = KC == 1 && D == 128;
 #pragma unroll 1
             for (int t = SB - 1; t >= 0; --t) {

@@ -105,38 +105,38 @@ struct ClusterFit {
 // fill it, run as fast as memory goes, whole chunks with a tail of the last round. A launch takes 3.4, the merge of a
 // cluster 1.6 more, the partials and their merge kernel 4.9 (slices) or, with what a share pays to begin its next chunk,
 // 9.6 (shares). The estimate was fitted at d = 128 with default slopes and knows neither the head size, the rows of a
-// chunk nor the slopes; of all cases measured it takes the fastest way or one within 6% of it. Measured, in us, launches in
+// chunk nor the slopes; of all cases measured it takes the fastest way or one within 8% of it. Measured, in us, launches in
 // one graph, caches colder than L2, whole / clusters of / slices / shares, the way taken first in brackets:
 //   sequences x KV heads (x G) x tokens x d
-//   1 x 32 x 2048 x 128        [8]   10.2 / 6.9 (8) 6.7 (4) 7.8 (5) / 9.6 / 9.8
-//   1 x 40 x 8192 x 128        [6]   30.7 / 13.2 (6) 14.5 (3) / 15.8 / 19.6
-//   1 x 8 (x 4) x 8192 x 128   [12]  29.9 / 7.0 (12) 7.8 (8) 8.4 (16) / 9.8 / 9.9
-//   1 x 8 (x 4) x 32768 x 128  [12]  88.6 / 12.6 (12) 15.9 (8) 15.2 (16) / 14.2 / 15.4
-//   1 x 4 (x 4) x 131071 x 128 [S]   323 / 26.5 (16) / 21.7 / 21.8
-//   4 x 8 (x 8) x 8192 x 128   [8]   37.6 / 13.5 (8) 14.2 (4) / 16.8 / 21.3
-//   2 x 40 x 8192 x 128        [3]   30.6 / 20.0 (3) 22.5 (2) / 25.5 / 27.4
-//   2 x 40 x 1024 x 128        [W]   7.2 / 7.9 (2) 7.9 (3) / 10.7 / 13.4
-//   4 x 40 x 4096 x 128        [W]   21.3 /    - /    - / 27.1
-//   16 x 8 (x 4) x 4097 x 128  [2]   19.5 / 17.6 (2) / 21.4 / 24.4
-//   8 x 8 (x 4) x 16384 x 128  [4]   50.5 / 28.1 (4) 30.3 (2) / 34.0 / 38.3
-//   8 x 8 (x 8) x 32768 x 128  [4]   119.5 / 52.8 (4) / 61.3 / 61.9
-//   9 x 37 x 16384 x 128       [E]   154 /    - /    - / 129.6
-//   16 x 40 x 4096 x 128       [W]   64.6 /    - /    - / 68.4
-//   64 x 40 x 8192 x 128       [W]   413 /    - /    - / 494 (of an earlier kernel)
-//   1 x 32 x 8192 x 64         [8]   19.0 / 8.6 (8) 8.8 (4) / 11.4 / 14.1
-//   8 x 16 (x 2) x 4 new, 2048 x 64  [W]  8.9 / 10.0 (2) / 15.3 / 18.1
-//   1 x 8 (x 8) x 16384 x 64   [12]  35.9 / 7.9 (12) 8.6 (8) / 10.3 / 10.5
-//   4 x 16 x 16384 x 64        [4]   32.1 / 16.6 (4) / 21.1 / 23.3
-//   1 x 2 (x 4) x 131071 x 64  [S]   200 / 16.5 (16) / 12.9 / 13.5
-//   1 x 32 x 16384 x 32        [8]   20.5 / 8.9 (8) / 11.8 / 14.2
-//   8 x 8 (x 4) x 16384 x 32   [4]   21.4 / 12.9 (4) / 15.9 / 18.9
-//   24 x 7 x 14336 x 32        [W]   27.3 /    - /    - / 27.1
-//   1 x 4 (x 8) x 65536 x 32   [16]  80.1 / 9.6 (16) / 10.2 / 10.4
+//   1 x 32 x 2048 x 128        [8]   10.3 / 7.0 (8) 6.7 (4) 7.9 (5) / 9.7 / 9.9
+//   1 x 40 x 8192 x 128        [6]   31.4 / 13.5 (6) 14.6 (3) / 15.6 / 19.8
+//   1 x 8 (x 4) x 8192 x 128   [12]  29.7 / 7.1 (12) 7.9 (8) 8.6 (16) / 9.9 / 10.0
+//   1 x 8 (x 4) x 32768 x 128  [12]  88.2 / 12.8 (12) 16.3 (8) 15.9 (16) / 14.3 / 15.4
+//   1 x 4 (x 4) x 131071 x 128 [S]   320 / 27.3 (16) / 21.0 / 22.0
+//   4 x 8 (x 8) x 8192 x 128   [8]   37.6 / 13.8 (8) 14.4 (4) / 16.5 / 21.3
+//   2 x 40 x 8192 x 128        [3]   30.4 / 20.6 (3) 23.9 (2) / 25.1 / 27.2
+//   2 x 40 x 1024 x 128        [W]   7.2 / 8.1 (2) 7.8 (3) / 10.7 / 13.5
+//   4 x 40 x 4096 x 128        [W]   22.3 /    - /    - / 26.8
+//   16 x 8 (x 4) x 4097 x 128  [2]   19.4 / 17.9 (2) / 21.4 / 24.3
+//   8 x 8 (x 4) x 16384 x 128  [4]   51.5 / 27.0 (4) 31.0 (2) / 33.6 / 37.7
+//   8 x 8 (x 8) x 32768 x 128  [4]   119.2 / 53.4 (4) / 60.7 / 61.6
+//   9 x 37 x 16384 x 128       [E]   153.5 /    - /    - / 127.9
+//   16 x 40 x 4096 x 128       [W]   64.5 /    - /    - / 68.3
+//   64 x 40 x 8192 x 128       [W]   408 /    - /    - / 494 (of an earlier kernel)
+//   1 x 32 x 8192 x 64         [8]   19.2 / 8.5 (8) 8.8 (4) / 11.4 / 13.9
+//   8 x 16 (x 2) x 4 new, 2048 x 64  [W]  8.8 / 10.0 (2) / 15.4 / 18.3
+//   1 x 8 (x 8) x 16384 x 64   [12]  35.9 / 7.8 (12) 8.7 (8) / 10.4 / 10.6
+//   4 x 16 x 16384 x 64        [4]   32.3 / 16.3 (4) / 20.0 / 22.7
+//   1 x 2 (x 4) x 131071 x 64  [S]   197 / 16.5 (16) / 13.0 / 13.5
+//   1 x 32 x 16384 x 32        [8]   21.0 / 8.8 (8) / 11.8 / 14.2
+//   8 x 8 (x 4) x 16384 x 32   [4]   21.5 / 12.5 (4) / 15.7 / 18.6
+//   24 x 7 x 14336 x 32        [W]   28.1 /    - /    - / 27.4
+//   1 x 4 (x 8) x 65536 x 32   [16]  81.3 / 9.7 (16) / 10.4 / 10.5
 //   no bias:
-//   1 x 40 x 8192 x 128        [6]   33.5 / 15.3 (6) 15.8 (3) / 17.2 / 19.9
-//   2 x 40 x 8192 x 128        [3]   33.8 / 24.1 (3) / 27.4 / 27.4
-//   16 x 8 (x 4) x 4097 x 128  [2]   19.8 / 20.0 (2) / 24.4 / 25.5
-//   1 x 8 (x 8) x 32768 x 128  [12]  148 / 18.3 (12) / 17.4 / 17.6
+//   1 x 40 x 8192 x 128        [6]   34.2 / 15.2 (6) 16.0 (3) / 17.6 / 20.1
+//   2 x 40 x 8192 x 128        [3]   34.4 / 24.2 (3) / 27.8 / 27.7
+//   16 x 8 (x 4) x 4097 x 128  [2]   19.7 / 20.3 (2) / 24.6 / 25.7
+//   1 x 8 (x 8) x 32768 x 128  [12]  150 / 18.6 (12) / 17.3 / 17.8
 inline Plan deal_of(long long units, int stages, int ctas, const ClusterFit &fit)
 {
     if (stages <= kWarps) return {Deal::Whole, 1};

@@ -1,6 +1,7 @@
-"""Decode over the 4-bit KV cache with more than 256 query heads, where the groups of 32 elements of a row differ widely in magnitude, and where
-queries and keys lie at the ends of bf16's range: against attention in 64 bits over the held values, within bounds
-that hold for each group by itself (kv4_ref.decode_by_group)."""
+"""Decode over the 4-bit KV cache with more than 256 query heads, where the groups of 32 elements of a row differ
+widely in magnitude, where queries and keys lie at the ends of bf16's range, and with large logits and slopes: against
+attention in 64 bits over the held values, within bounds that hold for each group by itself
+(kv4_ref.decode_by_group)."""
 import numpy as np
 import pytest
 
