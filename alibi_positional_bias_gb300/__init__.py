@@ -27,6 +27,7 @@ __all__ = [
     "alibi_slopes_explicit", "alibi_attn_probs_f32_ex", "AlibiFwdOptions", "alibi_attn_bwd", "alibi_attn_bwd_f32",
     "alibi_kv_block_norms", "alibi_attn_decode_skip",
     "alibi_kv4_block_bytes", "alibi_kv4_cache", "alibi_kv4_write", "alibi_kv4_read", "alibi_attn_decode_kv4",
+    "AlibiPages", "AlibiRows", "AlibiRotation", "alibi_pages", "alibi_paged_append", "alibi_attn_decode_paged",
 ]
 
 ALIBI_OK, ALIBI_ERR_INVALID, ALIBI_ERR_UNSUPPORTED, ALIBI_ERR_CUDA, ALIBI_ERR_TIMEOUT, ALIBI_ERR_CHECK = 0, -1, -2, -3, -4, -5
@@ -42,6 +43,24 @@ class AlibiFwdOptions(ctypes.Structure):
     """The C struct alibi_fwd_options (include/alibi.h)."""
     _fields_ = [("flags", ctypes.c_uint), ("clamp_min", ctypes.c_float), ("softcap_z", ctypes.c_float),
                 ("slopes", ctypes.POINTER(ctypes.c_float))]
+
+
+class AlibiPages(ctypes.Structure):
+    """The C struct alibi_pages (include/alibi.h)."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v")]
+                + [(n, ctypes.c_longlong) for n in ("k_page", "k_head", "k_slot", "v_page", "v_head", "v_slot")]
+                + [("table", ctypes.c_void_p)] + [(n, ctypes.c_int) for n in ("pages", "heads", "slots", "width", "d")])
+
+
+class AlibiRows(ctypes.Structure):
+    """The C struct alibi_rows (include/alibi.h)."""
+    _fields_ = [("data", ctypes.c_void_p)] + [(n, ctypes.c_longlong) for n in ("batch", "head", "token")]
+
+
+class AlibiRotation(ctypes.Structure):
+    """The C struct alibi_rotation (include/alibi.h)."""
+    _fields_ = [("dims", ctypes.c_int), ("interleaved", ctypes.c_int), ("base", ctypes.c_double),
+                ("freqs", ctypes.POINTER(ctypes.c_double))]
 
 
 class AlibiError(RuntimeError):
@@ -114,6 +133,11 @@ def load(build_if_missing: bool = False):
         lib.alibi_kv4_read.restype = I
         lib.alibi_attn_decode_kv4.argtypes = [vp, vp, vp, vp, vp, I, I, I, I, I, I, I, ctypes.POINTER(F), vp]
         lib.alibi_attn_decode_kv4.restype = I
+        pages, rows = ctypes.POINTER(AlibiPages), ctypes.POINTER(AlibiRows)
+        lib.alibi_paged_append.argtypes = [rows, rows, pages, vp, vp, I, I, ctypes.POINTER(AlibiRotation), rows, vp, I, vp]
+        lib.alibi_paged_append.restype = I
+        lib.alibi_attn_decode_paged.argtypes = [vp, pages, vp, vp, vp, I, I, I, I, ctypes.POINTER(F), vp]
+        lib.alibi_attn_decode_paged.restype = I
         for name in ("alibi_attn_fwd", "alibi_attn_fwd_f32", "alibi_attn_decode", "alibi_attn_decode_splits",
                      "alibi_attn_probs_f32",
                      "alibi_attn_underflow_bf16", "alibi_check_error", "alibi_slopes"):
@@ -610,6 +634,176 @@ def alibi_attn_decode_kv4(q, cache, lens=None, L=None, out=None, lse=None, slope
             raise AlibiError(status, "alibi_attn_decode_kv4")
     else:
         _call_kv4(index, lib.alibi_attn_decode_kv4, "alibi_attn_decode_kv4", stream, *args)
+    return out, lse
+
+
+def alibi_pages(P: int, H: int, S: int, d: int, device=None):
+    """Pools for a paged KV cache of P pages of S tokens (a power of two in [8, 1024]) and H KV heads of size d: k_pages
+    and v_pages, bf16 [P, H, S, d], uninitialised (rows are used once written). The paged calls take any tensors of that
+    shape whose last dimension is contiguous and whose other strides are multiples of 8."""
+    import torch
+    device = "cuda" if device is None else device
+    return tuple(torch.empty((P, H, S, d), dtype=torch.bfloat16, device=device) for _ in range(2))
+
+
+def _row_strides(t, shape, stride, name):
+    """Strides of all dimensions but the last; of one that has a single index any will do, and it gets that of a dense row."""
+    if stride[-1] != 1 and shape[-1] != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    return [s if n > 1 else -(-shape[-1] // 8) * 8 for n, s in zip(shape[:-1], stride)]
+
+
+def _strided(t, dtype, dims, name, index=None):
+    """_need without contiguity: a CUDA tensor of `dims` dimensions, on device `index` where one is given."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got shape {tuple(t.shape)}")
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+
+
+def _paged_ints(t, B, index, name):
+    """The address of int32 [B], or None."""
+    int32 = _kv4_names()[2]
+    if t is None:
+        return None
+    if not (t.dtype is int32 and t.shape == (B,) and t.get_device() == index and t.is_contiguous()):
+        _need_on(t, int32, (B,), name, index)
+    return t.data_ptr()
+
+
+def _paged_cache(k_pages, v_pages, table, B, d, index):
+    """The C struct of a paged cache, its tensors checked."""
+    bfloat16, _, int32, _, _, _, _ = _kv4_names()
+    _strided(k_pages, bfloat16, 4, "k_pages", index)
+    _strided(v_pages, bfloat16, 4, "v_pages", index)
+    shape = k_pages.shape
+    if v_pages.shape != shape or shape[3] != d:
+        raise ValueError(f"k_pages and v_pages must have one shape (pages, heads, slots, {d}), got {tuple(shape)} and "
+                         f"{tuple(v_pages.shape)}")
+    _need_on(table, int32, None, "table", index)
+    if table.dim() != 2 or table.shape[0] != B:
+        raise ValueError(f"table must have shape ({B}, pages of a sequence), got {tuple(table.shape)}")
+    if max(shape) > 2 ** 31 - 1 or table.shape[1] > 2 ** 31 - 1:
+        raise AlibiError(ALIBI_ERR_UNSUPPORTED, "paged cache")
+    return AlibiPages(k_pages.data_ptr(), v_pages.data_ptr(), *_row_strides(k_pages, shape, k_pages.stride(), "k_pages"),
+                      *_row_strides(v_pages, shape, v_pages.stride(), "v_pages"), table.data_ptr(), shape[0], shape[1], shape[2],
+                      table.shape[1], d)
+
+
+def _rows_struct(t, shape, name):
+    return AlibiRows(t.data_ptr(), *_row_strides(t, shape, t.stride(), name))
+
+
+def alibi_paged_append(k, v, k_pages, v_pages, table, pos=None, count=None, rotate: int = 0, base: float = 10000.0, freqs=None,
+                       interleaved: bool = False, q=None, q_out=None, stream=None):
+    """Append new keys and values [B, H_kv, T, d] (bf16, any strides that are multiples of 8) to the pages of a pool: token
+    t < count[b] of sequence b to row pos[b] + t, which is slot j % S of page table[b, j // S]. k_pages, v_pages: [P, H_kv, S, d]
+    (alibi_pages); table: int32 [B, pages of a sequence]; pos and count: int32 CUDA tensors [B] (None: 0 and T).
+    rotate > 0 turns the first `rotate` elements (a multiple of 16) of the keys by their positions, and those of
+    the queries q [B, H, T, d] into q_out, which is returned; frequencies base^(-2 i / rotate), or freqs (rotate / 2 numbers,
+    radians per token); pairs of elements i and i + rotate / 2, or 2 i and 2 i + 1 (interleaved). Sequences that do not fit
+    and tokens without a page are left out and reported by alibi_check_error."""
+    bfloat16, _, _, _, _, _, lib = _kv4_names()
+    _strided(k, bfloat16, 4, "k")
+    shape, index = k.shape, k.get_device()
+    B, H, T, d = shape
+    _strided(v, bfloat16, 4, "v", index)
+    if v.shape != shape:
+        raise ValueError(f"v must have shape {tuple(shape)}, got {tuple(v.shape)}")
+    pages = _paged_cache(k_pages, v_pages, table, B, d, index)
+    if pages.heads != H:
+        raise ValueError(f"k_pages must have {H} heads, got {pages.heads}")
+    if max(B, T) > 2 ** 31 - 1:
+        raise AlibiError(ALIBI_ERR_INVALID, "alibi_paged_append")
+    rotation = f = None
+    if rotate:
+        if not 0 < rotate <= d or rotate % 16:
+            raise ValueError(f"rotate must be a multiple of 16 and at most {d}, got {rotate}")
+        if freqs is not None:
+            f = np.ascontiguousarray(freqs, dtype=np.float64)
+            if f.shape != (rotate // 2,):
+                raise ValueError(f"freqs: expected shape ({rotate // 2},), got {f.shape}")
+            f = f.ctypes.data_as(ctypes.POINTER(ctypes.c_double))
+        rotation = AlibiRotation(rotate, int(bool(interleaved)), base, f)
+    rows = None
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out needs q")
+    else:
+        if not rotate:
+            raise ValueError("q needs rotate")
+        _strided(q, bfloat16, 4, "q", index)
+        if q.shape[0] != B or q.shape[2:] != shape[2:]:
+            raise ValueError(f"q must have shape ({B}, heads, {T}, {d}), got {tuple(q.shape)}")
+        rows = _rows_struct(q, q.shape, "q")
+        if q_out is None:
+            import torch
+            q_out = (torch.empty(q.shape, dtype=bfloat16, device=q.device) if stream is None
+                     else _empty_on(stream, index, q.shape, bfloat16))
+        else:
+            _need_on(q_out, bfloat16, q.shape, "q_out", index)
+    _call_kv4(index, lib.alibi_paged_append, "alibi_paged_append", stream, _rows_struct(k, shape, "k"), _rows_struct(v, shape, "v"),
+              pages, _paged_ints(pos, B, index, "pos"), _paged_ints(count, B, index, "count"), B, T, rotation, rows,
+              None if q is None else q_out.data_ptr(), 0 if q is None else q.shape[1])
+    return q_out
+
+
+def _slope_array(slopes, H):
+    """A ctypes pointer to H slopes, or None; it keeps the array."""
+    if slopes is None:
+        return None
+    m = np.ascontiguousarray(slopes, dtype=np.float32)
+    if m.shape != (H,):
+        raise ValueError(f"slopes: expected shape ({H},), got {m.shape}")
+    return m.ctypes.data_as(ctypes.POINTER(ctypes.c_float))
+
+
+def _paged_bound(L, pages, where):
+    """The bound on the lengths: L, or what the table has room for."""
+    C = pages.width * pages.slots
+    L = C if L is None else int(L)
+    if not 0 < L <= C:
+        raise AlibiError(ALIBI_ERR_INVALID, where)
+    if C > 1 << 24:
+        raise AlibiError(ALIBI_ERR_UNSUPPORTED, where)
+    return L
+
+
+def alibi_attn_decode_paged(q, k_pages, v_pages, table, lens=None, L=None, out=None, lse=None, slopes=None, stream=None):
+    """ALiBi attention of the newest T tokens (at most 16) of each sequence over the pages that hold them. q: bf16 [B, H, T, d],
+    or [B, H, d] for one token; k_pages, v_pages: [P, H_kv, S, d], H a multiple of H_kv and at most 384; table: int32 [B, pages of
+    a sequence]; lens: int32 CUDA tensor [B] of lengths (None: all L); L: a bound on them (None: what the table has
+    room for); slopes: H values (None: alibi_slopes(H)). Returns (out, lse): bf16 like q, fp32 without the last
+    dimension; those made here belong to `stream`."""
+    bfloat16, _, _, float32, raw_stream, current, lib = _kv4_names()
+    _need(q, bfloat16, None, "q")
+    shape, dims = q.shape, q.dim()
+    if not 3 <= dims <= 4:
+        raise ValueError(f"q must have 3 or 4 dimensions, got shape {tuple(shape)}")
+    B, H, d, index = shape[0], shape[1], shape[-1], q.get_device()
+    pages = _paged_cache(k_pages, v_pages, table, B, d, index)
+    L = _paged_bound(L, pages, "alibi_attn_decode_paged")
+    import torch
+    if out is None:
+        out = (torch.empty(shape, dtype=bfloat16, device=q.device) if stream is None
+               else _empty_on(stream, index, shape, bfloat16))
+    else:
+        _need_on(out, bfloat16, shape, "out", index)
+    if lse is None:
+        lse = (torch.empty(shape[:-1], dtype=float32, device=q.device) if stream is None
+               else _empty_on(stream, index, shape[:-1], float32))
+    else:
+        _need_on(lse, float32, shape[:-1], "lse", index)
+    _call_kv4(index, lib.alibi_attn_decode_paged, "alibi_attn_decode_paged", stream, q.data_ptr(), pages,
+              _paged_ints(lens, B, index, "lens"), out.data_ptr(), lse.data_ptr(), B, H, shape[2] if dims == 4 else 1, L,
+              _slope_array(slopes, H))
     return out, lse
 
 

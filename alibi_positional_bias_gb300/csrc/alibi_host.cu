@@ -364,7 +364,7 @@ const char *alibi_status_str(int status)
         case ALIBI_ERR_CUDA: return "ALIBI_ERR_CUDA: CUDA call or kernel launch failed";
         case ALIBI_ERR_TIMEOUT: return "ALIBI_ERR_TIMEOUT: a bounded device-side wait expired";
         case ALIBI_ERR_CHECK: return "ALIBI_ERR_CHECK: a debug-build address check failed";
-        case ALIBI_ERR_RANGE: return "ALIBI_ERR_RANGE: a position or length in device memory is outside the cache";
+        case ALIBI_ERR_RANGE: return "ALIBI_ERR_RANGE: a position, length or page number in device memory is outside the cache";
         default: return "unknown alibi status";
     }
 }

@@ -57,8 +57,8 @@ typedef enum {
     ALIBI_ERR_TIMEOUT = -4,     /* a bounded device-side wait expired (see alibi_check_error) */
     ALIBI_ERR_CHECK = -5,       /* debug-checks build only: a kernel found a bad TMA / TMEM / shared
                                    address, recorded it and skipped the access */
-    ALIBI_ERR_RANGE = -6        /* a kernel found a position or length in device memory outside the
-                                   cache and left that sequence out (see alibi_check_error) */
+    ALIBI_ERR_RANGE = -6        /* a kernel found a position, length or page number in device memory outside
+                                   the cache and left that sequence out (see alibi_check_error) */
 } alibi_status;
 
 /* Library version as an integer (major * 10000 + minor * 100 + patch). */
@@ -378,6 +378,78 @@ ALIBI_API int alibi_attn_decode_kv4(const void *q, const void *cache, const int 
                                     int H, int Hkv, int T, int L, int C, int d, const float *slopes, void *stream);
 
 /*
+ * Paged KV cache. The pages' KV-cache paragraph ("ALiBi: Attention with Linear Biases") keeps the keys and values of
+ * a sequence in one piece; a server that holds many sequences of different lengths keeps them in pages of a
+ * common pool instead, and a table of page numbers per sequence. Row j of sequence b is slot j % slots of page
+ * table[b][j / slots]; element e of KV head h of slot s of page p is k[p k_page + h k_head + s k_slot + e], and v
+ * likewise. The strides, in elements, are multiples of 8 and at least d, so that [pages, heads, slots, d],
+ * [pages, slots, heads, d] and pools that hold K and V side by side all serve. Page numbers are read from the table only
+ * where a sequence has tokens; several sequences may share pages that none of them is written to.
+ */
+typedef struct alibi_pages {
+    void *k, *v;                        /* device bf16, 16-byte aligned                              */
+    long long k_page, k_head, k_slot;   /* strides in elements                                       */
+    long long v_page, v_head, v_slot;
+    const int *table;                   /* device int32 [B, width], page numbers in [0, pages)       */
+    int pages, heads, slots, width, d;  /* heads: KV heads, at most 384; slots: a power of two in [8, 1024]; width slots
+                                           at most 2^24; d in {16, 32, 64, 128}                      */
+} alibi_pages;
+
+/* Rows of new tokens: element e of head h of token t of sequence b is data[b batch + h head + t token + e]. */
+typedef struct alibi_rows {
+    const void *data;              /* device bf16, 16-byte aligned             */
+    long long batch, head, token;  /* strides in elements, multiples of 8      */
+} alibi_rows;
+
+/*
+ * Rotation of the first `dims` elements of a row by its position n (for heads without a bias, whose slope is zero; the pages
+ * have no counterpart to it): pair i of elements turns by the angle n f_i, with f_i = freqs[i], or base^(-2 i / dims)
+ * where freqs is NULL. Pair i is elements i and i + dims / 2, or 2 i and 2 i + 1 where interleaved = 1:
+ *   x' = x cos - y sin,  y' = y cos + x sin.
+ */
+typedef struct alibi_rotation {
+    int dims;             /* a multiple of 16, at most d; 0: none            */
+    int interleaved;      /* 0 or 1                                          */
+    double base;          /* used where freqs is NULL                        */
+    const double *freqs;  /* HOST array of dims / 2 frequencies in radians per token, of magnitude at most 1e6, or NULL */
+} alibi_rotation;
+
+/*
+ * Append new tokens: token t < count[b] of sequence b of k and v (H_kv = pages->heads heads, T tokens) goes to row
+ * pos[b] + t of its pages. pos, count: device int32 [B], or NULL for 0 and T. With a rotation (NULL: none) the keys
+ * are rotated by their positions on the way, in fp32, rounded once; and so are, where q is not NULL, the queries of H heads
+ * (at most 384), into q_out, device bf16 [B, H, T, d]. Other rows of the pages, and tokens of q_out from count[b] on, are left
+ * as they were. A sequence with pos[b] < 0, count[b] < 0, count[b] > T or pos[b] + count[b] > width slots is left
+ * out whole, a token whose page number is outside [0, pages) is not written, and alibi_check_error returns ALIBI_ERR_RANGE.
+ * Two tokens of one call that go to the same slot race. The angle is reduced exactly: it is off by less than
+ * 2^-22 rad at every position.
+ */
+ALIBI_API int alibi_paged_append(const alibi_rows *k, const alibi_rows *v, const alibi_pages *pages, const int *pos,
+                                 const int *count, int B, int T, const alibi_rotation *rotation, const alibi_rows *q,
+                                 void *q_out, int H, void *stream);
+
+/*
+ * Decode over the pages: the attention of the newest T tokens of each sequence, whose keys and values are in its pages
+ * already. Query t of sequence b has position i = len[b] - T + t and sees rows j <= i:
+ *   x_j = q.k_j / sqrt(d) - m_h (i - j),  out = sum_j softmax_j(x) v_j.
+ * q, out: device bf16 [B, H, T, d]; lse: device fp32 [B, H, T] = ln sum_j exp(x_j), or NULL. H query heads share
+ * pages->heads KV heads, consecutive ones each (H a multiple, at most 384). T in [1, 16]. lens: device int32 [B], the
+ * lengths with the T tokens included, or NULL (every sequence has L); 0 <= lens[b] <= L <= width slots. L bounds the work
+ * that is planned: pass the largest length if it is known, or width slots in a graph that is replayed while the
+ * sequences grow. A query with i < 0 sees no row: its out is 0 and its lse -inf. A sequence with lens[b] outside
+ * [0, L], or with a page number outside [0, pages) among those of its rows, gets NaN in out and lse (of the latter, every
+ * head), and alibi_check_error returns ALIBI_ERR_RANGE. slopes: optional HOST array of H slopes as in
+ * alibi_fwd_options (NULL: alibi_slopes(H)); with slopes of zero there is no bias.
+ * Rows that a query does not see are not used, whatever they hold; a NaN in a key that it sees makes its out and lse NaN.
+ * Products are exact in fp32 sums, weights are fp32 numbers (one below 2^-126 of the row's largest counts as zero) and
+ * enter the values' products as two bf16 numbers, off by 2^-16 of themselves. out and lse are the same bits for the
+ * same arguments. A call takes up to 11 MB of scratch from the library's stream-ordered pool where it splits sequences
+ * over several CTAs and merges them in a second kernel.
+ */
+ALIBI_API int alibi_attn_decode_paged(const void *q, const alibi_pages *pages, const int *lens, void *out, float *lse, int B,
+                                      int H, int T, int L, const float *slopes, void *stream);
+
+/*
  * Attention weights of the fp32 path (test and analysis export):
  * P[b,h,i,j] = exp(q_i.k_j/sqrt(d) - m_h (i - j) - lse[b,h,i]) for j <= i,
  * 0 for j > i. q, k: device fp32 [B, H, N, d]; lse: device fp32 [B, H, N]
@@ -450,8 +522,8 @@ ALIBI_API int alibi_selftest_fwd_timeout(const void *q, const void *k, const voi
  * ALIBI_ERR_CHECK if a kernel of the debug-checks build (the same library compiled
  * with -DALIBI_CHECKS: every TMA coordinate, TMEM address and shared-memory operand
  * tested before use) found a bad one (the second word of the status records the
- * check and the value), ALIBI_ERR_RANGE if a call on the 4-bit cache found a position or
- * length outside it, else ALIBI_OK. The word accumulates until it is collected here, but an
+ * check and the value), ALIBI_ERR_RANGE if a call on the 4-bit or the paged cache found a
+ * position, length or page number outside it, else ALIBI_OK. The word accumulates until it is collected here, but an
  * uncollected error does not affect later calls: a kernel's waits give up early
  * only on a failure inside the same CTA, so calls made after a timeout compute
  * their results normally (the timeout is still reported by the next check).
