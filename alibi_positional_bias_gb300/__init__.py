@@ -28,6 +28,7 @@ __all__ = [
     "alibi_kv_block_norms", "alibi_attn_decode_skip",
     "alibi_kv4_block_bytes", "alibi_kv4_cache", "alibi_kv4_write", "alibi_kv4_read", "alibi_attn_decode_kv4",
     "AlibiPages", "AlibiRows", "AlibiRotation", "alibi_pages", "alibi_paged_append", "alibi_attn_decode_paged",
+    "alibi_attn_fwd_paged",
 ]
 
 ALIBI_OK, ALIBI_ERR_INVALID, ALIBI_ERR_UNSUPPORTED, ALIBI_ERR_CUDA, ALIBI_ERR_TIMEOUT, ALIBI_ERR_CHECK = 0, -1, -2, -3, -4, -5
@@ -138,6 +139,8 @@ def load(build_if_missing: bool = False):
         lib.alibi_paged_append.restype = I
         lib.alibi_attn_decode_paged.argtypes = [vp, pages, vp, vp, vp, I, I, I, I, ctypes.POINTER(F), vp]
         lib.alibi_attn_decode_paged.restype = I
+        lib.alibi_attn_fwd_paged.argtypes = [vp, pages, vp, vp, vp, vp, I, I, I, I, ctypes.POINTER(F), vp]
+        lib.alibi_attn_fwd_paged.restype = I
         for name in ("alibi_attn_fwd", "alibi_attn_fwd_f32", "alibi_attn_decode", "alibi_attn_decode_splits",
                      "alibi_attn_probs_f32",
                      "alibi_attn_underflow_bf16", "alibi_check_error", "alibi_slopes"):
@@ -776,13 +779,29 @@ def _paged_bound(L, pages, where):
     return L
 
 
+def _paged_outputs(out, lse, shape, index, device, stream):
+    """out and lse of queries of `shape`, made where they are not given."""
+    import torch
+    bfloat16, _, _, float32, _, _, _ = _kv4_names()
+    if out is None:
+        out = torch.empty(shape, dtype=bfloat16, device=device) if stream is None else _empty_on(stream, index, shape, bfloat16)
+    else:
+        _need_on(out, bfloat16, shape, "out", index)
+    if lse is None:
+        lse = (torch.empty(shape[:-1], dtype=float32, device=device) if stream is None
+               else _empty_on(stream, index, shape[:-1], float32))
+    else:
+        _need_on(lse, float32, shape[:-1], "lse", index)
+    return out, lse
+
+
 def alibi_attn_decode_paged(q, k_pages, v_pages, table, lens=None, L=None, out=None, lse=None, slopes=None, stream=None):
     """ALiBi attention of the newest T tokens (at most 16) of each sequence over the pages that hold them. q: bf16 [B, H, T, d],
     or [B, H, d] for one token; k_pages, v_pages: [P, H_kv, S, d], H a multiple of H_kv and at most 384; table: int32 [B, pages of
     a sequence]; lens: int32 CUDA tensor [B] of lengths (None: all L); L: a bound on them (None: what the table has
     room for); slopes: H values (None: alibi_slopes(H)). Returns (out, lse): bf16 like q, fp32 without the last
     dimension; those made here belong to `stream`."""
-    bfloat16, _, _, float32, raw_stream, current, lib = _kv4_names()
+    bfloat16, _, _, _, _, _, lib = _kv4_names()
     _need(q, bfloat16, None, "q")
     shape, dims = q.shape, q.dim()
     if not 3 <= dims <= 4:
@@ -790,19 +809,31 @@ def alibi_attn_decode_paged(q, k_pages, v_pages, table, lens=None, L=None, out=N
     B, H, d, index = shape[0], shape[1], shape[-1], q.get_device()
     pages = _paged_cache(k_pages, v_pages, table, B, d, index)
     L = _paged_bound(L, pages, "alibi_attn_decode_paged")
-    import torch
-    if out is None:
-        out = (torch.empty(shape, dtype=bfloat16, device=q.device) if stream is None
-               else _empty_on(stream, index, shape, bfloat16))
-    else:
-        _need_on(out, bfloat16, shape, "out", index)
-    if lse is None:
-        lse = (torch.empty(shape[:-1], dtype=float32, device=q.device) if stream is None
-               else _empty_on(stream, index, shape[:-1], float32))
-    else:
-        _need_on(lse, float32, shape[:-1], "lse", index)
+    out, lse = _paged_outputs(out, lse, shape, index, q.device, stream)
     _call_kv4(index, lib.alibi_attn_decode_paged, "alibi_attn_decode_paged", stream, q.data_ptr(), pages,
               _paged_ints(lens, B, index, "lens"), out.data_ptr(), lse.data_ptr(), B, H, shape[2] if dims == 4 else 1, L,
+              _slope_array(slopes, H))
+    return out, lse
+
+
+def alibi_attn_fwd_paged(q, k_pages, v_pages, table, lens=None, count=None, L=None, out=None, lse=None, slopes=None, stream=None):
+    """ALiBi attention of up to T new tokens of each sequence, a prompt or a part of one, over the pages that hold them
+    and what came before. q: bf16 [B, H, T, d]; count: int32 CUDA tensor [B], the new tokens of each sequence (None: T); lens:
+    their lengths, the new tokens included; k_pages, v_pages, table, L and slopes as in alibi_attn_decode_paged. Query t <
+    count[b] has position lens[b] - count[b] + t; out and lse of tokens from count[b] on are left as they were.
+    Returns (out, lse): bf16 [B, H, T, d] and fp32 [B, H, T]; those made here belong to `stream`."""
+    bfloat16, _, _, _, _, _, lib = _kv4_names()
+    _need(q, bfloat16, None, "q")
+    shape = q.shape
+    if q.dim() != 4:
+        raise ValueError(f"q must have 4 dimensions, got shape {tuple(shape)}")
+    B, H, T, d = shape
+    index = q.get_device()
+    pages = _paged_cache(k_pages, v_pages, table, B, d, index)
+    L = _paged_bound(L, pages, "alibi_attn_fwd_paged")
+    out, lse = _paged_outputs(out, lse, shape, index, q.device, stream)
+    _call_kv4(index, lib.alibi_attn_fwd_paged, "alibi_attn_fwd_paged", stream, q.data_ptr(), pages,
+              _paged_ints(lens, B, index, "lens"), _paged_ints(count, B, index, "count"), out.data_ptr(), lse.data_ptr(), B, H, T, L,
               _slope_array(slopes, H))
     return out, lse
 

@@ -342,6 +342,20 @@ bool encode_tmap_bf16_3d(CUtensorMap *map, const void *base, uint64_t dim0, uint
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_tmap_bf16_4d(CUtensorMap *map, const void *base, const uint64_t (&dims)[4], const uint64_t (&strides)[3],
+                         uint32_t box0, uint32_t box1)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t n[4] = {dims[0], dims[1], dims[2], dims[3]};
+    const cuuint64_t stride[3] = {strides[0], strides[1], strides[2]};
+    const cuuint32_t box[4] = {box0, box1, 1, 1};
+    const cuuint32_t estride[4] = {1, 1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), n, stride, box, estride,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace alibi
 
 using namespace alibi;

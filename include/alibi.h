@@ -450,6 +450,21 @@ ALIBI_API int alibi_attn_decode_paged(const void *q, const alibi_pages *pages, c
                                       int H, int T, int L, const float *slopes, void *stream);
 
 /*
+ * Prefill over the pages: the attention of up to T new tokens of each sequence, a prompt or a part of one, whose keys and
+ * values are in its pages already. Query t < count[b] of sequence b has position i = len[b] - count[b] + t and sees rows
+ * j <= i; formulas, q, out, lse (the latter may be NULL), heads, lens, L and slopes as in alibi_attn_decode_paged, with T up to
+ * 2^24. count: device int32 [B], or NULL for T; out and lse of tokens from count[b] on are left as they were. A
+ * query with i < 0 sees no row: its out is 0 and its lse -inf. A sequence with count[b] outside [0, T] or lens[b]
+ * outside [0, L] gets NaN in out and lse (of all T tokens where count[b] is at fault), one with a page number outside
+ * [0, pages) in the blocks of 256 queries that read it, and alibi_check_error returns ALIBI_ERR_RANGE.
+ * Runs the tensor-core pipeline of alibi_attn_fwd (weights are rounded to bf16 for the P V product). Rows that a
+ * query does not see are not used, whatever they hold; a value that is not finite makes its element of out NaN (or,
+ * in tiles of 128 rows that all of the 256 queries see, infinite) for the queries that see it.
+ */
+ALIBI_API int alibi_attn_fwd_paged(const void *q, const alibi_pages *pages, const int *lens, const int *count, void *out,
+                                   float *lse, int B, int H, int T, int L, const float *slopes, void *stream);
+
+/*
  * Attention weights of the fp32 path (test and analysis export):
  * P[b,h,i,j] = exp(q_i.k_j/sqrt(d) - m_h (i - j) - lse[b,h,i]) for j <= i,
  * 0 for j > i. q, k: device fp32 [B, H, N, d]; lse: device fp32 [B, H, N]

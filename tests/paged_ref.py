@@ -75,7 +75,7 @@ def rotated(x, n, R, base=10000.0, freqs=None, interleaved=False):
     return out, err
 
 
-def attention(q, k, v, lens, counts, m, weight=2.0 ** -16, chain=64):
+def attention(q, k, v, lens, counts, m, weight=2.0 ** -16, chain=64, column=False):
     """Attention of q [B, H, T, d] over k, v [B, Hkv, N, d] (float64), query t < counts[b] of sequence b at position
     lens[b] - counts[b] + t: out, lse and the kernel's error bounds; other queries are NaN.
 
@@ -85,7 +85,12 @@ def attention(q, k, v, lens, counts, m, weight=2.0 ** -16, chain=64):
     by less than 2^-21 (m (i - j) + |x|). So dx_j. A weight is off by dx_j, 2^-19 for the exponential, for references that
     move and for the merges, and `weight`, the rounding of p for the values' products (two bf16 numbers: 2^-16); the
     normaliser by the mean of dx_j + 2^-19. The values' products are summed in chains of at most n / chain + 8 steps, each
-    17 2^-24 of the magnitudes."""
+    17 2^-24 of the magnitudes.
+
+    column: the kernel adds the part m c of the bias, c < 128 the key's place in its tile, to the product on the tensor core, one
+    more step whose cuts are relative to sum |q_e k_e| / sqrt(d) + 128 m, and takes m (i - k_0) off with one rounding, of
+    numbers up to m (i - j) + 128 m: dx_j grows by 17 2^-24 (sum |q_e k_e| / sqrt(d) + 128 m) + 2^-24 128 m. (Slopes above
+    4 / log2(e) are taken whole.)"""
     B, H, T, d = q.shape
     G = H // k.shape[1]
     out, lse = np.full(q.shape, np.nan), np.full(q.shape[:-1], np.nan)
@@ -110,6 +115,8 @@ def attention(q, k, v, lens, counts, m, weight=2.0 ** -16, chain=64):
                 lse[b, h, :c] = (M + np.log(l))[:, 0]
             dx = 17 * d / 16 * 2.0 ** -24 * (np.abs(Q) @ np.abs(K).T) / np.sqrt(d) + \
                 2.0 ** -21 * (bias + np.where(dist >= 0, np.abs(x), 0.0)) + 2.0 ** -19
+            if column:
+                dx += 17 * 2.0 ** -24 * (np.abs(Q) @ np.abs(K).T) / np.sqrt(d) + (18 * 2.0 ** -24 * 128 * m[h] if m[h] < 2.78 else 0.0)
             D = (W * dx).sum(-1, keepdims=True)
             steps = 17 * 2.0 ** -24 * (n / chain + 8)
             e_out[b, h, :c] = (W * (weight + steps + dx + D)) @ np.abs(V)

@@ -206,3 +206,43 @@ def test_arguments_that_do_not_fit(fake):
         with pytest.raises(error):
             call()
     assert not fake.calls
+
+
+def prefill(lib, pg, q=P, lens=P, count=P, out=P, lse=P, B=1, H=2, T=1, L=64, slopes=None):
+    return lib.alibi_attn_fwd_paged(q, pg, lens, count, out, lse, B, H, T, L, slopes, None)
+
+
+@pytest.mark.parametrize("change,status", BAD_PAGES)
+def test_caches_that_the_prefill_refuses(lib, change, status):
+    assert prefill(lib, pages(**change)) == status
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(q=None), INVALID), (dict(out=None), INVALID), (dict(q=MIS), INVALID), (dict(out=MIS), INVALID), (dict(lens=ODD), INVALID),
+    (dict(count=ODD), INVALID), (dict(lse=ODD), INVALID), (dict(B=0), INVALID), (dict(H=0), INVALID), (dict(H=3), INVALID),
+    (dict(T=0), INVALID), (dict(L=0), INVALID), (dict(L=65), INVALID), (dict(T=(1 << 24) + 1), UNSUPPORTED), (dict(H=386), UNSUPPORTED),
+    (dict(B=1 << 29, H=4), UNSUPPORTED), (dict(B=1 << 20, T=1 << 24), UNSUPPORTED),
+    (dict(slopes=(ctypes.c_float * 2)(0.5, -1.0)), INVALID)])
+def test_prefills_that_are_refused(lib, change, status):
+    assert prefill(lib, pages(), **change) == status
+
+
+def test_prefill_arguments_that_do_not_fit(fake):
+    i32, f32 = torch.int32, torch.float32
+    q, kp, table = on(2, 4, 3, 64), on(4, 2, 16, 64), on(2, 4, dtype=i32)
+    lse = on(2, 4, 3, dtype=f32)
+    for error, call in [
+        (ValueError, lambda: ab.alibi_attn_fwd_paged(on(2, 4, 64), kp, kp, table)),
+        (ValueError, lambda: ab.alibi_attn_fwd_paged(q.transpose(1, 2), kp, kp, table)),
+        (ValueError, lambda: ab.alibi_attn_fwd_paged(q, kp, kp, table, out=q, lse=lse, count=on(3, dtype=i32))),
+        (TypeError, lambda: ab.alibi_attn_fwd_paged(q, kp, kp, table, out=q, lse=lse, lens=on(2, dtype=f32))),
+        (TypeError, lambda: ab.alibi_attn_fwd_paged(q, kp, kp, table, out=lse, lse=lse)),
+        (ValueError, lambda: ab.alibi_attn_fwd_paged(q, kp, kp, table, out=q, lse=on(2, 4, dtype=f32))),
+        (ab.AlibiError, lambda: ab.alibi_attn_fwd_paged(q, kp, kp, table, out=q, lse=lse, L=65)),
+        (ab.AlibiError, lambda: ab.alibi_attn_fwd_paged(q, kp, kp, table, out=q, lse=lse, L=2 ** 32 + 5)),
+    ]:
+        with pytest.raises(error):
+            call()
+    assert not fake.calls
+    ab.alibi_attn_fwd_paged(q, kp, kp, table, out=q, lse=lse)
+    assert fake.calls[-1][1][6:10] == (2, 4, 3, 64)
