@@ -13,6 +13,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 import threading
 
 import numpy as np
@@ -649,7 +650,7 @@ def alibi_pages(P: int, H: int, S: int, d: int, device=None):
     return tuple(torch.empty((P, H, S, d), dtype=torch.bfloat16, device=device) for _ in range(2))
 
 
-def _row_strides(t, shape, stride, name):
+def _row_strides(shape, stride, name):
     """Strides of all dimensions but the last; of one that has a single index any will do, and it gets that of a dense row."""
     if stride[-1] != 1 and shape[-1] != 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
@@ -673,16 +674,47 @@ def _strided(t, dtype, dims, name, index=None):
 
 def _paged_ints(t, B, index, name):
     """The address of int32 [B], or None."""
-    int32 = _kv4_names()[2]
     if t is None:
         return None
-    if not (t.dtype is int32 and t.shape == (B,) and t.get_device() == index and t.is_contiguous()):
-        _need_on(t, int32, (B,), name, index)
+    if not (t.dtype is _kv4_names()[2] and t.shape == (B,) and t.get_device() == index and t.is_contiguous()):
+        _need_on(t, _kv4_names()[2], (B,), name, index)
     return t.data_ptr()
+
+
+_pack_pages = struct.Struct("=QQqqqqqqQiiiii").pack_into
 
 
 def _paged_cache(k_pages, v_pages, table, B, d, index):
     """The C struct of a paged cache, its tensors checked."""
+    bfloat16, _, int32, _, _, _, _ = _kv4_names()
+    try:
+        shape, M = k_pages.shape, table.shape
+        P, H, S, dk = shape
+        good = (k_pages.dtype is bfloat16 and v_pages.dtype is bfloat16 and table.dtype is int32 and v_pages.shape == shape
+                and dk == d and len(M) == 2 and M[0] == B and index == k_pages.get_device() == v_pages.get_device()
+                == table.get_device() >= 0 and table.is_contiguous() and P < 1 << 31 and H < 1 << 31 and S < 1 << 31 and M[1] < 1 << 31)
+    except (AttributeError, TypeError, ValueError):
+        good = False
+    if not good:
+        _explain_paged(k_pages, v_pages, table, B, d, index)
+    if k_pages.is_contiguous():
+        kp, kh, ks = H * S * d, S * d, d
+    else:
+        kp, kh, ks = _row_strides(shape, k_pages.stride(), "k_pages")
+    if v_pages.is_contiguous():
+        vp, vh, vs = H * S * d, S * d, d
+    else:
+        vp, vh, vs = _row_strides(shape, v_pages.stride(), "v_pages")
+    pages = AlibiPages()
+    try:  # field by field this would take 1.2 us more
+        _pack_pages(pages, 0, k_pages.data_ptr(), v_pages.data_ptr(), kp, kh, ks, vp, vh, vs, table.data_ptr(), P, H, S, M[1], d)
+    except struct.error:  # d beyond 32 bits
+        raise AlibiError(ALIBI_ERR_UNSUPPORTED, "paged cache") from None
+    return pages
+
+
+def _explain_paged(k_pages, v_pages, table, B, d, index):
+    """Raise what is wrong with a paged cache."""
     bfloat16, _, int32, _, _, _, _ = _kv4_names()
     _strided(k_pages, bfloat16, 4, "k_pages", index)
     _strided(v_pages, bfloat16, 4, "v_pages", index)
@@ -693,15 +725,28 @@ def _paged_cache(k_pages, v_pages, table, B, d, index):
     _need_on(table, int32, None, "table", index)
     if table.dim() != 2 or table.shape[0] != B:
         raise ValueError(f"table must have shape ({B}, pages of a sequence), got {tuple(table.shape)}")
-    if max(shape) > 2 ** 31 - 1 or table.shape[1] > 2 ** 31 - 1:
-        raise AlibiError(ALIBI_ERR_UNSUPPORTED, "paged cache")
-    return AlibiPages(k_pages.data_ptr(), v_pages.data_ptr(), *_row_strides(k_pages, shape, k_pages.stride(), "k_pages"),
-                      *_row_strides(v_pages, shape, v_pages.stride(), "v_pages"), table.data_ptr(), shape[0], shape[1], shape[2],
-                      table.shape[1], d)
+    raise AlibiError(ALIBI_ERR_UNSUPPORTED, "paged cache")
+
+
+_pack_rows = struct.Struct("=Qqqq").pack_into
 
 
 def _rows_struct(t, shape, name):
-    return AlibiRows(t.data_ptr(), *_row_strides(t, shape, t.stride(), name))
+    """The C struct of rows [B, H, T, d]."""
+    rows = AlibiRows()
+    if t.is_contiguous():
+        n = shape[2] * shape[3]
+        _pack_rows(rows, 0, t.data_ptr(), shape[1] * n, n, shape[3])
+    else:
+        _pack_rows(rows, 0, t.data_ptr(), *_row_strides(shape, t.stride(), name))
+    return rows
+
+
+def _is_rows(t, dtype, shape, index) -> bool:
+    try:
+        return t.dtype is dtype and t.shape == shape and t.get_device() == index >= 0
+    except AttributeError:
+        return False
 
 
 def alibi_paged_append(k, v, k_pages, v_pages, table, pos=None, count=None, rotate: int = 0, base: float = 10000.0, freqs=None,
@@ -714,16 +759,20 @@ def alibi_paged_append(k, v, k_pages, v_pages, table, pos=None, count=None, rota
     radians per token); pairs of elements i and i + rotate / 2, or 2 i and 2 i + 1 (interleaved). Sequences that do not fit
     and tokens without a page are left out and reported by alibi_check_error."""
     bfloat16, _, _, _, _, _, lib = _kv4_names()
-    _strided(k, bfloat16, 4, "k")
-    shape, index = k.shape, k.get_device()
-    B, H, T, d = shape
-    _strided(v, bfloat16, 4, "v", index)
-    if v.shape != shape:
-        raise ValueError(f"v must have shape {tuple(shape)}, got {tuple(v.shape)}")
+    try:
+        shape, index = k.shape, k.get_device()
+        B, H, T, d = shape
+        good = k.dtype is bfloat16 and _is_rows(v, bfloat16, shape, index)
+    except (AttributeError, TypeError, ValueError):
+        good = False
+    if not good:
+        _strided(k, bfloat16, 4, "k")
+        _strided(v, bfloat16, 4, "v", k.get_device())
+        raise ValueError(f"v must have shape {tuple(k.shape)}, got {tuple(v.shape)}")
     pages = _paged_cache(k_pages, v_pages, table, B, d, index)
     if pages.heads != H:
         raise ValueError(f"k_pages must have {H} heads, got {pages.heads}")
-    if max(B, T) > 2 ** 31 - 1:
+    if B >= 1 << 31 or T >= 1 << 31:
         raise AlibiError(ALIBI_ERR_INVALID, "alibi_paged_append")
     rotation = f = None
     if rotate:
@@ -779,18 +828,32 @@ def _paged_bound(L, pages, where):
     return L
 
 
-def _paged_outputs(out, lse, shape, index, device, stream):
-    """out and lse of queries of `shape`, made where they are not given."""
+def _paged_query(q, dims):
+    """Shape and device index of queries of so many dimensions."""
+    bfloat16 = _kv4_names()[0]
+    try:
+        shape, index = q.shape, q.get_device()
+        good = q.dtype is bfloat16 and len(shape) in dims and index >= 0 and q.is_contiguous()
+    except (AttributeError, TypeError):
+        good = False
+    if not good:
+        _need(q, bfloat16, None, "q")
+        raise ValueError(f"q must have {' or '.join(map(str, dims))} dimensions, got shape {tuple(q.shape)}")
+    return shape, index
+
+
+def _paged_outputs(out, lse, q, shape, index, stream):
+    """out and lse of the queries q, made where they are not given."""
     import torch
     bfloat16, _, _, float32, _, _, _ = _kv4_names()
     if out is None:
-        out = torch.empty(shape, dtype=bfloat16, device=device) if stream is None else _empty_on(stream, index, shape, bfloat16)
-    else:
+        out = torch.empty_like(q) if stream is None else _empty_on(stream, index, shape, bfloat16)
+    elif not (_is_rows(out, bfloat16, shape, index) and out.is_contiguous()):
         _need_on(out, bfloat16, shape, "out", index)
     if lse is None:
-        lse = (torch.empty(shape[:-1], dtype=float32, device=device) if stream is None
+        lse = (torch.empty(shape[:-1], dtype=float32, device=q.device) if stream is None
                else _empty_on(stream, index, shape[:-1], float32))
-    else:
+    elif not (_is_rows(lse, float32, shape[:-1], index) and lse.is_contiguous()):
         _need_on(lse, float32, shape[:-1], "lse", index)
     return out, lse
 
@@ -802,16 +865,13 @@ def alibi_attn_decode_paged(q, k_pages, v_pages, table, lens=None, L=None, out=N
     room for); slopes: H values (None: alibi_slopes(H)). Returns (out, lse): bf16 like q, fp32 without the last
     dimension; those made here belong to `stream`."""
     bfloat16, _, _, _, _, _, lib = _kv4_names()
-    _need(q, bfloat16, None, "q")
-    shape, dims = q.shape, q.dim()
-    if not 3 <= dims <= 4:
-        raise ValueError(f"q must have 3 or 4 dimensions, got shape {tuple(shape)}")
-    B, H, d, index = shape[0], shape[1], shape[-1], q.get_device()
+    shape, index = _paged_query(q, (3, 4))
+    B, H, d = shape[0], shape[1], shape[-1]
     pages = _paged_cache(k_pages, v_pages, table, B, d, index)
     L = _paged_bound(L, pages, "alibi_attn_decode_paged")
-    out, lse = _paged_outputs(out, lse, shape, index, q.device, stream)
+    out, lse = _paged_outputs(out, lse, q, shape, index, stream)
     _call_kv4(index, lib.alibi_attn_decode_paged, "alibi_attn_decode_paged", stream, q.data_ptr(), pages,
-              _paged_ints(lens, B, index, "lens"), out.data_ptr(), lse.data_ptr(), B, H, shape[2] if dims == 4 else 1, L,
+              _paged_ints(lens, B, index, "lens"), out.data_ptr(), lse.data_ptr(), B, H, shape[2] if len(shape) == 4 else 1, L,
               _slope_array(slopes, H))
     return out, lse
 
@@ -823,15 +883,11 @@ def alibi_attn_fwd_paged(q, k_pages, v_pages, table, lens=None, count=None, L=No
     count[b] has position lens[b] - count[b] + t; out and lse of tokens from count[b] on are left as they were.
     Returns (out, lse): bf16 [B, H, T, d] and fp32 [B, H, T]; those made here belong to `stream`."""
     bfloat16, _, _, _, _, _, lib = _kv4_names()
-    _need(q, bfloat16, None, "q")
-    shape = q.shape
-    if q.dim() != 4:
-        raise ValueError(f"q must have 4 dimensions, got shape {tuple(shape)}")
+    shape, index = _paged_query(q, (4,))
     B, H, T, d = shape
-    index = q.get_device()
     pages = _paged_cache(k_pages, v_pages, table, B, d, index)
     L = _paged_bound(L, pages, "alibi_attn_fwd_paged")
-    out, lse = _paged_outputs(out, lse, shape, index, q.device, stream)
+    out, lse = _paged_outputs(out, lse, q, shape, index, stream)
     _call_kv4(index, lib.alibi_attn_fwd_paged, "alibi_attn_fwd_paged", stream, q.data_ptr(), pages,
               _paged_ints(lens, B, index, "lens"), _paged_ints(count, B, index, "count"), out.data_ptr(), lse.data_ptr(), B, H, T, L,
               _slope_array(slopes, H))
