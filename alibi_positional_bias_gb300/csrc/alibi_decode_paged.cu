@@ -5,9 +5,11 @@
 //   x_j = q.k_j / sqrt(d) - m_h (i - j),  j <= i,   out = sum_j softmax_j(x) v_j.
 //
 // The G T rows of a KV head share its keys: a chunk of up to 8, 16 or 32 rows is what a CTA takes over all or a part of the
-// sequence. Each warp streams stages of 8 KB (16 tokens' keys and values of d = 128) through a ring of its own
-// in shared memory, by cp.async of 16 bytes per lane: a page may lie anywhere and have any strides, rows past the length are
-// filled with zeros, and no synchronisation between warps is needed. Per tile of 16 tokens:
+// sequence. Each warp streams stages of 8 KB (16 tokens' keys and values of d = 128) through a ring of its own in shared memory,
+// by TMA: boxes of up to a page's slots of one head, swizzled as ldmatrix reads them, one mbarrier per stage and no
+// synchronisation between warps. (cp.async of 16 bytes per lane took 200 instructions per stage, and a warp's step 1350
+// cycles.) The slots past a sequence's length are loaded too, whatever they hold, and their values set to zero in shared
+// memory. Per tile of 16 tokens:
 //
 //   scores   S^T = K Q^T, mma.m16n8k16 in bf16 with fp32 sums: exact products. The tokens are the 16 rows, so that 8 query
 //            rows fill the 8 columns.
@@ -22,11 +24,13 @@
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <mutex>
 
 #include "alibi.h"
 #include "kv4_deal.h"
+#include "paged_deal.h"
 #include "pages.cuh"
 #include "ptx.cuh"
 #include "split_merge.cuh"
@@ -34,16 +38,17 @@
 namespace alibi {
 namespace {
 
-constexpr int kPgWarps = 4;        // of a CTA, two CTAs per SM
+constexpr int kPgWarps = paged::kWarps;
 constexpr int kPgStages = 3;       // ring depth of each warp
 constexpr int kPgStageBytes = 8192;
 constexpr int kPgRing = kPgWarps * kPgStages * kPgStageBytes;
 constexpr int kMostRows = 32;      // query rows of a chunk
 
 KV4_HD constexpr int pg_tokens(int D) { return 2048 / D; }  // of a stage
-KV4_HD constexpr int pg_smem(int D, int NT) { return kPgRing + (NT > 2 ? kMostRows * D * 2 : 0); }
+KV4_HD constexpr int pg_smem(int D, int NT) { return kPgRing + (NT > 2 ? kMostRows * D * 2 : 0) + 1024; }  // 1024: alignment
 
 struct DecodePagedParams {
+    CUtensorMap tk, tv;      // [pages, heads, slots, d] by strides, box {min(d, 64), min(slots, tokens of a stage), 1, 1}
     const __nv_bfloat16 *q;  // [B, H, T, d]: the G T rows of a KV head are consecutive
     Pages pg;
     const int *lens;         // [B] or null
@@ -60,14 +65,6 @@ struct DecodePagedParams {
     HeadSlopes slopes;
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr)
 {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -81,19 +78,27 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr)
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Byte of the 16-byte piece `piece` of row `row` of a tile of bf16 rows of D elements: the eight rows that an ldmatrix reads
-// lie in the eight 16-byte banks.
-template <int D>
+// Byte of the 16-byte piece `piece` of row `row` of a tile of N bf16 rows of D elements, as TMA's swizzle leaves them: the
+// eight rows that an ldmatrix reads lie in the eight 16-byte banks. D = 128: the first halves of all rows, then the second.
+template <int D, int N>
 __device__ __forceinline__ uint32_t place(int row, int piece)
 {
+    if constexpr (D == 128) return (piece >> 3) * (N * 128) + row * 128 + (((piece ^ row) & 7) << 4);
     const int turn = D >= 64 ? row & 7 : D == 32 ? (row >> 1) & 3 : (row >> 2) & 1;
     return static_cast<uint32_t>(row * (2 * D) + ((piece ^ turn) << 4));
+}
+
+// The same for pieces 2 m + i of a lane's row, from place(row, i): the swizzle turns only the lower bits, and m those above i.
+template <int D, int N>
+__device__ __forceinline__ uint32_t step(uint32_t at, int m)
+{
+    return D == 128 ? (at ^ ((m & 3) << 5)) + (m >> 2) * (N * 128) : at ^ (m << 5);
 }
 
 // State of one warp: NT groups of 8 rows; a lane has rows 8 n + 2 c + k.
@@ -115,7 +120,7 @@ __device__ __forceinline__ void add_values_apart(Rows8<D, NT> &st, uint32_t v, c
     for (int i = last; i > last - T; --i) {  // positions of the query tokens
         for (int x = lane; x < 16 * TT * (D / 8); x += 32)
             if (j0 + x / (D / 8) > i)
-                asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(v + place<D>(x / (D / 8), x % (D / 8))), "r"(0)
+                asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(v + place<D, 16 * TT>(x / (D / 8), x % (D / 8))), "r"(0)
                              : "memory");
         __syncwarp();
 #pragma unroll
@@ -123,7 +128,7 @@ __device__ __forceinline__ void add_values_apart(Rows8<D, NT> &st, uint32_t v, c
 #pragma unroll
             for (int m = 0; m < D / 16; ++m) {
                 uint32_t a[4];
-                ldmatrix4_trans(a, v + place<D>(16 * t + (lane & 7) + (lane >> 4) * 8, 2 * m + ((lane >> 3) & 1)));
+                ldmatrix4_trans(a, v + place<D, 16 * TT>(16 * t + (lane & 7) + (lane >> 4) * 8, 2 * m + ((lane >> 3) & 1)));
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     float y[4] = {0.f, 0.f, 0.f, 0.f};
@@ -136,6 +141,8 @@ __device__ __forceinline__ void add_values_apart(Rows8<D, NT> &st, uint32_t v, c
             }
         __syncwarp();
     }
+    fence_proxy_async_smem();  // the zeros before the next copies
+    __syncwarp();
 }
 
 // 16 TT tokens from j0: keys at shared-memory address k, values at v.
@@ -144,44 +151,58 @@ __device__ __forceinline__ void tokens16(Rows8<D, NT> &st, uint32_t k, uint32_t 
                                          int T, int lane)
 {
     constexpr int CH = TT * NT == 1 ? 2 : 1;  // chains of products
+    constexpr int kRow = D < 64 ? 2 * D : 128;  // bytes from row to row
+    const uint32_t ka = place<D, 16 * TT>(lane & 15, lane >> 4), va = place<D, 16 * TT>((lane & 7) + (lane >> 4) * 8, (lane >> 3) & 1);
+    // Operands are read in batches, the products that take them after that: one by one, each would wait for its own read.
+    constexpr int kBatch = NT > 2 ? (D < 64 ? D / 16 : 4) : D / 16;
     float s[TT][NT][CH][4] = {};
 #pragma unroll
-    for (int m = 0; m < D / 16; ++m) {
-        uint32_t b[NT][2];
-        if constexpr (NT > 2) {
+    for (int m0 = 0; m0 < D / 16; m0 += kBatch) {
+        uint32_t a[TT][kBatch][4], b[kBatch][NT][2];
 #pragma unroll
-            for (int n = 0; n < NT; n += 2) {
-                uint32_t w[4];
-                ldmatrix4(w, sq + place<D>(8 * n + (lane & 7) + (lane >> 4) * 8, 2 * m + ((lane >> 3) & 1)));
-                b[n][0] = w[0], b[n][1] = w[1], b[n + 1][0] = w[2], b[n + 1][1] = w[3];
+        for (int m = 0; m < kBatch; ++m) {
+#pragma unroll
+            for (int t = 0; t < TT; ++t) ldmatrix4(a[t][m], step<D, 16 * TT>(k + ka, m0 + m) + 16 * t * kRow);
+            if constexpr (NT > 2) {
+#pragma unroll
+                for (int n = 0; n < NT; n += 2) {
+                    uint32_t w[4];
+                    ldmatrix4(w, sq + place<D, kMostRows>(8 * n + (lane & 7) + (lane >> 4) * 8, 2 * (m0 + m) + ((lane >> 3) & 1)));
+                    b[m][n][0] = w[0], b[m][n][1] = w[1], b[m][n + 1][0] = w[2], b[m][n + 1][1] = w[3];
+                }
+            } else {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) b[m][n][0] = st.q[m0 + m][n][0], b[m][n][1] = st.q[m0 + m][n][1];
             }
-        } else {
-#pragma unroll
-            for (int n = 0; n < NT; ++n) b[n][0] = st.q[m][n][0], b[n][1] = st.q[m][n][1];
         }
 #pragma unroll
-        for (int t = 0; t < TT; ++t) {
-            uint32_t a[4];
-            ldmatrix4(a, k + place<D>(16 * t + (lane & 15), 2 * m + (lane >> 4)));
+        for (int m = 0; m < kBatch; ++m)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma_bf16(s[t][n][m % CH], a, b[n][0], b[n][1]);
-        }
+            for (int t = 0; t < TT; ++t)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma_bf16(s[t][n][m % CH], a[t][m], b[m][n][0], b[m][n][1]);
     }
     // logits: element e of s is token 16 t + g + 8 (e / 2), row 2c + e % 2
     float top = -INFINITY;
+    const bool masked = j0 + 16 * TT > last - T + 2;  // some row does not see all of them
 #pragma unroll
-    for (int t = 0; t < TT; ++t)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int i = 0; i < 2; ++i) {
+            const float behind0 = static_cast<float>(j0) - st.pos[n][i];  // whole numbers below 2^24: exact
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                // token less position, in whole numbers below 2^24: exact
-                const float behind = static_cast<float>(j0 + 16 * t + 8 * (e >> 1)) - st.pos[n][e & 1];
-                const float y = CH == 2 ? s[t][n][0][e] + s[t][n][CH - 1][e] : s[t][n][0][e];
-                const float x = behind <= 0.0f ? fmaf(y, c1, st.slope[n][e & 1] * behind) : -INFINITY;
-                s[t][n][0][e] = x;
-                top = fmaxf(top, x - st.R[n][e & 1]);
-            }
+            for (int t = 0; t < TT; ++t)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int e = 2 * h + i;
+                    const float behind = behind0 + static_cast<float>(16 * t + 8 * h);
+                    const float y = CH == 2 ? s[t][n][0][e] + s[t][n][CH - 1][e] : s[t][n][0][e];
+                    float x = fmaf(y, c1, st.slope[n][i] * behind);
+                    if (masked) x = behind <= 0.0f ? x : -INFINITY;
+                    s[t][n][0][e] = x;
+                    top = fmaxf(top, x - st.R[n][i]);
+                }
+        }
     if (__any_sync(0xffffffffu, top > 8.0f)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -218,7 +239,7 @@ __device__ __forceinline__ void tokens16(Rows8<D, NT> &st, uint32_t k, uint32_t 
                 hi[t][n][h] = transpose8(__byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632));
                 lo[t][n][h] = transpose8(pack_bf16x2(rest(p0), rest(p1)));
             }
-    if (T > 1 && j0 + 16 * TT > last - T + 2) {  // some row does not see all of them
+    if (T > 1 && masked) {
         bool odd = false;
         for (int x = lane; x < 16 * TT * (D / 8); x += 32) {
             uint32_t w[4];
@@ -232,14 +253,19 @@ __device__ __forceinline__ void tokens16(Rows8<D, NT> &st, uint32_t k, uint32_t 
 #pragma unroll
     for (int t = 0; t < TT; ++t)
 #pragma unroll
-        for (int m = 0; m < D / 16; ++m) {
-            uint32_t a[4];
-            ldmatrix4_trans(a, v + place<D>(16 * t + (lane & 7) + (lane >> 4) * 8, 2 * m + ((lane >> 3) & 1)));
+        for (int m0 = 0; m0 < D / 16; m0 += kBatch) {
+            uint32_t a[kBatch][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                mma_bf16(st.acc[m][n], a, lo[t][n][0], lo[t][n][1]);
-                mma_bf16(st.acc[m][n], a, hi[t][n][0], hi[t][n][1]);
-            }
+            for (int m = 0; m < kBatch; ++m)
+                ldmatrix4_trans(a[m], step<D, 16 * TT>(v + va, m0 + m) + 16 * t * kRow);
+#pragma unroll
+            for (int m = 0; m < kBatch; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma_bf16(st.acc[m0 + m][n], a[m], lo[t][n][0], lo[t][n][1]);
+#pragma unroll
+            for (int m = 0; m < kBatch; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma_bf16(st.acc[m0 + m][n], a[m], hi[t][n][0], hi[t][n][1]);
         }
 }
 
@@ -312,10 +338,11 @@ __global__ void __launch_bounds__(kPgWarps * 32, 2) decode_paged_kernel(const __
 {
     constexpr int TK = pg_tokens(D), ROWS = 8 * NT, kRowStride = D + 4;
     constexpr int TT = D == 128 ? 1 : 2;           // tiles of 16 tokens taken at once
-    constexpr int kGroups = TK / 8;                // groups of 8 tokens of a stage: of one page each
-    constexpr int kCopies = kPgStageBytes / 2 / 512;  // of 16 bytes per lane, keys or values of a stage
-    static_assert(kCopies == 8 && ROWS * (kRowStride + 2) * 4 <= kPgStages * kPgStageBytes, "a warp's partial fits its ring");
-    extern __shared__ __align__(128) uint8_t smem[];
+    static_assert(ROWS * kRowStride * 4 <= kPgStages * kPgStageBytes, "a warp's partial fits its ring");
+    static_assert(D < 128 || (TK == 16 * TT), "a tile of halves is a stage");
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ __align__(8) uint64_t full[kPgWarps][kPgStages];
     __shared__ float2 merged_rl[kMostRows];
     __shared__ float2 warp_rl[kPgWarps][kMostRows];
     __shared__ kv4::Share sh;
@@ -324,6 +351,17 @@ __global__ void __launch_bounds__(kPgWarps * 32, 2) decode_paged_kernel(const __
     const int U = p.Hkv * p.chunks;
 
     if (SHARES) griddep_launch_dependents();  // the merge kernel
+    if (threadIdx.x == 0) {
+        cta_err_init(kWaitLimitNs);
+        cta_check_init(p.status, smem_raw, pg_smem(D, NT));
+        tma_prefetch_desc(&p.tk);
+        tma_prefetch_desc(&p.tv);
+    }
+    if (lane == 0) {
+        for (int i = 0; i < kPgStages; ++i) mbar_init(&full[warp][i], 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
     griddep_wait();  // the kernel before, which may have written what this one reads, is done
     // The second half of the CTAs, which join the first on their SMs, take the shares from the end.
     const int half = gridDim.x / 2;
@@ -333,7 +371,12 @@ __global__ void __launch_bounds__(kPgWarps * 32, 2) decode_paged_kernel(const __
         if (threadIdx.x == 0) row = all;
         if (sh.left <= 0) return;
     }
-    const uint32_t ring = smem_u32(smem) + warp * (kPgStages * kPgStageBytes), sq = smem_u32(smem) + kPgRing;
+    uint8_t *const mine = smem + warp * (kPgStages * kPgStageBytes), *const queries = smem + kPgRing;
+    const uint32_t ring = smem_u32(mine), sq = smem_u32(queries);
+    // A stage is boxes of `box` slots; lanes i and 16 + i load box i of the keys and of the values.
+    const int box = min(1 << p.pg.shift, TK), part = (lane & 15) * box;
+    int slot = 0;
+    uint32_t phase = 0;
 
     while (true) {
         const int whole_chunk = p.by_count.of(blockIdx.x);  // chunk of all sequences
@@ -349,7 +392,7 @@ __global__ void __launch_bounds__(kPgWarps * 32, 2) decode_paged_kernel(const __
                 const int r = x / (D / 8), piece = x % (D / 8);
                 uint4 w = make_uint4(0, 0, 0, 0);
                 if (r < nrows) w = *reinterpret_cast<const uint4 *>(q0 + r * D + 8 * piece);
-                *reinterpret_cast<uint4 *>(smem + kPgRing + place<D>(r, piece)) = w;
+                *reinterpret_cast<uint4 *>(queries + place<D, kMostRows>(r, piece)) = w;
             }
         } else {
 #pragma unroll
@@ -374,34 +417,32 @@ __global__ void __launch_bounds__(kPgWarps * 32, 2) decode_paged_kernel(const __
         if (bad && unit == 0 && threadIdx.x == 0) atomicOr(p.status, ALIBI_DEV_RANGE);
         bool lost = false;  // a page number that is none
 
-        // Page of this lane's group of 8 tokens of stage s.
+        // Page of this lane's box of stage s; past the length, one beyond the pool, whose box is filled with zeros.
         const auto page_at = [&](int s) {
-            const int j = s * TK + 8 * lane;
-            return lane < kGroups && s >= s0 && j < len ? p.pg.page_of(b, j) : 0;
+            const int j = s * TK + part;
+            return part < TK && s >= s0 && j < len ? p.pg.page_of(b, j) : p.pg.pages;
         };
-        const auto fetch = [&](int s, int slot, int page) {
-            if (s >= s0) {
-                const int j = s * TK + 8 * lane;
-                if (page < 0) lost = true, page = 0;
-                const int first = p.pg.slot_of(j);
-                const long long ko = page * p.pg.k_page + first * p.pg.k_slot + hk * p.pg.k_head;
-                const long long vo = page * p.pg.v_page + first * p.pg.v_slot + hk * p.pg.v_head;
-                const uint32_t kd = ring + slot * kPgStageBytes, vd = kd + kPgStageBytes / 2;
+        const auto fetch = [&](int s, int slot_, int page) {
+            if (s < s0) return;
+            if (page < 0) lost = true, page = p.pg.pages;
+            if (lane == 0) mbar_arrive_expect_tx(&full[warp][slot_], kPgStageBytes);
+            __syncwarp();
+            if (part < TK) {
+                constexpr int W = D < 64 ? D : 64;  // elements of a box's row
+                const bool values = lane >= 16;
+                uint8_t *to = mine + slot_ * kPgStageBytes + (values ? kPgStageBytes / 2 : 0) + part * (2 * W);
 #pragma unroll
-                for (int i = 0; i < kCopies; ++i) {
-                    const int x = i * 32 + lane, r = x / (D / 8), piece = x % (D / 8);
-                    const long long kg = __shfl_sync(0xffffffffu, ko, r >> 3), vg = __shfl_sync(0xffffffffu, vo, r >> 3);
-                    const uint32_t bytes = s * TK + r < len ? 16u : 0u, to = place<D>(r, piece);
-                    const int inside = s * TK + r < len ? r & 7 : 0;
-                    cp_async16(kd + to, p.pg.k + kg + inside * p.pg.k_slot + 8 * piece, bytes);
-                    cp_async16(vd + to, p.pg.v + vg + inside * p.pg.v_slot + 8 * piece, bytes);
-                }
+                for (int i = 0; i < D / W; ++i)
+                    tma_load_4d(to + i * (TK * 2 * W), values ? &p.tv : &p.tk, W * i, p.pg.slot_of(s * TK + part), hk, page,
+                                box * 2 * W, &full[warp][slot_]);
             }
-            cp_commit();
         };
         int s = s1 - 1 - (SHARES ? warp : at + warp * count);  // this warp's stages: s, s - step, ...
-#pragma unroll
-        for (int i = 0; i < kPgStages; ++i) fetch(s - i * step, i, page_at(s - i * step));
+        for (int i = 0, k = slot; i < kPgStages; ++i) {
+            fetch(s - i * step, k, page_at(s - i * step));
+            if (++k == kPgStages) k = 0;
+        }
+        int page = page_at(s - kPgStages * step);  // of the stage to be fetched next, read an iteration ahead
 
 #pragma unroll
         for (int i = 0; i < NT; ++i)
@@ -421,12 +462,17 @@ __global__ void __launch_bounds__(kPgWarps * 32, 2) decode_paged_kernel(const __
                 for (int e = 0; e < 4; ++e) st.acc[m][i][e] = 0.0f;
         if constexpr (NT > 2) __syncthreads();  // the queries in shared memory
 
-        int slot = 0;
         for (; s >= s0; s -= step) {
-            const int next = s - kPgStages * step, page = page_at(next);
-            cp_wait<kPgStages - 1>();
-            __syncwarp();
+            const int next = s - kPgStages * step, ahead = page_at(next - step);
+            if (!__all_sync(0xffffffffu, mbar_wait(&full[warp][slot], phase, p.status, 0x70))) break;
             const uint32_t k = ring + slot * kPgStageBytes, v = k + kPgStageBytes / 2;
+            if ((s + 1) * TK > len) {  // slots past the length: their weights are zero, and so are to be their values
+                for (int x = (len - s * TK) * (D / 8) + lane; x < TK * (D / 8); x += 32)
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(v + place<D, TK>(x / (D / 8), x % (D / 8))), "r"(0)
+                                 : "memory");
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
 #pragma unroll 1
             for (int t = TK / (16 * TT) - 1; t >= 0; --t) {
                 const int j0 = s * TK + t * 16 * TT;
@@ -435,15 +481,20 @@ __global__ void __launch_bounds__(kPgWarps * 32, 2) decode_paged_kernel(const __
             }
             __syncwarp();
             fetch(next, slot, page);
-            if (++slot == kPgStages) slot = 0;
+            page = ahead;
+            if (++slot == kPgStages) slot = 0, phase ^= 1u;
         }
-        cp_wait<0>();
+        // a wait ran out (recorded): let the copies in flight land before the ring is reused
+        for (int i = 0; i < kPgStages && s >= s0; ++i, s -= step) {
+            mbar_wait(&full[warp][slot], phase, p.status, 0x71, true);
+            if (++slot == kPgStages) slot = 0, phase ^= 1u;
+        }
         __syncwarp();
 
         // the warp's partial: reference R, l = sum of p, and the mean of v (never beyond the largest |v|)
         lost = __any_sync(0xffffffffu, lost);
         if (lost && lane == 0) atomicOr(p.status, ALIBI_DEV_RANGE);
-        float *pw = reinterpret_cast<float *>(smem + warp * (kPgStages * kPgStageBytes));  // [ROWS][D + 4]
+        float *pw = reinterpret_cast<float *>(mine);  // [ROWS][D + 4]
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -501,7 +552,8 @@ __global__ void __launch_bounds__(kPgWarps * 32, 2) decode_paged_kernel(const __
             cluster_wait();
             return;
         }
-        __syncthreads();  // the partials were read, and the share's place, before either changes
+        fence_proxy_async_smem();  // the partials were written and read before the next copies overwrite them
+        __syncthreads();           // and the share's place read before it changes
         if (threadIdx.x == 0) {
             sh.left -= take;
             sh.at += take;
@@ -523,8 +575,45 @@ __global__ void __launch_bounds__(kPgWarps * 32, 2) decode_paged_kernel(const __
 
 bool aligned(const void *p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// Clusters of c CTAs that the current device holds at once, asked for once, with the most shared memory that any of the kernels
+// takes: two CTAs per SM as with the least.
+template <class Kernel>
+cudaError_t cluster_fit(Kernel kernel, int smem, int (&fit)[paged::kMostCluster + 1])
+{
+    constexpr int kDevices = 64;  // a device beyond is asked every time
+    static std::mutex mu;
+    static int known[kDevices][paged::kMostCluster + 1];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> g(mu);
+    if (dev >= kDevices || known[dev][1] == 0) {
+        e = prepare_kernel(reinterpret_cast<const void *>(kernel), smem, 0, true);
+        if (e != cudaSuccess) return e;
+        fit[0] = 0, fit[1] = 1;
+        for (int c = 2; c <= paged::kMostCluster; ++c) {
+            cudaLaunchAttribute attr = {};
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = static_cast<unsigned>(c);
+            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(static_cast<unsigned>(c));
+            cfg.blockDim = dim3(kPgWarps * 32);
+            cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            e = cudaOccupancyMaxActiveClusters(&fit[c], kernel, &cfg);
+            if (e != cudaSuccess) return e;
+        }
+        if (dev < kDevices) std::copy(fit, fit + paged::kMostCluster + 1, known[dev]);
+        return cudaSuccess;
+    }
+    std::copy(known[dev], known[dev] + paged::kMostCluster + 1, fit);
+    return cudaSuccess;
+}
+
 template <int D, int NT>
-cudaError_t launch(DecodePagedParams &p, cudaStream_t stream)
+cudaError_t launch(DecodePagedParams &p, const alibi_pages *pages, cudaStream_t stream)
 {
     constexpr int ROWS = 8 * NT, smem = pg_smem(D, NT);
     p.chunks = (p.rows + ROWS - 1) / ROWS;
@@ -535,22 +624,22 @@ cudaError_t launch(DecodePagedParams &p, cudaStream_t stream)
     const int busy = (stages + kPgWarps - 1) / kPgWarps;  // CTAs that a chunk can keep busy
     const auto chunks = &decode_paged_kernel<D, NT, false>;
     const auto shared = &decode_paged_kernel<D, NT, true>;
+    if (!encode_pages(&p.tk, &p.tv, pages, std::min(D, 64), std::min(pages->slots, pg_tokens(D)))) return cudaErrorInvalidValue;
     p.part = nullptr;
     p.head = nullptr;
-    int count = 1;
-    while (2 * count <= 8 && 2 * count * units <= ctas && 2 * count <= busy) count *= 2;
-    p.count = count;
-    p.by_count = Divisor(static_cast<uint32_t>(count));
-    const bool split = (units * count < ctas - ctas / 8 && busy > 2 * count) || (units * count > ctas && units < 4 * ctas && busy > 2);
-    if (!split) {
+    int fit[paged::kMostCluster + 1];
+    cudaError_t e = cluster_fit(chunks, pg_smem(128, 4), fit);
+    if (e != cudaSuccess) return e;
+    const int count = paged::ctas_of_chunk(units, stages, ctas, fit, paged::step_us(D, NT));
+    p.count = std::max(count, 1);
+    p.by_count = Divisor(static_cast<uint32_t>(p.count));
+    if (count > 0) {
         if (units * count > 0x7fffffffLL) return cudaErrorInvalidValue;
-        const cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(chunks), smem, 0, true);
+        e = prepare_kernel(reinterpret_cast<const void *>(chunks), pg_smem(128, 4), 0, true);
         if (e != cudaSuccess) return e;
         return launch_kernel(chunks, dim3(static_cast<unsigned>(units * count)), kPgWarps * 32, smem, stream, p, count);
     }
-    p.count = 1;
-    p.by_count = Divisor(1);
-    cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(shared), smem, 0);
+    e = prepare_kernel(reinterpret_cast<const void *>(shared), smem, 0);
     if (e != cudaSuccess) return e;
     const int shares = static_cast<int>(std::min<long long>(units * busy, ctas));
     const size_t bytes = static_cast<size_t>(shares) * 2 * part_floats(D, ROWS) * sizeof(float);
@@ -570,9 +659,9 @@ cudaError_t launch(DecodePagedParams &p, cudaStream_t stream)
 }
 
 template <int D>
-cudaError_t launch_rows(DecodePagedParams &p, cudaStream_t stream)
+cudaError_t launch_rows(DecodePagedParams &p, const alibi_pages *pages, cudaStream_t stream)
 {
-    return p.rows <= 8 ? launch<D, 1>(p, stream) : p.rows <= 16 ? launch<D, 2>(p, stream) : launch<D, 4>(p, stream);
+    return p.rows <= 8 ? launch<D, 1>(p, pages, stream) : p.rows <= 16 ? launch<D, 2>(p, pages, stream) : launch<D, 4>(p, pages, stream);
 }
 
 }  // namespace
@@ -618,10 +707,10 @@ extern "C" int alibi_attn_decode_paged(const void *q, const alibi_pages *pages, 
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     switch (pages->d) {
-        case 128: e = launch_rows<128>(p, cs); break;
-        case 64: e = launch_rows<64>(p, cs); break;
-        case 32: e = launch_rows<32>(p, cs); break;
-        default: e = launch_rows<16>(p, cs); break;
+        case 128: e = launch_rows<128>(p, pages, cs); break;
+        case 64: e = launch_rows<64>(p, pages, cs); break;
+        case 32: e = launch_rows<32>(p, pages, cs); break;
+        default: e = launch_rows<16>(p, pages, cs); break;
     }
     return e == cudaSuccess ? ALIBI_OK : ALIBI_ERR_CUDA;
 }

@@ -104,21 +104,6 @@ __device__ __forceinline__ int paged_index(int k)
 
 __device__ __forceinline__ bool paged_active(const PagedItem &t, int s, int it) { return s == 1 ? t.q1valid : it >= t.first0; }
 
-// 4-D tiled load of one box into shared memory, completing on `bar`.
-__device__ __forceinline__ void tma_load_4d(void *dst, const void *tmap, int x, int y, int z, int w, uint32_t bytes, uint64_t *bar)
-{
-#ifdef ALIBI_CHECKS
-    if (!check::tma_x_aligned(x)) return check_fail(check::TMA_LOAD, static_cast<uint32_t>(x));
-    if (!check_smem(smem_u32(dst), bytes, 1024)) return check_fail(check::TMA_LOAD, smem_u32(dst));
-#endif
-    (void)bytes;
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
-        : "memory");
-}
-
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_constant__ FwdPagedParams p)
 {
@@ -612,11 +597,8 @@ cudaError_t launch(FwdPagedParams &p, const alibi_pages *pages, const void *q, c
     using C = Cfg<D>;
     const uint64_t d = static_cast<uint64_t>(pages->d);
     const uint32_t box = static_cast<uint32_t>(std::min(pages->slots, BN));
-    const uint64_t dims[4] = {d, static_cast<uint64_t>(pages->slots), static_cast<uint64_t>(pages->heads), static_cast<uint64_t>(pages->pages)};
-    const uint64_t ks[3] = {2ull * pages->k_slot, 2ull * pages->k_head, 2ull * pages->k_page};
-    const uint64_t vs[3] = {2ull * pages->v_slot, 2ull * pages->v_head, 2ull * pages->v_page};
     if (!encode_tmap_bf16_3d(&p.tq, q, d, p.T, p.BH, 64, BM) || !encode_tmap_bf16_3d(&p.tout, p.out, d, p.T, p.BH, 32, 32, false) ||
-        !encode_tmap_bf16_4d(&p.tk, pages->k, dims, ks, 64, box) || !encode_tmap_bf16_4d(&p.tv, pages->v, dims, vs, 64, box))
+        !encode_pages(&p.tk, &p.tv, pages, 64, box))
         return cudaErrorInvalidValue;
     const auto kern = &fwd_paged_kernel<D>;
     const cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(kern), C::kSmem, kLaunchRegs);

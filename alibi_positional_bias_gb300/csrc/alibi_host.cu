@@ -80,6 +80,22 @@ EncodeTiledFn encode_fn()
     return fn;
 }
 
+// The driver's encoder wants a current context, which a host thread that has called only what needs none does not have yet:
+// the runtime then makes its device's current.
+template <class... Args>
+bool encode_tiled(Args... args)
+{
+    const EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    CUresult r = fn(args...);
+    if (r == CUDA_ERROR_INVALID_CONTEXT || r == CUDA_ERROR_NOT_INITIALIZED) {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return false;
+        r = fn(args...);
+    }
+    return r == CUDA_SUCCESS;
+}
+
 int to_status(cudaError_t e)
 {
     return e == cudaSuccess ? ALIBI_OK : ALIBI_ERR_CUDA;
@@ -330,30 +346,29 @@ void fill_slopes_from(int H, const float *nat, Slopes *s)
 bool encode_tmap_bf16_3d(CUtensorMap *map, const void *base, uint64_t dim0, uint64_t dim1, uint64_t dim2,
                          uint32_t box0, uint32_t box1, bool swizzle128)
 {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
     const cuuint64_t dims[3] = {dim0, dim1, dim2};
     const cuuint64_t strides[2] = {dim0 * 2, dim0 * dim1 * 2};  // bytes, dims 1 and 2
     const cuuint32_t box[3] = {box0, box1, 1};
     const cuuint32_t estride[3] = {1, 1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estride,
+    return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3u, const_cast<void *>(base), dims, strides, box, estride,
               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 bool encode_tmap_bf16_4d(CUtensorMap *map, const void *base, const uint64_t (&dims)[4], const uint64_t (&strides)[3],
                          uint32_t box0, uint32_t box1)
 {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
     const cuuint64_t n[4] = {dims[0], dims[1], dims[2], dims[3]};
     const cuuint64_t stride[3] = {strides[0], strides[1], strides[2]};
     const cuuint32_t box[4] = {box0, box1, 1, 1};
     const cuuint32_t estride[4] = {1, 1, 1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), n, stride, box, estride,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4u, const_cast<void *>(base), n, stride, box, estride,
+              CU_TENSOR_MAP_INTERLEAVE_NONE,
+              box0 == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
+              : box0 == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                           : CU_TENSOR_MAP_SWIZZLE_32B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 }  // namespace alibi

@@ -5,6 +5,7 @@
 
 #include "alibi.h"
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace alibi {
 
@@ -55,6 +56,32 @@ inline Pages pages_of(const alibi_pages *p)
     g.width = p->width;
     g.d = p->d;
     return g;
+}
+
+// 4-D tiled load of one box of `bytes` bytes, a power of two, into shared memory, completing on `bar`. It lies on a multiple of
+// its size or of 1024, where the swizzle's pattern begins anew.
+__device__ __forceinline__ void tma_load_4d(void *dst, const void *tmap, int x, int y, int z, int w, uint32_t bytes, uint64_t *bar)
+{
+#ifdef ALIBI_CHECKS
+    if (!check::tma_x_aligned(x)) return check_fail(check::TMA_LOAD, static_cast<uint32_t>(x));
+    if (!check_smem(smem_u32(dst), bytes, bytes < 1024 ? bytes : 1024)) return check_fail(check::TMA_LOAD, smem_u32(dst));
+#endif
+    (void)bytes;
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// Maps of the keys' and values' pools for boxes of `box0` elements of `box1` slots of one head of one page.
+inline bool encode_pages(CUtensorMap *tk, CUtensorMap *tv, const alibi_pages *p, uint32_t box0, uint32_t box1)
+{
+    const uint64_t dims[4] = {static_cast<uint64_t>(p->d), static_cast<uint64_t>(p->slots), static_cast<uint64_t>(p->heads),
+                              static_cast<uint64_t>(p->pages)};
+    const uint64_t ks[3] = {2ull * p->k_slot, 2ull * p->k_head, 2ull * p->k_page};
+    const uint64_t vs[3] = {2ull * p->v_slot, 2ull * p->v_head, 2ull * p->v_page};
+    return encode_tmap_bf16_4d(tk, p->k, dims, ks, box0, box1) && encode_tmap_bf16_4d(tv, p->v, dims, vs, box0, box1);
 }
 
 }  // namespace alibi
