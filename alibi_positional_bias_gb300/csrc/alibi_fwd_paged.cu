@@ -14,19 +14,23 @@
 //             loaded from beyond the tensor, which fills zeros.
 //   diagonal  positions begin anywhere in a tile, so a slot's rows end inside two tiles, and a row may see nothing of the first
 //             tile that its slot visits.
-//   values    that some row of the item does not see meet a weight of zero, which an infinity or a NaN would turn into NaN: two
-//             warps look through the first tiles' values, those that some row does not see whole (up to three of an item),
-//             put zeros in place of what is not finite and note per column the first such row, from which on the
-//             outputs are NaN. The scores and the softmax of the tile run meanwhile.
+//   values    that a row does not see meet a weight of zero, which an infinity or a NaN would turn into NaN. Two warps set the
+//             values past the length to zero. If an output is not finite all the same, the CTA takes its items once more: the
+//             two warps then look through the first tiles' values, those that some row of the item does not see (up to three
+//             tiles), put zeros in place of what is not finite and note per column the first such row, from which on the
+//             outputs are NaN. (Looking through them at once took 15% of the time of prompts of 2048 tokens.)
 //   rows      past count_b are left as they were: of a box of 32 rows that reaches there the lanes store their own.
+//   parts     items that do not fill a round of one per SM are cut into parts of their tiles, which run one after another over
+//             all SMs, part by part, so that the CTAs of a KV head pass its tiles at the same time; a part leaves its mean,
+//             maximum and sum in scratch, and a second kernel merges them. (Equal shares of all items' tiles for every CTA, as the
+//             decode has them, fill the device as well, but the tiles then come from memory for each: 2.0 us a tile, not 1.6.)
 //
-// Steep heads (slopes above 4 / log2(e)) take the bias element by element from the whole distance, where the column part on
-// the tensor core and the row part would cancel with a rounding of 2^-24 of 128 slopes.
+// Where some head is steep (a slope above 4 / log2(e)), the bias is taken element by element from the whole distance: the
+// column part on the tensor core and the row part would cancel with a rounding of 2^-24 of 128 slopes.
 
 #include <algorithm>
 #include <cmath>
 #include <cuda.h>
-#include <type_traits>
 
 #include "alibi.h"
 #include "divide.h"
@@ -38,6 +42,7 @@ namespace alibi {
 namespace {
 
 constexpr float kSteep = 4.0f;  // m log2(e)
+constexpr int kMostParts = 16;
 
 struct FwdPagedParams {
     CUtensorMap tq;      // [B H, T, d] bf16, box {64, 128, 1}, 128-byte swizzle
@@ -49,6 +54,10 @@ struct FwdPagedParams {
     float *lse;
     uint32_t *err;
     int T, L, BH, H, num_items, blocks;  // blocks of 256 rows of a head
+    int whole, rest, parts;              // items that are not cut, those after them, parts of each of these
+    int num_units;                       // whole + rest parts
+    Divisor div_rest;
+    float *part;                         // [rest][parts] partials
     Divisor div_bh, div_h, div_g;        // by B H, H and H / H_kv
     float c1;                            // log2(e) / sqrt(d)
     float slope[kMaxQueryHeads];         // m log2(e)
@@ -56,22 +65,26 @@ struct FwdPagedParams {
 
 enum : uint32_t {
     SITE_PG_Q = 0x401, SITE_PG_UNIT = 0x402, SITE_PG_FIX = 0x403, SITE_PG_P = 0x404, SITE_PG_O = 0x405, SITE_PG_DONE = 0x406,
-    SITE_PG_S = 0x407,
+    SITE_PG_S = 0x407, SITE_PG_AGAIN = 0x408,
 };
+
+// A partial: D means of 256 rows, [D][256], then M and l of the rows, [2][256].
+__host__ __device__ constexpr int paged_part_floats(int D) { return (D + 2) * 2 * BM; }
 
 struct PagedItem {
     int bh, qb;
     int len, count;   // of the sequence
     int first;        // position of its query 0
-    int top, n;       // newest key tile, and tiles visited: top, top - 1, ..., 0
-    int n_fix;        // of which the first have keys that some row does not see
+    int top, n;       // newest key tile, and tiles visited: top, top - 1, ...
+    int n_fix;        // of which the first are looked through
     int first0;       // iteration at which slot 0 begins
     bool q1valid, bad;
+    int part;         // number of the partial it leaves, -1: whole
 };
 
-// Work item at position idx, or false where the sequence has no rows there. Longest first: round r holds block blocks - 1 - r
-// of every head.
-__device__ __forceinline__ bool paged_item(const FwdPagedParams &p, int idx, PagedItem &t)
+// Item idx, or false where its sequence has no rows there. Longest first: round r holds block blocks - 1 - r of every head.
+// careful: n_fix is the tiles that some row does not see whole; else the one that the sequence ends in.
+__device__ __forceinline__ bool paged_item(const FwdPagedParams &p, int idx, bool careful, PagedItem &t)
 {
     const int round = p.div_bh.of(idx);
     t.bh = idx - round * p.BH;
@@ -91,20 +104,95 @@ __device__ __forceinline__ bool paged_item(const FwdPagedParams &p, int idx, Pag
     const int top0 = max(0, min(i0 + BM - 1, t.len - 1)) >> 7, top1 = max(0, min(i0 + 2 * BM - 1, t.len - 1)) >> 7;
     t.top = t.q1valid ? top1 : top0;
     t.n = t.top + 1;
-    t.n_fix = max(1, t.top + 1 - ((max(i0, 0) + 1) >> 7));
+    t.n_fix = careful ? max(1, t.top + 1 - ((max(i0, 0) + 1) >> 7)) : (t.top + 1) * BN > t.len ? 1 : 0;
     t.first0 = t.top - top0;
+    t.part = -1;
     return true;
 }
 
-__device__ __forceinline__ int paged_index(int k)
+// Tiles of an item of n before its part `q` of `parts`. Not 1: slot 0 may begin at tile 1, and a part has tiles of both slots.
+__device__ __forceinline__ int part_begin(int n, int q, int parts)
 {
-    const int G = gridDim.x, c = blockIdx.x;
-    return (k & 1) ? (k + 1) * G - 1 - c : k * G + c;
+    const int c = static_cast<int>(static_cast<long long>(n) * q / parts);
+    return c == 1 && n > 1 ? 0 : c;
 }
+
+// The items of a CTA, or its parts of items, one after another.
+struct PagedWalk {
+    int k = 0;
+
+    __device__ __forceinline__ bool next(const FwdPagedParams &p, bool careful, PagedItem &t)
+    {
+        while (true) {
+            const int G = gridDim.x, c = blockIdx.x, unit = (k & 1) ? (k + 1) * G - 1 - c : k * G + c;
+            if (unit >= p.num_units) return false;
+            ++k;
+            const int q = unit < p.whole ? 0 : p.div_rest.of(unit - p.whole), i = unit - q * p.rest;  // part, item
+            if (!paged_item(p, i, careful, t)) continue;
+            if (unit < p.whole) return true;
+            const int a = part_begin(t.n, q, p.parts), b = part_begin(t.n, q + 1, p.parts);
+            if (a == b) continue;
+            t.part = (i - p.whole) * p.parts + q;
+            t.n = b - a;
+            t.top -= a;
+            t.n_fix = max(0, min(t.n_fix - a, t.n));
+            if (a > 0) t.first0 = 0;
+            return true;
+        }
+    }
+};
+
+// What a softmax warp keeps from item to item, and of an item until its tiles are done.
+struct SoftmaxState {
+    int k;                     // its walk
+    int pass, items, outputs;  // of its CTA's, items begun, outputs written
+    int part, bh, count, row0, first, flags;
+};
+
+// And the MMA issuer.
+struct IssuerState {
+    int k, pass, items;
+    int fixed, outputs;  // parities: of the tiles looked through, of the outputs of each slot
+};
 
 __device__ __forceinline__ bool paged_active(const PagedItem &t, int s, int it) { return s == 1 ? t.q1valid : it >= t.first0; }
 
-template <int D>
+// A bounded wait of a role that other items may leave idle for long: the limit holds from one item of the MMA issuer, which
+// it counts in `progress`, to the next. It sleeps between its looks: warps that poll for as long as an item takes cost the
+// softmax warps of their schedulers a third of their time.
+__device__ __forceinline__ bool wait_idle(uint64_t *bar, uint32_t parity, const int *progress, uint32_t *err, uint32_t site)
+{
+    uint64_t t0 = 0;
+    int seen = 0;
+    uint32_t sleep = 50;
+#pragma unroll 1
+    for (uint32_t n = 0;; ++n) {
+        if (mbar_test(bar, parity)) return true;
+        __nanosleep(sleep);
+        sleep = min(2 * sleep, 2000u);
+        if ((n & 255u) != 255u) continue;
+        if (*(volatile uint32_t *)&cta_abort != 0u) return false;
+        const uint64_t t = global_timer_ns();
+        const int now = *reinterpret_cast<const volatile int *>(progress);
+        if (t0 == 0 || now != seen) {
+            t0 = t, seen = now;
+        } else if (t - t0 > *(volatile uint64_t *)&cta_wait_ns) {
+            report_error(err, ALIBI_DEV_TIMEOUT, site);
+            *(volatile uint32_t *)&cta_abort = ALIBI_DEV_TIMEOUT;
+            return false;
+        }
+    }
+}
+
+// The CTA's warps meet after a pass over its items: is there to be another one?
+__device__ __forceinline__ bool again(uint64_t *met, const int *progress, const int *redo, uint32_t *err)
+{
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(met);
+    return __all_sync(0xffffffffu, wait_idle(met, 0, progress, err, SITE_PG_AGAIN)) && *reinterpret_cast<const volatile int *>(redo) != 0;
+}
+
+template <int D, bool STEEP>
 __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_constant__ FwdPagedParams p)
 {
     using C = Cfg<D>;
@@ -112,23 +200,27 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
     // of the items in flight, two at most: the first row of each column of V that is not finite, whether each half of the
     // columns has one, and whether a page number is none
     __shared__ int odd_from[2][D];
-    __shared__ int odd_any[2][2], lost[2];
+    __shared__ int odd_any[2][2], lost[2], redo, progress;
+    __shared__ SoftmaxState states[8];
+    __shared__ IssuerState issuer;
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kBar);
-    uint64_t *q_full = bars + 0;      // both Q tiles of the item loaded
-    uint64_t *q_empty = bars + 1;
-    uint64_t *unit_full = bars + 2;   // [2] ring unit of stage s loaded (K(u) and V(u - 1))
-    uint64_t *unit_empty = bars + 4;  // [2] ring unit of stage s read by the MMAs
-    uint64_t *s_full = bars + 6;      // [2]
-    uint64_t *p_full = bars + 8;      // [2] P of keys 0..63 written
-    uint64_t *p_hi = bars + 10;       // [2] P of keys 64..127 written
-    uint64_t *o_full = bars + 12;     // [2]
-    uint64_t *o_empty = bars + 14;    // [2]
-    uint64_t *bias_full = bars + 16;  // [2] column-bias operand of item k written (buffer k & 1)
-    uint64_t *v_ready = bars + 18;    // values that some row does not see have landed
-    uint64_t *v_fixed = bars + 19;    // and are finite
-    uint64_t *mma_done = bars + 20;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 21);
+    // In static shared memory, whose addresses are constants: the softmax loop has no registers for them.
+    __shared__ uint64_t q_full[1];      // both Q tiles of the item loaded
+    __shared__ uint64_t q_empty[1];
+    __shared__ uint64_t unit_full[2];   // ring unit of stage s loaded (K(u) and V(u - 1))
+    __shared__ uint64_t unit_empty[2];  // ring unit of stage s read by the MMAs
+    __shared__ uint64_t s_full[2];
+    __shared__ uint64_t p_full[2];      // P of keys 0..63 written
+    __shared__ uint64_t p_hi[2];        // P of keys 64..127 written
+    __shared__ uint64_t o_full[2];
+    __shared__ uint64_t o_empty[2];
+    __shared__ uint64_t bias_full[2];   // column-bias operand of item k written (buffer k & 1)
+    __shared__ uint64_t begun[1];       // the MMA issuer has begun an item: all before it is computed
+    __shared__ uint64_t v_ready[1];     // values to be looked through have landed
+    __shared__ uint64_t v_fixed[1];     // and are finite
+    __shared__ uint64_t met[1];         // the warps after their first pass
+    __shared__ uint64_t mma_done[1];
+    __shared__ uint32_t tmem_slot[1];
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -137,6 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
     if (threadIdx.x == 0) {
         cta_err_init(kWaitLimitNs);
         cta_check_init(p.err, smem_raw, C::kSmem);
+        redo = progress = 0;
         for (int s = 0; s < 2; ++s) {
             mbar_init(&unit_full[s], 1);
             mbar_init(&unit_empty[s], 1);
@@ -145,13 +238,15 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
             mbar_init(&p_hi[s], 4);
             mbar_init(&o_full[s], 1);
             mbar_init(&o_empty[s], 4);
-            mbar_init(&bias_full[s], 4);  // the slot-0 softmax warps
+            mbar_init(&bias_full[s], 2);  // the two warps that write it
         }
         mbar_init(q_empty, 1);
         mbar_init(q_full, 1);
+        mbar_init(begun, 1);
         mbar_init(v_ready, 1);
         mbar_init(v_fixed, 2);  // the two warps that look through them
         mbar_init(mma_done, 1);
+        mbar_init(met, kThreads / 32);
         fence_mbar_init();
         tma_prefetch_desc(&p.tq);
         tma_prefetch_desc(&p.tk);
@@ -171,6 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    if (p.parts > 1) griddep_launch_dependents();  // the merge kernel
     griddep_wait();  // the kernel before, which may have written what this one reads, is done
 
     if (warp < 4) {
@@ -181,11 +277,14 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
         uint32_t uc = 0;  // ring units issued
         int kk = 0;       // items begun
         bool ok = true;
-        for (int k = 0; ok; ++k) {
-            const int w = paged_index(k);
-            if (w >= p.num_items) break;
+        PagedWalk walk;
+        for (int pass = 0; ok;) {
             PagedItem t;
-            if (!paged_item(p, w, t)) continue;
+            if (!walk.next(p, pass != 0, t)) {
+                if (pass++ || !again(met, &progress, &redo, err)) break;
+                walk = PagedWalk();
+                continue;
+            }
             const int b = p.div_h.of(t.bh), hk = p.div_g.of(p.div_h.rest(t.bh));
             // page of this lane's box of tile j
             const auto page_at = [&](int j) {
@@ -244,19 +343,40 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
         const uint32_t sV = smem_u32(smem + C::kV);
         const uint64_t auxd = smem_desc_sw128(smem_u32(smem + C::kAux), 16, 1024);
         uint32_t uc = 0;  // ring units consumed
-        uint32_t p_cnt[2] = {0, 0}, o_cnt[2] = {0, 0}, f_cnt = 0;
-        int kk = 0;
+        uint32_t p_cnt[2] = {0, 0};
+        // As the softmax warps' state, what the loop over tiles does not need waits in shared memory.
+        volatile IssuerState &st = issuer;
+        if (lane == 0) st.k = st.pass = st.items = st.fixed = st.outputs = 0;
+        __syncwarp();
         bool ok = true;
-        for (int k = 0; ok; ++k) {
-            const int w = paged_index(k);
-            if (w >= p.num_items) break;
+        while (ok) {
             PagedItem t;
-            if (!paged_item(p, w, t)) continue;
-            const bool aux = p.slope[p.div_h.rest(t.bh)] <= kSteep;
-            ok = mbar_wait(q_full, kk & 1, err, SITE_PG_Q);
-            if (ok) ok = mbar_wait(&bias_full[kk & 1], (kk >> 1) & 1, err, SITE_PG_Q);
+            uint32_t odd_item, outputs;  // parity of the item's number; of the outputs of each slot before it, bit s
+            {
+                PagedWalk walk;
+                walk.k = st.k;
+                const int pass = st.pass, items = st.items;
+                outputs = st.outputs;
+                const bool more = walk.next(p, pass != 0, t);
+                __syncwarp();
+                if (!more) {
+                    if (pass != 0 || !again(met, &progress, &redo, err)) break;
+                    if (lane == 0) st.k = 0, st.pass = 1;
+                    __syncwarp();
+                    continue;
+                }
+                if (lane == 0) {
+                    st.k = walk.k, st.items = items + 1, st.outputs = outputs ^ (t.q1valid ? 3 : 1);
+                    *reinterpret_cast<volatile int *>(&progress) = items;
+                }
+                __syncwarp();
+                odd_item = items & 1;
+                ok = mbar_wait(&bias_full[odd_item], (items >> 1) & 1, err, SITE_PG_Q);
+            }
+            if (ok) ok = mbar_wait(q_full, odd_item, err, SITE_PG_Q);
+            if (ok && lane == 0) mbar_arrive(begun);
             // an idle slot's epilogue of an earlier item reads what this item's values will overwrite (odd_from)
-            if (ok && !t.q1valid) ok = mbar_wait(&o_empty[1], (o_cnt[1] & 1) ^ 1, err, SITE_PG_O);
+            if (ok && !t.q1valid) ok = mbar_wait(&o_empty[1], (outputs >> 1 & 1) ^ 1, err, SITE_PG_O);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
 
@@ -269,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
                     const uint32_t step = ((m >> 2) * C::kChunkBytes + (m & 3) * 32) >> 4;
                     mma_ss_w(dst, qd + step, kd + step, idS, m > 0);
                 }
-                if (aux) mma_ss_w(dst, auxd, auxd + 2 * (1 + (kk & 1)), idS, 1u);
+                if (!STEEP) mma_ss_w(dst, auxd, auxd + 2 * (1 + odd_item), idS, 1u);
                 mma_commit_w(&s_full[s]);
             };
             auto issue_PV_half = [&](int s, uint32_t vst, bool first, int half) {
@@ -297,16 +417,20 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
                 const uint32_t vst = uc % 2, uph = (uc / 2) & 1;
                 ok = __all_sync(0xffffffffu, mbar_wait(&unit_full[vst], uph, err, SITE_PG_UNIT));
                 if (!ok) break;
-                bool fix = it < t.n_fix;
-                if (fix && lane == 0) mbar_arrive(v_ready);
+                if (it < t.n_fix) {
+                    const int fixed = st.fixed;
+                    __syncwarp();
+                    if (lane == 0) {
+                        st.fixed = fixed ^ 1;
+                        mbar_arrive(v_ready);
+                    }
+                    ok = __all_sync(0xffffffffu, mbar_wait(v_fixed, fixed, err, SITE_PG_FIX));
+                    if (!ok) break;
+                }
                 for (int s = 0; s < 2 && ok; ++s) {
                     if (paged_active(t, s, it)) {
                         ok = mbar_wait_spin(&p_full[s], p_cnt[s] & 1, err, SITE_PG_P);
-                        if (ok && first_pv[s]) ok = mbar_wait(&o_empty[s], (o_cnt[s] & 1) ^ 1, err, SITE_PG_O);
-                        if (ok && fix) {  // once a tile, whichever slot comes first
-                            ok = mbar_wait(v_fixed, f_cnt++ & 1, err, SITE_PG_FIX);
-                            fix = false;
-                        }
+                        if (ok && first_pv[s]) ok = mbar_wait(&o_empty[s], (outputs >> s & 1) ^ 1, err, SITE_PG_O);
                         ok = __all_sync(0xffffffffu, ok);
                         if (!ok) break;
                         tc_fence_after();
@@ -317,10 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
                         tc_fence_after();
                         issue_PV_half(s, vst, first_pv[s], 1);
                         first_pv[s] = false;
-                        if (it == t.n - 1) {
-                            mma_commit_w(&o_full[s]);
-                            ++o_cnt[s];
-                        }
+                        if (it == t.n - 1) mma_commit_w(&o_full[s]);
                     }
                     if (it + 1 < t.n && paged_active(t, s, it + 1)) issue_S(s, vst);
                 }
@@ -328,31 +449,51 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
                 ++uc;
             }
             mma_commit_w(q_empty);
-            ++kk;
         }
         // drain: every MMA issued above completes before TMEM is released
         mma_commit_w(mma_done);
         mbar_wait(mma_done, 0, err, SITE_PG_DONE, true);
     } else {
-        // ------------------------------------ values that some row does not see: what is not finite becomes zero
-        // Each of the two warps has half of the columns.
+        // ------------------------------------ bias operands; values past the length, and, in a second pass, those that are not
+        // finite, set to zero. Each of the two warps has half of the rows, and of the columns.
         constexpr int kPieces = D / 16;  // of 16 bytes of a row
         const int side = warp - 2;
-        uint32_t uc = 0, r_cnt = 0;
+        uint32_t uc = 0, r_cnt = 0, b_cnt = 0;
         int kk = 0;
         bool ok = true;
-        for (int k = 0; ok; ++k) {
-            const int w = paged_index(k);
-            if (w >= p.num_items) break;
+        PagedWalk walk, ahead;
+        // the column-bias operand of the next item of `ahead`
+        const auto write_bias = [&]() {
             PagedItem t;
-            if (!paged_item(p, w, t)) continue;
+            if (!ahead.next(p, false, t)) return;
+            const float scale = p.slope[p.div_h.rest(t.bh)] / p.c1;
+            for (int r = 64 * side + lane; r < 64 * side + 64; r += 32)
+                write_bias_row(smem + C::kAux, r, b_cnt & 1, scale * static_cast<float>(r));
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bias_full[b_cnt & 1]);
+            ++b_cnt;
+        };
+        write_bias();
+        for (int pass = 0; ok;) {
+            PagedItem t;
+            if (!walk.next(p, pass != 0, t)) {
+                if (pass++ || !again(met, &progress, &redo, err)) break;
+                walk = ahead = PagedWalk();
+                write_bias();
+                continue;
+            }
+            // The issuer is past the item before: one item ahead, whose buffer that one's products read.
+            ok = __all_sync(0xffffffffu, wait_idle(begun, kk & 1, &progress, err, SITE_PG_FIX));
+            if (!ok) break;
+            write_bias();
             int *from = odd_from[kk & 1];
             for (int it = 0; it < t.n_fix; ++it) {
                 // The MMA issuer has seen the tile land; it is past the item before, and so are the epilogues of the item
                 // before that, which read this item's buffers.
                 ok = __all_sync(0xffffffffu, mbar_wait(v_ready, r_cnt++ & 1, err, SITE_PG_FIX));
                 if (!ok) break;
-                if (it == 0) {
+                if (it == 0 && pass != 0) {
                     for (int e = lane; e < D / 2; e += 32) from[side * (D / 2) + e] = 0x7fffffff;
                     if (lane == 0) odd_any[kk & 1][side] = 0;
                     __syncwarp();
@@ -360,10 +501,21 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
                 const uint32_t st = (uc + it + 1) % 2;
                 uint8_t *v = smem + C::kV + st * C::kTileBytes;
                 const int row0 = (t.top - it) * BN;
-#pragma unroll 4
+                const auto place = [&](int row, int piece) {
+                    return v + piece / 8 * C::kChunkBytes + row * 128 + (((piece ^ row) & 7) << 4);
+                };
+                if (pass == 0) {
+                    for (int x = (t.len - row0) * kPieces + lane; x < BN * kPieces; x += 32)
+                        *reinterpret_cast<uint4 *>(place(x / kPieces, side * kPieces + x % kPieces)) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(v_fixed);
+                    continue;
+                }
+#pragma unroll 1
                 for (int x = lane; x < BN * kPieces; x += 32) {
                     const int row = x / kPieces, piece = side * kPieces + x % kPieces;
-                    uint8_t *at = v + piece / 8 * C::kChunkBytes + row * 128 + (((piece ^ row) & 7) << 4);
+                    uint8_t *at = place(row, piece);
                     const uint4 y = *reinterpret_cast<const uint4 *>(at);
                     // a half whose exponent is full overflows into bit 15 when one is added to it
                     const auto odd = [](uint32_t a) { return ((a & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };
@@ -396,44 +548,46 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
         const int quad = warp & 3;  // TMEM lane quadrant this warp may access
         const int r = quad * 32 + lane;
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-        uint32_t s_cnt = 0, o_cnt = 0;
-        int kk = 0, k_bias = 0, kk_bias = 0;  // items begun; of the bias operands, position of the next and number of it
+        // What the loop over tiles does not need waits in shared memory: the loop takes all registers.
+        volatile SoftmaxState &st = states[warp - 4];
+        if (lane == 0) st.k = st.pass = st.items = st.outputs = 0;
+        __syncwarp();
+        uint32_t s_phase = 0;
         bool ok = true;
-        for (int k = 0; ok; ++k) {
-            const int w = paged_index(k);
-            if (w >= p.num_items) break;
-            PagedItem t;
-            if (!paged_item(p, w, t)) continue;
-            if (s == 0) {
-                // Column-bias operand, one row per thread, one item ahead: every MMA that read that buffer for the item
-                // before the last completed before this warp's epilogue of the last one.
-                while (kk_bias <= kk + 1) {
-                    const int wn = paged_index(k_bias++);
-                    if (wn >= p.num_items) break;
-                    PagedItem tn;
-                    if (!paged_item(p, wn, tn)) continue;
-                    const float m = p.slope[p.div_h.rest(tn.bh)];
-                    write_bias_row(smem + C::kAux, r, kk_bias & 1, m <= kSteep ? m * static_cast<float>(r) / p.c1 : 0.0f);
-                    fence_proxy_async_smem();
+        while (ok) {
+            float di, sl2;  // of this row: position less that of the tile's first key; m log2(e)
+            int left;       // tiles
+            {
+                PagedItem t;
+                PagedWalk walk;
+                walk.k = st.k;
+                const int pass = st.pass, items = st.items;
+                const bool more = walk.next(p, pass != 0, t);
+                __syncwarp();
+                if (!more) {
+                    if (lane == 0) bulk_wait_all();  // the outputs of the first pass stand before those of the second
+                    if (pass != 0 || !again(met, &progress, &redo, err)) break;
+                    if (lane == 0) st.k = 0, st.pass = 1;
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&bias_full[kk_bias & 1]);
-                    ++kk_bias;
+                    continue;
                 }
+                const int row0 = (2 * t.qb + s) * BM + quad * 32, it0 = s == 0 ? t.first0 : 0;
+                if (lane == 0) {
+                    st.k = walk.k, st.items = items + 1;
+                    st.part = t.part, st.bh = t.bh, st.count = t.count, st.row0 = row0, st.first = t.first;
+                    st.flags = t.bad | (t.n_fix > 0) << 1;
+                }
+                __syncwarp();
+                if (s == 1 && !t.q1valid) continue;
+                di = static_cast<float>(t.first + row0 + lane - (t.top - it0) * BN);  // exact: below 2^24
+                sl2 = p.slope[p.div_h.rest(t.bh)];
+                left = t.n - it0;
             }
-            const int buf = kk++ & 1;
-            if (s == 1 && !t.q1valid) continue;
-            const int row0 = (2 * t.qb + s) * BM + quad * 32;  // query token of the warp's first row
-            const int i = t.first + row0 + lane;               // position of this thread's row
-            const int i_warp = t.first + row0;
-            const float sl2 = p.slope[p.div_h.rest(t.bh)];
-            const bool steep = sl2 > kSteep;
-            const int it0 = s == 0 ? t.first0 : 0;
             float M = 0.f, l = 0.f;
-            for (int it = it0; it < t.n; ++it) {
-                const int j = t.top - it;
-                ok = mbar_wait(&s_full[s], s_cnt & 1, err, SITE_PG_S);
-                ++s_cnt;
-                ok = __all_sync(0xffffffffu, ok);  // keep the warp converged for tcgen05.ld
+            if (s == 1) ok = __all_sync(0xffffffffu, wait_idle(&s_full[s], s_phase, &progress, err, SITE_PG_S));
+            for (; left > 0 && ok; --left, di += static_cast<float>(BN)) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&s_full[s], s_phase, err, SITE_PG_S));  // converged for tcgen05.ld
+                s_phase ^= 1;
                 if (!ok) break;
                 tc_fence_after();
                 uint32_t sraw[BN];
@@ -441,13 +595,10 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
                 for (int c = 0; c < BN / 32; ++c)
                     tmem_ld32(lane_addr + s * 128 + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sraw[c * 32]));
                 tmem_wait_ld();
-                // After a row's first tile x is relative to the running maximum M.
-                const bool rel = it != it0;
-                const float di = static_cast<float>(i - j * BN);  // exact: |i - k0| < 2^24
-                float x[BN];
-                if (!steep) {
+                float x[BN];  // relative to the running maximum M
+                if (!STEEP) {
                     const float2 c1v = make_float2(p.c1, p.c1);
-                    const float rb = -sl2 * di - (rel ? M : 0.f);
+                    const float rb = -sl2 * di - M;
                     const float2 rbv = make_float2(rb, rb);
 #pragma unroll
                     for (int u = 0; u < BN / 2; ++u) {
@@ -457,30 +608,25 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
                         x[2 * u + 1] = xv.y;
                     }
                 } else {
-                    const float less = rel ? -M : 0.f;
 #pragma unroll
                     for (int c = 0; c < BN; ++c)
-                        x[c] = fmaf(sl2, static_cast<float>(c) - di, fmaf(__uint_as_float(sraw[c]), p.c1, less));
+                        x[c] = fmaf(sl2, static_cast<float>(c) - di, fmaf(__uint_as_float(sraw[c]), p.c1, -M));
                 }
-                if (j * BN + BN - 1 > i_warp) {  // some row of the warp does not see all keys
-                    const int lim = i - j * BN;
+                if (__any_sync(0xffffffffu, di < static_cast<float>(BN - 1))) {  // some row of the warp does not see all keys
 #pragma unroll
-                    for (int c = 0; c < BN; ++c) x[c] = c > lim ? -INFINITY : x[c];
+                    for (int c = 0; c < BN; ++c) x[c] = static_cast<float>(c) > di ? -INFINITY : x[c];
                 }
                 const float mt = row_max128(x);
                 // Raise the running maximum lazily, only when this tile exceeds it by 2^8, or where the row has seen nothing
-                // so far (then M is 0 and O is 0). O_s is quiescent here: S_s(it) completing implies that the product
-                // before it has completed.
-                const bool none = l == 0.f;
-                const bool need = rel && (mt > kRescaleThreshold || (none && mt > -INFINITY));
-                if (it == it0) M = mt == -INFINITY ? 0.f : mt;
-                if (__any_sync(0xffffffffu, need)) {
-                    const float alpha = need && !none ? ex2_approx(-mt) : 1.0f;
-                    if (need) {
-                        M += mt;
-                        l *= alpha;
-                    }
-#pragma unroll
+                // so far (then M is 0, and there is nothing to rescale). O_s is quiescent here: S_s(it) completing implies that
+                // the product before it has completed.
+                const bool none = l == 0.f, need = mt > (none ? -INFINITY : kRescaleThreshold);
+                const float shift = need ? mt : 0.f;
+                M += shift;
+                if (__any_sync(0xffffffffu, need && !none)) {
+                    const float alpha = none ? 1.0f : ex2_approx(-shift);
+                    l *= alpha;
+#pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t o[32];
                         tmem_ld32(lane_addr + 256 + s * 128 + c * 32, o);
@@ -490,70 +636,74 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
                         tmem_st32(lane_addr + 256 + s * 128 + c * 32, o);
                     }
                 }
-                const float shift = rel ? (need ? mt : 0.f) : M;  // what the exponent still needs subtracted
                 float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                 // Two halves of 64 keys: the first half of P is handed to the MMA issuer while the second is exponentiated.
+                // (A second copy for the usual shift of zero costs more in the instruction cache than it saves: 779 -> 795 us at
+                // 16 heads x 16384 tokens.)
                 uint32_t pk[BN / 2];
-                auto exps = [&](auto sub_c) {
-                    const float2 negs = make_float2(-shift, -shift);
+                const float2 negs = make_float2(-shift, -shift);
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
+                for (int half = 0; half < 2; ++half) {
 #pragma unroll
-                        for (int u = half * (BN / 4); u < (half + 1) * (BN / 4); ++u) {
-                            float2 dv = make_float2(x[2 * u], x[2 * u + 1]);
-                            if (decltype(sub_c)::value) dv = __fadd2_rn(dv, negs);
-                            const float2 pv = make_float2(ex2_approx(dv.x), ex2_approx(dv.y));
-                            acc[u & 3] = __fadd2_rn(acc[u & 3], pv);
-                            pk[u] = pack_bf16x2(pv.x, pv.y);
-                        }
-                        tmem_st32(lane_addr + s * 128 + half * 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[half * 32]));
-                        tmem_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(half == 0 ? &p_full[s] : &p_hi[s]);
+                    for (int u = half * (BN / 4); u < (half + 1) * (BN / 4); ++u) {
+                        const float2 dv = __fadd2_rn(make_float2(x[2 * u], x[2 * u + 1]), negs);
+                        const float2 pv = make_float2(ex2_approx(dv.x), ex2_approx(dv.y));
+                        acc[u & 3] = __fadd2_rn(acc[u & 3], pv);
+                        pk[u] = pack_bf16x2(pv.x, pv.y);
                     }
-                };
-                if (__any_sync(0xffffffffu, shift != 0.f))
-                    exps(std::true_type{});
-                else
-                    exps(std::false_type{});
+                    tmem_st32(lane_addr + s * 128 + half * 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[half * 32]));
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(half == 0 ? &p_full[s] : &p_hi[s]);
+                }
                 const float2 a01 = __fadd2_rn(acc[0], acc[1]), a23 = __fadd2_rn(acc[2], acc[3]);
                 const float2 a = __fadd2_rn(a01, a23);
                 l += a.x + a.y;
             }
             if (!ok) break;
             // ------------------------------------------------------ epilogue
-            ok = mbar_wait(&o_full[s], o_cnt & 1, err, SITE_PG_O);
-            ++o_cnt;
+            const int outputs = st.outputs, buf = (st.items - 1) & 1;
+            __syncwarp();
+            if (lane == 0) st.outputs = outputs + 1;
+            ok = mbar_wait(&o_full[s], outputs & 1, err, SITE_PG_O);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
             const float nan = __uint_as_float(0x7fc00000u);
-            const bool bad = t.bad || *(volatile int *)&lost[buf];
+            const int flags = st.flags, count = st.count, bh = st.bh, row0 = st.row0, pass = st.pass;
+            const bool bad = (flags & 1) || *(volatile int *)&lost[buf];
             if (bad && quad == 0 && lane == 0) atomicOr(err, ALIBI_DEV_RANGE);
             const float inv_l = bad ? nan : l == 0.f ? 0.f : 1.0f / l;
-            const bool odd = (*(volatile int *)&odd_any[buf][0] | *(volatile int *)&odd_any[buf][1]) != 0;
-            const bool valid = row0 + lane < t.count;
+            const bool odd = pass != 0 && (flags & 2) && (*(volatile int *)&odd_any[buf][0] | *(volatile int *)&odd_any[buf][1]) != 0;
+            const bool valid = row0 + lane < count;
+            const int i = st.first + row0 + lane;  // position
             const int dr = D == 64 ? p.pg.d : D;
             // O / l goes out through a per-warp staging box and bulk tensor stores, so that the warp does not wait for its
             // stores before its next tile; of a box that reaches past the sequence's rows each lane stores its own row.
-            const bool box = row0 + 32 <= t.count;
+            const bool box = row0 + 32 <= count, whole = st.part < 0;
+            float *part = whole ? nullptr : p.part + static_cast<size_t>(st.part) * paged_part_floats(D) + s * BM + r;
+            float finite = 0.f;  // or NaN
             uint8_t *stg = smem + C::kStage + (warp - 4) * 2048;
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
-                if (c * 32 >= dr || row0 >= t.count) break;
+                if (c * 32 >= dr || row0 >= count) break;
                 uint32_t o[32];
                 tmem_ld32(lane_addr + 256 + s * 128 + c * 32, o);
                 tmem_wait_ld();
+                if (pass == 0) {
+#pragma unroll
+                    for (int u = 0; u < 32; ++u) finite = fmaf(__uint_as_float(o[u]), 0.f, finite);
+                }
+                if (!whole) {
+#pragma unroll
+                    for (int u = 0; u < 32; ++u) part[(c * 32 + u) * 2 * BM] = __uint_as_float(o[u]) * inv_l;
+                    continue;
+                }
                 uint32_t y[16];
 #pragma unroll
                 for (int u = 0; u < 16; ++u)
                     y[u] = pack_bf16x2(__uint_as_float(o[2 * u]) * inv_l, __uint_as_float(o[2 * u + 1]) * inv_l);
-                if (odd) {
-#pragma unroll
-                    for (int u = 0; u < 32; ++u)
-                        if (i >= odd_from[buf][c * 32 + u]) y[u / 2] |= 0x7fc0u << (16 * (u & 1));
-                }
                 if (box) {
                     if (lane == 0) bulk_wait_read();  // the previous box has left the staging
                     __syncwarp();
@@ -563,21 +713,39 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        tma_store_3d(&p.tout, stg, c * 32, row0, t.bh);
+                        tma_store_3d(&p.tout, stg, c * 32, row0, bh);
                         bulk_commit();
                     }
                 } else if (valid) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(p.out + (static_cast<size_t>(t.bh) * p.T + row0 + lane) * dr + c * 32);
+                    uint4 *dst = reinterpret_cast<uint4 *>(p.out + (static_cast<size_t>(bh) * p.T + row0 + lane) * dr + c * 32);
 #pragma unroll
                     for (int u = 0; u < 4; ++u)
                         if (c * 32 + 8 * u < dr) dst[u] = make_uint4(y[4 * u], y[4 * u + 1], y[4 * u + 2], y[4 * u + 3]);
                 }
             }
+            if (odd) {  // NaN over what was stored
+                if (lane == 0) bulk_wait_all();
+                __syncwarp();
+#pragma unroll 1
+                for (int e = 0; e < dr; ++e) {
+                    if (!valid || i < odd_from[buf][e]) continue;
+                    if (whole)
+                        p.out[(static_cast<size_t>(bh) * p.T + row0 + lane) * dr + e] = __ushort_as_bfloat16(0x7fffu);
+                    else
+                        part[e * 2 * BM] = nan;
+                }
+            }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&o_empty[s]);
+            if (pass == 0 && valid && !bad && finite != 0.f) redo = 1;
+            if (!whole) {
+                part[D * 2 * BM] = M;
+                part[(D + 1) * 2 * BM] = bad ? nan : l;
+                continue;
+            }
             if (valid && p.lse)
-                p.lse[static_cast<size_t>(t.bh) * p.T + row0 + lane] =
+                p.lse[static_cast<size_t>(bh) * p.T + row0 + lane] =
                     bad ? nan : l == 0.f ? -INFINITY : (M + __log2f(l)) * 0.69314718055994531f;
         }
     }
@@ -591,6 +759,71 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
     }
 }
 
+// Merge of the parts of item whole + blockIdx.x, 32 rows by CTA: lane r has row r, a warp every eighth column. The weights
+// l 2^(M - max M) are normalised before they meet the means, so nothing overflows; a part that the row sees nothing of has l = 0.
+template <int D>
+__global__ void __launch_bounds__(256) fwd_paged_merge_kernel(const __grid_constant__ FwdPagedParams p)
+{
+    constexpr int kCols = D / 8, kPart = paged_part_floats(D), kRows = 2 * BM;
+    __shared__ __nv_bfloat16 rows[32][D + 8];
+    griddep_wait();
+    PagedItem t;
+    if (!paged_item(p, p.whole + blockIdx.x, false, t)) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row0 = 256 * t.qb + 32 * static_cast<int>(blockIdx.y);
+    if (row0 >= t.count) return;
+    const float *part = p.part + static_cast<size_t>(blockIdx.x) * p.parts * kPart + 32 * blockIdx.y + lane;
+    float M[kMostParts], l[kMostParts], top = -INFINITY, sum = 0.f, o[kCols] = {};
+#pragma unroll
+    for (int q = 0; q < kMostParts; ++q) {
+        const bool in = q < p.parts && part_begin(t.n, q, p.parts) < part_begin(t.n, q + 1, p.parts);
+        M[q] = in ? __ldcg(part + q * kPart + D * kRows) : 0.f;
+        l[q] = in ? __ldcg(part + q * kPart + (D + 1) * kRows) : 0.f;
+    }
+#pragma unroll
+    for (int q = 0; q < kMostParts; ++q)
+        if (l[q] != 0.f) top = fmaxf(top, M[q]);
+#pragma unroll
+    for (int q = 0; q < kMostParts; ++q) {
+        if (l[q] != 0.f) l[q] *= ex2_approx(M[q] - top);
+        sum += l[q];
+    }
+    const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+#pragma unroll
+    for (int q = 0; q < kMostParts; ++q) {
+        if (l[q] == 0.f) continue;
+        const float *x = part + q * kPart + warp * kCols * kRows;
+        const float w = l[q] * inv;
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) o[c] = fmaf(__ldcg(x + c * kRows), w, o[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) rows[lane][warp * kCols + c] = __float2bfloat16_rn(o[c]);
+    if (warp == 0 && p.lse && row0 + lane < t.count)
+        p.lse[static_cast<size_t>(t.bh) * p.T + row0 + lane] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+    __syncthreads();
+    const int d = p.pg.d;
+    for (int x = threadIdx.x; x < 32 * (d / 8); x += 256) {
+        const int r = x / (d / 8), c = x % (d / 8) * 8;
+        if (row0 + r < t.count)
+            *reinterpret_cast<uint4 *>(p.out + (static_cast<size_t>(t.bh) * p.T + row0 + r) * d + c) =
+                *reinterpret_cast<const uint4 *>(&rows[r][c]);
+    }
+}
+
+// Parts into which the items of the last, incomplete round are cut: the number with the least estimated time of that round, in
+// tiles of 256 rows and 128 keys (1.6 us). An item costs some five tiles beside its own; the merge, ten.
+int paged_parts(int rest, int T, int L, int sms)
+{
+    const double tiles = std::max(1.0, (L - std::min(T, L) / 2) / 128.0);
+    const auto cost = [&](int parts) {
+        return ((static_cast<long long>(rest) * parts + sms - 1) / sms) * (tiles / parts + 5) + (parts > 1 ? 10 : 0);
+    };
+    int best = 1;
+    for (int n = 2; n <= kMostParts && rest * n <= 3 * sms; ++n)
+        if (cost(n) < cost(best)) best = n;
+    return best;
+}
+
 template <int D>
 cudaError_t launch(FwdPagedParams &p, const alibi_pages *pages, const void *q, cudaStream_t stream)
 {
@@ -600,10 +833,28 @@ cudaError_t launch(FwdPagedParams &p, const alibi_pages *pages, const void *q, c
     if (!encode_tmap_bf16_3d(&p.tq, q, d, p.T, p.BH, 64, BM) || !encode_tmap_bf16_3d(&p.tout, p.out, d, p.T, p.BH, 32, 32, false) ||
         !encode_pages(&p.tk, &p.tv, pages, 64, box))
         return cudaErrorInvalidValue;
-    const auto kern = &fwd_paged_kernel<D>;
-    const cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(kern), C::kSmem, kLaunchRegs);
+    const bool steep = *std::max_element(p.slope, p.slope + p.H) > kSteep;
+    const auto kern = steep ? &fwd_paged_kernel<D, true> : &fwd_paged_kernel<D, false>;
+    cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(kern), C::kSmem, kLaunchRegs);
     if (e != cudaSuccess) return e;
-    return launch_kernel(kern, dim3(static_cast<unsigned>(std::min(p.num_items, num_sms()))), kThreads, C::kSmem, stream, p);
+    const int sms = num_sms();
+    p.rest = p.num_items % sms;
+    p.whole = p.num_items - p.rest;
+    p.parts = p.rest ? paged_parts(p.rest, p.T, p.L, sms) : 1;
+    if (p.parts == 1) p.whole = p.num_items, p.rest = 0;
+    p.num_units = p.whole + p.rest * p.parts;
+    p.div_rest = Divisor(static_cast<uint32_t>(std::max(p.rest, 1)));
+    p.part = nullptr;
+    const dim3 grid(static_cast<unsigned>(std::min(p.num_units, sms)));
+    if (p.parts == 1) return launch_kernel(kern, grid, kThreads, C::kSmem, stream, p);
+    e = cudaMallocFromPoolAsync(reinterpret_cast<void **>(&p.part), static_cast<size_t>(p.rest) * p.parts * paged_part_floats(D) * sizeof(float),
+                                decode_pool(), stream);
+    if (e != cudaSuccess) return e;
+    e = launch_kernel(kern, grid, kThreads, C::kSmem, stream, p);
+    if (e == cudaSuccess)
+        e = launch_kernel(fwd_paged_merge_kernel<D>, dim3(static_cast<unsigned>(p.rest), std::min(8, (p.T + 31) / 32)), 256, 0, stream, p);
+    const cudaError_t f = cudaFreeAsync(p.part, stream);
+    return e != cudaSuccess ? e : f;
 }
 
 bool aligned(const void *p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }

@@ -211,6 +211,71 @@ def test_page_numbers_that_are_none(ab, number, S):
     check(out[::2], lse[::2], q[::2], k[::2], v[::2], [600] * 2, [150] * 2, oracle.slopes(4))
 
 
+# (B, Hkv, G, T, N, d): a bound on the lengths far beyond them makes the kernel share few items' tiles among all SMs
+SHARED = [(1, 1, 1, 300, 3000, 128), (1, 1, 2, 40, 9000, 64), (3, 2, 2, 260, 1500, 128), (2, 4, 1, 700, 700, 64), (5, 2, 3, 129, 400, 16),
+          (1, 1, 1, 1, 5, 128), (40, 4, 1, 30, 300, 64)]
+
+
+@pytest.mark.parametrize("B,Hkv,G,T,N,d", SHARED)
+@pytest.mark.parametrize("spread", ["equal", "ragged", "one long", "longer chunks"])
+def test_shared_items(ab, B, Hkv, G, T, N, d, spread):
+    import torch
+    q, k, v = case(N + B + T, B, Hkv, G, T, N, d)
+    lens = {"equal": [N] * B, "ragged": [N - (b * 7919) % N for b in range(B)], "one long": [N] + [b % 9 for b in range(1, B)],
+            "longer chunks": [N - (b * 7919) % N for b in range(B)]}[spread]
+    counts = [T - (13 * b) % T for b in range(B)]
+    if spread != "longer chunks":
+        counts = [min(n, c) for n, c in zip(lens, counts)]
+    out, lse, args = compare(ab, q, k, v, lens, counts, 32, L=100000, M=-(-100000 // 32), what=spread)
+    for _ in range(3):  # the same bits for the same arguments
+        o, l = out.clone(), lse.clone()
+        ab.alibi_attn_fwd_paged(*args, lens=ints(lens), count=ints(counts), L=100000, out=o, lse=l)
+        assert torch.equal(o, out) and torch.equal(l, lse)
+
+
+@pytest.mark.parametrize("N,T,at", [(300, 300, 130), (500, 260, 400), (2000, 260, 1990), (2000, 260, 700), (2000, 260, 1745)])
+def test_infinite_and_nan_rows_of_shared_items(ab, N, T, at):
+    import torch
+    d, S, L = 64, 16, 100000
+    q, k, v = case(d + N, 1, 1, 2, T, N, d)
+    kp, vp, table = ref.paged(k, v, [N], S, M=-(-L // S))
+    page, slot = int(table[0, at // S]), at % S
+    t = max(0, at - (N - T))
+    vp[page, 0, slot, 3] = float("nan")
+    out, lse = ab.alibi_attn_fwd_paged(bf16(q)[1], kp, vp, table, lens=ints([N]), L=L)
+    ab.alibi_check_error()
+    o = out.float()
+    assert bool(torch.isnan(o[:, :, t:, 3]).all())
+    o[:, :, t:, 3] = 0
+    v2 = v.copy()
+    v2[0, 0, at, 3] = 0.0
+    ro, rl, eo, el = ref.attention(q, k, v2, [N], [T], oracle.slopes(2), weight=2.0 ** -8, chain=16, column=True)
+    ro[:, :, t:, 3] = 0
+    assert (np.abs(host64(o) - ro) <= eo + half_ulp_bf16(ro) * 1.02).all()
+    assert (np.abs(host64(lse) - rl) <= el).all()
+
+
+def test_page_numbers_that_are_none_in_shared_items(ab):
+    q, k, v = case(10, 3, 2, 2, 150, 600, 64)
+    kp, vp, table = ref.paged(k, v, [600] * 3, 16, M=6250)
+    table[1, 5] = -1
+    out, lse = ab.alibi_attn_fwd_paged(bf16(q)[1], kp, vp, table, lens=ints([600] * 3), L=100000)
+    with pytest.raises(ab.AlibiError) as e:
+        ab.alibi_check_error()
+    assert e.value.status == ab.ALIBI_ERR_RANGE
+    assert bool(out[1].isnan().all()) and bool(lse[1].isnan().all())
+    check(out[::2], lse[::2], q[::2], k[::2], v[::2], [600] * 2, [150] * 2, oracle.slopes(4))
+
+
+@pytest.mark.parametrize("B,T", [(3, 300), (200, 40)])
+def test_slots_past_the_length_that_are_not_finite(ab, B, T):
+    # freshly allocated pages hold anything: NaN everywhere but in the rows of the sequences (which ref.paged does), of
+    # prompts whose first tiles are their last
+    q, k, v = case(T, B, 2, 1, T, T, 128)
+    lens = [T - (7 * b) % T for b in range(B)]
+    compare(ab, q, k, v, lens, lens, 64)
+
+
 def test_offsets_beyond_32_bits(ab):
     import torch
     S, H, d = 64, 8, 128
