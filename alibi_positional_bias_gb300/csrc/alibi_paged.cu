@@ -53,16 +53,33 @@ struct Turn {
     float c[8], s[8];
 };
 
-__device__ __forceinline__ void turn_of(const AppendParams &p, int vec, int n, Turn &t)
+// Lane that has the other elements of this lane's pairs (halves).
+__device__ __forceinline__ int partner(const AppendParams &p, int vec, bool on)
+{
+    const int lane = threadIdx.x & 31, half = p.R / 16;
+    return !on ? lane : vec < half ? lane + half : lane - half;
+}
+
+// All threads of the warp call it; `on`: this thread's elements turn.
+__device__ __forceinline__ void turn_of(const AppendParams &p, int vec, int n, bool on, Turn &t)
 {
     const bool upper = 16 * vec >= p.R;
-    const int first = p.interleaved ? 4 * vec : upper ? 8 * vec - p.R / 2 : 8 * vec;
+    // a lane and its partner turn by the same eight angles: each computes four
+    const int first = p.interleaved ? 4 * vec : upper ? 8 * vec - p.R / 2 + 4 : 8 * vec;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        if (e >= 4 && p.interleaved) break;
-        const uint64_t left = p.turn[first + e] * static_cast<uint64_t>(n);
+    for (int e = 0; e < 4; ++e) {
+        const uint64_t left = on ? p.turn[first + e] * static_cast<uint64_t>(n) : 0;
         sincospif(static_cast<float>(static_cast<int32_t>(left >> 32)) * 0x1p-31f, &t.s[e], &t.c[e]);
-        if (!p.interleaved && !upper) t.s[e] = -t.s[e];
+    }
+    if (p.interleaved) return;
+    const int other = partner(p, vec, on);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float c = __shfl_sync(0xffffffffu, t.c[e], other), s = __shfl_sync(0xffffffffu, t.s[e], other);
+        t.c[4 + e] = upper ? t.c[e] : c;
+        t.s[4 + e] = upper ? t.s[e] : -s;
+        t.c[e] = upper ? c : t.c[e];
+        t.s[e] = upper ? s : -t.s[e];
     }
 }
 
@@ -81,8 +98,7 @@ __device__ __forceinline__ uint4 rotated(const AppendParams &p, uint4 x, int vec
                 w[i] = pack_bf16x2(fmaf(a, t.c[i], -b * t.s[i]), fmaf(b, t.c[i], a * t.s[i]));
             }
     } else {
-        const int lane = threadIdx.x & 31, half = p.R / 16;
-        const int other = !on ? lane : vec < half ? lane + half : lane - half;
+        const int other = partner(p, vec, on);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint32_t y = __shfl_sync(0xffffffffu, w[i], other);
@@ -111,7 +127,7 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_con
     bool live = t < count;
     Turn turn;
     const bool on = ROTATE && 8 * vec < p.R;
-    if (ROTATE && live && on) turn_of(p, vec, n, turn);
+    if (ROTATE) turn_of(p, vec, n, on && live, turn);
 
     const bool queries = ROTATE && static_cast<int>(blockIdx.y) >= p.kv_groups;
     const int h0 = (queries ? blockIdx.y - p.kv_groups : blockIdx.y) * p.group + (row >> p.log_tok);
@@ -235,10 +251,12 @@ extern "C" int alibi_paged_append(const alibi_rows *k, const alibi_rows *v, cons
     const long long tokens = static_cast<long long>(B) * blocks;
     if (tokens > 0x7fffffffLL) return ALIBI_ERR_UNSUPPORTED;
     p.by_blocks = Divisor(static_cast<uint32_t>(blocks));
-    // Heads of a CTA: as few as its threads take at once while that fills the device, else four times as many.
+    // Heads of a CTA: as few as its threads take at once while that fills the device eight times, else up to sixteen times as
+    // many; with a rotation, whose sines are computed once per CTA, twice (2 x (6 + 24) heads x 1001 tokens of d = 64 9.7 us
+    // at two heads, 6.3 at four).
     const int most = std::max(pages->heads, p.H);
     p.group = step;
-    while (p.group < most && p.group < 4 * kUnroll * step && tokens * ((most + p.group - 1) / p.group) > 8LL * num_sms())
+    while (p.group < most && p.group < 4 * kUnroll * step && tokens * ((most + p.group - 1) / p.group) > (R ? 2LL : 8LL) * num_sms())
         p.group *= 2;
     p.kv_groups = (pages->heads + p.group - 1) / p.group;
     const int q_groups = (p.H + p.group - 1) / p.group;
