@@ -810,13 +810,14 @@ __global__ void __launch_bounds__(256) fwd_paged_merge_kernel(const __grid_const
     }
 }
 
-// Parts into which the items of the last, incomplete round are cut: the number with the least estimated time of that round, in
-// tiles of 256 rows and 128 keys (1.6 us). An item costs some five tiles beside its own; the merge, ten.
-int paged_parts(int rest, int T, int L, int sms)
+// Parts into which the items of the last, incomplete round, the shortest, are cut: the number with the least estimated time of that
+// round, in tiles of 256 rows and 128 keys (1.7 us). An item costs some five tiles beside its own; the merge, six and 0.02
+// for each partial.
+int paged_parts(int rest, int BH, int T, int L, int sms)
 {
-    const double tiles = std::max(1.0, (L - std::min(T, L) / 2) / 128.0);
+    const double tiles = (L - std::min(T, L)) / 128.0 + static_cast<double>(rest) / BH + 1;
     const auto cost = [&](int parts) {
-        return ((static_cast<long long>(rest) * parts + sms - 1) / sms) * (tiles / parts + 5) + (parts > 1 ? 10 : 0);
+        return ((static_cast<long long>(rest) * parts + sms - 1) / sms) * (tiles / parts + 5) + (parts > 1 ? 6 + 0.02 * rest * parts : 0);
     };
     int best = 1;
     for (int n = 2; n <= kMostParts && rest * n <= 3 * sms; ++n)
@@ -840,7 +841,7 @@ cudaError_t launch(FwdPagedParams &p, const alibi_pages *pages, const void *q, c
     const int sms = num_sms();
     p.rest = p.num_items % sms;
     p.whole = p.num_items - p.rest;
-    p.parts = p.rest ? paged_parts(p.rest, p.T, p.L, sms) : 1;
+    p.parts = p.rest ? paged_parts(p.rest, p.BH, p.T, p.L, sms) : 1;
     if (p.parts == 1) p.whole = p.num_items, p.rest = 0;
     p.num_units = p.whole + p.rest * p.parts;
     p.div_rest = Divisor(static_cast<uint32_t>(std::max(p.rest, 1)));

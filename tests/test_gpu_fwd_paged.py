@@ -82,7 +82,7 @@ def test_shapes(ab, B, Hkv, G, T, N, d, S, layout):
     import torch
     for _ in range(2):  # the same bits for the same arguments
         o, l = out.clone(), lse.clone()
-        ab.alibi_attn_fwd_paged(*args, lens=ints(lens), count=ints(counts), out=o, lse=l)
+        ab.alibi_attn_fwd_paged(*args, lens=ints(lens), count=ints(counts), L=N + 3, out=o, lse=l)
         assert torch.equal(o, out) and torch.equal(l, lse)
 
 
