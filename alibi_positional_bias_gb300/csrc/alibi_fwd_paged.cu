@@ -14,11 +14,12 @@
 //             loaded from beyond the tensor, which fills zeros.
 //   diagonal  positions begin anywhere in a tile, so a slot's rows end inside two tiles, and a row may see nothing of the first
 //             tile that its slot visits.
-//   values    that a row does not see meet a weight of zero, which an infinity or a NaN would turn into NaN. Two warps set the
-//             values past the length to zero. If an output is not finite all the same, the CTA takes its items once more: the
-//             two warps then look through the first tiles' values, those that some row of the item does not see (up to three
-//             tiles), put zeros in place of what is not finite and note per column the first such row, from which on the
-//             outputs are NaN. (Looking through them at once took 15% of the time of prompts of 2048 tokens.)
+//   values    that a row does not see meet a weight of zero, which an infinity or a NaN would turn into NaN. The loading warp
+//             sets the values past the length to zero before it hands their tile over. If an output is not finite all the
+//             same, the CTA takes its items once more: the warp then looks through the first tiles' values, those that some row
+//             of the item does not see (up to three tiles), puts zeros in place of what is not finite and notes per column the
+//             first such row, from which on the outputs are NaN. (Looking through them at once took 15% of the time of
+//             prompts of 2048 tokens; two warps of their own for it, and what the MMA issuer had to say to them, 2%.)
 //   rows      past count_b are left as they were: of a box of 32 rows that reaches there the lanes store their own.
 //   parts     items that do not fill a round of one per SM are cut into parts of their tiles, which run one after another over
 //             all SMs, part by part, so that the CTAs of a KV head pass its tiles at the same time; a part leaves its mean,
@@ -152,7 +153,7 @@ struct SoftmaxState {
 // And the MMA issuer.
 struct IssuerState {
     int k, pass, items;
-    int fixed, outputs;  // parities: of the tiles looked through, of the outputs of each slot
+    int outputs;  // parity of the outputs of each slot, bit s
 };
 
 __device__ __forceinline__ bool paged_active(const PagedItem &t, int s, int it) { return s == 1 ? t.q1valid : it >= t.first0; }
@@ -197,10 +198,10 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
 {
     using C = Cfg<D>;
     extern __shared__ uint8_t smem_raw[];
-    // of the items in flight, two at most: the first row of each column of V that is not finite, whether each half of the
-    // columns has one, and whether a page number is none
+    // of the items in flight, two at most: the first row of each column of V that is not finite, whether there is one, and
+    // whether a page number is none
     __shared__ int odd_from[2][D];
-    __shared__ int odd_any[2][2], lost[2], redo, progress;
+    __shared__ int odd_any[2], lost[2], redo, progress;
     __shared__ SoftmaxState states[8];
     __shared__ IssuerState issuer;
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -214,10 +215,8 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
     __shared__ uint64_t p_hi[2];        // P of keys 64..127 written
     __shared__ uint64_t o_full[2];
     __shared__ uint64_t o_empty[2];
-    __shared__ uint64_t bias_full[2];   // column-bias operand of item k written (buffer k & 1)
-    __shared__ uint64_t begun[1];       // the MMA issuer has begun an item: all before it is computed
-    __shared__ uint64_t v_ready[1];     // values to be looked through have landed
-    __shared__ uint64_t v_fixed[1];     // and are finite
+    __shared__ uint64_t bias_full[1];   // column-bias operand of the item written
+    __shared__ uint64_t v_landed[1];    // values to be looked through before their unit is handed over
     __shared__ uint64_t met[1];         // the warps after their first pass
     __shared__ uint64_t mma_done[1];
     __shared__ uint32_t tmem_slot[1];
@@ -238,15 +237,13 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
             mbar_init(&p_hi[s], 4);
             mbar_init(&o_full[s], 1);
             mbar_init(&o_empty[s], 4);
-            mbar_init(&bias_full[s], 2);  // the two warps that write it
         }
         mbar_init(q_empty, 1);
         mbar_init(q_full, 1);
-        mbar_init(begun, 1);
-        mbar_init(v_ready, 1);
-        mbar_init(v_fixed, 2);  // the two warps that look through them
+        mbar_init(bias_full, 1);
+        mbar_init(v_landed, 1);
         mbar_init(mma_done, 1);
-        mbar_init(met, kThreads / 32);
+        mbar_init(met, 10);  // of the loading, the issuing and the softmax warps
         fence_mbar_init();
         tma_prefetch_desc(&p.tq);
         tma_prefetch_desc(&p.tk);
@@ -276,6 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
         const int box = min(1 << p.pg.shift, BN), boxes = BN / box;  // rows of a box, boxes of a tile
         uint32_t uc = 0;  // ring units issued
         int kk = 0;       // items begun
+        uint32_t looked = 0;
         bool ok = true;
         PagedWalk walk;
         for (int pass = 0; ok;) {
@@ -295,24 +293,34 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
             ok = __all_sync(0xffffffffu, mbar_wait(q_empty, (kk & 1) ^ 1, err, SITE_PG_Q));
             if (!ok) break;
             if (lane == 0) {
-                lost[kk & 1] = 0;
+                lost[kk & 1] = odd_any[kk & 1] = 0;
                 mbar_arrive_expect_tx(q_full, 2 * C::kTileBytes);
                 for (int s = 0; s < 2; ++s)
                     for (int c = 0; c < C::kChunks; ++c)
                         tma_load_3d(smem + C::kQ + s * C::kTileBytes + c * C::kChunkBytes, &p.tq, 64 * c, (2 * t.qb + s) * BM,
                                     t.bh, q_full);
             }
+            if (pass != 0)
+                for (int e = lane; e < D; e += 32) odd_from[kk & 1][e] = 0x7fffffff;
             __syncwarp();
             // Unit u = 0 .. n: K(u) (u < n) and V(u - 1) (u >= 1), consumed in the MMA issuer's iteration u - 1.
             for (int u = 0; u <= t.n; ++u) {
                 const uint32_t st = uc % 2, ph = (uc / 2) & 1;
+                const bool look = u >= 1 && u <= t.n_fix;  // V goes by a barrier of its own, to be looked through
                 if (page < 0) lost[kk & 1] = 1, page = p.pg.pages;
                 const int ahead = page_at(t.top - u - 1);
                 ok = __all_sync(0xffffffffu, mbar_wait(&unit_empty[st], ph ^ 1, err, SITE_PG_UNIT));
                 if (!ok) break;
-                if (lane == 0)
-                    mbar_arrive_expect_tx(&unit_full[st], (u < t.n ? C::kTileBytes : 0u) + (u >= 1 ? C::kTileBytes : 0u));
+                if (lane == 0) {
+                    if (look) {
+                        mbar_arrive_expect_tx(v_landed, C::kTileBytes);
+                        if (u < t.n) mbar_expect_tx(&unit_full[st], C::kTileBytes);
+                    } else {
+                        mbar_arrive_expect_tx(&unit_full[st], (u < t.n ? C::kTileBytes : 0u) + (u >= 1 ? C::kTileBytes : 0u));
+                    }
+                }
                 __syncwarp();
+                uint8_t *const v = smem + C::kV + st * C::kTileBytes;
                 if (lane < boxes) {
                     const int at = lane * box * 128;  // of the box in a swizzle atom
                     for (int c = 0; c < C::kChunks; ++c) {
@@ -320,19 +328,61 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
                             tma_load_4d(smem + C::kK + st * C::kTileBytes + c * C::kChunkBytes + at, &p.tk, 64 * c,
                                         p.pg.slot_of((t.top - u) * BN + lane * box), hk, page, box * 128, &unit_full[st]);
                         if (u >= 1)
-                            tma_load_4d(smem + C::kV + st * C::kTileBytes + c * C::kChunkBytes + at, &p.tv, 64 * c,
-                                        p.pg.slot_of((t.top - u + 1) * BN + lane * box), hk, before, box * 128, &unit_full[st]);
+                            tma_load_4d(v + c * C::kChunkBytes + at, &p.tv, 64 * c, p.pg.slot_of((t.top - u + 1) * BN + lane * box), hk,
+                                        before, box * 128, look ? v_landed : &unit_full[st]);
                     }
+                }
+                __syncwarp();
+                if (u == 0 && !STEEP) {
+                    // the column-bias operand, whose last readers were the products of the item before
+                    const float scale = p.slope[p.div_h.rest(t.bh)] / p.c1;
+                    for (int r = lane; r < BN; r += 32) write_bias_row(smem + C::kAux, r, 0, scale * static_cast<float>(r));
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bias_full);
+                }
+                if (look) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(v_landed, looked++ & 1, err, SITE_PG_FIX));
+                    constexpr int kPieces = D / 8;  // of 16 bytes of a row
+                    const int row0 = (t.top - u + 1) * BN;
+                    // in a first pass the slots past the length, in a second one all
+                    for (int x = (pass == 0 ? t.len - row0 : 0) * kPieces + lane; x < BN * kPieces && ok; x += 32) {
+                        const int row = x / kPieces, piece = x % kPieces;
+                        uint4 *const at = reinterpret_cast<uint4 *>(v + piece / 8 * C::kChunkBytes + row * 128 + (((piece ^ row) & 7) << 4));
+                        if (row0 + row >= t.len) {
+                            *at = make_uint4(0, 0, 0, 0);
+                            continue;
+                        }
+                        const uint4 y = *at;
+                        // a half whose exponent is full overflows into bit 15 when one is added to it
+                        const auto odd = [](uint32_t a) { return ((a & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };
+                        if ((odd(y.x) | odd(y.y) | odd(y.z) | odd(y.w)) == 0u) continue;
+                        uint32_t a[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const uint32_t m = 0x7f80u << (16 * (e & 1));
+                            if ((a[e / 2] & m) != m) continue;
+                            a[e / 2] &= ~(0xffffu << (16 * (e & 1)));
+                            atomicMin(&odd_from[kk & 1][8 * piece + e], row0 + row);
+                            odd_any[kk & 1] = 1;
+                        }
+                        *at = make_uint4(a[0], a[1], a[2], a[3]);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&unit_full[st]);  // after an error too: the copies into the unit may be waited for
                 }
                 before = page;
                 page = ahead;
                 ++uc;
+                if (!ok) break;
             }
             ++kk;  // after an error too: the item's Q was issued
         }
         // Drain (also after an error): the last Q load and the last load into each ring stage has landed before the CTA can
         // exit. Earlier loads into a stage were consumed, hence complete, before the stage was reused.
         if (kk > 0) mbar_wait(q_full, (kk - 1) & 1, err, SITE_PG_Q, true);
+        if (looked > 0) mbar_wait(v_landed, (looked - 1) & 1, err, SITE_PG_FIX, true);
         for (uint32_t n = uc > 2 ? uc - 2 : 0; n < uc; ++n) mbar_wait(&unit_full[n % 2], (n / 2) & 1, err, SITE_PG_UNIT, true);
     } else if (warp == 1) {
         // -------------------------------------------------------- MMA issuer (converged; one elected lane issues)
@@ -346,12 +396,12 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
         uint32_t p_cnt[2] = {0, 0};
         // As the softmax warps' state, what the loop over tiles does not need waits in shared memory.
         volatile IssuerState &st = issuer;
-        if (lane == 0) st.k = st.pass = st.items = st.fixed = st.outputs = 0;
+        if (lane == 0) st.k = st.pass = st.items = st.outputs = 0;
         __syncwarp();
         bool ok = true;
         while (ok) {
             PagedItem t;
-            uint32_t odd_item, outputs;  // parity of the item's number; of the outputs of each slot before it, bit s
+            uint32_t outputs;  // parity of the outputs of each slot before the item, bit s
             {
                 PagedWalk walk;
                 walk.k = st.k;
@@ -370,11 +420,9 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
                     *reinterpret_cast<volatile int *>(&progress) = items;
                 }
                 __syncwarp();
-                odd_item = items & 1;
-                ok = mbar_wait(&bias_full[odd_item], (items >> 1) & 1, err, SITE_PG_Q);
+                ok = mbar_wait(q_full, items & 1, err, SITE_PG_Q);
+                if (ok && !STEEP) ok = mbar_wait(bias_full, items & 1, err, SITE_PG_Q);
             }
-            if (ok) ok = mbar_wait(q_full, odd_item, err, SITE_PG_Q);
-            if (ok && lane == 0) mbar_arrive(begun);
             // an idle slot's epilogue of an earlier item reads what this item's values will overwrite (odd_from)
             if (ok && !t.q1valid) ok = mbar_wait(&o_empty[1], (outputs >> 1 & 1) ^ 1, err, SITE_PG_O);
             ok = __all_sync(0xffffffffu, ok);
@@ -389,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
                     const uint32_t step = ((m >> 2) * C::kChunkBytes + (m & 3) * 32) >> 4;
                     mma_ss_w(dst, qd + step, kd + step, idS, m > 0);
                 }
-                if (!STEEP) mma_ss_w(dst, auxd, auxd + 2 * (1 + odd_item), idS, 1u);
+                if (!STEEP) mma_ss_w(dst, auxd, auxd + 2, idS, 1u);
                 mma_commit_w(&s_full[s]);
             };
             auto issue_PV_half = [&](int s, uint32_t vst, bool first, int half) {
@@ -417,16 +465,6 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
                 const uint32_t vst = uc % 2, uph = (uc / 2) & 1;
                 ok = __all_sync(0xffffffffu, mbar_wait(&unit_full[vst], uph, err, SITE_PG_UNIT));
                 if (!ok) break;
-                if (it < t.n_fix) {
-                    const int fixed = st.fixed;
-                    __syncwarp();
-                    if (lane == 0) {
-                        st.fixed = fixed ^ 1;
-                        mbar_arrive(v_ready);
-                    }
-                    ok = __all_sync(0xffffffffu, mbar_wait(v_fixed, fixed, err, SITE_PG_FIX));
-                    if (!ok) break;
-                }
                 for (int s = 0; s < 2 && ok; ++s) {
                     if (paged_active(t, s, it)) {
                         ok = mbar_wait_spin(&p_full[s], p_cnt[s] & 1, err, SITE_PG_P);
@@ -453,93 +491,6 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
         // drain: every MMA issued above completes before TMEM is released
         mma_commit_w(mma_done);
         mbar_wait(mma_done, 0, err, SITE_PG_DONE, true);
-    } else {
-        // ------------------------------------ bias operands; values past the length, and, in a second pass, those that are not
-        // finite, set to zero. Each of the two warps has half of the rows, and of the columns.
-        constexpr int kPieces = D / 16;  // of 16 bytes of a row
-        const int side = warp - 2;
-        uint32_t uc = 0, r_cnt = 0, b_cnt = 0;
-        int kk = 0;
-        bool ok = true;
-        PagedWalk walk, ahead;
-        // the column-bias operand of the next item of `ahead`
-        const auto write_bias = [&]() {
-            PagedItem t;
-            if (!ahead.next(p, false, t)) return;
-            const float scale = p.slope[p.div_h.rest(t.bh)] / p.c1;
-            for (int r = 64 * side + lane; r < 64 * side + 64; r += 32)
-                write_bias_row(smem + C::kAux, r, b_cnt & 1, scale * static_cast<float>(r));
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bias_full[b_cnt & 1]);
-            ++b_cnt;
-        };
-        write_bias();
-        for (int pass = 0; ok;) {
-            PagedItem t;
-            if (!walk.next(p, pass != 0, t)) {
-                if (pass++ || !again(met, &progress, &redo, err)) break;
-                walk = ahead = PagedWalk();
-                write_bias();
-                continue;
-            }
-            // The issuer is past the item before: one item ahead, whose buffer that one's products read.
-            ok = __all_sync(0xffffffffu, wait_idle(begun, kk & 1, &progress, err, SITE_PG_FIX));
-            if (!ok) break;
-            write_bias();
-            int *from = odd_from[kk & 1];
-            for (int it = 0; it < t.n_fix; ++it) {
-                // The MMA issuer has seen the tile land; it is past the item before, and so are the epilogues of the item
-                // before that, which read this item's buffers.
-                ok = __all_sync(0xffffffffu, mbar_wait(v_ready, r_cnt++ & 1, err, SITE_PG_FIX));
-                if (!ok) break;
-                if (it == 0 && pass != 0) {
-                    for (int e = lane; e < D / 2; e += 32) from[side * (D / 2) + e] = 0x7fffffff;
-                    if (lane == 0) odd_any[kk & 1][side] = 0;
-                    __syncwarp();
-                }
-                const uint32_t st = (uc + it + 1) % 2;
-                uint8_t *v = smem + C::kV + st * C::kTileBytes;
-                const int row0 = (t.top - it) * BN;
-                const auto place = [&](int row, int piece) {
-                    return v + piece / 8 * C::kChunkBytes + row * 128 + (((piece ^ row) & 7) << 4);
-                };
-                if (pass == 0) {
-                    for (int x = (t.len - row0) * kPieces + lane; x < BN * kPieces; x += 32)
-                        *reinterpret_cast<uint4 *>(place(x / kPieces, side * kPieces + x % kPieces)) = make_uint4(0, 0, 0, 0);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(v_fixed);
-                    continue;
-                }
-#pragma unroll 1
-                for (int x = lane; x < BN * kPieces; x += 32) {
-                    const int row = x / kPieces, piece = side * kPieces + x % kPieces;
-                    uint8_t *at = place(row, piece);
-                    const uint4 y = *reinterpret_cast<const uint4 *>(at);
-                    // a half whose exponent is full overflows into bit 15 when one is added to it
-                    const auto odd = [](uint32_t a) { return ((a & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };
-                    if ((odd(y.x) | odd(y.y) | odd(y.z) | odd(y.w)) == 0u) continue;
-                    uint32_t a[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const uint32_t m = 0x7f80u << (16 * (e & 1));
-                        if ((a[e / 2] & m) != m) continue;
-                        a[e / 2] &= ~(0xffffu << (16 * (e & 1)));
-                        if (row0 + row < t.len) {
-                            atomicMin(&from[8 * piece + e], row0 + row);
-                            odd_any[kk & 1][side] = 1;
-                        }
-                    }
-                    *reinterpret_cast<uint4 *>(at) = make_uint4(a[0], a[1], a[2], a[3]);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(v_fixed);
-            }
-            uc += t.n + 1;
-            ++kk;
-        }
     }
     } else {
         // ------------------------------------------------ softmax warpgroups
@@ -575,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
                 if (lane == 0) {
                     st.k = walk.k, st.items = items + 1;
                     st.part = t.part, st.bh = t.bh, st.count = t.count, st.row0 = row0, st.first = t.first;
-                    st.flags = t.bad | (t.n_fix > 0) << 1;
+                    st.flags = t.bad;
                 }
                 __syncwarp();
                 if (s == 1 && !t.q1valid) continue;
@@ -621,33 +572,37 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
                 // so far (then M is 0, and there is nothing to rescale). O_s is quiescent here: S_s(it) completing implies that
                 // the product before it has completed.
                 const bool none = l == 0.f, need = mt > (none ? -INFINITY : kRescaleThreshold);
-                const float shift = need ? mt : 0.f;
-                M += shift;
-                if (__any_sync(0xffffffffu, need && !none)) {
-                    const float alpha = none ? 1.0f : ex2_approx(-shift);
+                if (__any_sync(0xffffffffu, need)) {
+                    const float shift = need ? mt : 0.f, alpha = none ? 1.0f : ex2_approx(-shift);
+                    M += shift;
                     l *= alpha;
-#pragma unroll 1
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t o[32];
-                        tmem_ld32(lane_addr + 256 + s * 128 + c * 32, o);
-                        tmem_wait_ld();
+                    const float2 negs = make_float2(-shift, -shift);
 #pragma unroll
-                        for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * alpha);
-                        tmem_st32(lane_addr + 256 + s * 128 + c * 32, o);
+                    for (int u = 0; u < BN / 2; ++u) {
+                        const float2 xv = __fadd2_rn(make_float2(x[2 * u], x[2 * u + 1]), negs);
+                        x[2 * u] = xv.x;
+                        x[2 * u + 1] = xv.y;
+                    }
+                    if (__any_sync(0xffffffffu, need && !none)) {
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t o[32];
+                            tmem_ld32(lane_addr + 256 + s * 128 + c * 32, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * alpha);
+                            tmem_st32(lane_addr + 256 + s * 128 + c * 32, o);
+                        }
                     }
                 }
                 float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                 // Two halves of 64 keys: the first half of P is handed to the MMA issuer while the second is exponentiated.
-                // (A second copy for the usual shift of zero costs more in the instruction cache than it saves: 779 -> 795 us at
-                // 16 heads x 16384 tokens.)
                 uint32_t pk[BN / 2];
-                const float2 negs = make_float2(-shift, -shift);
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
 #pragma unroll
                     for (int u = half * (BN / 4); u < (half + 1) * (BN / 4); ++u) {
-                        const float2 dv = __fadd2_rn(make_float2(x[2 * u], x[2 * u + 1]), negs);
-                        const float2 pv = make_float2(ex2_approx(dv.x), ex2_approx(dv.y));
+                        const float2 pv = make_float2(ex2_approx(x[2 * u]), ex2_approx(x[2 * u + 1]));
                         acc[u & 3] = __fadd2_rn(acc[u & 3], pv);
                         pk[u] = pack_bf16x2(pv.x, pv.y);
                     }
@@ -675,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
             const bool bad = (flags & 1) || *(volatile int *)&lost[buf];
             if (bad && quad == 0 && lane == 0) atomicOr(err, ALIBI_DEV_RANGE);
             const float inv_l = bad ? nan : l == 0.f ? 0.f : 1.0f / l;
-            const bool odd = pass != 0 && (flags & 2) && (*(volatile int *)&odd_any[buf][0] | *(volatile int *)&odd_any[buf][1]) != 0;
+            const bool odd = pass != 0 && *(volatile int *)&odd_any[buf] != 0;
             const bool valid = row0 + lane < count;
             const int i = st.first + row0 + lane;  // position
             const int dr = D == 64 ? p.pg.d : D;
