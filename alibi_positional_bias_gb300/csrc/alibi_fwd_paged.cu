@@ -159,18 +159,18 @@ struct IssuerState {
 __device__ __forceinline__ bool paged_active(const PagedItem &t, int s, int it) { return s == 1 ? t.q1valid : it >= t.first0; }
 
 // A bounded wait of a role that other items may leave idle for long: the limit holds from one item of the MMA issuer, which
-// it counts in `progress`, to the next. It sleeps between its looks: warps that poll for as long as an item takes cost the
-// softmax warps of their schedulers a third of their time.
+// it counts in `progress`, to the next. It sleeps between its looks, as a warp that
+// polls takes issue slots of the softmax warps beside it.
 __device__ __forceinline__ bool wait_idle(uint64_t *bar, uint32_t parity, const int *progress, uint32_t *err, uint32_t site)
 {
     uint64_t t0 = 0;
     int seen = 0;
-    uint32_t sleep = 50;
+    uint32_t sleep = 20;
 #pragma unroll 1
     for (uint32_t n = 0;; ++n) {
         if (mbar_test(bar, parity)) return true;
         __nanosleep(sleep);
-        sleep = min(2 * sleep, 2000u);
+        sleep = min(2 * sleep, 200u);
         if ((n & 255u) != 255u) continue;
         if (*(volatile uint32_t *)&cta_abort != 0u) return false;
         const uint64_t t = global_timer_ns();
@@ -306,14 +306,16 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
             // Unit u = 0 .. n: K(u) (u < n) and V(u - 1) (u >= 1), consumed in the MMA issuer's iteration u - 1.
             for (int u = 0; u <= t.n; ++u) {
                 const uint32_t st = uc % 2, ph = (uc / 2) & 1;
-                const bool look = u >= 1 && u <= t.n_fix;  // V goes by a barrier of its own, to be looked through
+                // V(u - 1) goes by a barrier of its own, to be looked through; the first one of an item is asked for with K(0),
+                // into a ring that is empty then.
+                const bool look = u >= 1 && u <= t.n_fix, with_k0 = u == 0 && t.n_fix > 0;
                 if (page < 0) lost[kk & 1] = 1, page = p.pg.pages;
                 const int ahead = page_at(t.top - u - 1);
                 ok = __all_sync(0xffffffffu, mbar_wait(&unit_empty[st], ph ^ 1, err, SITE_PG_UNIT));
                 if (!ok) break;
                 if (lane == 0) {
+                    if (with_k0 || (look && u > 1)) mbar_arrive_expect_tx(v_landed, C::kTileBytes);
                     if (look) {
-                        mbar_arrive_expect_tx(v_landed, C::kTileBytes);
                         if (u < t.n) mbar_expect_tx(&unit_full[st], C::kTileBytes);
                     } else {
                         mbar_arrive_expect_tx(&unit_full[st], (u < t.n ? C::kTileBytes : 0u) + (u >= 1 ? C::kTileBytes : 0u));
@@ -327,7 +329,10 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
                         if (u < t.n)
                             tma_load_4d(smem + C::kK + st * C::kTileBytes + c * C::kChunkBytes + at, &p.tk, 64 * c,
                                         p.pg.slot_of((t.top - u) * BN + lane * box), hk, page, box * 128, &unit_full[st]);
-                        if (u >= 1)
+                        if (with_k0)
+                            tma_load_4d(smem + C::kV + (st ^ 1) * C::kTileBytes + c * C::kChunkBytes + at, &p.tv, 64 * c,
+                                        p.pg.slot_of(t.top * BN + lane * box), hk, page, box * 128, v_landed);
+                        else if (u >= 1 && !(look && u == 1))
                             tma_load_4d(v + c * C::kChunkBytes + at, &p.tv, 64 * c, p.pg.slot_of((t.top - u + 1) * BN + lane * box), hk,
                                         before, box * 128, look ? v_landed : &unit_full[st]);
                     }
