@@ -685,7 +685,7 @@ _pack_pages = struct.Struct("=QQqqqqqqQiiiii").pack_into
 
 
 def _paged_cache(k_pages, v_pages, table, B, d, index):
-    """The C struct of a paged cache, its tensors checked."""
+    """The C struct of a paged cache, its tensors checked; its heads, and the tokens that the table has room for."""
     bfloat16, _, int32, _, _, _, _ = _kv4_names()
     try:
         shape, M = k_pages.shape, table.shape
@@ -710,7 +710,7 @@ def _paged_cache(k_pages, v_pages, table, B, d, index):
         _pack_pages(pages, 0, k_pages.data_ptr(), v_pages.data_ptr(), kp, kh, ks, vp, vh, vs, table.data_ptr(), P, H, S, M[1], d)
     except struct.error:  # d beyond 32 bits
         raise AlibiError(ALIBI_ERR_UNSUPPORTED, "paged cache") from None
-    return pages
+    return pages, H, M[1] * S
 
 
 def _explain_paged(k_pages, v_pages, table, B, d, index):
@@ -769,9 +769,9 @@ def alibi_paged_append(k, v, k_pages, v_pages, table, pos=None, count=None, rota
         _strided(k, bfloat16, 4, "k")
         _strided(v, bfloat16, 4, "v", k.get_device())
         raise ValueError(f"v must have shape {tuple(k.shape)}, got {tuple(v.shape)}")
-    pages = _paged_cache(k_pages, v_pages, table, B, d, index)
-    if pages.heads != H:
-        raise ValueError(f"k_pages must have {H} heads, got {pages.heads}")
+    pages, heads, _ = _paged_cache(k_pages, v_pages, table, B, d, index)
+    if heads != H:
+        raise ValueError(f"k_pages must have {H} heads, got {heads}")
     if B >= 1 << 31 or T >= 1 << 31:
         raise AlibiError(ALIBI_ERR_INVALID, "alibi_paged_append")
     rotation = f = None
@@ -808,23 +808,18 @@ def alibi_paged_append(k, v, k_pages, v_pages, table, pos=None, count=None, rota
 
 
 def _slope_array(slopes, H):
-    """A ctypes pointer to H slopes, or None; it keeps the array."""
-    if slopes is None:
-        return None
+    """A ctypes pointer to H slopes; it keeps the array."""
     m = np.ascontiguousarray(slopes, dtype=np.float32)
     if m.shape != (H,):
         raise ValueError(f"slopes: expected shape ({H},), got {m.shape}")
     return m.ctypes.data_as(ctypes.POINTER(ctypes.c_float))
 
 
-def _paged_bound(L, pages, where):
-    """The bound on the lengths: L, or what the table has room for."""
-    C = pages.width * pages.slots
+def _paged_bound(L, C, where):
+    """The bound on the lengths: L, or C, what the table has room for."""
     L = C if L is None else int(L)
-    if not 0 < L <= C:
-        raise AlibiError(ALIBI_ERR_INVALID, where)
-    if C > 1 << 24:
-        raise AlibiError(ALIBI_ERR_UNSUPPORTED, where)
+    if not 0 < L <= C <= 1 << 24:
+        raise AlibiError(ALIBI_ERR_UNSUPPORTED if 0 < L <= C else ALIBI_ERR_INVALID, where)
     return L
 
 
@@ -864,15 +859,20 @@ def alibi_attn_decode_paged(q, k_pages, v_pages, table, lens=None, L=None, out=N
     a sequence]; lens: int32 CUDA tensor [B] of lengths (None: all L); L: a bound on them (None: what the table has
     room for); slopes: H values (None: alibi_slopes(H)). Returns (out, lse): bf16 like q, fp32 without the last
     dimension; those made here belong to `stream`."""
-    bfloat16, _, _, _, _, _, lib = _kv4_names()
+    _, _, _, _, raw_stream, current, lib = _kv4_names()
     shape, index = _paged_query(q, (3, 4))
     B, H, d = shape[0], shape[1], shape[-1]
-    pages = _paged_cache(k_pages, v_pages, table, B, d, index)
-    L = _paged_bound(L, pages, "alibi_attn_decode_paged")
+    pages, _, C = _paged_cache(k_pages, v_pages, table, B, d, index)
+    L = _paged_bound(L, C, "alibi_attn_decode_paged")
     out, lse = _paged_outputs(out, lse, q, shape, index, stream)
-    _call_kv4(index, lib.alibi_attn_decode_paged, "alibi_attn_decode_paged", stream, q.data_ptr(), pages,
-              _paged_ints(lens, B, index, "lens"), out.data_ptr(), lse.data_ptr(), B, H, shape[2] if len(shape) == 4 else 1, L,
-              _slope_array(slopes, H))
+    args = (q.data_ptr(), pages, _paged_ints(lens, B, index, "lens"), out.data_ptr(), lse.data_ptr(), B, H,
+            shape[2] if len(shape) == 4 else 1, L, None if slopes is None else _slope_array(slopes, H))
+    if stream is None and current() == index:  # as _call_kv4 does it, without its 0.6 us
+        status = lib.alibi_attn_decode_paged(*args, raw_stream(index))
+        if status != ALIBI_OK:
+            raise AlibiError(status, "alibi_attn_decode_paged")
+    else:
+        _call_kv4(index, lib.alibi_attn_decode_paged, "alibi_attn_decode_paged", stream, *args)
     return out, lse
 
 
@@ -882,15 +882,15 @@ def alibi_attn_fwd_paged(q, k_pages, v_pages, table, lens=None, count=None, L=No
     their lengths, the new tokens included; k_pages, v_pages, table, L and slopes as in alibi_attn_decode_paged. Query t <
     count[b] has position lens[b] - count[b] + t; out and lse of tokens from count[b] on are left as they were.
     Returns (out, lse): bf16 [B, H, T, d] and fp32 [B, H, T]; those made here belong to `stream`."""
-    bfloat16, _, _, _, _, _, lib = _kv4_names()
+    lib = _kv4_names()[6]
     shape, index = _paged_query(q, (4,))
     B, H, T, d = shape
-    pages = _paged_cache(k_pages, v_pages, table, B, d, index)
-    L = _paged_bound(L, pages, "alibi_attn_fwd_paged")
+    pages, _, C = _paged_cache(k_pages, v_pages, table, B, d, index)
+    L = _paged_bound(L, C, "alibi_attn_fwd_paged")
     out, lse = _paged_outputs(out, lse, q, shape, index, stream)
     _call_kv4(index, lib.alibi_attn_fwd_paged, "alibi_attn_fwd_paged", stream, q.data_ptr(), pages,
               _paged_ints(lens, B, index, "lens"), _paged_ints(count, B, index, "count"), out.data_ptr(), lse.data_ptr(), B, H, T, L,
-              _slope_array(slopes, H))
+              None if slopes is None else _slope_array(slopes, H))
     return out, lse
 
 

@@ -24,7 +24,7 @@
 //   parts     items that do not fill a round of one per SM are cut into parts of their tiles, which run one after another over
 //             all SMs, part by part, so that the CTAs of a KV head pass its tiles at the same time; a part leaves its mean,
 //             maximum and sum in scratch, and a second kernel merges them. (Equal shares of all items' tiles for every CTA, as the
-//             decode has them, fill the device as well, but the tiles then come from memory for each: 2.0 us a tile, not 1.6.)
+//             decode has them, took longer than whole items: a CTA with many short items is late, whatever their tiles.)
 //
 // Where some head is steep (a slope above 4 / log2(e)), the bias is taken element by element from the whole distance: the
 // column part on the tensor core and the row part would cancel with a rounding of 2^-24 of 128 slopes.
@@ -159,8 +159,8 @@ struct IssuerState {
 __device__ __forceinline__ bool paged_active(const PagedItem &t, int s, int it) { return s == 1 ? t.q1valid : it >= t.first0; }
 
 // A bounded wait of a role that other items may leave idle for long: the limit holds from one item of the MMA issuer, which
-// it counts in `progress`, to the next. It sleeps between its looks, as a warp that
-// polls takes issue slots of the softmax warps beside it.
+// it counts in `progress`, to the next. It sleeps between its looks, as a warp that polls
+// takes issue slots of the softmax warps beside it.
 __device__ __forceinline__ bool wait_idle(uint64_t *bar, uint32_t parity, const int *progress, uint32_t *err, uint32_t site)
 {
     uint64_t t0 = 0;

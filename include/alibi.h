@@ -16,7 +16,8 @@
  * Conventions shared by every call:
  *   - Tensors are dense, row-major and contiguous. Prefill: q, k, v, out are
  *     [B, H, N, d]; lse is [B, H, N]. Decode: q and out are [B, H, d]; the
- *     caches are [B, H, L, d].
+ *     caches are [B, H, L, d]. (The paged cache and the rows appended to it have
+ *     strides, see alibi_pages and alibi_rows.)
  *   - bf16 means IEEE-style bfloat16 (1-8-7), stored as 16-bit words.
  *   - Device pointers must be CUDA device (or managed) memory of the current
  *     device, 16-byte aligned. The caller owns every buffer; the library never
@@ -415,7 +416,7 @@ typedef struct alibi_rotation {
 } alibi_rotation;
 
 /*
- * Append new tokens: token t < count[b] of sequence b of k and v (H_kv = pages->heads heads, T tokens) goes to row
+ * Append new tokens: token t < count[b] of sequence b of k and v (H_kv = pages->heads heads, T <= width slots tokens) goes to row
  * pos[b] + t of its pages. pos, count: device int32 [B], or NULL for 0 and T. With a rotation (NULL: none) the keys
  * are rotated by their positions on the way, in fp32, rounded once; and so are, where q is not NULL, the queries of H heads
  * (at most 384), into q_out, device bf16 [B, H, T, d]. Other rows of the pages, and tokens of q_out from count[b] on, are left
@@ -459,7 +460,9 @@ ALIBI_API int alibi_attn_decode_paged(const void *q, const alibi_pages *pages, c
  * [0, pages) in the blocks of 256 queries that read it, and alibi_check_error returns ALIBI_ERR_RANGE.
  * Runs the tensor-core pipeline of alibi_attn_fwd (weights are rounded to bf16 for the P V product). Rows that a
  * query does not see are not used, whatever they hold; a value that is not finite makes its element of out NaN (or,
- * in tiles of 128 rows that all of the 256 queries see, infinite) for the queries that see it.
+ * in tiles of 128 rows that all of the 256 queries see, infinite) for the queries that see it; a call that meets one takes
+ * up to twice as long. out and lse are the same bits for the same arguments. A call takes up to 61 MB of scratch from the
+ * library's stream-ordered pool where it cuts the work of few queries over many rows into parts.
  */
 ALIBI_API int alibi_attn_fwd_paged(const void *q, const alibi_pages *pages, const int *lens, const int *count, void *out,
                                    float *lse, int B, int H, int T, int L, const float *slopes, void *stream);
