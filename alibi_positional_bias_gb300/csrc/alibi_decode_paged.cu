@@ -48,7 +48,7 @@ KV4_HD constexpr int pg_tokens(int D) { return 2048 / D; }  // of a stage
 KV4_HD constexpr int pg_smem(int D, int NT) { return kPgRing + (NT > 2 ? kMostRows * D * 2 : 0) + 1024; }  // 1024: alignment
 
 struct DecodePagedParams {
-    CUtensorMap tk, tv;      // [pages, heads, slots, d] by strides, box {min(d, 64), min(slots, tokens of a stage), 1, 1}
+    CUtensorMap tk, tv;      // of encode_pages, boxes of min(slots, tokens of a stage) slots
     const __nv_bfloat16 *q;  // [B, H, T, d]: the G T rows of a KV head are consecutive
     Pages pg;
     const int *lens;         // [B] or null
@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(kPgWarps * 32, 2) decode_paged_kernel(const __
     uint8_t *const mine = smem + warp * (kPgStages * kPgStageBytes), *const queries = smem + kPgRing;
     const uint32_t ring = smem_u32(mine), sq = smem_u32(queries);
     // A stage is boxes of `box` slots; lanes i and 16 + i load box i of the keys and of the values.
-    const int box = min(1 << p.pg.shift, TK), part = (lane & 15) * box;
+    const int box = min(1 << p.pg.shift, TK), part = (lane & 15) * box, copies = box == TK ? 1 : (D + 63) / 64;
     int slot = 0;
     uint32_t phase = 0;
 
@@ -417,24 +417,25 @@ __global__ void __launch_bounds__(kPgWarps * 32, 2) decode_paged_kernel(const __
         if (bad && unit == 0 && threadIdx.x == 0) atomicOr(p.status, ALIBI_DEV_RANGE);
         bool lost = false;  // a page number that is none
 
-        // Page of this lane's box of stage s; past the length, one beyond the pool, whose box is filled with zeros.
-        const auto page_at = [&](int s) {
-            const int j = s * TK + part;
-            return part < TK && s >= s0 && j < len ? p.pg.page_of(b, j) : p.pg.pages;
-        };
+        // Page number of this lane's box of stage s, as the table has it: looked at when the copy is issued, a step after it was
+        // asked for.
+        const auto is_there = [&](int s) { return part < TK && s >= s0 && s * TK + part < len; };
+        const auto page_at = [&](int s) { return is_there(s) ? p.pg.number(b, s * TK + part) : 0; };
         const auto fetch = [&](int s, int slot_, int page) {
             if (s < s0) return;
-            if (page < 0) lost = true, page = p.pg.pages;
+            const bool in = static_cast<unsigned>(page) < static_cast<unsigned>(p.pg.pages), there = is_there(s);
+            lost |= there && !in;
+            // past the length, and for a number that is none, one beyond the pool, whose box is filled with zeros
+            if (!(there && in)) page = p.pg.pages;
             if (lane == 0) mbar_arrive_expect_tx(&full[warp][slot_], kPgStageBytes);
             __syncwarp();
             if (part < TK) {
                 constexpr int W = D < 64 ? D : 64;  // elements of a box's row
                 const bool values = lane >= 16;
-                uint8_t *to = mine + slot_ * kPgStageBytes + (values ? kPgStageBytes / 2 : 0) + part * (2 * W);
-#pragma unroll
-                for (int i = 0; i < D / W; ++i)
-                    tma_load_4d(to + i * (TK * 2 * W), values ? &p.tv : &p.tk, W * i, p.pg.slot_of(s * TK + part), hk, page,
-                                box * 2 * W, &full[warp][slot_]);
+                uint8_t *const to = mine + slot_ * kPgStageBytes + (values ? kPgStageBytes / 2 : 0) + part * (2 * W);
+                for (int h = 0; h < copies; ++h)
+                    load_box(to + h * (TK * 2 * W), values ? &p.tv : &p.tk, p.pg.slot_of(s * TK + part), h, hk, page, box * 2 * W,
+                             &full[warp][slot_]);
             }
         };
         int s = s1 - 1 - (SHARES ? warp : at + warp * count);  // this warp's stages: s, s - step, ...
@@ -624,7 +625,7 @@ cudaError_t launch(DecodePagedParams &p, const alibi_pages *pages, cudaStream_t 
     const int busy = (stages + kPgWarps - 1) / kPgWarps;  // CTAs that a chunk can keep busy
     const auto chunks = &decode_paged_kernel<D, NT, false>;
     const auto shared = &decode_paged_kernel<D, NT, true>;
-    if (!encode_pages(&p.tk, &p.tv, pages, std::min(D, 64), std::min(pages->slots, pg_tokens(D)))) return cudaErrorInvalidValue;
+    if (!encode_pages(&p.tk, &p.tv, pages, std::min(D, 64), std::min(pages->slots, pg_tokens(D)), pages->slots >= pg_tokens(D))) return cudaErrorInvalidValue;
     p.part = nullptr;
     p.head = nullptr;
     int fit[paged::kMostCluster + 1];

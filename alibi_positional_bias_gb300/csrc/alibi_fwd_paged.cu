@@ -47,7 +47,7 @@ constexpr int kMostParts = 16;
 
 struct FwdPagedParams {
     CUtensorMap tq;      // [B H, T, d] bf16, box {64, 128, 1}, 128-byte swizzle
-    CUtensorMap tk, tv;  // [pages, heads, slots, d] by strides, box {64, min(slots, 128), 1, 1}, 128-byte swizzle
+    CUtensorMap tk, tv;  // of encode_pages, boxes of min(slots, 128) slots, 128-byte swizzle
     CUtensorMap tout;    // [B H, T, d] bf16, box {32, 32, 1}, no swizzle (epilogue stores)
     Pages pg;
     const int *lens, *count;
@@ -271,6 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
     if (warp == 0) {
         // ------------------------------------------------------ TMA producer
         const int box = min(1 << p.pg.shift, BN), boxes = BN / box;  // rows of a box, boxes of a tile
+        const int copies = boxes == 1 ? 1 : C::kChunks;
         uint32_t uc = 0;  // ring units issued
         int kk = 0;       // items begun
         uint32_t looked = 0;
@@ -325,16 +326,16 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
                 uint8_t *const v = smem + C::kV + st * C::kTileBytes;
                 if (lane < boxes) {
                     const int at = lane * box * 128;  // of the box in a swizzle atom
-                    for (int c = 0; c < C::kChunks; ++c) {
+                    for (int c = 0; c < copies; ++c) {
                         if (u < t.n)
-                            tma_load_4d(smem + C::kK + st * C::kTileBytes + c * C::kChunkBytes + at, &p.tk, 64 * c,
-                                        p.pg.slot_of((t.top - u) * BN + lane * box), hk, page, box * 128, &unit_full[st]);
+                            load_box(smem + C::kK + st * C::kTileBytes + c * C::kChunkBytes + at, &p.tk,
+                                     p.pg.slot_of((t.top - u) * BN + lane * box), c, hk, page, box * 128, &unit_full[st]);
                         if (with_k0)
-                            tma_load_4d(smem + C::kV + (st ^ 1) * C::kTileBytes + c * C::kChunkBytes + at, &p.tv, 64 * c,
-                                        p.pg.slot_of(t.top * BN + lane * box), hk, page, box * 128, v_landed);
+                            load_box(smem + C::kV + (st ^ 1) * C::kTileBytes + c * C::kChunkBytes + at, &p.tv,
+                                     p.pg.slot_of(t.top * BN + lane * box), c, hk, page, box * 128, v_landed);
                         else if (u >= 1 && !(look && u == 1))
-                            tma_load_4d(v + c * C::kChunkBytes + at, &p.tv, 64 * c, p.pg.slot_of((t.top - u + 1) * BN + lane * box), hk,
-                                        before, box * 128, look ? v_landed : &unit_full[st]);
+                            load_box(v + c * C::kChunkBytes + at, &p.tv, p.pg.slot_of((t.top - u + 1) * BN + lane * box), c, hk, before,
+                                     box * 128, look ? v_landed : &unit_full[st]);
                     }
                 }
                 __syncwarp();
@@ -792,7 +793,7 @@ cudaError_t launch(FwdPagedParams &p, const alibi_pages *pages, const void *q, c
     const uint64_t d = static_cast<uint64_t>(pages->d);
     const uint32_t box = static_cast<uint32_t>(std::min(pages->slots, BN));
     if (!encode_tmap_bf16_3d(&p.tq, q, d, p.T, p.BH, 64, BM) || !encode_tmap_bf16_3d(&p.tout, p.out, d, p.T, p.BH, 32, 32, false) ||
-        !encode_pages(&p.tk, &p.tv, pages, 64, box))
+        !encode_pages(&p.tk, &p.tv, pages, 64, box, box == static_cast<uint32_t>(BN)))
         return cudaErrorInvalidValue;
     const bool steep = *std::max_element(p.slope, p.slope + p.H) > kSteep;
     const auto kern = steep ? &fwd_paged_kernel<D, true> : &fwd_paged_kernel<D, false>;

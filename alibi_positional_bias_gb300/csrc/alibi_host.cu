@@ -356,14 +356,14 @@ bool encode_tmap_bf16_3d(CUtensorMap *map, const void *base, uint64_t dim0, uint
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
-bool encode_tmap_bf16_4d(CUtensorMap *map, const void *base, const uint64_t (&dims)[4], const uint64_t (&strides)[3],
-                         uint32_t box0, uint32_t box1)
+bool encode_tmap_bf16_5d(CUtensorMap *map, const void *base, const uint64_t (&dims)[5], const uint64_t (&strides)[4],
+                         uint32_t box0, uint32_t box1, uint32_t box2)
 {
-    const cuuint64_t n[4] = {dims[0], dims[1], dims[2], dims[3]};
-    const cuuint64_t stride[3] = {strides[0], strides[1], strides[2]};
-    const cuuint32_t box[4] = {box0, box1, 1, 1};
-    const cuuint32_t estride[4] = {1, 1, 1, 1};
-    return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4u, const_cast<void *>(base), n, stride, box, estride,
+    const cuuint64_t n[5] = {dims[0], dims[1], dims[2], dims[3], dims[4]};
+    const cuuint64_t stride[4] = {strides[0], strides[1], strides[2], strides[3]};
+    const cuuint32_t box[5] = {box0, box1, box2, 1, 1};
+    const cuuint32_t estride[5] = {1, 1, 1, 1, 1};
+    return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5u, const_cast<void *>(base), n, stride, box, estride,
               CU_TENSOR_MAP_INTERLEAVE_NONE,
               box0 == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
               : box0 == 32 ? CU_TENSOR_MAP_SWIZZLE_64B

@@ -52,10 +52,10 @@ cudaMemPool_t decode_pool();     // library-owned stream-ordered pool of the cur
 // epilogue's bulk stores use).
 bool encode_tmap_bf16_3d(CUtensorMap *map, const void *base, uint64_t dim0, uint64_t dim1, uint64_t dim2,
                          uint32_t box0, uint32_t box1, bool swizzle128 = true);
-// 4-D TMA map over a bf16 tensor of dims (fastest first) with strides (in bytes, of dims 1 to 3), box {box0, box1, 1, 1},
+// 5-D TMA map over a bf16 tensor of dims (fastest first) with strides (in bytes, of dims 1 to 4), box {box0, box1, box2, 1, 1},
 // swizzled over the box's rows (of 128, 64 or 32 bytes), zero fill out of bounds.
-bool encode_tmap_bf16_4d(CUtensorMap *map, const void *base, const uint64_t (&dims)[4], const uint64_t (&strides)[3],
-                         uint32_t box0, uint32_t box1);
+bool encode_tmap_bf16_5d(CUtensorMap *map, const void *base, const uint64_t (&dims)[5], const uint64_t (&strides)[4],
+                         uint32_t box0, uint32_t box1, uint32_t box2);
 
 // Launch in clusters of `cluster` CTAs with programmatic stream serialization: the grid may be scheduled while the kernel
 // before it drains, and executes griddepcontrol.wait in every thread before it touches memory.

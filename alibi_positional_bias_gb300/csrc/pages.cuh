@@ -16,10 +16,12 @@ struct Pages {
     int pages, heads, shift, width, d;                         // shift: log2 of a page's slots
 
     __device__ __forceinline__ int slot_of(int j) const { return j & ((1 << shift) - 1); }
+    // entry of the table for token j of sequence b
+    __device__ __forceinline__ int number(int b, int j) const { return table[static_cast<size_t>(b) * width + (j >> shift)]; }
     // page of token j of sequence b, -1 for a number that is none of a page
     __device__ __forceinline__ int page_of(int b, int j) const
     {
-        const int id = table[static_cast<size_t>(b) * width + (j >> shift)];
+        const int id = number(b, j);
         return static_cast<unsigned>(id) < static_cast<unsigned>(pages) ? id : -1;
     }
 };
@@ -58,30 +60,35 @@ inline Pages pages_of(const alibi_pages *p)
     return g;
 }
 
-// 4-D tiled load of one box of `bytes` bytes, a power of two, into shared memory, completing on `bar`. It lies on a multiple of
-// its size or of 1024, where the swizzle's pattern begins anew.
-__device__ __forceinline__ void tma_load_4d(void *dst, const void *tmap, int x, int y, int z, int w, uint32_t bytes, uint64_t *bar)
+// Load of one box of a page: slots from `slot` on of head `head`, 64 elements of each from 64 `half` on (or all of fewer), `bytes`
+// bytes, a power of two. It lies on a multiple of that or of 1024, where the swizzle's pattern begins anew, and completes on
+// `bar`. With a map of both halves the second half follows the first.
+__device__ __forceinline__ void load_box(void *dst, const void *tmap, int slot, int half, int head, int page, uint32_t bytes,
+                                         uint64_t *bar)
 {
 #ifdef ALIBI_CHECKS
-    if (!check::tma_x_aligned(x)) return check_fail(check::TMA_LOAD, static_cast<uint32_t>(x));
     if (!check_smem(smem_u32(dst), bytes, bytes < 1024 ? bytes : 1024)) return check_fail(check::TMA_LOAD, smem_u32(dst));
 #endif
     (void)bytes;
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(0), "r"(slot), "r"(half), "r"(head), "r"(page), "r"(smem_u32(bar))
         : "memory");
 }
 
-// Maps of the keys' and values' pools for boxes of `box0` elements of `box1` slots of one head of one page.
-inline bool encode_pages(CUtensorMap *tk, CUtensorMap *tv, const alibi_pages *p, uint32_t box0, uint32_t box1)
+// Maps of the keys' and values' pools for boxes of `box` slots of one head of one page: rows of `width` elements, of one half of
+// d = 128 or (`both`) of the one and then of the other: each copy that a warp issues takes it 40 cycles or more (64 x 40 x 8192
+// tokens decoded in 1448 us with one half at a time, 1407 with both).
+inline bool encode_pages(CUtensorMap *tk, CUtensorMap *tv, const alibi_pages *p, uint32_t width, uint32_t box, bool both)
 {
-    const uint64_t dims[4] = {static_cast<uint64_t>(p->d), static_cast<uint64_t>(p->slots), static_cast<uint64_t>(p->heads),
+    const uint64_t d = static_cast<uint64_t>(p->d), part = d < 64 ? d : 64;
+    const uint64_t dims[5] = {part, static_cast<uint64_t>(p->slots), d / part, static_cast<uint64_t>(p->heads),
                               static_cast<uint64_t>(p->pages)};
-    const uint64_t ks[3] = {2ull * p->k_slot, 2ull * p->k_head, 2ull * p->k_page};
-    const uint64_t vs[3] = {2ull * p->v_slot, 2ull * p->v_head, 2ull * p->v_page};
-    return encode_tmap_bf16_4d(tk, p->k, dims, ks, box0, box1) && encode_tmap_bf16_4d(tv, p->v, dims, vs, box0, box1);
+    const uint64_t ks[4] = {2ull * p->k_slot, 128, 2ull * p->k_head, 2ull * p->k_page};
+    const uint64_t vs[4] = {2ull * p->v_slot, 128, 2ull * p->v_head, 2ull * p->v_page};
+    const uint32_t halves = both ? static_cast<uint32_t>(d / part) : 1;
+    return encode_tmap_bf16_5d(tk, p->k, dims, ks, width, box, halves) && encode_tmap_bf16_5d(tv, p->v, dims, vs, width, box, halves);
 }
 
 }  // namespace alibi
