@@ -125,61 +125,45 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_con
     }
     const int n = first + t;
     bool live = t < count;
-    Turn turn;
-    const bool on = ROTATE && 8 * vec < p.R;
-    if (ROTATE) turn_of(p, vec, n, on && live, turn);
-
     const bool queries = ROTATE && static_cast<int>(blockIdx.y) >= p.kv_groups;
     const int h0 = (queries ? blockIdx.y - p.kv_groups : blockIdx.y) * p.group + (row >> p.log_tok);
-    if (queries) {
-        const __nv_bfloat16 *src = p.q.data + b * p.q.batch + t * p.q.token + 8 * vec;
-        __nv_bfloat16 *dst = p.q_out + (static_cast<size_t>(b) * p.H * p.T + t) * p.pg.d + 8 * vec;
-        for (int i = 0; i < p.group; i += kUnroll * step) {
-            uint4 x[kUnroll];
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int o = i + u * step, h = h0 + o;
-                x[u] = make_uint4(0, 0, 0, 0);
-                if (live && o < p.group && h < p.H) x[u] = __ldcs(reinterpret_cast<const uint4 *>(src + h * p.q.head));
-            }
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int o = i + u * step, h = h0 + o;
-                x[u] = rotated(p, x[u], vec, on, turn);
-                if (live && o < p.group && h < p.H)
-                    *reinterpret_cast<uint4 *>(dst + static_cast<size_t>(h) * p.T * p.pg.d) = x[u];
-            }
-        }
-        return;
-    }
-    const int page = live ? p.pg.page_of(b, n) : 0;
+    const Rows from = queries ? p.q : p.k;
+    const int heads = queries ? p.H : p.pg.heads, page = live && !queries ? p.pg.page_of(b, n) : 0, slot = p.pg.slot_of(n);
     if (page < 0) {
         atomicOr(p.status, ALIBI_DEV_RANGE);
         live = false;
     }
-    const int slot = p.pg.slot_of(n);
-    const __nv_bfloat16 *ks = p.k.data + b * p.k.batch + t * p.k.token + 8 * vec;
+    const __nv_bfloat16 *src = from.data + b * from.batch + t * from.token + 8 * vec;
     const __nv_bfloat16 *vs = p.v.data + b * p.v.batch + t * p.v.token + 8 * vec;
-    __nv_bfloat16 *kd = p.pg.k + page * p.pg.k_page + slot * p.pg.k_slot + 8 * vec;
+    __nv_bfloat16 *dst = (queries ? p.q_out + (static_cast<size_t>(b) * p.H * p.T + t) * p.pg.d
+                                  : p.pg.k + page * p.pg.k_page + slot * p.pg.k_slot) + 8 * vec;
     __nv_bfloat16 *vd = p.pg.v + page * p.pg.v_page + slot * p.pg.v_slot + 8 * vec;
-    for (int i = 0; i < p.group; i += kUnroll * step) {
-        uint4 x[kUnroll], y[kUnroll];
+    const long long dst_head = queries ? static_cast<long long>(p.T) * p.pg.d : p.pg.k_head;
+    uint4 x[kUnroll], y[kUnroll];
+    const auto load = [&](int i) {
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             const int o = i + u * step, h = h0 + o;
             x[u] = y[u] = make_uint4(0, 0, 0, 0);
-            if (live && o < p.group && h < p.pg.heads) {
-                x[u] = __ldcs(reinterpret_cast<const uint4 *>(ks + h * p.k.head));
-                y[u] = __ldcs(reinterpret_cast<const uint4 *>(vs + h * p.v.head));
+            if (live && o < p.group && h < heads) {
+                x[u] = __ldcs(reinterpret_cast<const uint4 *>(src + h * from.head));
+                if (!queries) y[u] = __ldcs(reinterpret_cast<const uint4 *>(vs + h * p.v.head));
             }
         }
+    };
+    if (ROTATE) load(0);
+    Turn turn;
+    const bool on = ROTATE && 8 * vec < p.R;
+    if (ROTATE) turn_of(p, vec, n, on && live, turn);  // while the first rows are on their way
+    for (int i = 0; i < p.group; i += kUnroll * step) {
+        if (!ROTATE || i > 0) load(i);
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             const int o = i + u * step, h = h0 + o;
             if (ROTATE) x[u] = rotated(p, x[u], vec, on, turn);
-            if (live && o < p.group && h < p.pg.heads) {
-                *reinterpret_cast<uint4 *>(kd + h * p.pg.k_head) = x[u];
-                *reinterpret_cast<uint4 *>(vd + h * p.pg.v_head) = y[u];
+            if (live && o < p.group && h < heads) {
+                *reinterpret_cast<uint4 *>(dst + h * dst_head) = x[u];
+                if (!queries) *reinterpret_cast<uint4 *>(vd + h * p.pg.v_head) = y[u];
             }
         }
     }
@@ -253,7 +237,7 @@ extern "C" int alibi_paged_append(const alibi_rows *k, const alibi_rows *v, cons
     p.by_blocks = Divisor(static_cast<uint32_t>(blocks));
     // Heads of a CTA: as few as its threads take at once while that fills the device eight times, else up to sixteen times as
     // many; with a rotation, whose sines are computed once per CTA, twice (2 x (6 + 24) heads x 1001 tokens of d = 64 9.7 us
-    // at two heads, 6.3 at four).
+    // at two heads, 6.3 at eight).
     const int most = std::max(pages->heads, p.H);
     p.group = step;
     while (p.group < most && p.group < 4 * kUnroll * step && tokens * ((most + p.group - 1) / p.group) > (R ? 2LL : 8LL) * num_sms())

@@ -15,7 +15,7 @@ constexpr int kWarps = 4;          // of a CTA, two CTAs per SM
 constexpr int kMostCluster = 16;
 
 // us of a warp's step, one stage, of head size d with `groups` groups of 8 rows, where its SM has no other CTA: the
-// chain of its own instructions, whatever memory gives.
+// chain of its own instructions, whatever memory gives (0.63 at d = 128 when last measured; 0.70 chooses no worse).
 inline double step_us(int d, int groups)
 {
     const double t = d == 128 ? 0.70 : d == 64 ? 0.72 : d == 32 ? 1.08 : 1.8;
@@ -27,25 +27,25 @@ inline double step_us(int d, int groups)
 // with theirs 9.5; memory gives a stage per 1.1 ns, a tenth less to clusters, and half of an SM's room takes
 // a step 1.5 times as long. Measured, in us, launches in one graph over caches that together are larger than
 // L2, whole / clusters of / shares, what is taken in brackets (sequences x KV heads (x G) x tokens x d):
-//   1 x 1 x 8192 x 128           [S]   87.8 / 15.5 (8) 9.8 (16) / 8.2
-//   1 x 32 x 2048 x 128          [6]   25.4 / 12.5 (4) 10.5 (6) 10.6 (8) / 14.4
-//   1 x 40 x 8192 x 128          [6]   91.3 / 34.7 (3) 29.7 (5) 28.7 (6) / 33.8
-//   1 x 8 (x 4) x 8192 x 128     [12]  93.7 / 20.6 (6) 15.4 (10) 14.3 (12) 13.5 (16) / 13.5
-//   1 x 8 (x 4) x 32768 x 128    [S]   353 / 39.6 (12) 36.5 (16) / 28.9
-//   1 x 4 (x 4) x 131071 x 128   [S]   1439 / 144 (12) 126 (16) / 49.0
-//   4 x 8 (x 8) x 8192 x 128     [8]   95.4 / 33.4 (4) 25.9 (6) 25.6 (8) / 30.8
-//   2 x 40 x 8192 x 128          [3]   90.5 / 58.8 (2) 52.6 (3) / 57.5
-//   2 x 40 x 1024 x 128          [3]   14.4 / 11.8 (2) 11.6 (3) / 15.5
-//   4 x 40 x 4096 x 128          [W]   52.8 /   -   / 57.5
-//   16 x 8 (x 4) x 4097 x 128    [2]   48.9 / 45.1 (2) / 50.2
-//   8 x 8 (x 4) x 16384 x 128    [4]   184 / 101.8 (2) 83.6 (3) 85.7 (4) / 87.1
-//   8 x 8 (x 8) x 32768 x 128    [4]   366 / 161.5 (3) 169.5 (4) / 166.4
-//   16 x 40 x 4096 x 128         [S]   207 /   -   / 200
-//   9 x 37 x 8192 x 128          [S]   253 /   -   / 206
-//   1 x 32 x 8192 x 64           [8]   49.7 / 18.7 (4) 16.5 (6) 15.7 (8) / 18.5
-//   8 x 16 (x 2) x 4 new, 2048 x 64  [2]  15.8 / 15.7 (2) / 21.4
-//   1 x 8 (x 8) x 16384 x 64     [S]   94.2 / 19.3 (8) 14.2 (12) 13.2 (16) / 13.4
-//   1 x 32 x 16384 x 32          [8]   72.5 / 20.2 (6) 17.6 (8) / 20.5
+//   1 x 1 x 8192 x 128           [S]   82.6 / 14.2 (8) 9.2 (16) / 8.1
+//   1 x 32 x 2048 x 128          [6]   23.5 / 10.9 (4) 10.3 (6) 10.6 (8) / 14.4
+//   1 x 40 x 8192 x 128          [6]   83.9 / 32.7 (3) 28.9 (5) 28.7 (6) / 34.2
+//   1 x 8 (x 4) x 8192 x 128     [16]  83.9 / 19.1 (6) 13.9 (10) 12.7 (12) 12.0 (16) / 13.7
+//   1 x 8 (x 4) x 32768 x 128    [S]   325 / 33.0 (12) 28.7 (16) / 28.9
+//   1 x 4 (x 4) x 131071 x 128   [S]   1288 / 113 (12) 90.7 (16) / 49.4
+//   4 x 8 (x 8) x 8192 x 128     [8]   84.4 / 27.0 (4) 25.4 (6) 25.2 (8) / 31.2
+//   2 x 40 x 8192 x 128          [3]   84.3 / 53.5 (2) 52.9 (3) / 58.6
+//   2 x 40 x 1024 x 128          [3]   14.0 / 11.6 (2) 11.3 (3) / 15.8
+//   4 x 40 x 4096 x 128          [W]   52.2 /   -   / 58.3
+//   16 x 8 (x 4) x 4097 x 128    [2]   46.0 / 45.1 (2) / 50.3
+//   8 x 8 (x 4) x 16384 x 128    [4]   165 / 87.2 (2) 81.7 (3) 84.1 (4) / 88.5
+//   8 x 8 (x 8) x 32768 x 128    [4]   326 / 155.5 (3) 160.6 (4) / 168.0
+//   16 x 40 x 4096 x 128         [S]   207 /   -   / 202
+//   9 x 37 x 8192 x 128          [S]   249 /   -   / 208
+//   1 x 32 x 8192 x 64           [8]   44.6 / 16.2 (4) 15.6 (6) 15.5 (8) / 18.6
+//   8 x 16 (x 2) x 4 new, 2048 x 64  [2]  15.0 / 15.2 (2) / 21.3
+//   1 x 8 (x 8) x 16384 x 64     [16]  85.1 / 16.0 (8) 12.8 (12) 12.1 (16) / 13.3
+//   1 x 32 x 16384 x 32          [8]   61.4 / 18.3 (6) 16.1 (8) / 20.9
 inline int ctas_of_chunk(long long units, int stages, int ctas, const int (&fit)[kMostCluster + 1], double step)
 {
     constexpr double kStage = 0.0011;
