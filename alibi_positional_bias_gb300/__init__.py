@@ -791,16 +791,21 @@ def alibi_paged_append(k, v, k_pages, v_pages, table, pos=None, count=None, rota
     else:
         if not rotate:
             raise ValueError("q needs rotate")
-        _strided(q, bfloat16, 4, "q", index)
-        if q.shape[0] != B or q.shape[2:] != shape[2:]:
+        try:
+            qs = q.shape
+            good = _is_rows(q, bfloat16, (B, qs[1], T, d), index)
+        except (AttributeError, IndexError):
+            good = False
+        if not good:
+            _strided(q, bfloat16, 4, "q", index)
             raise ValueError(f"q must have shape ({B}, heads, {T}, {d}), got {tuple(q.shape)}")
-        rows = _rows_struct(q, q.shape, "q")
+        rows = _rows_struct(q, qs, "q")
         if q_out is None:
             import torch
-            q_out = (torch.empty(q.shape, dtype=bfloat16, device=q.device) if stream is None
-                     else _empty_on(stream, index, q.shape, bfloat16))
-        else:
-            _need_on(q_out, bfloat16, q.shape, "q_out", index)
+            q_out = (torch.empty(qs, dtype=bfloat16, device=q.device) if stream is None
+                     else _empty_on(stream, index, qs, bfloat16))
+        elif not (_is_rows(q_out, bfloat16, qs, index) and q_out.is_contiguous()):
+            _need_on(q_out, bfloat16, qs, "q_out", index)
     _call_kv4(index, lib.alibi_paged_append, "alibi_paged_append", stream, _rows_struct(k, shape, "k"), _rows_struct(v, shape, "v"),
               pages, _paged_ints(pos, B, index, "pos"), _paged_ints(count, B, index, "count"), B, T, rotation, rows,
               None if q is None else q_out.data_ptr(), 0 if q is None else q.shape[1])

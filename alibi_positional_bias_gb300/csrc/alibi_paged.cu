@@ -9,7 +9,12 @@
 //
 // What has to move: 2 bytes in and 2 bytes out of each element. A thread takes 16 bytes of a row; rows of consecutive tokens
 // of one head follow one another, and a thread keeps its token from head to head, so that the page is looked up and the
-// sines are computed once per thread. Four heads' loads are issued together.
+// sines are computed once per thread. Four heads' loads are issued together, with a rotation before the sines are computed.
+//
+// Measured, launches in one graph over tensors colder than L2: prompts of 4 x 32 heads x 2048 tokens of d = 128 (268 MB) 42.7
+// us, 6.3 TB/s, and with the keys and as many heads of queries rotated (403 MB) 66 us, 6.1 TB/s: bound by HBM. One token of
+// 64 x 40 heads 2.1 us, 2 x (6 + 24) heads x 1001 tokens of d = 64 rotated (18 MB) 5.8 us: a launch, the way from length to
+// page to row, one round of CTAs.
 
 #include <algorithm>
 #include <cmath>
@@ -237,7 +242,7 @@ extern "C" int alibi_paged_append(const alibi_rows *k, const alibi_rows *v, cons
     p.by_blocks = Divisor(static_cast<uint32_t>(blocks));
     // Heads of a CTA: as few as its threads take at once while that fills the device eight times, else up to sixteen times as
     // many; with a rotation, whose sines are computed once per CTA, twice (2 x (6 + 24) heads x 1001 tokens of d = 64 9.7 us
-    // at two heads, 6.3 at eight).
+    // at two heads, 6.3 at eight, with the loads after the sines).
     const int most = std::max(pages->heads, p.H);
     p.group = step;
     while (p.group < most && p.group < 4 * kUnroll * step && tokens * ((most + p.group - 1) / p.group) > (R ? 2LL : 8LL) * num_sms())
