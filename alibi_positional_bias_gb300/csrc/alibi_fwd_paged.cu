@@ -31,10 +31,13 @@
 //
 // Measured (d = 128, launches in one graph): 16 heads x 16384 tokens 730 us (the dense prefill 695), 32 heads x 2048 new tokens
 // of 32768 716 to 731 us (1460 to 1488 TFLOP/s), 4 x 32 prompts of up to 2048 134 us (889 TFLOP/s), 8 (x 4) heads x 256 new of 32768
-// 118 us; 2 x 6 heads x 100 new of up to 999, d = 64, 15.4 us. What bounds it is what bounds the dense prefill: the chain from S
+// 113 us; 2 x 6 heads x 100 new of up to 999, d = 64, 14.1 us. What bounds it is what bounds the dense prefill: the chain from S
 // over the softmax to P V (tensor pipe 63 to 65% of active cycles in long items, 48% in prompts of 2048), and the instruction
 // cache, which the roles' code does not fit (0.6 to 0.8 cycles per issue without an instruction; the text of a second copy of
 // the exponentials, or waits out of line, cost 2 to 6%).
+// The place of the loops counts too, by whole lines of 128 bytes: 16 to 96 bytes of instructions before the roles make 723 / 715 us
+// (16 heads x 16384, 32 x 2048 of 32768) into 747 to 773 / 753 to 788, in the issuer's or the softmax's role alone into 726 to 750;
+// as it stands it is at the best of the eight places for both. Measure again after any change to this kernel.
 
 #include <algorithm>
 #include <cmath>
@@ -727,26 +730,40 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
     }
 }
 
-// Merge of the parts of item whole + blockIdx.x, 32 rows by CTA: lane r has row r, a warp every eighth column. The weights
-// l 2^(M - max M) are normalised before they meet the means, so nothing overflows; a part that the row sees nothing of has l = 0.
-template <int D>
+// Merge of the parts of item whole + blockIdx.x, 32 rows and 8 COLS columns by CTA: lane r has row r, a warp COLS columns. As many
+// parts are asked for at once as 64 registers hold (one part after another: 2 x 6 heads x 100 new of 999 tokens 16.1 us and not
+// 15.0). The weights l 2^(M - max M) are normalised before they meet the means, so nothing overflows; a part that the row sees
+// nothing of has l = 0 and means that do not count.
+template <int D, int COLS>
 __global__ void __launch_bounds__(256) fwd_paged_merge_kernel(const __grid_constant__ FwdPagedParams p)
 {
-    constexpr int kCols = D / 8, kPart = paged_part_floats(D), kRows = 2 * BM;
-    __shared__ __nv_bfloat16 rows[32][D + 8];
+    constexpr int kPart = paged_part_floats(D), kRows = 2 * BM, kBatch = 64 / COLS;
+    static_assert(kMostParts % kBatch == 0);
+    __shared__ __align__(16) __nv_bfloat16 rows[32][8 * COLS + 8];
     griddep_wait();
     PagedItem t;
     if (!paged_item(p, p.whole + blockIdx.x, false, t)) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row0 = 256 * t.qb + 32 * static_cast<int>(blockIdx.y);
     if (row0 >= t.count) return;
+    const int col0 = 8 * COLS * static_cast<int>(blockIdx.z);
     const float *part = p.part + static_cast<size_t>(blockIdx.x) * p.parts * kPart + 32 * blockIdx.y + lane;
-    float M[kMostParts], l[kMostParts], top = -INFINITY, sum = 0.f, o[kCols] = {};
+    // the parts that have tiles
+    const uint32_t some = __ballot_sync(
+        0xffffffffu, lane < p.parts && part_begin(t.n, lane, p.parts) < part_begin(t.n, lane + 1, p.parts));
+    const auto in = [&](int q) { return (some >> q & 1) != 0; };
+    float M[kMostParts], l[kMostParts], x[kBatch][COLS], top = -INFINITY, sum = 0.f, o[COLS] = {};
+    const auto load = [&](int q0) {
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q)
+#pragma unroll
+            for (int c = 0; c < COLS; ++c) x[q][c] = in(q0 + q) ? __ldcg(part + (q0 + q) * kPart + (col0 + COLS * warp + c) * kRows) : 0.f;
+    };
 #pragma unroll
     for (int q = 0; q < kMostParts; ++q) {
-        const bool in = q < p.parts && part_begin(t.n, q, p.parts) < part_begin(t.n, q + 1, p.parts);
-        M[q] = in ? __ldcg(part + q * kPart + D * kRows) : 0.f;
-        l[q] = in ? __ldcg(part + q * kPart + (D + 1) * kRows) : 0.f;
+        M[q] = in(q) ? __ldcg(part + q * kPart + D * kRows) : 0.f;
+        l[q] = in(q) ? __ldcg(part + q * kPart + (D + 1) * kRows) : 0.f;
     }
+    load(0);
 #pragma unroll
     for (int q = 0; q < kMostParts; ++q)
         if (l[q] != 0.f) top = fmaxf(top, M[q]);
@@ -757,35 +774,52 @@ __global__ void __launch_bounds__(256) fwd_paged_merge_kernel(const __grid_const
     }
     const float inv = sum == 0.f ? 0.f : 1.0f / sum;
 #pragma unroll
-    for (int q = 0; q < kMostParts; ++q) {
-        if (l[q] == 0.f) continue;
-        const float *x = part + q * kPart + warp * kCols * kRows;
-        const float w = l[q] * inv;
+    for (int q0 = 0; q0 < kMostParts; q0 += kBatch) {
+        if (q0 >= p.parts) break;
+        if (q0 > 0) load(q0);
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) o[c] = fmaf(__ldcg(x + c * kRows), w, o[c]);
+        for (int q = 0; q < kBatch; ++q)
+#pragma unroll
+            for (int c = 0; c < COLS; ++c) o[c] = l[q0 + q] == 0.f ? o[c] : fmaf(x[q][c], l[q0 + q] * inv, o[c]);
     }
 #pragma unroll
-    for (int c = 0; c < kCols; ++c) rows[lane][warp * kCols + c] = __float2bfloat16_rn(o[c]);
-    if (warp == 0 && p.lse && row0 + lane < t.count)
+    for (int c = 0; c < COLS; c += 2) *reinterpret_cast<uint32_t *>(&rows[lane][COLS * warp + c]) = pack_bf16x2(o[c], o[c + 1]);
+    if (warp == 0 && col0 == 0 && p.lse && row0 + lane < t.count)
         p.lse[static_cast<size_t>(t.bh) * p.T + row0 + lane] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
     __syncthreads();
     const int d = p.pg.d;
-    for (int x = threadIdx.x; x < 32 * (d / 8); x += 256) {
-        const int r = x / (d / 8), c = x % (d / 8) * 8;
-        if (row0 + r < t.count)
-            *reinterpret_cast<uint4 *>(p.out + (static_cast<size_t>(t.bh) * p.T + row0 + r) * d + c) =
+    for (int i = threadIdx.x; i < 32 * COLS; i += 256) {  // pieces of 8 elements
+        const int r = i / COLS, c = i % COLS * 8;
+        if (row0 + r < t.count && col0 + c < d)
+            *reinterpret_cast<uint4 *>(p.out + (static_cast<size_t>(t.bh) * p.T + row0 + r) * d + col0 + c) =
                 *reinterpret_cast<const uint4 *>(&rows[r][c]);
     }
 }
 
 // Parts into which the items of the last, incomplete round, the shortest, are cut: the number with the least estimated time of that
-// round, in tiles of 256 rows and 128 keys (1.7 us). An item costs some five tiles beside its own; the merge, six and 0.02
-// for each partial.
+// round, in tiles of 256 rows and 128 keys (1.4 to 1.6 us): of the longest item where all parts run at once, else of the mean one.
+// An item costs some four tiles beside its own; the merge, 1.6 and what reading each partial takes. Measured, in us, uncut /
+// in 2 / 3 / 4 / 6 / 8 parts, what is taken in brackets (heads x new tokens of length):
+//   2 x 6 x 100 of 999 (d = 64)  [4]  18.3 / 16.4 / 14.0 / 14.1 / 14.5 / 14.9
+//   32 x 64 of 1024              [4]  18.3 / 15.8 / 14.5 / 13.9 / 18.6 / 18.7
+//   6 x 100 of 500               [2]  13.1 / 12.6 / 13.1 / 13.0 / 13.0 / 13.1
+//   6 x 1024 of 1024             [4]  20.6 / 18.2 / 16.8 / 17.2 / 17.4 / 21.7
+//   4 x 8 x 128 of 4096          [4]  51.2 / 34.5 / 28.3 / 25.7 / 33.5 / 30.6
+//   32 x 256 of 32768            [4]  405 / 211 / 146 / 113 / 154 / 122
+//   40 x 512 of 8192             [3]  108 / 120 / 93.4 / 107 /  -  /  -
+//   32 x 2048 of 32768           [4]  794 / 799 / 803 / 722 /  -  /  -
+//   16 x 700 of 700              [1]  20.4 / 20.7 / 19.4 / 24.8 / 25.5 / 23.7
+//   16 x 2048 of 2048            [1]  35.6 / 47.7 / 50.3 /  -  /  -  /  -
 int paged_parts(int rest, int BH, int T, int L, int sms)
 {
-    const double tiles = (L - std::min(T, L)) / 128.0 + static_cast<double>(rest) / BH + 1;
+    const int before = L - std::min(T, L);
+    const double blocks = static_cast<double>(rest) / BH, rows = std::min(T, 256) / 256.0;
+    const double mean = std::ceil((before + std::min<double>(T, 128 * (blocks + 1))) / 128);
+    const double longest = std::ceil((before + std::min<double>(T, 256 * std::ceil(blocks))) / 128);
     const auto cost = [&](int parts) {
-        return ((static_cast<long long>(rest) * parts + sms - 1) / sms) * (tiles / parts + 5) + (parts > 1 ? 6 + 0.02 * rest * parts : 0);
+        const long long rounds = (static_cast<long long>(rest) * parts + sms - 1) / sms;
+        return rounds * (std::ceil((rounds == 1 ? longest : mean) / parts) + 4) +
+               (parts > 1 ? 1.6 + (0.02 + 0.008 * rows) * rest * parts : 0);
     };
     int best = 1;
     for (int n = 2; n <= kMostParts && rest * n <= 3 * sms; ++n)
@@ -820,8 +854,13 @@ cudaError_t launch(FwdPagedParams &p, const alibi_pages *pages, const void *q, c
                                 decode_pool(), stream);
     if (e != cudaSuccess) return e;
     e = launch_kernel(kern, grid, kThreads, C::kSmem, stream, p);
+    // Of few partials a warp merges four columns, of many its eighth of all (32 x 64 new of 1024 tokens 14.7 us in eighths and 14.1
+    // in fours, 32 x 256 of 32768 112.5 and 116.3).
+    const unsigned rows = std::min(8, (p.T + 31) / 32), slices = static_cast<unsigned>(pages->d + 31) / 32;
+    const bool few = p.rest * rows * slices <= 2u * sms;
     if (e == cudaSuccess)
-        e = launch_kernel(fwd_paged_merge_kernel<D>, dim3(static_cast<unsigned>(p.rest), std::min(8, (p.T + 31) / 32)), 256, 0, stream, p);
+        e = launch_kernel(few ? fwd_paged_merge_kernel<D, 4> : fwd_paged_merge_kernel<D, D / 8>,
+                          dim3(static_cast<unsigned>(p.rest), rows, few ? slices : 1), 256, 0, stream, p);
     const cudaError_t f = cudaFreeAsync(p.part, stream);
     return e != cudaSuccess ? e : f;
 }
