@@ -118,11 +118,13 @@ __device__ __forceinline__ void finish(__nv_bfloat16 *out, float *lse, int d, si
 
 // Merge of the chunks that several shares worked on: CTA (i, r) looks at row r of chunk i. Its partials are slot 1 of the
 // share it began in and slot 0 of the shares up to the one it ends in. The loads of a thread are issued
-// together: with 76 partials the merge waits for three round trips to L2 and not for 76.
+// together: with 76 partials the merge waits for three round trips to L2 and not for 76. At most 64 registers, so that a CTA
+// finds room beside the two of a decode on its SM and waits there for their end: 1 x 4 (x 4) x 131071 tokens over pages 48.2 us (48.8
+// with 8 means at once, 49.1 with 12 and 74 registers), 1 x 1 x 8192 7.2 (7.9), over the 4-bit cache 16.3 (17.0).
 template <int D, int ROWS>
-__global__ void __launch_bounds__(kMergeThreads) split_merge_kernel(const __grid_constant__ MergeParams p)
+__global__ void __launch_bounds__(kMergeThreads, 4) split_merge_kernel(const __grid_constant__ MergeParams p)
 {
-    constexpr int kPart = part_floats(D, ROWS), kItems = D / 4, kGroups = kMergeThreads / kItems, kDepth = 8;
+    constexpr int kPart = part_floats(D, ROWS), kItems = D / 4, kGroups = kMergeThreads / kItems, kDepth = 10;
     __shared__ float weight[kv4::kMostShares];
     __shared__ float red[2][kMergeThreads / 32];
     __shared__ float4 sum[kMergeThreads];
