@@ -443,8 +443,9 @@ ALIBI_API int alibi_paged_append(const alibi_rows *k, const alibi_rows *v, const
  * alibi_fwd_options (NULL: alibi_slopes(H)); with slopes of zero there is no bias.
  * Rows that a query does not see are not used, whatever they hold; a NaN in a key that it sees makes its out and lse NaN.
  * Products are exact in fp32 sums, weights are fp32 numbers (one below 2^-126 of the row's largest counts as zero) and
- * enter the values' products as two bf16 numbers, off by 2^-16 of themselves. out and lse are the same bits for the
- * same arguments. A call takes up to 11 MB of scratch from the library's stream-ordered pool where it splits sequences
+ * enter the values' products as two bf16 numbers, off by 2^-16 of themselves. Those sums are divided by the weights' at
+ * the end: values beyond 2^120 / L in magnitude may overflow them, where 2^96 is safe for every L. out and lse are the same bits
+ * for the same arguments. A call takes up to 11 MB of scratch from the library's stream-ordered pool where it splits sequences
  * over several CTAs and merges them in a second kernel.
  */
 ALIBI_API int alibi_attn_decode_paged(const void *q, const alibi_pages *pages, const int *lens, void *out, float *lse, int B,
@@ -458,7 +459,8 @@ ALIBI_API int alibi_attn_decode_paged(const void *q, const alibi_pages *pages, c
  * query with i < 0 sees no row: its out is 0 and its lse -inf. A sequence with count[b] outside [0, T] or lens[b]
  * outside [0, L] gets NaN in out and lse (of all T tokens where count[b] is at fault), one with a page number outside
  * [0, pages) in the blocks of 256 queries that read it, and alibi_check_error returns ALIBI_ERR_RANGE.
- * Runs the tensor-core pipeline of alibi_attn_fwd (weights are rounded to bf16 for the P V product). Rows that a
+ * Runs the tensor-core pipeline of alibi_attn_fwd (weights are rounded to bf16 for the P V product; values as large as in
+ * alibi_attn_decode_paged). Rows that a
  * query does not see are not used, whatever they hold; a value that is not finite makes its element of out NaN (or,
  * in tiles of 128 rows that all of the 256 queries see, infinite) for the queries that see it; a call that meets one takes
  * up to twice as long. out and lse are the same bits for the same arguments. A call takes up to 61 MB of scratch from the

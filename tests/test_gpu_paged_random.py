@@ -128,3 +128,20 @@ def test_first_calls_of_a_process_in_a_graph(shape):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", FIRST_CALL.format(shape)], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("power", [-95, -40, 60, 96])
+def test_magnitudes_of_values(ab, power):
+    # out is linear in the values: with them times a power of two it is that power times the same bits
+    import torch
+    for B, Hkv, G, N, d in ((1, 2, 2, 700, 128), (1, 1, 4, 20000, 64), (2, 8, 1, 4100, 128)):
+        q, k, v = decode.case(N, B, Hkv, G, 1, N, d)
+        qd, (kp, vp, table) = decode.bf16(q)[1], ref.paged(k, v, [N] * B, 16)
+        big = torch.ldexp(vp, torch.tensor(power, device="cuda")).to(torch.bfloat16)
+        for call, x in ((ab.alibi_attn_decode_paged, qd), (ab.alibi_attn_fwd_paged, qd.expand(-1, -1, 5, -1).contiguous())):
+            (a, la), (b, lb) = call(x, kp, vp, table, L=N), call(x, kp, big, table, L=N)
+            ab.alibi_check_error()
+            assert torch.equal(la, lb) and bool(torch.isfinite(b).all())
+            # bf16 and fp32 numbers this far from their ends scale exactly, but for the smallest elements of `out`
+            want = torch.ldexp(a.float(), torch.tensor(power, device="cuda"))
+            assert torch.allclose(b.float(), want, rtol=2.0 ** -8, atol=2.0 ** (power - 20)), (power, N)
