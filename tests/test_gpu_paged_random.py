@@ -145,3 +145,27 @@ def test_magnitudes_of_values(ab, power):
             # bf16 and fp32 numbers this far from their ends scale exactly, but for the smallest elements of `out`
             want = torch.ldexp(a.float(), torch.tensor(power, device="cuda"))
             assert torch.allclose(b.float(), want, rtol=2.0 ** -8, atol=2.0 ** (power - 20)), (power, N)
+
+
+def test_two_graphs_of_prefills_in_parts_at_once(ab):
+    # captured prefills whose items are cut into parts, replayed at the same time, each in its own scratch
+    import torch
+    jobs = []
+    for s in range(2):
+        q, k, v = decode.case(30 + s, 1, 2, 2, 40, 9000 + 77 * s, 64)
+        n = k.shape[2]
+        args = (decode.bf16(q)[1], *ref.paged(k, v, [n], 64, seed=s))
+        want = ab.alibi_attn_fwd_paged(*args, lens=ints([n]))
+        torch.cuda.synchronize()
+        g, stream, lens = torch.cuda.CUDAGraph(), torch.cuda.Stream(), ints([n])
+        with torch.cuda.graph(g, stream=stream):
+            got = ab.alibi_attn_fwd_paged(*args, lens=lens)
+        jobs.append((g, stream, got, want, args, lens))
+    for _ in range(20):
+        for g, stream, *_ in jobs:
+            with torch.cuda.stream(stream):
+                g.replay()
+    torch.cuda.synchronize()
+    ab.alibi_check_error()
+    for _, _, got, want, _, _ in jobs:
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
