@@ -26,6 +26,10 @@
 //             maximum and sum in scratch, and a second kernel merges them. (Equal shares of all items' tiles for every CTA, as the
 //             decode has them, took longer than whole items: a CTA with many short items is late, whatever their tiles.)
 //
+// Of up to 128 tokens the rows of the G heads of a group may go together, as one head with G T rows of which each has its own
+// slope and token (`together` below): they pass the group's keys once and fill the tiles (64 x 8 (x 8) heads x 17 new of 2048 tokens
+// 648 -> 139 us).
+//
 // Where some head is steep (a slope above 4 / log2(e)), the bias is taken element by element from the whole distance: the
 // column part on the tensor core and the row part would cancel with a rounding of 2^-24 of 128 slopes.
 //
@@ -64,12 +68,14 @@ struct FwdPagedParams {
     __nv_bfloat16 *out;
     float *lse;
     uint32_t *err;
-    int T, L, BH, H, num_items, blocks;  // blocks of 256 rows of a head
+    int T, L, BH, H, num_items, blocks;  // blocks of 256 rows of a head; together: BH and H count KV heads
+    int rows, G;                         // rows of a head: T, together G T
     int whole, rest, parts;              // items that are not cut, those after them, parts of each of these
     int num_units;                       // whole + rest parts
     Divisor div_rest;
     float *part;                         // [rest][parts] partials
-    Divisor div_bh, div_h, div_g;        // by B H, H and H / H_kv
+    Divisor div_bh, div_h, div_g;        // by B H, H and H / H_kv (together 1)
+    Divisor div_t;                       // by T
     float c1;                            // log2(e) / sqrt(d)
     float slope[kMaxQueryHeads];         // m log2(e)
 };
@@ -94,7 +100,9 @@ struct PagedItem {
 };
 
 // Item idx, or false where its sequence has no rows there. Longest first: round r holds block blocks - 1 - r of every head.
-// careful: n_fix is the tiles that some row does not see whole; else the one that the sequence ends in.
+// careful: n_fix is the tiles that some row does not see whole; else the one that the sequence ends in. TOGETHER: the rows are those
+// of all heads of a KV head, T of each, which all end in the newest tiles.
+template <bool TOGETHER>
 __device__ __forceinline__ bool paged_item(const FwdPagedParams &p, int idx, bool careful, PagedItem &t)
 {
     const int round = p.div_bh.of(idx);
@@ -108,8 +116,17 @@ __device__ __forceinline__ bool paged_item(const FwdPagedParams &p, int idx, boo
         t.len = 0;
         if (t.count < 0 || t.count > p.T) t.count = p.T;
     }
-    if (256 * t.qb >= t.count) return false;
+    if (TOGETHER ? t.count == 0 : 256 * t.qb >= t.count) return false;
     t.first = t.len - t.count;
+    if constexpr (TOGETHER) {
+        t.q1valid = 256 * t.qb + BM < p.rows;
+        t.top = max(0, t.len - 1) >> 7;
+        t.n = t.top + 1;
+        t.n_fix = careful ? max(1, t.top + 1 - ((max(t.first, 0) + 1) >> 7)) : (t.top + 1) * BN > t.len ? 1 : 0;
+        t.first0 = 0;
+        t.part = -1;
+        return true;
+    }
     t.q1valid = 256 * t.qb + BM < t.count;
     const int i0 = t.first + 256 * t.qb;  // position of the item's first row
     const int top0 = max(0, min(i0 + BM - 1, t.len - 1)) >> 7, top1 = max(0, min(i0 + 2 * BM - 1, t.len - 1)) >> 7;
@@ -128,7 +145,18 @@ __device__ __forceinline__ int part_begin(int n, int q, int parts)
     return c == 1 && n > 1 ? 0 : c;
 }
 
+// Token of a row of an item, and its head's place in the group.
+template <bool TOGETHER>
+__device__ __forceinline__ int token_of(const FwdPagedParams &p, int row, int &head)
+{
+    if constexpr (!TOGETHER) return row;
+    row = min(row, p.rows - 1);
+    head = p.div_t.of(row);
+    return row - head * p.T;
+}
+
 // The items of a CTA, or its parts of items, one after another.
+template <bool TOGETHER>
 struct PagedWalk {
     int k = 0;
 
@@ -139,7 +167,7 @@ struct PagedWalk {
             if (unit >= p.num_units) return false;
             ++k;
             const int q = unit < p.whole ? 0 : p.div_rest.of(unit - p.whole), i = unit - q * p.rest;  // part, item
-            if (!paged_item(p, i, careful, t)) continue;
+            if (!paged_item<TOGETHER>(p, i, careful, t)) continue;
             if (unit < p.whole) return true;
             const int a = part_begin(t.n, q, p.parts), b = part_begin(t.n, q + 1, p.parts);
             if (a == b) continue;
@@ -203,10 +231,12 @@ __device__ __forceinline__ bool again(uint64_t *met, const int *progress, const 
     return __all_sync(0xffffffffu, wait_idle(met, 0, progress, err, SITE_PG_AGAIN)) && *reinterpret_cast<const volatile int *>(redo) != 0;
 }
 
-template <int D, bool STEEP>
+template <int D, bool STEEP, bool TOGETHER>
 __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_constant__ FwdPagedParams p)
 {
     using C = Cfg<D>;
+    using PagedWalk = PagedWalk<TOGETHER>;
+    static_assert(STEEP || !TOGETHER, "rows of several heads have no column part in common");
     extern __shared__ uint8_t smem_raw[];
     // of the items in flight, two at most: the first row of each column of V that is not finite, whether there is one, and
     // whether a page number is none
@@ -546,8 +576,10 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
                 }
                 __syncwarp();
                 if (s == 1 && !t.q1valid) continue;
-                di = static_cast<float>(t.first + row0 + lane - (t.top - it0) * BN);  // exact: below 2^24
-                sl2 = p.slope[p.div_h.rest(t.bh)];
+                int head = 0;
+                const int token = token_of<TOGETHER>(p, row0 + lane, head);
+                di = static_cast<float>(t.first + token - (t.top - it0) * BN);  // exact: below 2^24
+                sl2 = p.slope[TOGETHER ? p.div_h.rest(t.bh) * p.G + head : p.div_h.rest(t.bh)];
                 left = t.n - it0;
             }
             float M = 0.f, l = 0.f;
@@ -647,18 +679,21 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
             if (bad && quad == 0 && lane == 0) atomicOr(err, ALIBI_DEV_RANGE);
             const float inv_l = bad ? nan : l == 0.f ? 0.f : 1.0f / l;
             const bool odd = pass != 0 && *(volatile int *)&odd_any[buf] != 0;
-            const bool valid = row0 + lane < count;
-            const int i = st.first + row0 + lane;  // position
+            int head = 0;
+            const int token = token_of<TOGETHER>(p, row0 + lane, head);
+            const bool valid = token < count && (!TOGETHER || row0 + lane < p.rows);
+            const int i = st.first + token;  // position
             const int dr = D == 64 ? p.pg.d : D;
             // O / l goes out through a per-warp staging box and bulk tensor stores, so that the warp does not wait for its
             // stores before its next tile; of a box that reaches past the sequence's rows each lane stores its own row.
-            const bool box = row0 + 32 <= count, whole = st.part < 0;
+            const bool box = TOGETHER ? __all_sync(0xffffffffu, valid) : row0 + 32 <= count, whole = st.part < 0;
+            const bool none = TOGETHER ? !__any_sync(0xffffffffu, valid) : row0 >= count;
             float *part = whole ? nullptr : p.part + static_cast<size_t>(st.part) * paged_part_floats(D) + s * BM + r;
             float finite = 0.f;  // or NaN
             uint8_t *stg = smem + C::kStage + (warp - 4) * 2048;
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
-                if (c * 32 >= dr || row0 >= count) break;
+                if (c * 32 >= dr || none) break;
                 uint32_t o[32];
                 tmem_ld32(lane_addr + 256 + s * 128 + c * 32, o);
                 tmem_wait_ld();
@@ -688,7 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
                         bulk_commit();
                     }
                 } else if (valid) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(p.out + (static_cast<size_t>(bh) * p.T + row0 + lane) * dr + c * 32);
+                    uint4 *dst = reinterpret_cast<uint4 *>(p.out + (static_cast<size_t>(bh) * p.rows + row0 + lane) * dr + c * 32);
 #pragma unroll
                     for (int u = 0; u < 4; ++u)
                         if (c * 32 + 8 * u < dr) dst[u] = make_uint4(y[4 * u], y[4 * u + 1], y[4 * u + 2], y[4 * u + 3]);
@@ -701,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
                 for (int e = 0; e < dr; ++e) {
                     if (!valid || i < odd_from[buf][e]) continue;
                     if (whole)
-                        p.out[(static_cast<size_t>(bh) * p.T + row0 + lane) * dr + e] = __ushort_as_bfloat16(0x7fffu);
+                        p.out[(static_cast<size_t>(bh) * p.rows + row0 + lane) * dr + e] = __ushort_as_bfloat16(0x7fffu);
                     else
                         part[e * 2 * BM] = nan;
                 }
@@ -716,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
                 continue;
             }
             if (valid && p.lse)
-                p.lse[static_cast<size_t>(bh) * p.T + row0 + lane] =
+                p.lse[static_cast<size_t>(bh) * p.rows + row0 + lane] =
                     bad ? nan : l == 0.f ? -INFINITY : (M + __log2f(l)) * 0.69314718055994531f;
         }
     }
@@ -734,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
 // parts are asked for at once as 64 registers hold (one part after another: 2 x 6 heads x 100 new of 999 tokens 16.1 us and not
 // 15.0). The weights l 2^(M - max M) are normalised before they meet the means, so nothing overflows; a part that the row sees
 // nothing of has l = 0 and means that do not count.
-template <int D, int COLS>
+template <int D, int COLS, bool TOGETHER>
 __global__ void __launch_bounds__(256) fwd_paged_merge_kernel(const __grid_constant__ FwdPagedParams p)
 {
     constexpr int kPart = paged_part_floats(D), kRows = 2 * BM, kBatch = 64 / COLS;
@@ -742,9 +777,13 @@ __global__ void __launch_bounds__(256) fwd_paged_merge_kernel(const __grid_const
     __shared__ __align__(16) __nv_bfloat16 rows[32][8 * COLS + 8];
     griddep_wait();
     PagedItem t;
-    if (!paged_item(p, p.whole + blockIdx.x, false, t)) return;
+    if (!paged_item<TOGETHER>(p, p.whole + blockIdx.x, false, t)) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row0 = 256 * t.qb + 32 * static_cast<int>(blockIdx.y);
-    if (row0 >= t.count) return;
+    if (row0 >= (TOGETHER ? p.rows : t.count)) return;
+    const auto valid = [&](int row) {
+        int head;
+        return token_of<TOGETHER>(p, row, head) < t.count && (!TOGETHER || row < p.rows);
+    };
     const int col0 = 8 * COLS * static_cast<int>(blockIdx.z);
     const float *part = p.part + static_cast<size_t>(blockIdx.x) * p.parts * kPart + 32 * blockIdx.y + lane;
     // the parts that have tiles
@@ -752,6 +791,7 @@ __global__ void __launch_bounds__(256) fwd_paged_merge_kernel(const __grid_const
         0xffffffffu, lane < p.parts && part_begin(t.n, lane, p.parts) < part_begin(t.n, lane + 1, p.parts));
     const auto in = [&](int q) { return (some >> q & 1) != 0; };
     float M[kMostParts], l[kMostParts], x[kBatch][COLS], top = -INFINITY, sum = 0.f, o[COLS] = {};
+    uint32_t seen = 0;  // parts that the row sees something of: a NaN among their means stays one whatever its weight
     const auto load = [&](int q0) {
 #pragma unroll
         for (int q = 0; q < kBatch; ++q)
@@ -766,7 +806,7 @@ __global__ void __launch_bounds__(256) fwd_paged_merge_kernel(const __grid_const
     load(0);
 #pragma unroll
     for (int q = 0; q < kMostParts; ++q)
-        if (l[q] != 0.f) top = fmaxf(top, M[q]);
+        if (l[q] != 0.f) top = fmaxf(top, M[q]), seen |= 1u << q;
 #pragma unroll
     for (int q = 0; q < kMostParts; ++q) {
         if (l[q] != 0.f) l[q] *= ex2_approx(M[q] - top);
@@ -780,18 +820,18 @@ __global__ void __launch_bounds__(256) fwd_paged_merge_kernel(const __grid_const
 #pragma unroll
         for (int q = 0; q < kBatch; ++q)
 #pragma unroll
-            for (int c = 0; c < COLS; ++c) o[c] = l[q0 + q] == 0.f ? o[c] : fmaf(x[q][c], l[q0 + q] * inv, o[c]);
+            for (int c = 0; c < COLS; ++c) o[c] = seen >> (q0 + q) & 1 ? fmaf(x[q][c], l[q0 + q] * inv, o[c]) : o[c];
     }
 #pragma unroll
     for (int c = 0; c < COLS; c += 2) *reinterpret_cast<uint32_t *>(&rows[lane][COLS * warp + c]) = pack_bf16x2(o[c], o[c + 1]);
-    if (warp == 0 && col0 == 0 && p.lse && row0 + lane < t.count)
-        p.lse[static_cast<size_t>(t.bh) * p.T + row0 + lane] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+    if (warp == 0 && col0 == 0 && p.lse && valid(row0 + lane))
+        p.lse[static_cast<size_t>(t.bh) * p.rows + row0 + lane] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
     __syncthreads();
     const int d = p.pg.d;
     for (int i = threadIdx.x; i < 32 * COLS; i += 256) {  // pieces of 8 elements
         const int r = i / COLS, c = i % COLS * 8;
-        if (row0 + r < t.count && col0 + c < d)
-            *reinterpret_cast<uint4 *>(p.out + (static_cast<size_t>(t.bh) * p.T + row0 + r) * d + col0 + c) =
+        if (valid(row0 + r) && col0 + c < d)
+            *reinterpret_cast<uint4 *>(p.out + (static_cast<size_t>(t.bh) * p.rows + row0 + r) * d + col0 + c) =
                 *reinterpret_cast<const uint4 *>(&rows[r][c]);
     }
 }
@@ -810,10 +850,14 @@ __global__ void __launch_bounds__(256) fwd_paged_merge_kernel(const __grid_const
 //   32 x 2048 of 32768           [4]  794 / 799 / 803 / 722 /  -  /  -
 //   16 x 700 of 700              [1]  20.4 / 20.7 / 19.4 / 24.8 / 25.5 / 23.7
 //   16 x 2048 of 2048            [1]  35.6 / 47.7 / 50.3 /  -  /  -  /  -
-int paged_parts(int rest, int BH, int T, int L, int sms)
+struct Parts {
+    int parts;
+    double cost;  // of the last round
+};
+Parts paged_parts(int rest, int BH, int T, int head_rows, int L, int sms)  // head_rows: T, together G T
 {
     const int before = L - std::min(T, L);
-    const double blocks = static_cast<double>(rest) / BH, rows = std::min(T, 256) / 256.0;
+    const double blocks = static_cast<double>(rest) / BH, rows = std::min(head_rows, 256) / 256.0;
     const double mean = std::ceil((before + std::min<double>(T, 128 * (blocks + 1))) / 128);
     const double longest = std::ceil((before + std::min<double>(T, 256 * std::ceil(blocks))) / 128);
     const auto cost = [&](int parts) {
@@ -821,29 +865,52 @@ int paged_parts(int rest, int BH, int T, int L, int sms)
         return rounds * (std::ceil((rounds == 1 ? longest : mean) / parts) + 4) +
                (parts > 1 ? 1.6 + (0.02 + 0.008 * rows) * rest * parts : 0);
     };
-    int best = 1;
+    Parts best = {1, rest > 0 ? cost(1) : 0};
     for (int n = 2; n <= kMostParts && rest * n <= 3 * sms; ++n)
-        if (cost(n) < cost(best)) best = n;
+        if (rest > 0 && cost(n) < best.cost) best = {n, cost(n)};
     return best;
 }
 
-template <int D>
+// Whether the rows of the heads of a group go together: of few tokens a query tile of 128 rows has room for those of several heads,
+// which then pass the keys once, at the price of a bias that is computed element by element from the whole distance
+// (1.25). Of up to 128 tokens, so that the rows of a block read the same pages either way. Measured, in us, apart / together, what is
+// taken in brackets (heads (x G) x new tokens of length, d = 128):
+//   8 x 8 (x 4) x 32 of 2048    [t]  54.8 / 28.2       8 x 8 (x 8) x 64 of 2048    [t]  97.1 / 42.7
+//   8 x 8 (x 8) x 20 of 8192    [t]  312 / 78.3        64 x 8 (x 8) x 17 of 2048   [t]  648 / 139
+//   32 x 8 (x 4) x 48 of 1000   [t]  106 / 48.5        1 x 8 (x 4) x 32 of 32768   [t]  95.5 / 41.6
+//   16 x 4 (x 2) x 64 of 4096   [t]  51.3 / 41.8       16 x 8 (x 2) x 100 of 2048  [t]  55.1 / 42.4
+//   1 x 8 (x 4) x 128 of 8192   [t]  34.0 / 31.4       4 x 8 (x 4) x 128 of 4096   [t]  51.9 / 49.6
+//   1 x 8 (x 4) x 64 of 1024    [a]  14.1 / 15.8       2 x 2 (x 3) x 128 of 700    [a]  16.3 / 17.8
+bool together(const FwdPagedParams &p, int Hkv, int sms)
+{
+    const int G = p.H / Hkv, rows = G * p.T;
+    if (G == 1 || p.T > BM) return false;
+    const double tiles = std::ceil(p.L / 128.0);
+    const auto cost = [&](int items, int head_rows) {
+        return static_cast<double>(items / sms) * (tiles + 4) + paged_parts(items % sms, items, p.T, head_rows, p.L, sms).cost;
+    };
+    return 1.25 * cost(p.BH / G * ((rows + 255) / 256), rows) < cost(p.BH, p.T);
+}
+
+template <int D, bool TOGETHER>
 cudaError_t launch(FwdPagedParams &p, const alibi_pages *pages, const void *q, cudaStream_t stream)
 {
     using C = Cfg<D>;
     const uint64_t d = static_cast<uint64_t>(pages->d);
     const uint32_t box = static_cast<uint32_t>(std::min(pages->slots, BN));
-    if (!encode_tmap_bf16_3d(&p.tq, q, d, p.T, p.BH, 64, BM) || !encode_tmap_bf16_3d(&p.tout, p.out, d, p.T, p.BH, 32, 32, false) ||
+    if (!encode_tmap_bf16_3d(&p.tq, q, d, p.rows, p.BH, 64, BM) || !encode_tmap_bf16_3d(&p.tout, p.out, d, p.rows, p.BH, 32, 32, false) ||
         !encode_pages(&p.tk, &p.tv, pages, 64, box, box == static_cast<uint32_t>(BN)))
         return cudaErrorInvalidValue;
-    const bool steep = *std::max_element(p.slope, p.slope + p.H) > kSteep;
-    const auto kern = steep ? &fwd_paged_kernel<D, true> : &fwd_paged_kernel<D, false>;
+    const auto kern = [&] {
+        if constexpr (TOGETHER) return &fwd_paged_kernel<D, true, true>;
+        else return *std::max_element(p.slope, p.slope + p.H) > kSteep ? &fwd_paged_kernel<D, true, false> : &fwd_paged_kernel<D, false, false>;
+    }();
     cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(kern), C::kSmem, kLaunchRegs);
     if (e != cudaSuccess) return e;
     const int sms = num_sms();
     p.rest = p.num_items % sms;
     p.whole = p.num_items - p.rest;
-    p.parts = p.rest ? paged_parts(p.rest, p.BH, p.T, p.L, sms) : 1;
+    p.parts = paged_parts(p.rest, p.BH, p.T, p.rows, p.L, sms).parts;
     if (p.parts == 1) p.whole = p.num_items, p.rest = 0;
     p.num_units = p.whole + p.rest * p.parts;
     p.div_rest = Divisor(static_cast<uint32_t>(std::max(p.rest, 1)));
@@ -856,10 +923,10 @@ cudaError_t launch(FwdPagedParams &p, const alibi_pages *pages, const void *q, c
     e = launch_kernel(kern, grid, kThreads, C::kSmem, stream, p);
     // Of few partials a warp merges four columns, of many its eighth of all (32 x 64 new of 1024 tokens 14.7 us in eighths and 14.1
     // in fours, 32 x 256 of 32768 112.5 and 116.3).
-    const unsigned rows = std::min(8, (p.T + 31) / 32), slices = static_cast<unsigned>(pages->d + 31) / 32;
+    const unsigned rows = std::min(8, (p.rows + 31) / 32), slices = static_cast<unsigned>(pages->d + 31) / 32;
     const bool few = p.rest * rows * slices <= 2u * sms;
     if (e == cudaSuccess)
-        e = launch_kernel(few ? fwd_paged_merge_kernel<D, 4> : fwd_paged_merge_kernel<D, D / 8>,
+        e = launch_kernel(few ? fwd_paged_merge_kernel<D, 4, TOGETHER> : fwd_paged_merge_kernel<D, D / 8, TOGETHER>,
                           dim3(static_cast<unsigned>(p.rest), rows, few ? slices : 1), 256, 0, stream, p);
     const cudaError_t f = cudaFreeAsync(p.part, stream);
     return e != cudaSuccess ? e : f;
@@ -905,13 +972,24 @@ extern "C" int alibi_attn_fwd_paged(const void *q, const alibi_pages *pages, con
     p.L = L;
     p.BH = B * H;
     p.H = H;
+    p.rows = T;
+    p.G = H / pages->heads;
     p.blocks = blocks;
-    p.num_items = p.BH * blocks;
+    const bool join = together(p, pages->heads, num_sms());
+    if (join) {
+        p.BH = B * pages->heads;
+        p.H = pages->heads;
+        p.rows = p.G * T;
+        p.blocks = (p.rows + 255) / 256;
+    }
+    p.num_items = p.BH * p.blocks;
     p.div_bh = Divisor(static_cast<uint32_t>(p.BH));
-    p.div_h = Divisor(static_cast<uint32_t>(H));
-    p.div_g = Divisor(static_cast<uint32_t>(H / pages->heads));
+    p.div_h = Divisor(static_cast<uint32_t>(p.H));
+    p.div_g = Divisor(static_cast<uint32_t>(p.H / pages->heads));
+    p.div_t = Divisor(static_cast<uint32_t>(T));
     p.c1 = 1.4426950408889634f / sqrtf(static_cast<float>(pages->d));
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = pages->d == 128 ? launch<128>(p, pages, q, cs) : launch<64>(p, pages, q, cs);
+    const cudaError_t e = pages->d == 128 ? (join ? launch<128, true>(p, pages, q, cs) : launch<128, false>(p, pages, q, cs))
+                                          : (join ? launch<64, true>(p, pages, q, cs) : launch<64, false>(p, pages, q, cs));
     return e == cudaSuccess ? ALIBI_OK : ALIBI_ERR_CUDA;
 }

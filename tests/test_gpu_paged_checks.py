@@ -23,6 +23,8 @@ SWEEPS = [
     "test_gpu_fwd_paged.py::test_shapes",
     "test_gpu_fwd_paged.py::test_shared_items",
     "test_gpu_fwd_paged.py::test_infinite_and_nan_rows_that_a_query_does_not_see",
+    "test_gpu_fwd_paged_together.py::test_shapes",
+    "test_gpu_fwd_paged_together.py::test_infinite_and_nan_rows",
 ]
 
 
