@@ -3,9 +3,9 @@
 // Token t < count_b of sequence b has position n = pos_b + t and goes to slot n % S of page table[b, n / S]. A rotation turns
 // each pair (x, y) of elements, of frequency f_i, by the angle n f_i:
 //   x' = x cos - y sin,  y' = y cos + x sin,
-// in fp32, rounded once. The angle is reduced exactly: f_i / 2 pi is held as a 64-bit fraction of a turn, and
-// n times it modulo 2^64 is the fraction of a turn that is left, off by n 2^-53 of f_i / 2 pi; its upper 32 bits go to
-// sincospi. (In fp32 the angle of position 100000 would be off by 0.004.)
+// in fp32, rounded once. The angle is reduced exactly: f_i / 2 pi is held as a 64-bit fraction of a turn (turns.h), and
+// n times it modulo 2^64 is the fraction of a turn that is left, off by 2^-39 at most; its upper 32 bits go, as a float of half
+// turns (off by 2^-26 of a turn), to sincospi. (In fp32 the angle of position 100000 would be off by 0.004.)
 //
 // What has to move: 2 bytes in and 2 bytes out of each element. A thread takes 16 bytes of a row; rows of consecutive tokens
 // of one head follow one another, and a thread keeps its token from head to head, so that the page is looked up and the
@@ -24,6 +24,7 @@
 #include "divide.h"
 #include "pages.cuh"
 #include "ptx.cuh"
+#include "turns.h"
 
 namespace alibi {
 namespace {
@@ -219,8 +220,7 @@ extern "C" int alibi_paged_append(const alibi_rows *k, const alibi_rows *v, cons
     for (int i = 0; i < R / 2; ++i) {
         const double f = rotation->freqs ? rotation->freqs[i] : std::pow(rotation->base, -2.0 * i / R);
         if (!std::isfinite(f) || std::fabs(f) > 1e6) return ALIBI_ERR_INVALID;
-        const double turns = f / 6.283185307179586476925;
-        p.turn[i] = static_cast<uint64_t>(std::ldexp(turns - std::floor(turns), 63)) << 1;
+        p.turn[i] = turns_of(f);
     }
     p.k = rows_of(k);
     p.v = rows_of(v);

@@ -423,7 +423,7 @@ typedef struct alibi_rotation {
  * as they were. A sequence with pos[b] < 0, count[b] < 0, count[b] > T or pos[b] + count[b] > width slots is left
  * out whole, a token whose page number is outside [0, pages) is not written, and alibi_check_error returns ALIBI_ERR_RANGE.
  * Two tokens of one call that go to the same slot race. The angle is reduced exactly: it is off by less than
- * 2^-22 rad at every position.
+ * 2^-22 rad at every position and every frequency.
  */
 ALIBI_API int alibi_paged_append(const alibi_rows *k, const alibi_rows *v, const alibi_pages *pages, const int *pos,
                                  const int *count, int B, int T, const alibi_rotation *rotation, const alibi_rows *q,
