@@ -78,6 +78,14 @@ struct FwdPagedParams {
     Divisor div_t;                       // by T
     float c1;                            // log2(e) / sqrt(d)
     float slope[kMaxQueryHeads];         // m log2(e)
+    uint64_t wait_ns;                    // limit of every bounded wait (the self-test's kernel; the others have kWaitLimitNs)
+    int hold;                            // the self-test's barrier (HOLD_...), -1: none
+};
+
+// Barriers that the self-test of the failure path (the plain steep kernels carry it) makes wait for an arrival that nobody makes.
+enum : int {
+    HOLD_Q_FULL, HOLD_UNIT_FULL, HOLD_UNIT_EMPTY, HOLD_S_FULL, HOLD_P_FULL, HOLD_O_FULL, HOLD_O_EMPTY, HOLD_V_LANDED, HOLD_MET,
+    HOLD_COUNT,
 };
 
 enum : uint32_t {
@@ -266,24 +274,25 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
     uint32_t *err = p.err;
 
     if (threadIdx.x == 0) {
-        cta_err_init(kWaitLimitNs);
+        const auto held = [&](int barrier) -> uint32_t { return STEEP && !TOGETHER && p.hold == barrier; };
+        cta_err_init(STEEP && !TOGETHER ? p.wait_ns : kWaitLimitNs);
         cta_check_init(p.err, smem_raw, C::kSmem);
         redo = progress = 0;
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&unit_full[s], 1);
-            mbar_init(&unit_empty[s], 1);
-            mbar_init(&s_full[s], 1);
-            mbar_init(&p_full[s], 4);  // one arrival per softmax warp
+            mbar_init(&unit_full[s], 1 + (s == 0 ? held(HOLD_UNIT_FULL) : 0));
+            mbar_init(&unit_empty[s], 1 + (s == 1 ? held(HOLD_UNIT_EMPTY) : 0));
+            mbar_init(&s_full[s], 1 + held(HOLD_S_FULL));
+            mbar_init(&p_full[s], 4 + held(HOLD_P_FULL));  // one arrival per softmax warp
             mbar_init(&p_hi[s], 4);
-            mbar_init(&o_full[s], 1);
-            mbar_init(&o_empty[s], 4);
+            mbar_init(&o_full[s], 1 + held(HOLD_O_FULL));
+            mbar_init(&o_empty[s], 4 + held(HOLD_O_EMPTY));
         }
         mbar_init(q_empty, 1);
-        mbar_init(q_full, 1);
+        mbar_init(q_full, 1 + held(HOLD_Q_FULL));
         mbar_init(bias_full, 1);
-        mbar_init(v_landed, 1);
+        mbar_init(v_landed, 1 + held(HOLD_V_LANDED));
         mbar_init(mma_done, 1);
-        mbar_init(met, 10);  // of the loading, the issuing and the softmax warps
+        mbar_init(met, 10 + held(HOLD_MET));  // of the loading, the issuing and the softmax warps
         fence_mbar_init();
         tma_prefetch_desc(&p.tq);
         tma_prefetch_desc(&p.tk);
@@ -314,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
         const int copies = boxes == 1 ? 1 : C::kChunks;
         uint32_t uc = 0;  // ring units issued
         int kk = 0;       // items begun
-        uint32_t looked = 0;
+        uint32_t looked = 0;  // tiles of V asked for by v_landed: the last may be in flight where the item ends early
         bool ok = true;
         PagedWalk walk;
         for (int pass = 0; ok;) {
@@ -354,8 +363,10 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
                 const int ahead = page_at(t.top - u - 1);
                 ok = __all_sync(0xffffffffu, mbar_wait(&unit_empty[st], ph ^ 1, err, SITE_PG_UNIT));
                 if (!ok) break;
+                const bool to_look = with_k0 || (look && u > 1);  // a V goes out by v_landed
+                looked += to_look;
                 if (lane == 0) {
-                    if (with_k0 || (look && u > 1)) mbar_arrive_expect_tx(v_landed, C::kTileBytes);
+                    if (to_look) mbar_arrive_expect_tx(v_landed, C::kTileBytes);
                     if (look) {
                         if (u < t.n) mbar_expect_tx(&unit_full[st], C::kTileBytes);
                     } else {
@@ -388,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
                     if (lane == 0) mbar_arrive(bias_full);
                 }
                 if (look) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(v_landed, looked++ & 1, err, SITE_PG_FIX));
+                    ok = __all_sync(0xffffffffu, mbar_wait(v_landed, (looked - 1) & 1, err, SITE_PG_FIX));
                     constexpr int kPieces = D / 8;  // of 16 bytes of a row
                     const int row0 = (t.top - u + 1) * BN;
                     // in a first pass the slots past the length, in a second one all
@@ -903,7 +914,7 @@ cudaError_t launch(FwdPagedParams &p, const alibi_pages *pages, const void *q, c
         return cudaErrorInvalidValue;
     const auto kern = [&] {
         if constexpr (TOGETHER) return &fwd_paged_kernel<D, true, true>;
-        else return *std::max_element(p.slope, p.slope + p.H) > kSteep ? &fwd_paged_kernel<D, true, false> : &fwd_paged_kernel<D, false, false>;
+        else return p.hold >= 0 || *std::max_element(p.slope, p.slope + p.H) > kSteep ? &fwd_paged_kernel<D, true, false> : &fwd_paged_kernel<D, false, false>;
     }();
     cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(kern), C::kSmem, kLaunchRegs);
     if (e != cudaSuccess) return e;
@@ -934,13 +945,9 @@ cudaError_t launch(FwdPagedParams &p, const alibi_pages *pages, const void *q, c
 
 bool aligned(const void *p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-}  // namespace
-}  // namespace alibi
-
-using namespace alibi;
-
-extern "C" int alibi_attn_fwd_paged(const void *q, const alibi_pages *pages, const int *lens, const int *count, void *out,
-                                    float *lse, int B, int H, int T, int L, const float *slopes, void *stream)
+// hold, wait_ns: of the self-test, else -1 and the usual limit
+int fwd_paged(const void *q, const alibi_pages *pages, const int *lens, const int *count, void *out, float *lse, int B, int H, int T,
+              int L, const float *slopes, void *stream, int hold, uint64_t wait_ns)
 {
     const int st = check_pages(pages);
     if (st != ALIBI_OK) return st;
@@ -975,7 +982,9 @@ extern "C" int alibi_attn_fwd_paged(const void *q, const alibi_pages *pages, con
     p.rows = T;
     p.G = H / pages->heads;
     p.blocks = blocks;
-    const bool join = together(p, pages->heads, num_sms());
+    p.hold = hold;
+    p.wait_ns = wait_ns;
+    const bool join = hold < 0 && together(p, pages->heads, num_sms());
     if (join) {
         p.BH = B * pages->heads;
         p.H = pages->heads;
@@ -992,4 +1001,22 @@ extern "C" int alibi_attn_fwd_paged(const void *q, const alibi_pages *pages, con
     const cudaError_t e = pages->d == 128 ? (join ? launch<128, true>(p, pages, q, cs) : launch<128, false>(p, pages, q, cs))
                                           : (join ? launch<64, true>(p, pages, q, cs) : launch<64, false>(p, pages, q, cs));
     return e == cudaSuccess ? ALIBI_OK : ALIBI_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace alibi
+
+using namespace alibi;
+
+extern "C" int alibi_attn_fwd_paged(const void *q, const alibi_pages *pages, const int *lens, const int *count, void *out,
+                                    float *lse, int B, int H, int T, int L, const float *slopes, void *stream)
+{
+    return fwd_paged(q, pages, lens, count, out, lse, B, H, T, L, slopes, stream, -1, kWaitLimitNs);
+}
+
+extern "C" int alibi_selftest_fwd_paged_timeout(const void *q, const alibi_pages *pages, const int *lens, const int *count, void *out,
+                                                float *lse, int B, int H, int T, int L, int barrier, int wait_us, void *stream)
+{
+    if (barrier < 0 || barrier >= HOLD_COUNT || wait_us < 1 || wait_us > 1000000) return ALIBI_ERR_INVALID;
+    return fwd_paged(q, pages, lens, count, out, lse, B, H, T, L, nullptr, stream, barrier, static_cast<uint64_t>(wait_us) * 1000u);
 }
