@@ -239,6 +239,31 @@ __device__ __forceinline__ bool again(uint64_t *met, const int *progress, const 
     return __all_sync(0xffffffffu, wait_idle(met, 0, progress, err, SITE_PG_AGAIN)) && *reinterpret_cast<const volatile int *>(redo) != 0;
 }
 
+// After a wait that ran out: NaN for every row of the CTA's items, of which some were not computed, and for those that its parts go
+// into (the merge would take whatever the scratch holds). `thread`: of 256.
+template <int D, bool TOGETHER>
+__device__ __forceinline__ void leave_nan(const FwdPagedParams &p, int thread)
+{
+    const float nan = __uint_as_float(0x7fc00000u);
+    PagedWalk<TOGETHER> walk;
+    PagedItem t;
+#pragma unroll 1
+    while (walk.next(p, false, t)) {
+        if (t.part >= 0) {
+            p.part[static_cast<size_t>(t.part) * paged_part_floats(D) + (D + 1) * 2 * BM + thread] = nan;
+            continue;
+        }
+        int head = 0;
+        const int row = 256 * t.qb + thread, token = token_of<TOGETHER>(p, row, head);
+        if (token >= t.count || row >= p.rows) continue;
+        const size_t at = static_cast<size_t>(t.bh) * p.rows + row;
+#pragma unroll 1
+        for (int e = 0; e < p.pg.d; e += 8)
+            *reinterpret_cast<uint4 *>(p.out + at * p.pg.d + e) = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
+        if (p.lse) p.lse[at] = nan;
+    }
+}
+
 template <int D, bool STEEP, bool TOGETHER>
 __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_constant__ FwdPagedParams p)
 {
@@ -774,6 +799,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
+    if (warp >= 4 && *(volatile uint32_t *)&cta_abort != 0u) leave_nan<D, TOGETHER>(p, threadIdx.x - 128);
 }
 
 // Merge of the parts of item whole + blockIdx.x, 32 rows and 8 COLS columns by CTA: lane r has row r, a warp COLS columns. As many

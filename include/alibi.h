@@ -464,7 +464,8 @@ ALIBI_API int alibi_attn_decode_paged(const void *q, const alibi_pages *pages, c
  * query does not see are not used, whatever they hold; a value that is not finite makes its element of out NaN (or,
  * in tiles of 128 rows that all of the 256 queries see, infinite) for the queries that see it; a call that meets one takes
  * up to twice as long. out and lse are the same bits for the same arguments. A call takes up to 61 MB of scratch from the
- * library's stream-ordered pool where it cuts the work of few queries over many rows into parts.
+ * library's stream-ordered pool where it cuts the work of few queries over many rows into parts. Where a wait inside the kernel runs
+ * out (ALIBI_ERR_TIMEOUT), out and lse of the blocks of 256 queries concerned are NaN.
  */
 ALIBI_API int alibi_attn_fwd_paged(const void *q, const alibi_pages *pages, const int *lens, const int *count, void *out,
                                    float *lse, int B, int H, int T, int L, const float *slopes, void *stream);
@@ -541,7 +542,7 @@ ALIBI_API int alibi_selftest_fwd_timeout(const void *q, const void *k, const voi
  * arrival that nobody makes: 0 Q loaded, 1 keys and values loaded (first unit of the ring), 2 a unit (the second) read, 3 scores
  * computed, 4 weights written, 5 outputs computed, 6 outputs read, 7 values to be looked through loaded, 8 all roles done. The
  * kernel records ALIBI_ERR_TIMEOUT, waits for its loads and MMAs, frees TMEM and returns, and the context stays usable. out and lse
- * are left undefined. (Barriers 2 and 6 are waited for where a CTA has more than one item, or an item more than one tile.)
+ * of the rows of such a CTA are NaN. (Barriers 2 and 6 are waited for where a CTA has more than one item, or an item more than one tile.)
  */
 ALIBI_API int alibi_selftest_fwd_paged_timeout(const void *q, const alibi_pages *pages, const int *lens, const int *count, void *out,
                                                float *lse, int B, int H, int T, int L, int barrier, int wait_us, void *stream);

@@ -37,3 +37,26 @@ def test_prefill_timeout_drains_and_context_survives(ab, sizes, barrier, d):
     ab.alibi_selftest_fwd_paged_timeout(bf16(q)[1], kp, vp, table, barrier, lens=ints([N] * B), L=N)
     timed_out(ab)
     compare_prefill(ab, q, k, v, [N] * B, [T] * B)
+
+
+@pytest.mark.parametrize("d", [16, 64, 128])
+@pytest.mark.parametrize("sizes,barrier", [(TWO_ITEMS, b) for b in (0, 2, 3, 5, 6, 7)] + [(PARTS, b) for b in (0, 1, 4, 7)])
+def test_prefill_rows_that_were_not_computed_are_nan(ab, sizes, barrier, d):
+    # whatever was in out, and in the scratch of the parts, is not taken for a result
+    import torch
+    B, N, T = sizes
+    q, k, v = case(B + d, B, 1, 1, T, N, d)
+    counts = [T - b % 3 for b in range(B)]
+    out, lse, args = compare_prefill(ab, q, k, v, [N] * B, counts)
+    o, l = torch.full_like(out, 7.0), torch.full_like(lse, 7.0)
+    ab.alibi_selftest_fwd_paged_timeout(*args, barrier, lens=ints([N] * B), count=ints(counts), L=N, out=o, lse=l)
+    timed_out(ab)
+    ctas = torch.cuda.get_device_properties(0).multi_processor_count
+    for b, c in enumerate(counts):
+        # barriers 2 and 6 stop the CTAs that have two items, the last ones
+        if barrier in (2, 6) and b < 2 * ctas - B:
+            assert (o[b, :, :c].float() - out[b, :, :c].float()).abs().max() < 0.05
+            assert (l[b, :, :c] - lse[b, :, :c]).abs().max() < 0.05
+        else:
+            assert bool(o[b, :, :c].isnan().all()) and bool(l[b, :, :c].isnan().all()), (b, c)
+        assert bool((o[b, :, c:] == 7.0).all()) and bool((l[b, :, c:] == 7.0).all())
