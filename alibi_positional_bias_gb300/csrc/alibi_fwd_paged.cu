@@ -39,9 +39,10 @@
 // over the softmax to P V (tensor pipe 63 to 65% of active cycles in long items, 48% in prompts of 2048), and the instruction
 // cache, which the roles' code does not fit (0.6 to 0.8 cycles per issue without an instruction; the text of a second copy of
 // the exponentials, or waits out of line, cost 2 to 6%).
-// The place of the loops counts too, by whole lines of 128 bytes: 16 to 96 bytes of instructions before the roles make 723 / 715 us
-// (16 heads x 16384, 32 x 2048 of 32768) into 747 to 773 / 753 to 788, in the issuer's or the softmax's role alone into 726 to 750;
-// as it stands it is at the best of the eight places for both. Measure again after any change to this kernel.
+// The place of the loops counts too, by whole lines of 128 bytes: with 0 to 7 instructions of 16 bytes at the end of the loading role
+// 32 x 2048 of 32768 takes 741 / 739 / 739 / 737 / 720 / 721 / 737 / 756 us, 16 heads x 16384 749 / 757 / 753 / 747 / 732 / 742 / 760
+// / 760, 4 x 32 prompts 134.8 / 134.2 / 134.6 / 134.4 / 132.4 / 132.9 / 135.3 / 135.6; four stand there. Measure again after any change
+// to this kernel.
 
 #include <algorithm>
 #include <cmath>
@@ -348,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
         const int copies = boxes == 1 ? 1 : C::kChunks;
         uint32_t uc = 0;  // ring units issued
         int kk = 0;       // items begun
-        uint32_t looked = 0;  // tiles of V asked for by v_landed: the last may be in flight where the item ends early
+        uint32_t looked = 0;
         bool ok = true;
         PagedWalk walk;
         for (int pass = 0; ok;) {
@@ -387,11 +388,12 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
                 if (page < 0) lost[kk & 1] = 1, page = p.pg.pages;
                 const int ahead = page_at(t.top - u - 1);
                 ok = __all_sync(0xffffffffu, mbar_wait(&unit_empty[st], ph ^ 1, err, SITE_PG_UNIT));
-                if (!ok) break;
-                const bool to_look = with_k0 || (look && u > 1);  // a V goes out by v_landed
-                looked += to_look;
+                if (!ok) {
+                    looked += u == 1 && look;  // V(0), asked for with K(0), is in flight
+                    break;
+                }
                 if (lane == 0) {
-                    if (to_look) mbar_arrive_expect_tx(v_landed, C::kTileBytes);
+                    if (with_k0 || (look && u > 1)) mbar_arrive_expect_tx(v_landed, C::kTileBytes);
                     if (look) {
                         if (u < t.n) mbar_expect_tx(&unit_full[st], C::kTileBytes);
                     } else {
@@ -424,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
                     if (lane == 0) mbar_arrive(bias_full);
                 }
                 if (look) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(v_landed, (looked - 1) & 1, err, SITE_PG_FIX));
+                    ok = __all_sync(0xffffffffu, mbar_wait(v_landed, looked++ & 1, err, SITE_PG_FIX));
                     constexpr int kPieces = D / 8;  // of 16 bytes of a row
                     const int row0 = (t.top - u + 1) * BN;
                     // in a first pass the slots past the length, in a second one all
@@ -466,6 +468,9 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
         if (kk > 0) mbar_wait(q_full, (kk - 1) & 1, err, SITE_PG_Q, true);
         if (looked > 0) mbar_wait(v_landed, (looked - 1) & 1, err, SITE_PG_FIX, true);
         for (uint32_t n = uc > 2 ? uc - 2 : 0; n < uc; ++n) mbar_wait(&unit_full[n % 2], (n / 2) & 1, err, SITE_PG_UNIT, true);
+        // Four instructions of 16 bytes, run once: the loops of the roles that follow keep their best place (the head of this file).
+#pragma unroll
+        for (int i = 0; i < 4; ++i) __nanosleep(0);
     } else if (warp == 1) {
         // -------------------------------------------------------- MMA issuer (converged; one elected lane issues)
         constexpr uint32_t idS = idesc_bf16_f32(BM, BN, 0);
