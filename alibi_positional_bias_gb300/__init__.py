@@ -29,7 +29,7 @@ __all__ = [
     "alibi_kv_block_norms", "alibi_attn_decode_skip",
     "alibi_kv4_block_bytes", "alibi_kv4_cache", "alibi_kv4_write", "alibi_kv4_read", "alibi_attn_decode_kv4",
     "AlibiPages", "AlibiRows", "AlibiRotation", "alibi_pages", "alibi_paged_append", "alibi_attn_decode_paged",
-    "alibi_attn_fwd_paged", "alibi_selftest_fwd_paged_timeout",
+    "alibi_attn_fwd_paged", "alibi_selftest_fwd_paged_timeout", "alibi_selftest_decode_paged_timeout",
 ]
 
 ALIBI_OK, ALIBI_ERR_INVALID, ALIBI_ERR_UNSUPPORTED, ALIBI_ERR_CUDA, ALIBI_ERR_TIMEOUT, ALIBI_ERR_CHECK = 0, -1, -2, -3, -4, -5
@@ -144,6 +144,8 @@ def load(build_if_missing: bool = False):
         lib.alibi_attn_fwd_paged.restype = I
         lib.alibi_selftest_fwd_paged_timeout.argtypes = [vp, pages, vp, vp, vp, vp, I, I, I, I, I, I, vp]
         lib.alibi_selftest_fwd_paged_timeout.restype = I
+        lib.alibi_selftest_decode_paged_timeout.argtypes = [vp, pages, vp, vp, vp, I, I, I, I, I, vp]
+        lib.alibi_selftest_decode_paged_timeout.restype = I
         for name in ("alibi_attn_fwd", "alibi_attn_fwd_f32", "alibi_attn_decode", "alibi_attn_decode_splits",
                      "alibi_attn_probs_f32",
                      "alibi_attn_underflow_bf16", "alibi_check_error", "alibi_slopes"):
@@ -979,6 +981,19 @@ def alibi_selftest_fwd_timeout(q, k, v, wait_us: int = 20000, out=None, lse=None
         lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
     _check(load().alibi_selftest_fwd_timeout(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, H, N, d,
                                              int(wait_us), _stream(stream, q.device)), "alibi_selftest_fwd_timeout")
+    return out, lse
+
+
+def alibi_selftest_decode_paged_timeout(q, k_pages, v_pages, table, lens=None, L=None, out=None, lse=None, wait_us: int = 20000,
+                                        stream=None):
+    """Run the decode over pages with a wait of every CTA that must run out and a short limit (failure-path self-test)."""
+    shape, index = _paged_query(q, (4,))
+    B, H, T, d = shape
+    pages, _, C = _paged_cache(k_pages, v_pages, table, B, d, index)
+    L = _paged_bound(L, C, "alibi_selftest_decode_paged_timeout")
+    out, lse = _paged_outputs(out, lse, q, shape, index, stream)
+    _call_kv4(index, load().alibi_selftest_decode_paged_timeout, "alibi_selftest_decode_paged_timeout", stream, q.data_ptr(), pages,
+              _paged_ints(lens, B, index, "lens"), out.data_ptr(), lse.data_ptr(), B, H, T, L, int(wait_us))
     return out, lse
 
 

@@ -68,6 +68,8 @@ struct DecodePagedParams {
     int rows, chunks;        // G T, chunks of a KV head
     Divisor by_chunks, by_U, by_T, by_count;  // U: chunks of a sequence
     int count;               // CTAs of a cluster
+    int hold;                // 1: the self-test's, whose warps 0 wait for an arrival that nobody makes
+    uint64_t wait_ns;        // limit of every bounded wait
     float c1;                // log2(e) / sqrt(d)
     HeadSlopes slopes;
 };
@@ -359,13 +361,13 @@ __global__ void __launch_bounds__(kPgWarps * 32, 2) decode_paged_kernel(const __
 
     if (SHARES) griddep_launch_dependents();  // the merge kernel
     if (threadIdx.x == 0) {
-        cta_err_init(kWaitLimitNs);
+        cta_err_init(p.wait_ns);
         cta_check_init(p.status, smem_raw, pg_smem(D, NT));
         tma_prefetch_desc(&p.tk);
         tma_prefetch_desc(&p.tv);
     }
     if (lane == 0) {
-        for (int i = 0; i < kPgStages; ++i) mbar_init(&full[warp][i], 1);
+        for (int i = 0; i < kPgStages; ++i) mbar_init(&full[warp][i], 1 + (warp == 0 && i == 0 ? p.hold : 0));
         fence_mbar_init();
     }
     __syncthreads();
@@ -446,6 +448,8 @@ __global__ void __launch_bounds__(kPgWarps * 32, 2) decode_paged_kernel(const __
             }
         };
         int s = s1 - 1 - (SHARES ? warp : at + warp * count);  // this warp's stages: s, s - step, ...
+        // after a wait that ran out in an earlier chunk the ring may be out of step: nothing more is loaded into it
+        if (SHARES && *(volatile uint32_t *)&cta_abort != 0u) s = s0 - 1;
         for (int i = 0, k = slot; i < kPgStages; ++i) {
             fetch(s - i * step, k, page_at(s - i * step));
             if (++k == kPgStages) k = 0;
@@ -502,6 +506,8 @@ __global__ void __launch_bounds__(kPgWarps * 32, 2) decode_paged_kernel(const __
         // the warp's partial: reference R, l = sum of p, and the mean of v (never beyond the largest |v|)
         lost = __any_sync(0xffffffffu, lost);
         if (lost && lane == 0) atomicOr(p.status, ALIBI_DEV_RANGE);
+        // after a wait that ran out, here or in an earlier chunk, what was summed is not all that there is
+        lost |= *(volatile uint32_t *)&cta_abort != 0u;
         float *pw = reinterpret_cast<float *>(mine);  // [ROWS][D + 4]
 #pragma unroll
         for (int i = 0; i < NT; ++i)
@@ -672,13 +678,9 @@ cudaError_t launch_rows(DecodePagedParams &p, const alibi_pages *pages, cudaStre
     return p.rows <= 8 ? launch<D, 1>(p, pages, stream) : p.rows <= 16 ? launch<D, 2>(p, pages, stream) : launch<D, 4>(p, pages, stream);
 }
 
-}  // namespace
-}  // namespace alibi
-
-using namespace alibi;
-
-extern "C" int alibi_attn_decode_paged(const void *q, const alibi_pages *pages, const int *lens, void *out, float *lse, int B,
-                                       int H, int T, int L, const float *slopes, void *stream)
+// hold, wait_ns: of the self-test, else 0 and the usual limit
+int decode_paged(const void *q, const alibi_pages *pages, const int *lens, void *out, float *lse, int B, int H, int T, int L,
+                 const float *slopes, void *stream, int hold, uint64_t wait_ns)
 {
     const int st = check_pages(pages);
     if (st != ALIBI_OK) return st;
@@ -710,6 +712,8 @@ extern "C" int alibi_attn_decode_paged(const void *q, const alibi_pages *pages, 
     p.G = H / pages->heads;
     p.L = L;
     p.rows = p.G * T;
+    p.hold = hold;
+    p.wait_ns = wait_ns;
     p.by_T = Divisor(static_cast<uint32_t>(T));
     p.c1 = 1.4426950408889634f / sqrtf(static_cast<float>(pages->d));
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
@@ -721,4 +725,22 @@ extern "C" int alibi_attn_decode_paged(const void *q, const alibi_pages *pages, 
         default: e = launch_rows<16>(p, pages, cs); break;
     }
     return e == cudaSuccess ? ALIBI_OK : ALIBI_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace alibi
+
+using namespace alibi;
+
+extern "C" int alibi_attn_decode_paged(const void *q, const alibi_pages *pages, const int *lens, void *out, float *lse, int B,
+                                       int H, int T, int L, const float *slopes, void *stream)
+{
+    return decode_paged(q, pages, lens, out, lse, B, H, T, L, slopes, stream, 0, kWaitLimitNs);
+}
+
+extern "C" int alibi_selftest_decode_paged_timeout(const void *q, const alibi_pages *pages, const int *lens, void *out, float *lse,
+                                                   int B, int H, int T, int L, int wait_us, void *stream)
+{
+    if (wait_us < 1 || wait_us > 1000000) return ALIBI_ERR_INVALID;
+    return decode_paged(q, pages, lens, out, lse, B, H, T, L, nullptr, stream, 1, static_cast<uint64_t>(wait_us) * 1000u);
 }

@@ -446,7 +446,8 @@ ALIBI_API int alibi_paged_append(const alibi_rows *k, const alibi_rows *v, const
  * enter the values' products as two bf16 numbers, off by 2^-16 of themselves. Those sums are divided by the weights' at
  * the end: values beyond 2^120 / L in magnitude may overflow them, where 2^96 is safe for every L. out and lse are the same bits
  * for the same arguments. A call takes up to 11 MB of scratch from the library's stream-ordered pool where it splits sequences
- * over several CTAs and merges them in a second kernel.
+ * over several CTAs and merges them in a second kernel. Where a wait inside the kernel runs out (ALIBI_ERR_TIMEOUT), out and lse of
+ * the rows concerned are NaN.
  */
 ALIBI_API int alibi_attn_decode_paged(const void *q, const alibi_pages *pages, const int *lens, void *out, float *lse, int B,
                                       int H, int T, int L, const float *slopes, void *stream);
@@ -535,6 +536,13 @@ ALIBI_API int alibi_selftest_timeout(void *stream);
  */
 ALIBI_API int alibi_selftest_fwd_timeout(const void *q, const void *k, const void *v, void *out, float *lse, int B,
                                          int H, int N, int d, int wait_us, void *stream);
+
+/*
+ * The same through the decode over pages (arguments and checks of alibi_attn_decode_paged): every bounded wait gives up after wait_us
+ * microseconds, and the first warp of every CTA waits for an arrival that nobody makes. out and lse of sequences with rows are NaN.
+ */
+ALIBI_API int alibi_selftest_decode_paged_timeout(const void *q, const alibi_pages *pages, const int *lens, void *out, float *lse,
+                                                  int B, int H, int T, int L, int wait_us, void *stream);
 
 /*
  * The same through the prefill over pages (arguments and checks of alibi_attn_fwd_paged; the kernel of steep slopes, heads

@@ -5,7 +5,7 @@ import pytest
 import paged_ref as ref
 from paged_ref import bf16, ints
 from test_gpu_fwd_paged import compare as compare_prefill
-from test_gpu_paged import case
+from test_gpu_paged import case, compare as compare_decode
 
 pytestmark = pytest.mark.gpu
 
@@ -60,3 +60,18 @@ def test_prefill_rows_that_were_not_computed_are_nan(ab, sizes, barrier, d):
         else:
             assert bool(o[b, :, :c].isnan().all()) and bool(l[b, :, :c].isnan().all()), (b, c)
         assert bool((o[b, :, c:] == 7.0).all()) and bool((l[b, :, c:] == 7.0).all())
+
+
+# (sequences, KV heads, heads of each, new tokens, length, d): whole chunks, clusters, equal shares that go on from chunk to chunk,
+# two and four groups of rows
+@pytest.mark.parametrize("B,Hkv,G,T,N,d", [(300, 2, 1, 1, 70, 128), (1, 4, 2, 1, 3000, 128), (1, 1, 1, 1, 9000, 128), (9, 37, 1, 1, 2000, 64),
+                                           (3, 2, 3, 4, 500, 64), (5, 2, 5, 5, 700, 32), (2, 1, 40, 1, 300, 16)])
+def test_decode_rows_of_a_wait_that_ran_out_are_nan(ab, B, Hkv, G, T, N, d):
+    # a sum over some of the keys looks like a result
+    q, k, v = case(B + N, B, Hkv, G, T, N, d)
+    lens = [N - (7 * b) % (N // 2) for b in range(B)]
+    kp, vp, table = ref.paged(k, v, lens, 16)
+    out, lse = ab.alibi_selftest_decode_paged_timeout(bf16(q)[1], kp, vp, table, lens=ints(lens), L=N)
+    timed_out(ab)
+    assert bool(out.isnan().all()) and bool(lse.isnan().all())
+    compare_decode(ab, q, k, v, lens)
