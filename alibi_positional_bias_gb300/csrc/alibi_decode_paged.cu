@@ -443,8 +443,8 @@ __global__ void __launch_bounds__(kPgWarps * 32, 2) decode_paged_kernel(const __
                 const bool values = lane >= 16;
                 uint8_t *const to = mine + slot_ * kPgStageBytes + (values ? kPgStageBytes / 2 : 0) + part * (2 * W);
                 for (int h = 0; h < copies; ++h)
-                    load_box(to + h * (TK * 2 * W), values ? &p.tv : &p.tk, p.pg.slot_of(s * TK + part), h, hk, page, box * 2 * W,
-                             &full[warp][slot_]);
+                    load_box<W>(to + h * (TK * 2 * W), values ? &p.tv : &p.tk, p.pg, box, D / W / copies, p.pg.slot_of(s * TK + part),
+                                h, hk, page, &full[warp][slot_]);
             }
         };
         int s = s1 - 1 - (SHARES ? warp : at + warp * count);  // this warp's stages: s, s - step, ...

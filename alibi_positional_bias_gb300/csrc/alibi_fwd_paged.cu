@@ -406,14 +406,14 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_paged_kernel(const __grid_con
                     const int at = lane * box * 128;  // of the box in a swizzle atom
                     for (int c = 0; c < copies; ++c) {
                         if (u < t.n)
-                            load_box(smem + C::kK + st * C::kTileBytes + c * C::kChunkBytes + at, &p.tk,
-                                     p.pg.slot_of((t.top - u) * BN + lane * box), c, hk, page, box * 128, &unit_full[st]);
+                            load_box<64>(smem + C::kK + st * C::kTileBytes + c * C::kChunkBytes + at, &p.tk, p.pg, box, C::kChunks / copies,
+                                         p.pg.slot_of((t.top - u) * BN + lane * box), c, hk, page, &unit_full[st]);
                         if (with_k0)
-                            load_box(smem + C::kV + (st ^ 1) * C::kTileBytes + c * C::kChunkBytes + at, &p.tv,
-                                     p.pg.slot_of(t.top * BN + lane * box), c, hk, page, box * 128, v_landed);
+                            load_box<64>(smem + C::kV + (st ^ 1) * C::kTileBytes + c * C::kChunkBytes + at, &p.tv, p.pg, box, C::kChunks / copies,
+                                         p.pg.slot_of(t.top * BN + lane * box), c, hk, page, v_landed);
                         else if (u >= 1 && !(look && u == 1))
-                            load_box(v + c * C::kChunkBytes + at, &p.tv, p.pg.slot_of((t.top - u + 1) * BN + lane * box), c, hk, before,
-                                     box * 128, look ? v_landed : &unit_full[st]);
+                            load_box<64>(v + c * C::kChunkBytes + at, &p.tv, p.pg, box, C::kChunks / copies,
+                                         p.pg.slot_of((t.top - u + 1) * BN + lane * box), c, hk, before, look ? v_landed : &unit_full[st]);
                     }
                 }
                 __syncwarp();

@@ -27,6 +27,7 @@ enum : uint32_t {
     TMEM_LANES = 4,  // TMEM lanes outside the warp's quadrant
     SMEM_DESC = 5,   // MMA / copy operand outside the shared-memory window
     BULK_LOAD = 6,   // untiled load: source, destination or size off the 16-byte grid, or destination outside the window
+    PAGE_BOX = 7,    // box of a page: coordinates outside the page or the pool
 };
 
 // 16-bit elements: a tiled copy starts on a 16-byte boundary when x is a multiple of 8.
@@ -65,6 +66,20 @@ ALIBI_HD inline uint32_t idesc_n(uint32_t idesc) { return ((idesc >> 17) & 0x3Fu
 
 // Start address (bytes) in a shared-memory matrix descriptor (16-byte units, bits 0-13).
 ALIBI_HD inline uint32_t desc_addr(uint64_t desc) { return static_cast<uint32_t>(desc & 0x3FFFu) << 4; }
+
+// A box of pages: `box` slots (a power of two) of `halves` parts of head `head` of page `page`, from slot `slot` of part `half` on, in
+// pools of `pages` pages of `heads` heads of `slots` slots of `parts` parts of a row. Boxes begin on multiples of their size; page number
+// `pages`, one beyond the pool, is what a box of zeros has.
+ALIBI_HD inline bool page_box(int slot, int half, int head, int page, int box, int halves, int slots, int parts, int heads, int pages)
+{
+    return slot >= 0 && slot < slots && box > 0 && (slot & (box - 1)) == 0 && box <= slots - slot && half >= 0 && halves > 0 &&
+           halves <= parts - half && head >= 0 && head < heads && page >= 0 && page <= pages;
+}
+
+// Bytes of such a box in shared memory, of rows of `width` elements of 16 bits, and the boundary it starts on: its size, or where the
+// swizzle's pattern begins anew, whichever is less.
+ALIBI_HD inline uint32_t page_box_bytes(int box, int halves, int width) { return static_cast<uint32_t>(box * halves * width) * 2u; }
+ALIBI_HD inline uint32_t page_box_align(int box, int width) { return box * width * 2 < 1024 ? static_cast<uint32_t>(box * width) * 2u : 1024u; }
 
 // The site word a failed check records.
 ALIBI_HD inline uint32_t site(uint32_t id, uint32_t value) { return (id << 24) | (value & 0xFFFFFFu); }

@@ -60,16 +60,20 @@ inline Pages pages_of(const alibi_pages *p)
     return g;
 }
 
-// Load of one box of a page: slots from `slot` on of head `head`, 64 elements of each from 64 `half` on (or all of fewer), `bytes`
-// bytes, a power of two. It lies on a multiple of that or of 1024, where the swizzle's pattern begins anew, and completes on
-// `bar`. With a map of both halves the second half follows the first.
-__device__ __forceinline__ void load_box(void *dst, const void *tmap, int slot, int half, int head, int page, uint32_t bytes,
-                                         uint64_t *bar)
+// Load of one box of a page: `box` slots from `slot` on of head `head`, WIDTH elements of each from WIDTH `half` on (a row of fewer is
+// filled up with zeros), of `halves` parts, as the map has them, one after the other. It completes on `bar`.
+template <int WIDTH>
+__device__ __forceinline__ void load_box(void *dst, const void *tmap, const Pages &pg, int box, int halves, int slot, int half, int head,
+                                         int page, uint64_t *bar)
 {
 #ifdef ALIBI_CHECKS
-    if (!check_smem(smem_u32(dst), bytes, bytes < 1024 ? bytes : 1024)) return check_fail(check::TMA_LOAD, smem_u32(dst));
+    const int parts = pg.d > WIDTH ? pg.d / WIDTH : 1;
+    if (!check::page_box(slot, half, head, page, box, halves, 1 << pg.shift, parts, pg.heads, pg.pages))
+        return check_fail(check::PAGE_BOX, static_cast<uint32_t>(slot));
+    if (!check_smem(smem_u32(dst), check::page_box_bytes(box, halves, WIDTH), check::page_box_align(box, WIDTH)))
+        return check_fail(check::TMA_LOAD, smem_u32(dst));
 #endif
-    (void)bytes;
+    (void)pg, (void)box, (void)halves;
     asm volatile(
         "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
