@@ -27,7 +27,7 @@
 //             decode has them, took longer than whole items: a CTA with many short items is late, whatever their tiles.)
 //
 // Of up to 128 tokens the rows of the G heads of a group may go together, as one head with G T rows of which each has its own
-// slope and token (`together` below): they pass the group's keys once and fill the tiles (64 x 8 (x 8) heads x 17 new of 2048 tokens
+// slope and token (paged_parts.h): they pass the group's keys once and fill the tiles (64 x 8 (x 8) heads x 17 new of 2048 tokens
 // 648 -> 139 us).
 //
 // Where some head is steep (a slope above 4 / log2(e)), the bias is taken element by element from the whole distance: the
@@ -51,6 +51,7 @@
 #include "alibi.h"
 #include "divide.h"
 #include "fwd_tiles.cuh"
+#include "paged_parts.h"
 #include "pages.cuh"
 #include "ptx.cuh"
 
@@ -58,7 +59,7 @@ namespace alibi {
 namespace {
 
 constexpr float kSteep = 4.0f;  // m log2(e)
-constexpr int kMostParts = 16;
+using paged::kMostParts;
 
 struct FwdPagedParams {
     CUtensorMap tq;      // [B H, T, d] bf16, box {64, 128, 1}, 128-byte swizzle
@@ -878,62 +879,6 @@ __global__ void __launch_bounds__(256) fwd_paged_merge_kernel(const __grid_const
     }
 }
 
-// Parts into which the items of the last, incomplete round, the shortest, are cut: the number with the least estimated time of that
-// round, in tiles of 256 rows and 128 keys (1.4 to 1.6 us): of the longest item where all parts run at once, else of the mean one.
-// An item costs some four tiles beside its own; the merge, 1.6 and what reading each partial takes. Measured, in us, uncut /
-// in 2 / 3 / 4 / 6 / 8 parts, what is taken in brackets (heads x new tokens of length):
-//   2 x 6 x 100 of 999 (d = 64)  [4]  18.3 / 16.4 / 14.0 / 14.1 / 14.5 / 14.9
-//   32 x 64 of 1024              [4]  18.3 / 15.8 / 14.5 / 13.9 / 18.6 / 18.7
-//   6 x 100 of 500               [2]  13.1 / 12.6 / 13.1 / 13.0 / 13.0 / 13.1
-//   6 x 1024 of 1024             [4]  20.6 / 18.2 / 16.8 / 17.2 / 17.4 / 21.7
-//   4 x 8 x 128 of 4096          [4]  51.2 / 34.5 / 28.3 / 25.7 / 33.5 / 30.6
-//   32 x 256 of 32768            [4]  405 / 211 / 146 / 113 / 154 / 122
-//   40 x 512 of 8192             [3]  108 / 120 / 93.4 / 107 /  -  /  -
-//   32 x 2048 of 32768           [4]  794 / 799 / 803 / 722 /  -  /  -
-//   16 x 700 of 700              [1]  20.4 / 20.7 / 19.4 / 24.8 / 25.5 / 23.7
-//   16 x 2048 of 2048            [1]  35.6 / 47.7 / 50.3 /  -  /  -  /  -
-struct Parts {
-    int parts;
-    double cost;  // of the last round
-};
-Parts paged_parts(int rest, int BH, int T, int head_rows, int L, int sms)  // head_rows: T, together G T
-{
-    const int before = L - std::min(T, L);
-    const double blocks = static_cast<double>(rest) / BH, rows = std::min(head_rows, 256) / 256.0;
-    const double mean = std::ceil((before + std::min<double>(T, 128 * (blocks + 1))) / 128);
-    const double longest = std::ceil((before + std::min<double>(T, 256 * std::ceil(blocks))) / 128);
-    const auto cost = [&](int parts) {
-        const long long rounds = (static_cast<long long>(rest) * parts + sms - 1) / sms;
-        return rounds * (std::ceil((rounds == 1 ? longest : mean) / parts) + 4) +
-               (parts > 1 ? 1.6 + (0.02 + 0.008 * rows) * rest * parts : 0);
-    };
-    Parts best = {1, rest > 0 ? cost(1) : 0};
-    for (int n = 2; n <= kMostParts && rest * n <= 3 * sms; ++n)
-        if (rest > 0 && cost(n) < best.cost) best = {n, cost(n)};
-    return best;
-}
-
-// Whether the rows of the heads of a group go together: of few tokens a query tile of 128 rows has room for those of several heads,
-// which then pass the keys once, at the price of a bias that is computed element by element from the whole distance
-// (1.25). Of up to 128 tokens, so that the rows of a block read the same pages either way. Measured, in us, apart / together, what is
-// taken in brackets (heads (x G) x new tokens of length, d = 128):
-//   8 x 8 (x 4) x 32 of 2048    [t]  54.8 / 28.2       8 x 8 (x 8) x 64 of 2048    [t]  97.1 / 42.7
-//   8 x 8 (x 8) x 20 of 8192    [t]  312 / 78.3        64 x 8 (x 8) x 17 of 2048   [t]  648 / 139
-//   32 x 8 (x 4) x 48 of 1000   [t]  106 / 48.5        1 x 8 (x 4) x 32 of 32768   [t]  95.5 / 41.6
-//   16 x 4 (x 2) x 64 of 4096   [t]  51.3 / 41.8       16 x 8 (x 2) x 100 of 2048  [t]  55.1 / 42.4
-//   1 x 8 (x 4) x 128 of 8192   [t]  34.0 / 31.4       4 x 8 (x 4) x 128 of 4096   [t]  51.9 / 49.6
-//   1 x 8 (x 4) x 64 of 1024    [a]  14.1 / 15.8       2 x 2 (x 3) x 128 of 700    [a]  16.3 / 17.8
-bool together(const FwdPagedParams &p, int Hkv, int sms)
-{
-    const int G = p.H / Hkv, rows = G * p.T;
-    if (G == 1 || p.T > BM) return false;
-    const double tiles = std::ceil(p.L / 128.0);
-    const auto cost = [&](int items, int head_rows) {
-        return static_cast<double>(items / sms) * (tiles + 4) + paged_parts(items % sms, items, p.T, head_rows, p.L, sms).cost;
-    };
-    return 1.25 * cost(p.BH / G * ((rows + 255) / 256), rows) < cost(p.BH, p.T);
-}
-
 template <int D, bool TOGETHER>
 cudaError_t launch(FwdPagedParams &p, const alibi_pages *pages, const void *q, cudaStream_t stream)
 {
@@ -952,7 +897,7 @@ cudaError_t launch(FwdPagedParams &p, const alibi_pages *pages, const void *q, c
     const int sms = num_sms();
     p.rest = p.num_items % sms;
     p.whole = p.num_items - p.rest;
-    p.parts = paged_parts(p.rest, p.BH, p.T, p.rows, p.L, sms).parts;
+    p.parts = paged::parts_of(p.rest, p.BH, p.T, p.rows, p.L, sms).parts;
     if (p.parts == 1) p.whole = p.num_items, p.rest = 0;
     p.num_units = p.whole + p.rest * p.parts;
     p.div_rest = Divisor(static_cast<uint32_t>(std::max(p.rest, 1)));
@@ -1015,7 +960,7 @@ int fwd_paged(const void *q, const alibi_pages *pages, const int *lens, const in
     p.blocks = blocks;
     p.hold = hold;
     p.wait_ns = wait_ns;
-    const bool join = hold < 0 && together(p, pages->heads, num_sms());
+    const bool join = hold < 0 && paged::together(p.BH, p.G, T, L, num_sms());
     if (join) {
         p.BH = B * pages->heads;
         p.H = pages->heads;
