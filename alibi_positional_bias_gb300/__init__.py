@@ -889,7 +889,8 @@ def alibi_attn_fwd_paged(q, k_pages, v_pages, table, lens=None, count=None, L=No
     """ALiBi attention of up to T new tokens of each sequence, a prompt or a part of one, over the pages that hold them
     and what came before. q: bf16 [B, H, T, d]; count: int32 CUDA tensor [B], the new tokens of each sequence (None: T); lens:
     their lengths, the new tokens included; k_pages, v_pages, table, L and slopes as in alibi_attn_decode_paged. Query t <
-    count[b] has position lens[b] - count[b] + t; out and lse of tokens from count[b] on are left as they were.
+    count[b] has position lens[b] - count[b] + t; out and lse of tokens from count[b] on are left as they were, and a
+    sequence with a count of 0 is not looked at, whatever its length.
     Returns (out, lse): bf16 [B, H, T, d] and fp32 [B, H, T]; those made here belong to `stream`."""
     lib = _kv4_names()[6]
     shape, index = _paged_query(q, (4,))

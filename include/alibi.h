@@ -459,7 +459,8 @@ ALIBI_API int alibi_attn_decode_paged(const void *q, const alibi_pages *pages, c
  * 2^24. count: device int32 [B], or NULL for T; out and lse of tokens from count[b] on are left as they were. A
  * query with i < 0 sees no row: its out is 0 and its lse -inf. A sequence with count[b] outside [0, T] or lens[b]
  * outside [0, L] gets NaN in out and lse (of all T tokens where count[b] is at fault), one with a page number outside
- * [0, pages) in the blocks of 256 queries that read it, and alibi_check_error returns ALIBI_ERR_RANGE.
+ * [0, pages) in the blocks of 256 queries that read it, and alibi_check_error returns ALIBI_ERR_RANGE. A sequence with count[b] = 0
+ * has no queries and is not looked at: its length and page numbers may be anything, and nothing is reported of them.
  * Runs the tensor-core pipeline of alibi_attn_fwd (weights are rounded to bf16 for the P V product; values as large as in
  * alibi_attn_decode_paged). Rows that a
  * query does not see are not used, whatever they hold; a value that is not finite makes its element of out NaN (or,
