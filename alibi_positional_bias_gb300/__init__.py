@@ -680,7 +680,11 @@ def _paged_ints(t, B, index, name):
     """The address of int32 [B], or None."""
     if t is None:
         return None
-    if not (t.dtype is _kv4_names()[2] and t.shape == (B,) and t.get_device() == index and t.is_contiguous()):
+    try:
+        good = t.dtype is _kv4_names()[2] and t.shape == (B,) and t.get_device() == index and t.is_contiguous()
+    except AttributeError:
+        good = False
+    if not good:
         _need_on(t, _kv4_names()[2], (B,), name, index)
     return t.data_ptr()
 
