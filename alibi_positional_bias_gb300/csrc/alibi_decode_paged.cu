@@ -22,9 +22,10 @@
 // mma.sync and not tcgen05.mma: of 8 rows a tile of 128 would be empty but for 1/16.
 //
 // Measured, launches in one graph over caches that together are larger than L2: 64 x 40 heads x 8192 tokens of d = 128 (10.7 GB)
-// 1407 to 1428 us, 7.5 to 7.6 TB/s, bound by HBM; 1 x 40 x 8192 28.8 us (5.8 TB/s), 16 x 8 (x 4) x 2049..4097 39 (5.7), 1 x 4
+// 1407 to 1448 us, 7.4 to 7.6 TB/s, bound by HBM; 1 x 40 x 8192 29 us (5.8 TB/s), 16 x 8 (x 4) x 2049..4097 39 (5.7), 1 x 4
 // (x 4) x 131071 47 (5.7): what a launch, the first loads and the merge take (4 to 8 us) over HBM's time; 8 x 16 (x 2) x 4
-// new tokens of 1025..2048, d = 64, 13.5 us: a warp's chain of 32 stages; 1 x 6 x 100 2.7 us: a launch. A warp's step (a stage
+// new tokens of 1025..2048, d = 64, 13.5 us: a launch, up to eight stages one after another in each warp of a cluster of two,
+// and the cluster's merge; 1 x 6 x 100 2.8 us: a launch. A warp's step (a stage
 // of one row group at d = 128) is 1240 to 1350 cycles when L2 has the pages: 700 of copies and waits, 970 of products and
 // softmax, partly at the same time; eight warps per SM keep up with HBM at 3000 cycles a step, four at 1500.
 

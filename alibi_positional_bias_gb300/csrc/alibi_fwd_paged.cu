@@ -33,9 +33,9 @@
 // Where some head is steep (a slope above 4 / log2(e)), the bias is taken element by element from the whole distance: the
 // column part on the tensor core and the row part would cancel with a rounding of 2^-24 of 128 slopes.
 //
-// Measured (d = 128, launches in one graph): 16 heads x 16384 tokens 730 us (the dense prefill 695), 32 heads x 2048 new tokens
-// of 32768 716 to 731 us (1460 to 1488 TFLOP/s), 4 x 32 prompts of up to 2048 134 us (889 TFLOP/s), 8 (x 4) heads x 256 new of 32768
-// 113 us; 2 x 6 heads x 100 new of up to 999, d = 64, 14.1 us. What bounds it is what bounds the dense prefill: the chain from S
+// Measured (d = 128, launches in one graph): 16 heads x 16384 tokens 726 to 748 us (the dense prefill 695 to 710), 32 heads x 2048 new
+// tokens of 32768 717 to 737 us (1447 to 1488 TFLOP/s), 4 x 32 prompts of up to 2048 133 us (895 TFLOP/s), 8 (x 4) heads x 256 new of
+// 32768 113 us; 2 x 6 heads x 100 new of up to 999, d = 64, 13.4 to 14.2 us. What bounds it is what bounds the dense prefill: the chain from S
 // over the softmax to P V (tensor pipe 63 to 65% of active cycles in long items, 48% in prompts of 2048), and the instruction
 // cache, which the roles' code does not fit (0.6 to 0.8 cycles per issue without an instruction; the text of a second copy of
 // the exponentials, or waits out of line, cost 2 to 6%).

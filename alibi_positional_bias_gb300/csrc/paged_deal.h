@@ -15,7 +15,8 @@ constexpr int kWarps = 4;          // of a CTA, two CTAs per SM
 constexpr int kMostCluster = 16;
 
 // us of a warp's step, one stage, of head size d with `groups` groups of 8 rows, where its SM has no other CTA: the
-// chain of its own instructions, whatever memory gives (0.63 at d = 128 when last measured; 0.70 chooses no worse).
+// chain of its own instructions, whatever memory gives (0.63 at d = 128 when last measured; 0.70 chooses no worse). The factors of
+// two and four groups are estimates that the last rows of the table below check.
 inline double step_us(int d, int groups)
 {
     const double t = d == 128 ? 0.70 : d == 64 ? 0.72 : d == 32 ? 1.08 : 1.8;
@@ -46,6 +47,18 @@ inline double step_us(int d, int groups)
 //   8 x 16 (x 2) x 4 new, 2048 x 64  [2]  15.0 / 15.2 (2) / 21.3
 //   1 x 8 (x 8) x 16384 x 64     [16]  85.1 / 16.0 (8) 12.8 (12) 12.1 (16) / 13.3
 //   1 x 32 x 16384 x 32          [8]   61.4 / 18.3 (6) 16.1 (8) / 20.9
+// and with 16 and 32 rows of a KV head, d = 128 and then 64. Shares are taken for too little there, as their estimate is of memory's time
+// alone and a step of four groups takes longer than that:
+//   8 x 8 (x 4) x 4 new, 2048    [4]   29.4 / 19.5 (2) 17.1 (4) / 25.3
+//   1 x 8 (x 4) x 4 new, 16384   [S]   200 / 31.5 (8) 24.0 (12) 21.6 (16) / 21.5
+//   16 x 8 (x 8) x 2 new, 4096   [2]   55.4 / 47.2 (2) / 58.7
+//   40 x 8 (x 4) x 4 new, 2048   [S]   76.6 /   -   / 74.2
+//   8 x 8 (x 8) x 4 new, 2048    [S]   43.2 / 27.6 (3) 24.2 (4) / 36.9
+//   8 x 8 (x 8) x 4 new, 8192    [S]   149 / 71.9 (3) 57.0 (4) / 70.2
+//   1 x 8 (x 8) x 4 new, 32768   [S]   561 / 80.2 (8) 55.7 (16) / 37.3
+//   64 x 8 (x 8) x 4 new, 2048   [W]   107 /   -   / 142
+//   8 x 16 (x 2) x 8 new, 2048   [2]   17.9 / 16.4 (2) / 27.5
+//   4 x 8 (x 4) x 8 new, 8192    [S]   83.6 / 27.1 (6) 23.3 (8) / 31.8
 inline int ctas_of_chunk(long long units, int stages, int ctas, const int (&fit)[kMostCluster + 1], double step)
 {
     constexpr double kStage = 0.0011;
