@@ -742,6 +742,6 @@ extern "C" int alibi_attn_decode_paged(const void *q, const alibi_pages *pages, 
 extern "C" int alibi_selftest_decode_paged_timeout(const void *q, const alibi_pages *pages, const int *lens, void *out, float *lse,
                                                    int B, int H, int T, int L, int wait_us, void *stream)
 {
-    if (wait_us < 1 || wait_us > 1000000) return ALIBI_ERR_INVALID;
+    if (!selftest_wait(wait_us)) return ALIBI_ERR_INVALID;
     return decode_paged(q, pages, lens, out, lse, B, H, T, L, nullptr, stream, 1, static_cast<uint64_t>(wait_us) * 1000u);
 }

@@ -993,6 +993,6 @@ extern "C" int alibi_attn_fwd_paged(const void *q, const alibi_pages *pages, con
 extern "C" int alibi_selftest_fwd_paged_timeout(const void *q, const alibi_pages *pages, const int *lens, const int *count, void *out,
                                                 float *lse, int B, int H, int T, int L, int barrier, int wait_us, void *stream)
 {
-    if (barrier < 0 || barrier >= HOLD_COUNT || wait_us < 1 || wait_us > 1000000) return ALIBI_ERR_INVALID;
+    if (barrier < 0 || barrier >= HOLD_COUNT || !selftest_wait(wait_us)) return ALIBI_ERR_INVALID;
     return fwd_paged(q, pages, lens, count, out, lse, B, H, T, L, nullptr, stream, barrier, static_cast<uint64_t>(wait_us) * 1000u);
 }

@@ -43,6 +43,10 @@ inline int check_pages(const alibi_pages *p)
     return ALIBI_OK;
 }
 
+// Limits that the self-tests of the failure paths take: the waits for copies and MMAs in flight have the same one, and these are to
+// have ended before the kernel does.
+inline bool selftest_wait(int wait_us) { return wait_us >= 1000 && wait_us <= 1000000; }
+
 inline Pages pages_of(const alibi_pages *p)
 {
     Pages g;

@@ -540,15 +540,16 @@ ALIBI_API int alibi_selftest_fwd_timeout(const void *q, const void *k, const voi
 
 /*
  * The same through the decode over pages (arguments and checks of alibi_attn_decode_paged): every bounded wait gives up after wait_us
- * microseconds, and the first warp of every CTA waits for an arrival that nobody makes. out and lse of sequences with rows are NaN.
+ * microseconds (1000 <= wait_us <= 1000000), and the first warp of every CTA waits for an arrival that nobody makes. out and lse of
+ * sequences with rows are NaN.
  */
 ALIBI_API int alibi_selftest_decode_paged_timeout(const void *q, const alibi_pages *pages, const int *lens, void *out, float *lse,
                                                   int B, int H, int T, int L, int wait_us, void *stream);
 
 /*
  * The same through the prefill over pages (arguments and checks of alibi_attn_fwd_paged; the kernel of steep slopes, heads
- * apart): every bounded wait gives up after wait_us microseconds, and one barrier of each CTA, `barrier` in [0, 9), waits for an
- * arrival that nobody makes: 0 Q loaded, 1 keys and values loaded (first unit of the ring), 2 a unit (the second) read, 3 scores
+ * apart): every bounded wait gives up after wait_us microseconds (1000 <= wait_us <= 1000000), and one barrier of each CTA, `barrier`
+ * in [0, 9), waits for an arrival that nobody makes: 0 Q loaded, 1 keys and values loaded (first unit of the ring), 2 a unit (the second) read, 3 scores
  * computed, 4 weights written, 5 outputs computed, 6 outputs read, 7 values to be looked through loaded, 8 all roles done. The
  * kernel records ALIBI_ERR_TIMEOUT, waits for its loads and MMAs, frees TMEM and returns, and the context stays usable. out and lse
  * of the rows of such a CTA are NaN. (Barriers 2 and 6 are waited for where a CTA has more than one item, or an item more than one tile.)
